@@ -449,6 +449,113 @@ nvfp4_status moe_expert_backward_ste(const moe_bf16_weights_t* w, int64_t T, int
                                      float* dw2_dev, float* dprob_dev, void* bwd_ws_dev, size_t bwd_ws_bytes,
                                      void* stream);
 
+/* ---- Routing of given logits -------------------------------------------------------------
+ * moe_route_topk takes the router's logits (moe_router_topk's logits_dev, or any other router's)
+ * where the step above is not the routing wanted: sigmoid scores, a balancing bias that only
+ * takes part in the choice, experts limited to groups, weights that are not renormalised or are
+ * scaled, masked experts, or logits of another type or number of experts.
+ *   s_e  = softmax(l)_e or 1 / (1 + e^-l_e) (FP32); an expert with l_e = -inf or NaN is masked:
+ *          s_e = 0, chosen only where fewer than k others are left
+ *   o_e  = l_e without bias, s_e + bias_e with one; larger o first, the lower expert id first on
+ *          equal o, masked experts (and those with o = -inf or NaN) last
+ *   with n_group > 1, the experts chosen come from the topk_group groups (of E / n_group
+ *          consecutive experts) with the largest group score, the lower group first on equal scores:
+ *          max o (MOE_GROUP_MAX) or the sum of the two largest s_e (+ bias_e) of the unmasked
+ *          (MOE_GROUP_TOP2)
+ *   w_j  = scale * s_j / sum of the k chosen s if renormalize (0 if that sum is 0), else scale * s_j
+ * Every row gives k different ids in [0, E).  A token's ids and weights do not depend on T or on
+ * the other tokens. */
+typedef enum { NVFP4_TYPE_F32 = 0, NVFP4_TYPE_BF16 = 1, NVFP4_TYPE_F16 = 2 } nvfp4_type;
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+typedef struct {
+    int32_t score;        /* MOE_SCORE_* */
+    int32_t k;            /* 1 <= k <= min(32, topk_group * E / n_group) */
+    int32_t n_group;      /* 1 <= n_group <= 32, a divisor of E */
+    int32_t topk_group;   /* 1 <= topk_group <= n_group */
+    int32_t group_score;  /* MOE_GROUP_*; not used with n_group = 1 */
+    int32_t renormalize;  /* 0 or 1 */
+    float scale;          /* finite */
+} moe_route_params;
+
+/*  logits_dev     [T][ld] of `type`, the first E of each row used; element aligned; 1 <= E <= 1024,
+ *                 ld >= E
+ *  bias_dev       float [E] or NULL
+ *  topk_ids_dev   int32 [T][k] out, topk_w_dev float [T][k] out, slot order
+ * Device error: NVFP4_ERR_NONFINITE (a logit is NaN or +inf; the outputs are as above, +inf as the
+ * limit of large logits). */
+nvfp4_status moe_route_topk(const void* logits_dev, int type, int64_t T, int E, int64_t ld,
+                            const moe_route_params* params, const float* bias_dev, int32_t* topk_ids_dev,
+                            float* topk_w_dev, void* stream);
+
+/* moe_route_topk_backward -- the gradient of moe_route_topk's weights with respect to its logits
+ * (the choice of the experts has none, nor has the bias); with moe_expert_backward_ste's dprob as
+ * dw_dev it carries the layer's gradient on to the router.  Of params only score, k, renormalize
+ * and scale are used.  With g_j = scale * dw_j and sums over the k chosen, FP32:
+ *   softmax, renormalised   dl_c = q_c (g_c - sum_j g_j q_j),  q = softmax over the chosen
+ *   sigmoid, renormalised   dl_c = q_c (1 - s_c) (g_c - sum_j g_j q_j),  q_c = s_c / sum_j s_j
+ *   softmax                 dl_e = s_e ([e chosen] g_e - sum_j g_j s_j), every expert
+ *   sigmoid                 dl_c = g_c s_c (1 - s_c)
+ * and 0 for every other expert.
+ *  topk_ids_dev   int32 [T][k], different ids, as moe_route_topk wrote them
+ *  dw_dev         float [T][k]
+ *  dlogits_dev    [T][ld_out] of `type` out, the first E of each row written; ld_out >= E
+ * Device error: NVFP4_ERR_BAD_EXPERT_ID (an id outside [0, E); its slot is left out). */
+nvfp4_status moe_route_topk_backward(const void* logits_dev, int type, int64_t T, int E, int64_t ld,
+                                     const moe_route_params* params, const int32_t* topk_ids_dev,
+                                     const float* dw_dev, void* dlogits_dev, int64_t ld_out, void* stream);
+
+/* ---- Dense 4-bit products ----------------------------------------------------------------
+ * "MXFP4 rows": E2M1 elements in the code layout above, and one E8M0 scale (value 2^(code - 127),
+ * 255 = NaN) per 32 elements: code = clamp(floor(log2 max|x|) - 2 + 127, 0, 254), 0 for a zero
+ * block, 255 (with zero elements) for a block with an Inf or NaN; element = E2M1_rne(x / scale),
+ * saturating.  The scale of row r, block b is at byte
+ *   ((r/128) * ceil(cols/128) + b/4) * 512 + (r%32)*16 + ((r%128)/32)*4 + b%4
+ * (512-byte tiles of 128 rows x 128 columns); the blocks past cols of the last tile are 0. */
+size_t mxfp4_sf_bytes(int64_t rows, int64_t cols);   /* 0 on bad input */
+
+/*  x_dev      [rows][ld] of `type`, element aligned; ld >= cols
+ *  rows >= 0; cols % 32 == 0, 32 <= cols <= 2^20
+ *  codes_dev  uint8 [nvfp4_rows_padded(rows)][cols/2], 16-byte aligned; sf_dev mxfp4_sf_bytes(rows,
+ *             cols) bytes, 16-byte aligned; rows past `rows` get zero codes and scales
+ * Device error: NVFP4_ERR_NONFINITE. */
+nvfp4_status mxfp4_quantize_rows(const void* x_dev, int type, int64_t rows, int64_t cols, int64_t ld,
+                                 void* codes_dev, void* sf_dev, void* stream);
+/* The values MXFP4 rows stand for, out_dev [rows][ld] of NVFP4_TYPE_F32 or NVFP4_TYPE_BF16 (both
+ * exact); a NaN scale gives NaN. */
+nvfp4_status mxfp4_dequantize_rows(const void* codes_dev, const void* sf_dev, int64_t rows, int64_t cols,
+                                   void* out_dev, int type, int64_t ld, void* stream);
+
+/* Quantised weights of a dense product: N rows (one per output) of K elements, as written by
+ * nvfp4_quantize_rows (g: float [N]) or mxfp4_quantize_rows (g NULL).  codes and sf 16-byte aligned. */
+typedef struct {
+    const void* codes;
+    const void* sf;
+    const float* g;
+    int64_t N, K;
+} fp4_linear_weights;
+
+/* out[t, n] = sum_k xq[t, k] wq[n, k] + bias[n]: x is quantised row by row (in the workspace) as
+ * the weights are, the products of the quantised values accumulate in FP32 on the tensor cores in
+ * one order of K, outer scales (NVFP4: (acc * g^x) * g^w) and the bias are applied in FP32, and the
+ * sum is rounded once to the output's type.  A token's output does not depend on T or on the other
+ * tokens.
+ *  x_dev      [T][ldx]; nvfp4_linear: BF16, 16-byte aligned, ldx % 8 == 0, K % 64 == 0,
+ *             64 <= K <= 8192; mxfp4_linear: of x_type, element aligned, K % 32 == 0, 32 <= K <= 2^20
+ *  0 <= T < 2^31 - 256; 1 <= N < 2^31 - 256
+ *  bias_dev   float [N] or NULL
+ *  out_dev    [T][ldo] of out_type, element aligned, ldo >= N
+ *  ws_dev     *_linear_workspace_bytes(T, K) bytes, 256-byte aligned
+ * Device errors: NVFP4_ERR_NONFINITE (a row of x with Inf or NaN), NVFP4_ERR_DEVICE_TIMEOUT. */
+size_t nvfp4_linear_workspace_bytes(int64_t T, int64_t K);
+size_t mxfp4_linear_workspace_bytes(int64_t T, int64_t K);
+nvfp4_status nvfp4_linear(const fp4_linear_weights* w, const void* x_dev, int64_t T, int64_t ldx,
+                          const float* bias_dev, void* out_dev, int out_type, int64_t ldo, void* ws_dev,
+                          size_t ws_bytes, void* stream);
+nvfp4_status mxfp4_linear(const fp4_linear_weights* w, const void* x_dev, int x_type, int64_t T, int64_t ldx,
+                          const float* bias_dev, void* out_dev, int out_type, int64_t ldo, void* ws_dev,
+                          size_t ws_bytes, void* stream);
+
 /* nvfp4_silu_table -- the SiLU that the FC1 epilogue applies to its BF16 gate values
  * ([RL/4.4]: SiLU(gate)*up in FP32), evaluated by the epilogue's own code for every input:
  * out_dev float [65536], entry i = silu(a) for the BF16 value a whose bit pattern is i, where

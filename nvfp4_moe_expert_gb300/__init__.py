@@ -8,14 +8,17 @@ entry points have the names of the C ABI in ``include/nvfp4_moe.h``:
     moe_fc1_swiglu_nvfp4, moe_fc1_swiglu_save_nvfp4, moe_requant_nvfp4, moe_fc2_nvfp4, moe_fc2_requant_nvfp4, moe_combine_bf16,
     moe_workspace_bytes, moe_workspace_layout_query, nvfp4_sf_bytes,
     nvfp4_rows_padded, nvfp4_get_device_error, nvfp4_status_string, nvfp4_silu_table,
-    moe_router_topk, the fixed-capacity moe_*_masked calls, and the
+    moe_router_topk, the fixed-capacity moe_*_masked calls, the
     straight-through backward: moe_backward_layout_query,
-    moe_backward_workspace_bytes, moe_expert_backward_ste
+    moe_backward_workspace_bytes, moe_expert_backward_ste, routing of given
+    logits: moe_route_topk, moe_route_topk_backward, and dense 4-bit products:
+    mxfp4_quantize_rows, mxfp4_dequantize_rows, mxfp4_linear, nvfp4_linear
 
 There is no CPU fallback: if the library is missing or a call fails, an
 exception is raised.
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -54,6 +57,16 @@ class moe_workspace_layout(ctypes.Structure):
     ] + [(n, ctypes.c_size_t) for n in (
         "a_codes", "a_sf", "a_g", "row_pair", "row_prob", "amax2", "pair_row", "a_sf_rows", "chunk_count", "chunk_base",
         "pair_rank", "expert_count", "route_end", "h", "a2_codes", "a2_sf", "a2_g", "y", "total")]
+
+
+class moe_route_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "k", "n_group", "topk_group", "group_score", "renormalize")] + [
+        ("scale", ctypes.c_float)]
+
+
+class fp4_linear_weights(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("sf", ctypes.c_void_p), ("g", ctypes.c_void_p),
+                ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
 
 
 class moe_bf16_weights_t(ctypes.Structure):
@@ -106,6 +119,17 @@ _SIGNATURES = {
     "moe_backward_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I32, _I32]),
     "moe_expert_backward_ste": (_I32, [ctypes.POINTER(moe_bf16_weights_t), _I64, _I32, _P, _P, _P, _P, _SZ, _P,
                                        _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_route_topk": (_I32, [_P, _I32, _I64, _I32, _I64, ctypes.POINTER(moe_route_params), _P, _P, _P, _P]),
+    "moe_route_topk_backward": (_I32, [_P, _I32, _I64, _I32, _I64, ctypes.POINTER(moe_route_params), _P, _P, _P, _I64,
+                                       _P]),
+    "mxfp4_sf_bytes": (_SZ, [_I64, _I64]),
+    "mxfp4_quantize_rows": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _P, _P]),
+    "mxfp4_dequantize_rows": (_I32, [_P, _P, _I64, _I64, _P, _I32, _I64, _P]),
+    "nvfp4_linear_workspace_bytes": (_SZ, [_I64, _I64]),
+    "mxfp4_linear_workspace_bytes": (_SZ, [_I64, _I64]),
+    "nvfp4_linear": (_I32, [ctypes.POINTER(fp4_linear_weights), _P, _I64, _I64, _P, _P, _I32, _I64, _P, _SZ, _P]),
+    "mxfp4_linear": (_I32, [ctypes.POINTER(fp4_linear_weights), _P, _I32, _I64, _I64, _P, _P, _I32, _I64, _P, _SZ,
+                            _P]),
 }
 
 _lib = None
@@ -391,6 +415,202 @@ def moe_combine_bf16(weights, T, k, out, ws, stream=None):
     _need_cuda(out, ws)
     _check("moe_combine_bf16", lib().moe_combine_bf16(
         weights.ref(), T, k, _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- routing of given logits
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"max": 0, "top2": 1}
+
+
+def _on_stream(stream):
+    """Context in which this call's buffers are allocated: they belong to the stream it runs on."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _need_rows(name, t, *types):
+    if t.dim() != 2 or t.dtype not in types:
+        raise ValueError(f"{name} must be a 2-D tensor of {', '.join(str(d) for d in types)}")
+    if not t.is_cuda or (t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a CUDA tensor with contiguous rows")
+
+
+def _need(name, t, dtype, shape, device):
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {device}")
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor (of one row: its length)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _choice(name, value, table):
+    if value not in table:
+        raise ValueError(f"{name} must be one of {', '.join(map(repr, table))}, not {value!r}")
+    return table[value]
+
+
+def moe_route_topk(logits, k, score="softmax", bias=None, n_group=1, topk_group=1, group_score="max",
+                   renormalize=True, scale=1.0, stream=None):
+    """Routing of given router logits: (topk_ids int32 [T, k], topk_w float32 [T, k]).
+
+    logits [T, E] float32, bfloat16 or float16, contiguous rows; score "softmax" or "sigmoid";
+    bias float32 [E], added to the scores for the choice only; with n_group > 1 the experts come
+    from the topk_group best groups of E / n_group consecutive experts, a group's score being
+    its largest value ("max") or the sum of its two largest ("top2"); renormalize: the weights
+    are divided by their sum; then multiplied by scale.  The larger first, the lower id first on
+    equal values; experts with a logit of -inf are masked."""
+    _need_rows("logits", logits, *_TYPES)
+    T, E = logits.shape
+    if bias is not None:
+        _need("bias", bias, torch.float32, (E,), logits.device)
+    p = moe_route_params(_choice("score", score, _SCORES), k, n_group, topk_group,
+                         _choice("group_score", group_score, _GROUP_SCORES), bool(renormalize), scale)
+    with _on_stream(stream):
+        ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
+        w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+    _check("moe_route_topk", lib().moe_route_topk(
+        logits.data_ptr(), _TYPES[logits.dtype], T, E, _ld(logits), p, None if bias is None else bias.data_ptr(),
+        ids.data_ptr(), w.data_ptr(), _stream(stream)))
+    return ids, w
+
+
+def moe_route_topk_backward(logits, topk_ids, dw, score="softmax", renormalize=True, scale=1.0, stream=None):
+    """Gradient of moe_route_topk's weights with respect to the logits: [T, E] of the logits' type,
+    from the ids it returned and dw float32 [T, k], the gradient of the weights."""
+    _need_rows("logits", logits, *_TYPES)
+    T, E = logits.shape
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be a 2-D tensor")
+    k = topk_ids.shape[1]
+    _need("topk_ids", topk_ids, torch.int32, (T, k), logits.device)
+    _need("dw", dw, torch.float32, (T, k), logits.device)
+    p = moe_route_params(_choice("score", score, _SCORES), k, 1, 1, 0, bool(renormalize), scale)
+    with _on_stream(stream):
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _check("moe_route_topk_backward", lib().moe_route_topk_backward(
+        logits.data_ptr(), _TYPES[logits.dtype], T, E, _ld(logits), p, topk_ids.data_ptr(), dw.data_ptr(),
+        dlogits.data_ptr(), E, _stream(stream)))
+    return dlogits
+
+
+# ---------------------------------------------------------------- dense 4-bit products
+def mxfp4_sf_bytes(rows, cols):
+    return lib().mxfp4_sf_bytes(rows, cols)
+
+
+def mxfp4_quantize_rows(x, stream=None):
+    """MXFP4-quantise each row of a float32, bfloat16 or float16 CUDA matrix [rows, cols]
+    (cols % 32 == 0): (codes uint8 [rows rounded up to 128, cols / 2], sf uint8)."""
+    _need_rows("x", x, *_TYPES)
+    rows, cols = x.shape
+    with _on_stream(stream):
+        codes = torch.empty((nvfp4_rows_padded(rows), cols // 2), dtype=torch.uint8, device=x.device)
+        sf = torch.empty(mxfp4_sf_bytes(rows, cols), dtype=torch.uint8, device=x.device)
+    _check("mxfp4_quantize_rows", lib().mxfp4_quantize_rows(
+        x.data_ptr(), _TYPES[x.dtype], rows, cols, _ld(x), codes.data_ptr(), sf.data_ptr(), _stream(stream)))
+    return codes, sf
+
+
+def mxfp4_dequantize_rows(codes, sf, rows, cols, dtype=torch.bfloat16, stream=None):
+    """The values of MXFP4 rows, [rows, cols] bfloat16 or float32 (both exact)."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("dtype must be torch.bfloat16 or torch.float32")
+    _need("codes", codes, torch.uint8, (nvfp4_rows_padded(rows), cols // 2), codes.device)
+    _need("sf", sf, torch.uint8, (mxfp4_sf_bytes(rows, cols),), codes.device)
+    _need_cuda(codes, sf)
+    with _on_stream(stream):
+        out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
+    _check("mxfp4_dequantize_rows", lib().mxfp4_dequantize_rows(
+        codes.data_ptr(), sf.data_ptr(), rows, cols, out.data_ptr(), _TYPES[dtype], cols, _stream(stream)))
+    return out
+
+
+class FP4Weight:
+    """Weights of a dense product in 4 bits, [N, K] (device tensors), and the C struct pointing at
+    them: NVFP4 rows with outer scales g (nvfp4_linear), or MXFP4 rows, g None (mxfp4_linear)."""
+
+    def __init__(self, codes, sf, g, N, K):
+        self.tensors = (codes, sf, g)
+        self.N, self.K, self.mx = N, K, g is None
+        self.struct = fp4_linear_weights(codes.data_ptr(), sf.data_ptr(), None if g is None else g.data_ptr(), N, K)
+
+
+def nvfp4_quantize_weight(w, stream=None):
+    """w bf16 [N, K] (one row per output) -> FP4Weight for nvfp4_linear."""
+    with _on_stream(stream):
+        codes, sf, g = nvfp4_quantize_rows(w, stream=stream)
+    return FP4Weight(codes, sf, g, *w.shape)
+
+
+def mxfp4_quantize_weight(w, stream=None):
+    """w float32, bfloat16 or float16 [N, K] (one row per output) -> FP4Weight for mxfp4_linear."""
+    codes, sf = mxfp4_quantize_rows(w, stream=stream)
+    return FP4Weight(codes, sf, None, *w.shape)
+
+
+def mxfp4_weight_from_codes(codes, scales):
+    """FP4Weight of weights that are MXFP4 already: codes uint8 [N, K / 2] (the even element in the
+    low nibble) and E8M0 scales uint8 [N, K / 32], as a checkpoint holds them."""
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or codes.dim() != 2 or scales.dim() != 2:
+        raise ValueError("codes and scales must be 2-D uint8 tensors")
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    if tuple(scales.shape) != (N, K // 32) or K % 32 or not codes.is_cuda or scales.device != codes.device:
+        raise ValueError(f"scales must be [{N}, {K // 32}] beside the codes, K a multiple of 32")
+    tiles, rp = (K + 127) // 128, nvfp4_rows_padded(N)
+    rows = torch.zeros((rp, 4 * tiles), dtype=torch.uint8, device=codes.device)
+    rows[:N, :K // 32] = scales
+    # [row tile, row / 32, row % 32, column tile, block] -> [row tile, column tile, row % 32, row / 32, block]
+    sf = rows.view(rp // 128, 4, 32, tiles, 4).permute(0, 3, 2, 1, 4).reshape(-1)
+    padded = torch.zeros((rp, K // 2), dtype=torch.uint8, device=codes.device)
+    padded[:N] = codes
+    return FP4Weight(padded, sf.contiguous(), None, N, K)
+
+
+def _linear(name, mx, x, weight, bias, out, out_dtype, stream):
+    _need_rows("x", x, *(_TYPES if mx else (torch.bfloat16,)))
+    if weight.mx != mx:
+        raise ValueError(f"{name} takes {'MXFP4' if mx else 'NVFP4'} weights")
+    T, K = x.shape
+    if K != weight.K or weight.tensors[0].device != x.device:
+        raise ValueError(f"x must be [T, {weight.K}] on {weight.tensors[0].device}")
+    if bias is not None:
+        _need("bias", bias, torch.float32, (weight.N,), x.device)
+    L = lib()
+    n = L.mxfp4_linear_workspace_bytes(T, K) if mx else L.nvfp4_linear_workspace_bytes(T, K)
+    with _on_stream(stream):
+        if out is None:
+            if out_dtype not in _TYPES:
+                raise ValueError("out_dtype must be torch.float32, torch.bfloat16 or torch.float16")
+            out = torch.empty((T, weight.N), dtype=out_dtype, device=x.device)
+        else:
+            _need_rows("out", out, *_TYPES)
+            if tuple(out.shape) != (T, weight.N) or out.device != x.device:
+                raise ValueError(f"out must be [{T}, {weight.N}] on {x.device}")
+        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    b = None if bias is None else bias.data_ptr()
+    if mx:
+        st = L.mxfp4_linear(weight.struct, x.data_ptr(), _TYPES[x.dtype], T, _ld(x), b, out.data_ptr(),
+                            _TYPES[out.dtype], _ld(out), ws.data_ptr(), n, _stream(stream))
+    else:
+        st = L.nvfp4_linear(weight.struct, x.data_ptr(), T, _ld(x), b, out.data_ptr(), _TYPES[out.dtype], _ld(out),
+                            ws.data_ptr(), n, _stream(stream))
+    _check(name, st)
+    return out
+
+
+def mxfp4_linear(x, weight, bias=None, out=None, out_dtype=torch.bfloat16, stream=None):
+    """x [T, K] float32, bfloat16 or float16 times the MXFP4 weight's transpose (plus bias
+    float32 [N]): x is quantised to MXFP4 rows, the products accumulate in FP32 and are rounded
+    once.  Returns out [T, N] (of out_dtype if not given)."""
+    return _linear("mxfp4_linear", True, x, weight, bias, out, out_dtype, stream)
+
+
+def nvfp4_linear(x, weight, bias=None, out=None, out_dtype=torch.bfloat16, stream=None):
+    """x bfloat16 [T, K] times the NVFP4 weight's transpose (plus bias float32 [N]): x is quantised
+    to NVFP4 rows as nvfp4_quantize_rows does.  Returns out [T, N] (of out_dtype if not given)."""
+    return _linear("nvfp4_linear", False, x, weight, bias, out, out_dtype, stream)
 
 
 # ---------------------------------------------------------------- straight-through backward

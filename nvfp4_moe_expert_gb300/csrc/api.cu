@@ -6,6 +6,7 @@
 
 #include "backward.cuh"
 #include "common.cuh"
+#include "ops.cuh"
 
 namespace nvfp4 {
 
@@ -648,6 +649,182 @@ nvfp4_status moe_expert_backward_ste(const moe_bf16_weights_t* w, int64_t T, int
     a.real_end = at<int32_t>(bwd_ws_dev, B.real_end);
     a.err = err;
     return from_cuda(launch_moe_backward_ste(a, st));
+}
+
+// ---- routing of given logits, and the dense 4-bit products
+
+namespace {
+
+int type_size(int type) { return type == NVFP4_TYPE_F32 ? 4 : 2; }
+bool type_ok(int type) { return type == NVFP4_TYPE_F32 || type == NVFP4_TYPE_BF16 || type == NVFP4_TYPE_F16; }
+
+// Every row start rows are read or written at stays inside 63-bit byte offsets.
+bool rows_ok(int64_t rows, int64_t ld) { return ld <= 0 || rows <= (int64_t(1) << 60) / ld; }
+
+// The parameters both routing calls use.
+bool route_params_ok(const moe_route_params& p, int E) {
+    return (p.score == MOE_SCORE_SOFTMAX || p.score == MOE_SCORE_SIGMOID) && (p.renormalize == 0 || p.renormalize == 1) &&
+           p.k >= 1 && p.k <= 32 && p.k <= E && p.scale - p.scale == 0.0f;
+}
+
+RouteParams route_params(const moe_route_params& p) {
+    return {p.score, p.k, p.n_group, p.topk_group, p.group_score, p.renormalize, p.scale};
+}
+
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 256;
+constexpr int64_t kMaxMxCols = int64_t(1) << 20;
+
+bool mx_shape_ok(int64_t rows, int64_t cols) {
+    return rows >= 0 && rows < kMaxTokens && cols >= kMxBlock && cols <= kMaxMxCols && cols % kMxBlock == 0;
+}
+bool nv_shape_ok(int64_t rows, int64_t cols) {
+    return rows >= 0 && rows < kMaxTokens && cols >= 64 && cols <= 8192 && cols % 64 == 0;
+}
+
+// Workspace of a dense product: the quantised rows of x.
+struct LinearLayout {
+    size_t codes, sf, g, total;
+};
+LinearLayout linear_layout(bool mx, int64_t T, int64_t K) {
+    const size_t rows = static_cast<size_t>(nvfp4_rows_padded(T));
+    LinearLayout L;
+    L.codes = 0;
+    L.sf = align_up(rows * (K / 2), 256);
+    L.g = align_up(L.sf + (mx ? mxfp4_sf_bytes(T, K) : nvfp4_sf_bytes(T, K)), 256);
+    L.total = mx ? L.g : align_up(L.g + rows * 4, 256);
+    return L;
+}
+
+nvfp4_status linear_impl(bool mx, const fp4_linear_weights* w, const void* x, int x_type, int64_t T, int64_t ldx,
+                         const float* bias, void* out, int out_type, int64_t ldo, void* ws, size_t ws_bytes,
+                         cudaStream_t st) {
+    if (!w) return NVFP4_ERR_INVALID_ARG;
+    if (!(mx ? mx_shape_ok(T, w->K) : nv_shape_ok(T, w->K)) || w->N < 1 || w->N >= kMaxTokens || ldx < w->K ||
+        ldo < w->N || !type_ok(x_type) || !type_ok(out_type) || (!mx && ldx % 8) || !rows_ok(T, ldx) || !rows_ok(T, ldo))
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!w->codes || !w->sf || (!mx && !w->g) || !aligned(w->codes, 16) || !aligned(w->sf, 16) || !aligned(w->g, 4))
+        return NVFP4_ERR_INVALID_ARG;
+    if (T == 0) return NVFP4_OK;
+    if (!x || !out || !ws || !aligned(x, mx ? type_size(x_type) : 16) || !aligned(out, type_size(out_type)) ||
+        !aligned(bias, 4) || !aligned(ws, 256))
+        return NVFP4_ERR_INVALID_ARG;
+    const LinearLayout L = linear_layout(mx, T, w->K);
+    if (ws_bytes < L.total) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
+    int* err = device_error_ptr();
+    if (!err) return NVFP4_ERR_CUDA;
+    LinearArgs a{};
+    a.mx = mx;
+    a.T = T;
+    a.N = static_cast<int>(w->N);
+    a.K = static_cast<int>(w->K);
+    a.a_codes = at<uint8_t>(ws, L.codes);
+    a.a_sf = at<uint8_t>(ws, L.sf);
+    a.a_g = mx ? nullptr : at<float>(ws, L.g);
+    a.b_codes = static_cast<const uint8_t*>(w->codes);
+    a.b_sf = static_cast<const uint8_t*>(w->sf);
+    a.b_g = w->g;
+    a.bias = bias;
+    a.out = out;
+    a.out_type = out_type;
+    a.ldo = ldo;
+    a.err = err;
+    const cudaError_t e =
+        mx ? launch_mxfp4_quantize_rows(x, x_type, T, w->K, ldx, at<uint8_t>(ws, L.codes), at<uint8_t>(ws, L.sf), err, st)
+           : launch_quantize_rows(static_cast<const uint16_t*>(x), T, w->K, ldx, at<uint8_t>(ws, L.codes),
+                                  at<uint8_t>(ws, L.sf), at<float>(ws, L.g), err, st);
+    if (e != cudaSuccess) return from_cuda(e);
+    return from_cuda(launch_linear(a, st, true));
+}
+
+}  // namespace
+
+nvfp4_status moe_route_topk(const void* logits_dev, int type, int64_t T, int E, int64_t ld,
+                            const moe_route_params* params, const float* bias_dev, int32_t* topk_ids_dev,
+                            float* topk_w_dev, void* stream) {
+    if (!params) return NVFP4_ERR_INVALID_ARG;
+    const moe_route_params& p = *params;
+    if (T < 0 || T >= kMaxTokens || E < 1 || E > 1024 || ld < E || !rows_ok(T, ld) || !type_ok(type) ||
+        !route_params_ok(p, E) || p.n_group < 1 || p.n_group > 32 || E % p.n_group || p.topk_group < 1 ||
+        p.topk_group > p.n_group || p.k > p.topk_group * (E / p.n_group) ||
+        (p.group_score != MOE_GROUP_MAX && p.group_score != MOE_GROUP_TOP2))
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return NVFP4_OK;
+    if (!logits_dev || !topk_ids_dev || !topk_w_dev || !aligned(logits_dev, type_size(type)) || !aligned(bias_dev, 4) ||
+        !aligned(topk_ids_dev, 4) || !aligned(topk_w_dev, 4))
+        return NVFP4_ERR_INVALID_ARG;
+    int* err = device_error_ptr();
+    if (!err) return NVFP4_ERR_CUDA;
+    return from_cuda(launch_route_topk(logits_dev, type, T, E, ld, route_params(p), bias_dev, topk_ids_dev, topk_w_dev,
+                                       err, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status moe_route_topk_backward(const void* logits_dev, int type, int64_t T, int E, int64_t ld,
+                                     const moe_route_params* params, const int32_t* topk_ids_dev, const float* dw_dev,
+                                     void* dlogits_dev, int64_t ld_out, void* stream) {
+    if (!params) return NVFP4_ERR_INVALID_ARG;
+    if (T < 0 || T >= kMaxTokens || E < 1 || E > 1024 || ld < E || ld_out < E || !rows_ok(T, ld) ||
+        !rows_ok(T, ld_out) || !type_ok(type) || !route_params_ok(*params, E))
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return NVFP4_OK;
+    if (!logits_dev || !topk_ids_dev || !dw_dev || !dlogits_dev || !aligned(logits_dev, type_size(type)) ||
+        !aligned(dlogits_dev, type_size(type)) || !aligned(topk_ids_dev, 4) || !aligned(dw_dev, 4))
+        return NVFP4_ERR_INVALID_ARG;
+    int* err = device_error_ptr();
+    if (!err) return NVFP4_ERR_CUDA;
+    return from_cuda(launch_route_topk_backward(logits_dev, type, T, E, ld, route_params(*params), topk_ids_dev, dw_dev,
+                                                dlogits_dev, ld_out, err, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mxfp4_sf_bytes(int64_t rows, int64_t cols) {
+    if (!mx_shape_ok(rows, cols)) return 0;
+    return static_cast<size_t>(nvfp4_rows_padded(rows) / kTileM) * mx_sf_tiles(cols) * kSfAtomBytes;
+}
+
+nvfp4_status mxfp4_quantize_rows(const void* x_dev, int type, int64_t rows, int64_t cols, int64_t ld, void* codes_dev,
+                                 void* sf_dev, void* stream) {
+    if (!mx_shape_ok(rows, cols) || ld < cols || !rows_ok(rows, ld) || !type_ok(type)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (rows == 0) return NVFP4_OK;
+    if (!x_dev || !codes_dev || !sf_dev || !aligned(x_dev, type_size(type)) || !aligned(codes_dev, 16) ||
+        !aligned(sf_dev, 16))
+        return NVFP4_ERR_INVALID_ARG;
+    int* err = device_error_ptr();
+    if (!err) return NVFP4_ERR_CUDA;
+    return from_cuda(launch_mxfp4_quantize_rows(x_dev, type, rows, cols, ld, static_cast<uint8_t*>(codes_dev),
+                                                static_cast<uint8_t*>(sf_dev), err,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status mxfp4_dequantize_rows(const void* codes_dev, const void* sf_dev, int64_t rows, int64_t cols, void* out_dev,
+                                   int type, int64_t ld, void* stream) {
+    if (!mx_shape_ok(rows, cols) || ld < cols || !rows_ok(rows, ld) ||
+        (type != NVFP4_TYPE_F32 && type != NVFP4_TYPE_BF16))
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (rows == 0) return NVFP4_OK;
+    if (!codes_dev || !sf_dev || !out_dev || !aligned(codes_dev, 16) || !aligned(sf_dev, 16) ||
+        !aligned(out_dev, type_size(type)))
+        return NVFP4_ERR_INVALID_ARG;
+    return from_cuda(launch_mxfp4_dequantize_rows(static_cast<const uint8_t*>(codes_dev),
+                                                  static_cast<const uint8_t*>(sf_dev), rows, cols, out_dev, type, ld,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+size_t nvfp4_linear_workspace_bytes(int64_t T, int64_t K) {
+    return nv_shape_ok(T, K) ? linear_layout(false, T, K).total : 0;
+}
+size_t mxfp4_linear_workspace_bytes(int64_t T, int64_t K) {
+    return mx_shape_ok(T, K) ? linear_layout(true, T, K).total : 0;
+}
+
+nvfp4_status nvfp4_linear(const fp4_linear_weights* w, const void* x_dev, int64_t T, int64_t ldx, const float* bias_dev,
+                          void* out_dev, int out_type, int64_t ldo, void* ws_dev, size_t ws_bytes, void* stream) {
+    return linear_impl(false, w, x_dev, NVFP4_TYPE_BF16, T, ldx, bias_dev, out_dev, out_type, ldo, ws_dev, ws_bytes,
+                       static_cast<cudaStream_t>(stream));
+}
+nvfp4_status mxfp4_linear(const fp4_linear_weights* w, const void* x_dev, int x_type, int64_t T, int64_t ldx,
+                          const float* bias_dev, void* out_dev, int out_type, int64_t ldo, void* ws_dev,
+                          size_t ws_bytes, void* stream) {
+    return linear_impl(true, w, x_dev, x_type, T, ldx, bias_dev, out_dev, out_type, ldo, ws_dev, ws_bytes,
+                       static_cast<cudaStream_t>(stream));
 }
 
 int nvfp4_last_cuda_error(void) { return static_cast<int>(t_last_cuda_error); }
