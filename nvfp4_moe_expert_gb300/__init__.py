@@ -18,7 +18,6 @@ There is no CPU fallback: if the library is missing or a call fails, an
 exception is raised.
 """
 
-import contextlib
 import ctypes
 import os
 
@@ -419,36 +418,48 @@ def moe_combine_bf16(weights, T, k, out, ws, stream=None):
 
 # ---------------------------------------------------------------- routing of given logits
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_BF16 = {torch.bfloat16: 1}
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _GROUP_SCORES = {"max": 0, "top2": 1}
 
 
-def _on_stream(stream):
-    """Context in which this call's buffers are allocated: they belong to the stream it runs on."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+# These calls are made once per layer and token while decoding, so their Python side is kept short: one
+# look at each property, and the current stream's handle without a Stream object around it.
+
+def _raw_stream(stream, t):
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
-def _need_rows(name, t, *types):
-    if t.dim() != 2 or t.dtype not in types:
-        raise ValueError(f"{name} must be a 2-D tensor of {', '.join(str(d) for d in types)}")
-    if not t.is_cuda or (t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1):
+def _empty(shape, dtype, device, stream):
+    """A buffer of the stream the call runs on (None: the current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(name, t, types):
+    """(type code, rows, columns, row stride) of a 2-D CUDA tensor with contiguous rows."""
+    code = types.get(t.dtype)
+    if code is None or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor of {', '.join(map(str, types))}")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if not t.is_cuda or (step != 1 and rows and cols > 1):
         raise ValueError(f"{name} must be a CUDA tensor with contiguous rows")
+    return code, rows, cols, ld if rows > 1 else cols
 
 
 def _need(name, t, dtype, shape, device):
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {device}")
-
-
-def _ld(t):
-    """Row stride of a 2-D tensor (of one row: its length)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
 
 
 def _choice(name, value, table):
-    if value not in table:
+    code = table.get(value)
+    if code is None:
         raise ValueError(f"{name} must be one of {', '.join(map(repr, table))}, not {value!r}")
-    return table[value]
+    return code
 
 
 def moe_route_topk(logits, k, score="softmax", bias=None, n_group=1, topk_group=1, group_score="max",
@@ -461,37 +472,38 @@ def moe_route_topk(logits, k, score="softmax", bias=None, n_group=1, topk_group=
     its largest value ("max") or the sum of its two largest ("top2"); renormalize: the weights
     are divided by their sum; then multiplied by scale.  The larger first, the lower id first on
     equal values; experts with a logit of -inf are masked."""
-    _need_rows("logits", logits, *_TYPES)
-    T, E = logits.shape
+    code, T, E, ld = _rows("logits", logits, _TYPES)
+    device = logits.device
     if bias is not None:
-        _need("bias", bias, torch.float32, (E,), logits.device)
+        _need("bias", bias, torch.float32, (E,), device)
     p = moe_route_params(_choice("score", score, _SCORES), k, n_group, topk_group,
-                         _choice("group_score", group_score, _GROUP_SCORES), bool(renormalize), scale)
-    with _on_stream(stream):
-        ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
-        w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
-    _check("moe_route_topk", lib().moe_route_topk(
-        logits.data_ptr(), _TYPES[logits.dtype], T, E, _ld(logits), p, None if bias is None else bias.data_ptr(),
-        ids.data_ptr(), w.data_ptr(), _stream(stream)))
+                         _choice("group_score", group_score, _GROUP_SCORES), 1 if renormalize else 0, scale)
+    shape = (T, k if k > 0 else 0)
+    ids = _empty(shape, torch.int32, device, stream)
+    w = _empty(shape, torch.float32, device, stream)
+    status = lib().moe_route_topk(logits.data_ptr(), code, T, E, ld, p, None if bias is None else bias.data_ptr(),
+                                  ids.data_ptr(), w.data_ptr(), _raw_stream(stream, logits))
+    if status:
+        _check("moe_route_topk", status)
     return ids, w
 
 
 def moe_route_topk_backward(logits, topk_ids, dw, score="softmax", renormalize=True, scale=1.0, stream=None):
     """Gradient of moe_route_topk's weights with respect to the logits: [T, E] of the logits' type,
     from the ids it returned and dw float32 [T, k], the gradient of the weights."""
-    _need_rows("logits", logits, *_TYPES)
-    T, E = logits.shape
+    code, T, E, ld = _rows("logits", logits, _TYPES)
+    device = logits.device
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids must be a 2-D tensor")
     k = topk_ids.shape[1]
-    _need("topk_ids", topk_ids, torch.int32, (T, k), logits.device)
-    _need("dw", dw, torch.float32, (T, k), logits.device)
-    p = moe_route_params(_choice("score", score, _SCORES), k, 1, 1, 0, bool(renormalize), scale)
-    with _on_stream(stream):
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    _check("moe_route_topk_backward", lib().moe_route_topk_backward(
-        logits.data_ptr(), _TYPES[logits.dtype], T, E, _ld(logits), p, topk_ids.data_ptr(), dw.data_ptr(),
-        dlogits.data_ptr(), E, _stream(stream)))
+    _need("topk_ids", topk_ids, torch.int32, (T, k), device)
+    _need("dw", dw, torch.float32, (T, k), device)
+    p = moe_route_params(_choice("score", score, _SCORES), k, 1, 1, 0, 1 if renormalize else 0, scale)
+    dlogits = _empty((T, E), logits.dtype, device, stream)
+    status = lib().moe_route_topk_backward(logits.data_ptr(), code, T, E, ld, p, topk_ids.data_ptr(), dw.data_ptr(),
+                                           dlogits.data_ptr(), E, _raw_stream(stream, logits))
+    if status:
+        _check("moe_route_topk_backward", status)
     return dlogits
 
 
@@ -503,13 +515,15 @@ def mxfp4_sf_bytes(rows, cols):
 def mxfp4_quantize_rows(x, stream=None):
     """MXFP4-quantise each row of a float32, bfloat16 or float16 CUDA matrix [rows, cols]
     (cols % 32 == 0): (codes uint8 [rows rounded up to 128, cols / 2], sf uint8)."""
-    _need_rows("x", x, *_TYPES)
-    rows, cols = x.shape
-    with _on_stream(stream):
-        codes = torch.empty((nvfp4_rows_padded(rows), cols // 2), dtype=torch.uint8, device=x.device)
-        sf = torch.empty(mxfp4_sf_bytes(rows, cols), dtype=torch.uint8, device=x.device)
-    _check("mxfp4_quantize_rows", lib().mxfp4_quantize_rows(
-        x.data_ptr(), _TYPES[x.dtype], rows, cols, _ld(x), codes.data_ptr(), sf.data_ptr(), _stream(stream)))
+    code, rows, cols, ld = _rows("x", x, _TYPES)
+    device = x.device
+    L = lib()
+    codes = _empty((L.nvfp4_rows_padded(rows), cols // 2), torch.uint8, device, stream)
+    sf = _empty((L.mxfp4_sf_bytes(rows, cols),), torch.uint8, device, stream)
+    status = L.mxfp4_quantize_rows(x.data_ptr(), code, rows, cols, ld, codes.data_ptr(), sf.data_ptr(),
+                                   _raw_stream(stream, x))
+    if status:
+        _check("mxfp4_quantize_rows", status)
     return codes, sf
 
 
@@ -517,13 +531,17 @@ def mxfp4_dequantize_rows(codes, sf, rows, cols, dtype=torch.bfloat16, stream=No
     """The values of MXFP4 rows, [rows, cols] bfloat16 or float32 (both exact)."""
     if dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("dtype must be torch.bfloat16 or torch.float32")
-    _need("codes", codes, torch.uint8, (nvfp4_rows_padded(rows), cols // 2), codes.device)
-    _need("sf", sf, torch.uint8, (mxfp4_sf_bytes(rows, cols),), codes.device)
-    _need_cuda(codes, sf)
-    with _on_stream(stream):
-        out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
-    _check("mxfp4_dequantize_rows", lib().mxfp4_dequantize_rows(
-        codes.data_ptr(), sf.data_ptr(), rows, cols, out.data_ptr(), _TYPES[dtype], cols, _stream(stream)))
+    L = lib()
+    device = codes.device
+    _need("codes", codes, torch.uint8, (L.nvfp4_rows_padded(rows), cols // 2), device)
+    _need("sf", sf, torch.uint8, (L.mxfp4_sf_bytes(rows, cols),), device)
+    if not codes.is_cuda:
+        raise ValueError("codes must be a CUDA tensor")
+    out = _empty((rows, cols), dtype, device, stream)
+    status = L.mxfp4_dequantize_rows(codes.data_ptr(), sf.data_ptr(), rows, cols, out.data_ptr(), _TYPES[dtype], cols,
+                                     _raw_stream(stream, codes))
+    if status:
+        _check("mxfp4_dequantize_rows", status)
     return out
 
 
@@ -533,15 +551,18 @@ class FP4Weight:
 
     def __init__(self, codes, sf, g, N, K):
         self.tensors = (codes, sf, g)
-        self.N, self.K, self.mx = N, K, g is None
+        self.N, self.K, self.mx, self.device = N, K, g is None, codes.device
         self.struct = fp4_linear_weights(codes.data_ptr(), sf.data_ptr(), None if g is None else g.data_ptr(), N, K)
 
 
 def nvfp4_quantize_weight(w, stream=None):
     """w bf16 [N, K] (one row per output) -> FP4Weight for nvfp4_linear."""
-    with _on_stream(stream):
-        codes, sf, g = nvfp4_quantize_rows(w, stream=stream)
-    return FP4Weight(codes, sf, g, *w.shape)
+    _, N, K, _ = _rows("w", w, _BF16)
+    codes = _empty((nvfp4_rows_padded(N), K // 2), torch.uint8, w.device, stream)
+    sf = _empty((max(nvfp4_sf_bytes(N, K), 1),), torch.uint8, w.device, stream)
+    g = _empty((N,), torch.float32, w.device, stream)
+    nvfp4_quantize_rows(w, codes, sf, g, stream=stream)
+    return FP4Weight(codes, sf, g, N, K)
 
 
 def mxfp4_quantize_weight(w, stream=None):
@@ -569,34 +590,35 @@ def mxfp4_weight_from_codes(codes, scales):
 
 
 def _linear(name, mx, x, weight, bias, out, out_dtype, stream):
-    _need_rows("x", x, *(_TYPES if mx else (torch.bfloat16,)))
+    code, T, K, ldx = _rows("x", x, _TYPES if mx else _BF16)
+    N, device = weight.N, x.device
     if weight.mx != mx:
         raise ValueError(f"{name} takes {'MXFP4' if mx else 'NVFP4'} weights")
-    T, K = x.shape
-    if K != weight.K or weight.tensors[0].device != x.device:
-        raise ValueError(f"x must be [T, {weight.K}] on {weight.tensors[0].device}")
+    if K != weight.K or weight.device != device:
+        raise ValueError(f"x must be [T, {weight.K}] on {weight.device}")
     if bias is not None:
-        _need("bias", bias, torch.float32, (weight.N,), x.device)
+        _need("bias", bias, torch.float32, (N,), device)
+    if out is None:
+        out_code, ldo = _TYPES.get(out_dtype), N
+        if out_code is None:
+            raise ValueError("out_dtype must be torch.float32, torch.bfloat16 or torch.float16")
+        out = _empty((T, N), out_dtype, device, stream)
+    else:
+        out_code, rows, cols, ldo = _rows("out", out, _TYPES)
+        if rows != T or cols != N or out.device != device:
+            raise ValueError(f"out must be [{T}, {N}] on {device}")
     L = lib()
-    n = L.mxfp4_linear_workspace_bytes(T, K) if mx else L.nvfp4_linear_workspace_bytes(T, K)
-    with _on_stream(stream):
-        if out is None:
-            if out_dtype not in _TYPES:
-                raise ValueError("out_dtype must be torch.float32, torch.bfloat16 or torch.float16")
-            out = torch.empty((T, weight.N), dtype=out_dtype, device=x.device)
-        else:
-            _need_rows("out", out, *_TYPES)
-            if tuple(out.shape) != (T, weight.N) or out.device != x.device:
-                raise ValueError(f"out must be [{T}, {weight.N}] on {x.device}")
-        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    need = L.mxfp4_linear_workspace_bytes(T, K) if mx else L.nvfp4_linear_workspace_bytes(T, K)
+    ws = _empty((need,), torch.uint8, device, stream)
     b = None if bias is None else bias.data_ptr()
     if mx:
-        st = L.mxfp4_linear(weight.struct, x.data_ptr(), _TYPES[x.dtype], T, _ld(x), b, out.data_ptr(),
-                            _TYPES[out.dtype], _ld(out), ws.data_ptr(), n, _stream(stream))
+        status = L.mxfp4_linear(weight.struct, x.data_ptr(), code, T, ldx, b, out.data_ptr(), out_code, ldo,
+                                ws.data_ptr(), need, _raw_stream(stream, x))
     else:
-        st = L.nvfp4_linear(weight.struct, x.data_ptr(), T, _ld(x), b, out.data_ptr(), _TYPES[out.dtype], _ld(out),
-                            ws.data_ptr(), n, _stream(stream))
-    _check(name, st)
+        status = L.nvfp4_linear(weight.struct, x.data_ptr(), T, ldx, b, out.data_ptr(), out_code, ldo, ws.data_ptr(),
+                                need, _raw_stream(stream, x))
+    if status:
+        _check(name, status)
     return out
 
 

@@ -728,6 +728,7 @@ nvfp4_status linear_impl(bool mx, const fp4_linear_weights* w, const void* x, in
     a.out_type = out_type;
     a.ldo = ldo;
     a.err = err;
+    if (linear_quantises_x(a)) return from_cuda(launch_linear_x({x, x_type, ldx}, a, st));
     const cudaError_t e =
         mx ? launch_mxfp4_quantize_rows(x, x_type, T, w->K, ldx, at<uint8_t>(ws, L.codes), at<uint8_t>(ws, L.sf), err, st)
            : launch_quantize_rows(static_cast<const uint16_t*>(x), T, w->K, ldx, at<uint8_t>(ws, L.codes),

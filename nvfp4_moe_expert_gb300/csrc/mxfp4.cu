@@ -6,73 +6,12 @@
 //   the smallest scale and zero codes; a block with an Inf or NaN has the NaN scale 255
 //   code = E2M1(x / scale), to nearest, ties to even, saturating: the quotient by a power of two
 //   is exact, so there is one rounding
-#include <cmath>
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "ops.cuh"
-#include "ptx.cuh"
+#include "mxfp4_quant.cuh"
 
 namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
-
-// Eight consecutive elements as FP32.
-template <bool kVec>
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    if (kVec) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __ldg(p + i);
-    }
-}
-template <bool kVec>
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-    uint32_t w[4];
-    if (kVec) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(q));
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __ldg(q + 2 * i) | (static_cast<uint32_t>(__ldg(q + 2 * i + 1)) << 16);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-}
-template <bool kVec>
-__device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
-    if (kVec) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __half2float(p[i]);
-    }
-}
-
-// E8M0 code of a block whose largest magnitude has the FP32 bits `top` (NaN and Inf: 255).
-__device__ __forceinline__ uint32_t e8m0_of_max(uint32_t top) {
-    if (top >= 0x7F800000u) return 255u;
-    if (top < 0x00800000u) return 0u;                 // zero or an FP32 subnormal: exponent below -127
-    const int e = static_cast<int>(top >> 23) - 2;    // biased exponent of the scale
-    return e > 0 ? static_cast<uint32_t>(e) : 0u;
-}
-// 2^(127 - code): the factor that divides by the scale; codes 0..252 occur (FP32 exponents).
-__device__ __forceinline__ float e8m0_inverse(uint32_t code) { return __uint_as_float((254u - code) << 23); }
 
 // Four threads per block of 32 elements, 16 threads per word of four scales: thread u of a row
 // takes elements 8u..8u+7, so the row is read in consecutive 16-byte (BF16, FP16) pieces.
@@ -99,25 +38,12 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = 0.0f;
         }
-        uint32_t top = 0u;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        uint32_t code = e8m0_of_max(top);
-        const float inv = code == 255u ? 0.0f : e8m0_inverse(code);
-        uint32_t word = 0u;
-        if (code == 255u) {
-            if (live) set_device_error(err, NVFP4_ERR_NONFINITE);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) word |= cvt_e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
-        }
-        if (!live) code = 0u;
-        uint32_t scales = code;                                      // this group of 16 threads' four scales
-        scales |= __shfl_down_sync(0xFFFFFFFFu, code, 4) << 8;
-        scales |= __shfl_down_sync(0xFFFFFFFFu, code, 8) << 16;
-        scales |= __shfl_down_sync(0xFFFFFFFFu, code, 12) << 24;
+        uint32_t word, scale;
+        mx_quantize8(v, word, scale, err);
+        uint32_t scales = scale;                                     // this group of 16 threads' four scales
+        scales |= __shfl_down_sync(0xFFFFFFFFu, scale, 4) << 8;
+        scales |= __shfl_down_sync(0xFFFFFFFFu, scale, 8) << 16;
+        scales |= __shfl_down_sync(0xFFFFFFFFu, scale, 12) << 24;
         if (in) {
             if (8 * u < cols) *reinterpret_cast<uint32_t*>(codes + r * (cols / 2) + 4 * u) = word;
             if ((u & 15) == 0) *reinterpret_cast<uint32_t*>(sf + mx_sf_offset(r, u / 4, cols)) = scales;

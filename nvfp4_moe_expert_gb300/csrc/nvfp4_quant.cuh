@@ -158,6 +158,25 @@ __device__ __forceinline__ void quantize_group(const uint4 (&v)[8], const uint32
     }
 }
 
+// One 16-element block (v0, v1) of a row with outer scale g: its codes as two words and its E4M3
+// scale, as quantize_group gives them.
+__device__ __forceinline__ void nv_quantize16(const uint4& v0, const uint4& v1, float g, uint32_t& w0, uint32_t& w1,
+                                              uint32_t& scale) {
+    const float d1 = __fmul_rn(g, 6.0f);
+    const float rc1 = d1 >= kMarksteinMinDivisor ? __frcp_rn(d1) : 0.0f;
+    const float bmx = __uint_as_float(block_absmax_bits(v0, v1));
+    const float r = rc1 != 0.0f ? div_markstein(bmx, d1, rc1) : div_rn_slow(bmx, d1);
+    scale = d1 > 0.0f ? cvt_e4m3(r) : 0u;
+    const float d2 = __fmul_rn(g, e4m3_value(scale));
+    w0 = w1 = 0u;
+    if (d2 > 0.0f) {
+        const bool mk = d2 >= kMarksteinMinDivisor;
+        const float rc = mk ? __frcp_rn(d2) : 0.0f;
+        w0 = codes8(v0, d2, rc, mk);
+        w1 = codes8(v1, d2, rc, mk);
+    }
+}
+
 __device__ __forceinline__ void load_group(const uint16_t* src, uint4 (&v)[8]) {
     const uint4* s = reinterpret_cast<const uint4*>(src);
 #pragma unroll

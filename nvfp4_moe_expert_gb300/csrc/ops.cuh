@@ -52,7 +52,20 @@ struct LinearArgs {
     int64_t ldo;
     int* err;
 };
+// The same with x not quantised yet, [T][ld] of NVFP4_TYPE_* (a's operand pointers unused): for the
+// few tokens linear_quantises_x(a) takes, which one kernel serves.
+struct LinearInput {
+    const void* x;
+    int type;
+    int64_t ld;
+};
+bool linear_quantises_x(const LinearArgs& a);
+cudaError_t launch_linear_x(const LinearInput& x, const LinearArgs& a, cudaStream_t st);
+
 // pdl: launched as a programmatic dependent of the kernel that quantises a
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st, bool pdl);
+// Its kernel for many tokens, and the pairs of CTAs that run at once.
+cudaError_t launch_linear_pair(const LinearArgs& a, cudaStream_t st, bool pdl);
+int linear_pair_count();
 
 }  // namespace nvfp4
