@@ -515,7 +515,7 @@ nvfp4_status moe_route_topk_backward(const void* logits_dev, int type, int64_t T
 size_t mxfp4_sf_bytes(int64_t rows, int64_t cols);   /* 0 on bad input */
 
 /*  x_dev      [rows][ld] of `type`, element aligned; ld >= cols
- *  rows >= 0; cols % 32 == 0, 32 <= cols <= 2^20
+ *  rows >= 0; cols % 32 == 0, 32 <= cols <= 2^20; (rows + 128) * ceil(cols / 256) < 2^31
  *  codes_dev  uint8 [nvfp4_rows_padded(rows)][cols/2], 16-byte aligned; sf_dev mxfp4_sf_bytes(rows,
  *             cols) bytes, 16-byte aligned; rows past `rows` get zero codes and scales
  * Device error: NVFP4_ERR_NONFINITE. */
@@ -541,7 +541,8 @@ typedef struct {
  * sum is rounded once to the output's type.  A token's output does not depend on T or on the other
  * tokens.
  *  x_dev      [T][ldx]; nvfp4_linear: BF16, 16-byte aligned, ldx % 8 == 0, K % 64 == 0,
- *             64 <= K <= 8192; mxfp4_linear: of x_type, element aligned, K % 32 == 0, 32 <= K <= 2^20
+ *             64 <= K <= 8192; mxfp4_linear: of x_type, element aligned, T x K as mxfp4_quantize_rows
+ *             takes
  *  0 <= T < 2^31 - 256; 1 <= N < 2^31 - 256
  *  bias_dev   float [N] or NULL
  *  out_dev    [T][ldo] of out_type, element aligned, ldo >= N

@@ -33,7 +33,7 @@ struct Params {
     void* out;
     int out_type;
     int64_t ldo;
-    int vec;              // rows of out start and end on 16-byte boundaries
+    int align;            // of out's rows: out_align()
     int a_rows;           // rows of A loaded per tile (a multiple of 8, at most 128)
     int stages, stage_bytes;
     int n_tiles;
@@ -57,22 +57,7 @@ __device__ __forceinline__ void epilogue_row(uint32_t taddr, bool live, int64_t 
         bcol[lane] = p.bias != nullptr && n < p.N ? __ldg(p.bias + n) : 0.0f;
         __syncwarp();
         tmem_ld_wait();
-#pragma unroll
-        for (int h = 0; h < 32; h += 16) {
-            float o[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float y = __uint_as_float(v[h + i]);
-                if (!kMx) y = __fmul_rn(__fmul_rn(y, ga), gcol[h + i]);
-                o[i] = __fadd_rn(y, bcol[h + i]);
-            }
-            const int at = n0 + c + h, left = p.N - at;
-            if (!live || left <= 0) continue;
-            const int64_t off = r * p.ldo + at;
-            if (p.out_type == NVFP4_TYPE_F32) store16(static_cast<float*>(p.out) + off, o, left, p.vec);
-            else if (p.out_type == NVFP4_TYPE_BF16) store16(static_cast<__nv_bfloat16*>(p.out) + off, o, left, p.vec);
-            else store16(static_cast<__half*>(p.out) + off, o, left, p.vec);
-        }
+        if (live && n0 + c < p.N) write_outputs<kMx, 32>(v, ga, gcol, bcol, r, n0 + c, p);
     }
 }
 
@@ -92,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tmem_full[2], tmem_empty[2], drain;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
-    __shared__ float s_col[kEpiWarps][2][32];
+    __shared__ __align__(8) float s_col[kEpiWarps][2][32];
     volatile int* abort_flag = &abort_word;
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int a_bytes = p.a_rows * kRowBytes;
@@ -314,7 +299,7 @@ struct DecodeParams {
     void* out;
     int out_type;
     int64_t ldo;
-    int vec;
+    int align;
     int batch_shift;      // log2 of the pieces of x that become ready together
     int stages, n_tiles;
     int* err;
@@ -335,35 +320,10 @@ __device__ __forceinline__ void sync_quantisers() { asm volatile("barrier.sync 1
 __device__ __forceinline__ void start_arrive() { asm volatile("barrier.arrive 2, %0;" ::"r"(kThreadsD) : "memory"); }
 __device__ __forceinline__ void start_wait() { asm volatile("barrier.sync 2, %0;" ::"r"(kThreadsD) : "memory"); }
 
-// Eight elements of a lane and piece, as they are loaded.
-template <typename X, bool kVec>
-struct Held {
-    static constexpr bool one_word = kVec && sizeof(X) == 2;
-    uint4 w;
-    float f[one_word ? 1 : 8];
-    __device__ __forceinline__ void load(const X* src, bool live) {
-        if constexpr (one_word) {
-            w = live ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-            if (live) load8<kVec>(src, f);
-        }
-    }
-    // the code word and, in every lane of a block's four, the scale
-    __device__ __forceinline__ void quantise(uint32_t& word, uint32_t& scale, int* err) const {
-        if constexpr (one_word) {
-            mx_quantize_word(static_cast<const X*>(nullptr), w, word, scale, err);
-        } else {
-            mx_quantize8(f, word, scale, err);
-        }
-    }
-};
-
 template <typename X, bool kVec>
 __device__ __forceinline__ void quantise_mx(const DecodeParams& p, int warp, int lane, uint8_t* codes, uint8_t* sf,
                                             uint64_t* a_full) {
-    using H = Held<X, kVec>;
+    using H = MxHeld<X, kVec>;
     constexpr int kCols = piece_cols<true>(), kHeld = pieces_held(H::one_word);
     const X* x = static_cast<const X*>(p.x);
     const int pieces = p.T * ((p.K + kCols - 1) / kCols);
@@ -507,7 +467,8 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
     __shared__ uint32_t row_max[kMaxT];
-    __shared__ float row_g[kMaxT], s_col[2][32];
+    __shared__ float row_g[kMaxT];
+    __shared__ __align__(8) float s_col[2][32];
     volatile int* abort_flag = &abort_word;
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int num_ks = (p.K + kStageK - 1) / kStageK;              // chunks of 256
@@ -707,7 +668,7 @@ cudaError_t launch_decode(const LinearInput& x, const LinearArgs& a, cudaStream_
     p.out = a.out;
     p.out_type = a.out_type;
     p.ldo = a.ldo;
-    p.vec = out_vec(a);
+    p.align = out_align(a);
     p.err = a.err;
     const int num_ks = (a.K + kStageK - 1) / kStageK, num_st = (num_ks + kPer - 1) / kPer;
     const int sf_bytes = (a.K + F::tile_k - 1) / F::tile_k * kSfAtomBytes;
@@ -748,7 +709,7 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t st, bool pdl) {
     p.out = a.out;
     p.out_type = a.out_type;
     p.ldo = a.ldo;
-    p.vec = out_vec(a);
+    p.align = out_align(a);
     p.a_rows = a.T >= kBM ? kBM : static_cast<int>((a.T + 15) / 16 * 16);
     p.stage_bytes = p.a_rows * kRowBytes + mma_n(BN) * kRowBytes + (1 + sets) * F::tiles * kSfAtomBytes;
     p.stage_bytes = (p.stage_bytes + 1023) / 1024 * 1024;

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <mutex>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -121,30 +122,111 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint64_t a, uint64_t b, 
 #undef LINEAR_NV2_STAGE
 #undef LINEAR_MX2_STAGE
 
-template <typename T>
-__device__ __forceinline__ T to_out(float v);
-template <>
-__device__ __forceinline__ float to_out<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half to_out<__half>(float v) { return __float2half_rn(v); }
+// ---- outputs
 
-// 16 consecutive outputs of a row, of which the first `n` exist.
+// Pairs of FP32 values in one 64-bit register (the first low); products and sums round each.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+// The 32-bit words of 16 outputs of type T.
 template <typename T>
-__device__ __forceinline__ void store16(T* p, const float (&v)[16], int n, bool vec) {
-    if (vec && n >= 16) {
-        T o[16];
+__device__ __forceinline__ void pack16(const uint64_t (&v)[8], uint32_t (&w)[4 * sizeof(T)]) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = to_out<T>(v[i]);
+    for (int i = 0; i < 8; ++i) {
+        float lo, hi;
+        unpair(v[i], lo, hi);
+        if constexpr (sizeof(T) == 4) {
+            w[2 * i] = __float_as_uint(lo);
+            w[2 * i + 1] = __float_as_uint(hi);
+        } else if constexpr (std::is_same<T, __half>::value) {
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(hi), "f"(lo));
+        } else {
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(hi), "f"(lo));
+        }
+    }
+}
+
+// 16 consecutive outputs of a row, of which the first `n` exist.  align: 2 where rows lie on 32-byte
+// boundaries (whole sectors in one store), 1 on 16-byte ones, 0 otherwise.
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const uint64_t (&v)[8], int n, int align) {
+    constexpr int kWords = 4 * sizeof(T);
+    uint32_t w[kWords];
+    pack16<T>(v, w);
+    if (n >= 16 && align == 2) {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
-            reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(o)[i];
+        for (int i = 0; i < kWords; i += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint32_t*>(p) + i),
+                         "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
+                         "r"(w[i + 7])
+                         : "memory");
+    } else if (n >= 16 && align == 1) {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4)
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            if (i < n) p[i] = to_out<T>(v[i]);
+            if (i >= n) break;
+            if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+            else reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
         }
+    }
+}
+
+// kCols outputs of row r at column n0 from a lane's accumulator values: NVFP4 outer scales (ga: the
+// row's, gcol: the columns'), the bias (bcol) if there is one, one rounding.  gcol, bcol: 8-byte aligned
+// shared memory.
+template <bool kMx, bool kBias, typename T, int kCols>
+__device__ __forceinline__ void outputs(const uint32_t* v, float ga, const float* gcol, const float* bcol, T* row, int left,
+                                        int align) {
+    const uint64_t g2 = pair(ga, ga);
+#pragma unroll
+    for (int h = 0; h < kCols; h += 16) {
+        if (left <= h) break;
+        uint64_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            o[i] = pair(__uint_as_float(v[h + 2 * i]), __uint_as_float(v[h + 2 * i + 1]));
+            if (!kMx) o[i] = pair_mul(pair_mul(o[i], g2), *reinterpret_cast<const uint64_t*>(gcol + h + 2 * i));
+            if (kBias) o[i] = pair_add(o[i], *reinterpret_cast<const uint64_t*>(bcol + h + 2 * i));
+        }
+        store16<T>(row + h, o, left - h, align);
+    }
+}
+template <bool kMx, int kCols, typename P>
+__device__ __forceinline__ void write_outputs(const uint32_t* v, float ga, const float* gcol, const float* bcol, int64_t r,
+                                              int n0, const P& p) {
+    const int64_t off = r * p.ldo + n0;
+    const int left = p.N - n0;
+    if (p.out_type == NVFP4_TYPE_BF16) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + off;
+        if (p.bias) outputs<kMx, true, __nv_bfloat16, kCols>(v, ga, gcol, bcol, o, left, p.align);
+        else outputs<kMx, false, __nv_bfloat16, kCols>(v, ga, gcol, bcol, o, left, p.align);
+    } else if (p.out_type == NVFP4_TYPE_F32) {
+        float* o = static_cast<float*>(p.out) + off;
+        if (p.bias) outputs<kMx, true, float, kCols>(v, ga, gcol, bcol, o, left, p.align);
+        else outputs<kMx, false, float, kCols>(v, ga, gcol, bcol, o, left, p.align);
+    } else {
+        __half* o = static_cast<__half*>(p.out) + off;
+        if (p.bias) outputs<kMx, true, __half, kCols>(v, ga, gcol, bcol, o, left, p.align);
+        else outputs<kMx, false, __half, kCols>(v, ga, gcol, bcol, o, left, p.align);
     }
 }
 
@@ -229,10 +311,10 @@ cudaError_t prepare(void (*kernel)(A...), int bytes, bool (&ready)[kMaxDevices])
     return cudaSuccess;
 }
 
-// Rows of out start and end on 16-byte boundaries.
-int out_vec(const LinearArgs& a) {
-    const int size = a.out_type == NVFP4_TYPE_F32 ? 4 : 2;
-    return (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && (a.ldo * size) % 16 == 0;
+// Rows of out lie on 32-byte (2) or 16-byte (1) boundaries, or neither (0).
+int out_align(const LinearArgs& a) {
+    const int64_t bits = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.out)) | (a.ldo * (a.out_type == NVFP4_TYPE_F32 ? 4 : 2));
+    return bits % 32 == 0 ? 2 : bits % 16 == 0 ? 1 : 0;
 }
 
 }  // namespace

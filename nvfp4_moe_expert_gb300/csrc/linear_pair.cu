@@ -45,7 +45,7 @@ struct PairParams {
     void* out;
     int out_type;
     int64_t ldo;
-    int vec;
+    int align;            // of out's rows: out_align()
     int n_tiles;
     int64_t tiles;
     int* err;
@@ -123,7 +123,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __shared__ uint64_t full[S::count], empty[S::count], tmem_full, tmem_empty, drain;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
-    __shared__ float s_col[kPairEpiWarps][2][64];
+    __shared__ __align__(8) float s_col[kPairEpiWarps][2][64];
     volatile int* abort_flag = &abort_word;
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t rank = uniform(cta_rank());
@@ -282,30 +282,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
             acc_phase ^= 1u;
             tc_fence_after();
-            uint32_t v[2][32];
-            tmem_ld_32x32b_x32(taddr, v[0]);
-            tmem_ld_32x32b_x32(taddr + 32, v[1]);
+            uint32_t v[64];
+            tmem_ld_32x32b_x32(taddr, *reinterpret_cast<uint32_t(*)[32]>(v));
+            tmem_ld_32x32b_x32(taddr + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_leader(empty_bar);
-            if (!live) continue;
-#pragma unroll
-            for (int h = 0; h < 64; h += 16) {
-                float o[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float y = __uint_as_float(v[h >> 5][(h & 31) + i]);
-                    if (!kMx) y = __fmul_rn(__fmul_rn(y, ga), gcol[h + i]);
-                    o[i] = p.bias != nullptr ? __fadd_rn(y, bcol[h + i]) : __fadd_rn(y, 0.0f);
-                }
-                const int left = p.N - n0 - h;
-                if (left <= 0) break;
-                const int64_t off = r * p.ldo + n0 + h;
-                if (p.out_type == NVFP4_TYPE_F32) store16(static_cast<float*>(p.out) + off, o, left, p.vec);
-                else if (p.out_type == NVFP4_TYPE_BF16) store16(static_cast<__nv_bfloat16*>(p.out) + off, o, left, p.vec);
-                else store16(static_cast<__half*>(p.out) + off, o, left, p.vec);
-            }
+            if (live && n0 < p.N) write_outputs<kMx, 64>(v, ga, gcol, bcol, r, n0, p);
         }
     }
 
@@ -334,7 +318,7 @@ cudaError_t launch_pair(const LinearArgs& a, cudaStream_t st, bool pdl) {
     p.out = a.out;
     p.out_type = a.out_type;
     p.ldo = a.ldo;
-    p.vec = out_vec(a);
+    p.align = out_align(a);
     p.err = a.err;
     p.n_tiles = (a.N + kPairN - 1) / kPairN;
     p.tiles = (a.T + 255) / 256 * p.n_tiles;

@@ -122,5 +122,30 @@ __device__ __forceinline__ void mx_quantize_word(const X* type, const uint4& w, 
     word = mx_codes8(v, scale);
 }
 
+// Eight elements of a lane as they are loaded: one word where they are 16 bits wide and aligned.
+template <typename X, bool kVec>
+struct MxHeld {
+    static constexpr bool one_word = kVec && sizeof(X) == 2;
+    uint4 w;
+    float f[one_word ? 1 : 8];
+    __device__ __forceinline__ void load(const X* src, bool live) {
+        if constexpr (one_word) {
+            w = live ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+            if (live) load8<kVec>(src, f);
+        }
+    }
+    // the code word and, in every lane of a block's four, the scale
+    __device__ __forceinline__ void quantise(uint32_t& word, uint32_t& scale, int* err) const {
+        if constexpr (one_word) {
+            mx_quantize_word(static_cast<const X*>(nullptr), w, word, scale, err);
+        } else {
+            mx_quantize8(f, word, scale, err);
+        }
+    }
+};
+
 }  // namespace
 }  // namespace nvfp4
