@@ -190,9 +190,19 @@ __device__ __forceinline__ void store16(T* p, const uint64_t (&v)[8], int n, int
     }
 }
 
-// kCols outputs of row r at column n0 from a lane's accumulator values: NVFP4 outer scales (ga: the
-// row's, gcol: the columns'), the bias (bcol) if there is one, one rounding.  gcol, bcol: 8-byte aligned
-// shared memory.
+// 16 outputs from a lane's accumulator values: NVFP4 outer scales (g2: the row's twice, gcol: the
+// columns'), the bias (bcol) if there is one.  gcol, bcol: 8-byte aligned shared memory.
+template <bool kMx, bool kBias>
+__device__ __forceinline__ void scale16(const uint32_t* v, uint64_t g2, const float* gcol, const float* bcol, uint64_t (&o)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        o[i] = pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        if (!kMx) o[i] = pair_mul(pair_mul(o[i], g2), *reinterpret_cast<const uint64_t*>(gcol + 2 * i));
+        if (kBias) o[i] = pair_add(o[i], *reinterpret_cast<const uint64_t*>(bcol + 2 * i));
+    }
+}
+
+// kCols outputs of a row, of which the first `left` exist, straight to memory.
 template <bool kMx, bool kBias, typename T, int kCols>
 __device__ __forceinline__ void outputs(const uint32_t* v, float ga, const float* gcol, const float* bcol, T* row, int left,
                                         int align) {
@@ -201,12 +211,7 @@ __device__ __forceinline__ void outputs(const uint32_t* v, float ga, const float
     for (int h = 0; h < kCols; h += 16) {
         if (left <= h) break;
         uint64_t o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            o[i] = pair(__uint_as_float(v[h + 2 * i]), __uint_as_float(v[h + 2 * i + 1]));
-            if (!kMx) o[i] = pair_mul(pair_mul(o[i], g2), *reinterpret_cast<const uint64_t*>(gcol + h + 2 * i));
-            if (kBias) o[i] = pair_add(o[i], *reinterpret_cast<const uint64_t*>(bcol + h + 2 * i));
-        }
+        scale16<kMx, kBias>(v + h, g2, gcol + h, bcol + h, o);
         store16<T>(row + h, o, left - h, align);
     }
 }

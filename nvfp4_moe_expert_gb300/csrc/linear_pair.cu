@@ -9,7 +9,9 @@
 // SM's tensor core scales with its own TMEM); every copy completes on the leader's barrier.  The leader's
 // warp 1 copies the scales of both CTAs to their TMEM and issues the MMAs; its commits free the stage in
 // both.  Warps 4-19 of each CTA take the accumulator (128 lanes x 256 columns) to registers, hand TMEM
-// back and write their rows while the next tile's MMAs run.
+// back, and put their 32 rows x 64 columns in shared memory for a TMA store while the next tile's MMAs
+// run.  (Stores straight from the lanes, 32 rows to an instruction, slowed the loads down: a tile of K = 8192
+// took 19700 cycles instead of 17200 without any stores, one of K = 1536 6300 instead of 3900.)
 #include "linear.cuh"
 
 namespace nvfp4 {
@@ -21,6 +23,7 @@ constexpr int kPairEpiWarps = 16;
 constexpr int kHalfBytes = 128 * kRowBytes;          // 128 rows of a stage: A, or half of B
 constexpr uint32_t kAccCols = 256;
 constexpr int kPairStatic = 9216;                    // room left for the kernel's static shared memory
+constexpr int kOutBytes = 4096;                      // an epilogue warp's outputs on their way: 32 rows of 128 bytes
 
 template <bool kMx>
 struct PairStage {
@@ -29,10 +32,11 @@ struct PairStage {
     static constexpr int sfb = sfa + tiles * kSfAtomBytes;         // then B's two sets
     static constexpr int bytes = (sfb + 2 * tiles * kSfAtomBytes + 1023) / 1024 * 1024;
     static constexpr uint32_t sf_cols = 12 * tiles;
-    static constexpr int by_smem = (kSmemLimit - kPairStatic - 1024) / bytes;
+    static constexpr int by_smem = (kSmemLimit - kPairStatic - 1024 - kPairEpiWarps * kOutBytes) / bytes;
     static constexpr int by_tmem = (kTmemCols - kAccCols) / sf_cols;
     static constexpr int count = by_smem < by_tmem ? by_smem : by_tmem;
-    static constexpr int dynamic = count * bytes + 1024;
+    static constexpr int out = count * bytes;                      // the epilogue warps' outputs
+    static constexpr int dynamic = out + kPairEpiWarps * kOutBytes + 1024;
     static_assert(count <= 32, "a lane sets up each stage's barriers");
 };
 
@@ -46,6 +50,7 @@ struct PairParams {
     int out_type;
     int64_t ldo;
     int align;            // of out's rows: out_align()
+    int staged;           // outputs go through the tensor map tmOut
     int n_tiles;
     int64_t tiles;
     int* err;
@@ -108,15 +113,61 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
                  : "memory");
 }
 #undef PAIR_ELECT
+// Relaxed: what it hands over is TMEM, read to the end before (tcgen05.wait::ld).  A release at cluster
+// scope also waits for the outputs the CTA's other warps are storing, 2000 cycles a tile.
 __device__ __forceinline__ void arrive_leader(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A warp's 64 columns at n0 of the 32 rows at row0 (this lane's: accumulator values v) through its
+// shared-memory buffer: rows of 128 bytes, 128B swizzle, one TMA store for 64 16-bit or 32 FP32 columns;
+// what lies past T or N is not written.
+template <bool kMx, bool kBias, typename T>
+__device__ __forceinline__ void outputs_staged(const uint32_t* v, float ga, const float* gcol, const float* bcol, uint8_t* buf,
+                                               const CUtensorMap* map, int n0, int row0, int N) {
+    constexpr int kCols = 128 / sizeof(T), kChunks = sizeof(T);   // columns of a store; 16-byte chunks of 16 columns
+    const int lane = threadIdx.x & 31;
+    const uint64_t g2 = pair(ga, ga);
+    const uint32_t row = smem_u32(buf) + lane * 128;
+#pragma unroll
+    for (int c = 0; c < 64; c += kCols) {
+        if (n0 + c >= N) break;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the buffer's last store has read it
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < kCols; h += 16) {
+            uint64_t o[8];
+            scale16<kMx, kBias>(v + c + h, g2, gcol + c + h, bcol + c + h, o);
+            uint32_t w[4 * kChunks];
+            pack16<T>(o, w);
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((h / 16 * kChunks + i) ^ (lane & 7)) << 4)),
+                             "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                             : "memory");
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0)
+            asm volatile(
+                "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\tcp.async.bulk.commit_group;" ::"l"(
+                    reinterpret_cast<uint64_t>(map)),
+                "r"(smem_u32(buf)), "r"(n0 + c), "r"(row0)
+                : "memory");
+    }
+}
+template <bool kMx, typename T>
+__device__ __forceinline__ void outputs_staged(const uint32_t* v, float ga, const float* gcol, const float* bcol, uint8_t* buf,
+                                               const CUtensorMap* map, int n0, int row0, const PairParams& p) {
+    if (p.bias != nullptr) outputs_staged<kMx, true, T>(v, ga, gcol, bcol, buf, map, n0, row0, p.N);
+    else outputs_staged<kMx, false, T>(v, ga, gcol, bcol, buf, map, n0, row0, p.N);
 }
 
 template <bool kMx>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmSfa, const __grid_constant__ CUtensorMap tmSfb,
-                       const PairParams p) {
+                       const __grid_constant__ CUtensorMap tmOut, const PairParams p) {
     using S = PairStage<kMx>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -260,6 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint32_t empty_bar = leader_addr(&tmem_empty);
         float* gcol = s_col[warp - 4][0];
         float* bcol = s_col[warp - 4][1];
+        uint8_t* buf = smem + S::out + (warp - 4) * kOutBytes;
         uint32_t acc_phase = 0;
         for (int64_t t = first; t < p.tiles; t += step) {
             const int64_t r = t / p.n_tiles * 256 + 128 * rank + q * 32 + lane;
@@ -289,8 +341,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_leader(empty_bar);
-            if (live && n0 < p.N) write_outputs<kMx, 64>(v, ga, gcol, bcol, r, n0, p);
+            if (p.staged) {
+                if (r - lane >= p.T) continue;         // the whole warp
+                const int row0 = static_cast<int>(r - lane);
+                if (p.out_type == NVFP4_TYPE_BF16) outputs_staged<kMx, __nv_bfloat16>(v, ga, gcol, bcol, buf, &tmOut, n0, row0, p);
+                else if (p.out_type == NVFP4_TYPE_F32) outputs_staged<kMx, float>(v, ga, gcol, bcol, buf, &tmOut, n0, row0, p);
+                else outputs_staged<kMx, __half>(v, ga, gcol, bcol, buf, &tmOut, n0, row0, p);
+            } else if (live && n0 < p.N) {
+                write_outputs<kMx, 64>(v, ga, gcol, bcol, r, n0, p);
+            }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     tc_fence_before();
@@ -300,6 +361,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }
+}
+
+// Map over out [T][N] for stores of 32 rows x 128 bytes (rows on 16-byte boundaries).
+bool make_out_map(CUtensorMap* m, const LinearArgs& a) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const int size = a.out_type == NVFP4_TYPE_F32 ? 4 : 2;
+    const CUtensorMapDataType type = a.out_type == NVFP4_TYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : a.out_type == NVFP4_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.N), static_cast<cuuint64_t>(a.T)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.ldo * size)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), 32};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, type, 2, a.out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool kMx>
@@ -323,14 +400,16 @@ cudaError_t launch_pair(const LinearArgs& a, cudaStream_t st, bool pdl) {
     p.n_tiles = (a.N + kPairN - 1) / kPairN;
     p.tiles = (a.T + 255) / 256 * p.n_tiles;
     const int64_t sf_tiles = (a.K + Format<kMx>::tile_k - 1) / Format<kMx>::tile_k;
-    CUtensorMap ma, mb, msa, msb;
+    CUtensorMap ma, mb, msa, msb, mo = {};
+    p.staged = p.align != 0;
+    if (p.staged && !make_out_map(&mo, a)) return cudaErrorInvalidValue;
     if (!make_map(&ma, a.a_codes, a.T, a.K / 2, 128) || !make_map(&mb, a.b_codes, a.N, a.K / 2, 128) ||
         !make_sf_map(&msa, a.a_sf, (a.T + 127) / 128, sf_tiles, S::tiles, 1) ||
         !make_sf_map(&msb, a.b_sf, (a.N + 127) / 128, sf_tiles, S::tiles, 2))
         return cudaErrorInvalidValue;
     const int64_t pairs = linear_pair_count();
     const unsigned grid = static_cast<unsigned>(2 * (p.tiles < pairs ? p.tiles : pairs));
-    return launch_pdl(pdl, linear_pair_kernel<kMx>, grid, kPairThreads, S::dynamic, st, ma, mb, msa, msb, p);
+    return launch_pdl(pdl, linear_pair_kernel<kMx>, grid, kPairThreads, S::dynamic, st, ma, mb, msa, msb, mo, p);
 }
 
 }  // namespace
