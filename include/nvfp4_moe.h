@@ -515,7 +515,7 @@ nvfp4_status moe_route_topk_backward(const void* logits_dev, int type, int64_t T
 size_t mxfp4_sf_bytes(int64_t rows, int64_t cols);   /* 0 on bad input */
 
 /*  x_dev      [rows][ld] of `type`, element aligned; ld >= cols
- *  rows >= 0; cols % 32 == 0, 32 <= cols <= 2^20; (rows + 128) * ceil(cols / 256) < 2^31
+ *  rows >= 0; cols % 32 == 0, 32 <= cols <= 2^20; (rows + 128) * ceil(cols / 128) < 2^29
  *  codes_dev  uint8 [nvfp4_rows_padded(rows)][cols/2], 16-byte aligned; sf_dev mxfp4_sf_bytes(rows,
  *             cols) bytes, 16-byte aligned; rows past `rows` get zero codes and scales
  * Device error: NVFP4_ERR_NONFINITE. */

@@ -676,7 +676,7 @@ constexpr int64_t kMaxMxCols = int64_t(1) << 20;
 
 bool mx_shape_ok(int64_t rows, int64_t cols) {
     return rows >= 0 && rows < kMaxTokens && cols >= kMxBlock && cols <= kMaxMxCols && cols % kMxBlock == 0 &&
-           (rows + kTileM) * ((cols + 255) / 256) < (int64_t(1) << 31);   // pieces of 256 columns
+           (rows + kTileM) * 4 * mx_sf_tiles(cols) < (int64_t(1) << 31);   // blocks of 32 elements
 }
 bool nv_shape_ok(int64_t rows, int64_t cols) {
     return rows >= 0 && rows < kMaxTokens && cols >= 64 && cols <= 8192 && cols % 64 == 0;

@@ -275,22 +275,25 @@ constexpr int kEpiWarp = 4;
 constexpr int kMaxK = 8192;
 constexpr int kChunkBytes = kMaxT * kRowBytes;       // one 256-element chunk of the 16 rows
 constexpr int kPer = 4;                              // chunks of the weights per stage: 1024 K-elements
-// A quantiser warp takes pieces of one row: 256 columns (MXFP4, 8 to a lane) or 512 (NVFP4, one
-// block of 16 to a lane), several loaded before the first is used.  The pieces are ordered by
-// columns, then rows, and a batch (all warps' pieces of one turn) becomes ready as a whole.
+// A quantiser warp takes pieces of one row: 1024 columns (MXFP4, one block of 32 to a lane) or 512 (NVFP4,
+// one of 16), several loaded before the first is used.  The pieces are ordered by columns, then rows, and a
+// batch (all warps' pieces of one turn) becomes ready as a whole.
 template <bool kMx>
-__host__ __device__ constexpr int piece_cols() { return kMx ? 256 : 512; }
-// Pieces a warp holds at once: eight where a lane's share is one 16-byte word, four of 32 bytes.
-__host__ __device__ constexpr int pieces_held(bool one_word) { return one_word ? 8 : 4; }
+__host__ __device__ constexpr int piece_cols() { return kMx ? 1024 : 512; }
+template <bool kMx>
+__host__ __device__ constexpr int pieces_held() { return kMx ? 1 : 4; }
+template <bool kMx>
+__host__ __device__ constexpr int batch_size() { return pieces_held<kMx>() * kQuantWarps; }
 constexpr int kMaxBatches = 8;                       // 16 rows of 8192
-static_assert(kMaxT * (kMaxK / piece_cols<true>()) <= kMaxBatches * pieces_held(false) * kQuantWarps, "batches");
+static_assert(kMaxT * (kMaxK / piece_cols<true>()) <= kMaxBatches * batch_size<true>(), "batches");
+static_assert(kMaxT * (kMaxK / piece_cols<false>()) <= kMaxBatches * batch_size<false>(), "batches");
 constexpr int kMaxStagesD = 8;
 
 struct DecodeParams {
     const void* x;
     int x_type;
     int64_t ldx;
-    int x_vec;            // rows of x start on 16-byte boundaries (NVFP4: always)
+    int x_align;          // of x's rows: mx_align()
     int T, N, K;
     uint32_t t_magic;     // ceil(2^16 / T): q / T = q * t_magic >> 16 for q < 4096
     const uint8_t* b_sf;
@@ -300,11 +303,10 @@ struct DecodeParams {
     int out_type;
     int64_t ldo;
     int align;
-    int batch_shift;      // log2 of the pieces of x that become ready together
     int stages, n_tiles;
     int* err;
 };
-static_assert(kMaxT * (kMaxK / piece_cols<true>()) + 128 <= 4096, "t_magic's range (a turn may pass the last piece)");
+static_assert(kMaxT * (kMaxK / piece_cols<false>()) + batch_size<false>() <= 4096, "t_magic's range (a turn may pass the last piece)");
 
 // Piece q: its row and its place among the row's pieces.
 __device__ __forceinline__ void piece(const DecodeParams& p, int q, int& r, int& i) {
@@ -320,49 +322,38 @@ __device__ __forceinline__ void sync_quantisers() { asm volatile("barrier.sync 1
 __device__ __forceinline__ void start_arrive() { asm volatile("barrier.arrive 2, %0;" ::"r"(kThreadsD) : "memory"); }
 __device__ __forceinline__ void start_wait() { asm volatile("barrier.sync 2, %0;" ::"r"(kThreadsD) : "memory"); }
 
-template <typename X, bool kVec>
+template <typename X, int kAlign>
 __device__ __forceinline__ void quantise_mx(const DecodeParams& p, int warp, int lane, uint8_t* codes, uint8_t* sf,
                                             uint64_t* a_full) {
-    using H = MxHeld<X, kVec>;
-    constexpr int kCols = piece_cols<true>(), kHeld = pieces_held(H::one_word);
+    constexpr int kCols = piece_cols<true>();
     const X* x = static_cast<const X*>(p.x);
     const int pieces = p.T * ((p.K + kCols - 1) / kCols);
     const int sf_cols = (p.K + kMxTileCols - 1) / kMxTileCols * kMxTileCols;   // the blocks past K get zero scales
-    H held[kHeld], next[kHeld];
-    auto load = [&](H(&h)[kHeld], int first) {
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int q = first + i * kQuantWarps + warp;
-            int r, at;
-            piece(p, q, r, at);
-            const int c = at * kCols + 8 * lane;
-            h[i].load(x + r * p.ldx + c, q < pieces && c < p.K);
-        }
+    MxBlock<X, kAlign> held, next;
+    auto load = [&](MxBlock<X, kAlign>& h, int q) {
+        int r, at;
+        piece(p, q, r, at);
+        const int c = at * kCols + kMxBlock * lane;
+        h.load(x + r * p.ldx + c, q < pieces && c < p.K);
     };
-    load(held, 0);
+    load(held, warp);
     start_wait();                                     // the first loads are on their way before the CTA is set up
-    for (int first = 0, batch = 0; first < pieces; first += kHeld * kQuantWarps, ++batch) {
-        if (H::one_word) load(next, first + kHeld * kQuantWarps);
-        else if (first > 0) load(held, first);
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int q = first + i * kQuantWarps + warp;
-            if (q >= pieces) break;                   // the whole warp
+    for (int first = 0, batch = 0; first < pieces; first += kQuantWarps, ++batch) {
+        const int q = first + warp;
+        load(next, q + kQuantWarps);
+        if (q < pieces) {
             int r, at;
             piece(p, q, r, at);
-            const int c = at * kCols + 8 * lane;
-            uint32_t word, scale;
-            held[i].quantise(word, scale, p.err);
-            if (c < p.K) *reinterpret_cast<uint32_t*>(codes + at * kChunkBytes + swizzled(r, lane)) = word;
-            if ((lane & 3) == 0 && c < sf_cols)
-                sf[c / kMxTileCols * kSfAtomBytes + r * 16 + (lane >> 2 & 3)] = static_cast<uint8_t>(scale);
+            const int c = at * kCols + kMxBlock * lane;
+            uint4 word;
+            uint32_t scale;
+            held.quantise(word, scale, p.err);
+            if (c < p.K) *reinterpret_cast<uint4*>(codes + c / kStageK * kChunkBytes + swizzled(r, 4 * (lane & 7))) = word;
+            if (c < sf_cols) sf[c / kMxTileCols * kSfAtomBytes + r * 16 + (lane & 3)] = static_cast<uint8_t>(scale);
         }
         fence_proxy_async_shared();
         mbar_arrive(&a_full[batch]);
-        if (H::one_word) {
-#pragma unroll
-            for (int i = 0; i < kHeld; ++i) held[i] = next[i];
-        }
+        held = next;
     }
 }
 
@@ -383,7 +374,7 @@ __device__ __forceinline__ bool nv_block(const DecodeParams& p, int q, int piece
 
 __device__ __forceinline__ void quantise_nv(const DecodeParams& p, int warp, int lane, uint8_t* codes, uint8_t* sf,
                                             uint32_t* row_max, float* row_g, uint64_t* a_full) {
-    constexpr int kCols = piece_cols<false>(), kHeld = pieces_held(false), kBatch = kHeld * kQuantWarps;
+    constexpr int kCols = piece_cols<false>(), kHeld = pieces_held<false>(), kBatch = batch_size<false>();
     const int pieces = p.T * ((p.K + kCols - 1) / kCols);
     uint4 v[kHeld][2];
     // the rows' maxima, then their outer scales; the last batch comes first, so that the first, which
@@ -434,6 +425,14 @@ __device__ __forceinline__ void quantise_nv(const DecodeParams& p, int warp, int
     }
 }
 
+template <typename X>
+__device__ __forceinline__ void quantise_mx_rows(const DecodeParams& p, int warp, int lane, uint8_t* codes, uint8_t* sf,
+                                                 uint64_t* a_full) {
+    if (p.x_align == 2) quantise_mx<X, 2>(p, warp, lane, codes, sf, a_full);
+    else if (p.x_align == 1) quantise_mx<X, 1>(p, warp, lane, codes, sf, a_full);
+    else quantise_mx<X, 0>(p, warp, lane, codes, sf, a_full);
+}
+
 // Quantise the T rows of x; warp 0..kQuantWarps-1 of the quantisers.
 template <bool kMx>
 __device__ __forceinline__ void quantise_x(const DecodeParams& p, int warp, int lane, uint8_t* codes, uint8_t* sf,
@@ -441,14 +440,11 @@ __device__ __forceinline__ void quantise_x(const DecodeParams& p, int warp, int 
     if (!kMx) {
         quantise_nv(p, warp, lane, codes, sf, row_max, row_g, a_full);
     } else if (p.x_type == NVFP4_TYPE_BF16) {
-        if (p.x_vec) quantise_mx<__nv_bfloat16, true>(p, warp, lane, codes, sf, a_full);
-        else quantise_mx<__nv_bfloat16, false>(p, warp, lane, codes, sf, a_full);
+        quantise_mx_rows<__nv_bfloat16>(p, warp, lane, codes, sf, a_full);
     } else if (p.x_type == NVFP4_TYPE_F16) {
-        if (p.x_vec) quantise_mx<__half, true>(p, warp, lane, codes, sf, a_full);
-        else quantise_mx<__half, false>(p, warp, lane, codes, sf, a_full);
+        quantise_mx_rows<__half>(p, warp, lane, codes, sf, a_full);
     } else {
-        if (p.x_vec) quantise_mx<float, true>(p, warp, lane, codes, sf, a_full);
-        else quantise_mx<float, false>(p, warp, lane, codes, sf, a_full);
+        quantise_mx_rows<float>(p, warp, lane, codes, sf, a_full);
     }
 }
 
@@ -563,7 +559,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 bool okf = true;
                 if (t == static_cast<int>(blockIdx.x)) {   // the batches that complete x's columns of this stage
                     const int whole = (kPer * st + chunks + piece_cols<kMx>() / kStageK - 1) / (piece_cols<kMx>() / kStageK);
-                    const int need = ((whole * p.T - 1) >> p.batch_shift) + 1;
+                    const int need = (whole * p.T - 1) / batch_size<kMx>() + 1;
                     while (okf && batch < need)
                         okf = mbar_wait_bounded(&a_full[batch++], 0, abort_flag, kWaitBudgetCycles);
                 }
@@ -654,10 +650,7 @@ cudaError_t launch_decode(const LinearInput& x, const LinearArgs& a, cudaStream_
     p.x = x.x;
     p.x_type = x.type;
     p.ldx = x.ld;
-    const int x_size = x.type == NVFP4_TYPE_F32 ? 4 : 2;
-    p.x_vec = (reinterpret_cast<uintptr_t>(x.x) & 15) == 0 && (x.ld * x_size) % 16 == 0;
-    p.batch_shift = kMx && p.x_vec && x_size == 2 ? 7 : 6;
-    static_assert(kQuantWarps * pieces_held(true) == 128 && kQuantWarps * pieces_held(false) == 64, "batch_shift");
+    p.x_align = mx_align(x.x, x.ld, x.type == NVFP4_TYPE_F32 ? 4 : 2);
     p.T = static_cast<int>(a.T);
     p.t_magic = (65536u + p.T - 1) / p.T;
     p.N = a.N;

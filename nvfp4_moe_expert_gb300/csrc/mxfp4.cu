@@ -13,57 +13,39 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// A warp's piece: 256 columns of a row (8 elements, a quarter of a block, to a lane, read as one 16-byte
-// word of BF16 or FP16), kPieces of them at once so that enough loads are in flight; pieces are counted
-// row by row.  One 4-byte word of codes to a lane (128 bytes to a warp), one of scales to 16 lanes.
-constexpr int kPieces = 4;
+// A lane takes whole blocks of 32 elements; a row's blocks are counted with those that fill up its last
+// scale word, and the rows with those that fill up the last tile (both get zeros).
+constexpr int kHeld = 2;           // blocks of a lane in flight
 
-struct Pieces {
-    uint32_t per_row, count;   // pieces of a row and of all rows
-    __device__ __forceinline__ void place(uint32_t i, uint32_t& r, uint32_t& at) const {
-        r = i / per_row;
-        at = i - r * per_row;
-    }
+struct Blocks {
+    uint32_t per_row, live, count;   // blocks of a row, those with elements, blocks of all rows
 };
 
-template <typename T, bool kVec>
+template <typename T, int kAlign>
 __global__ void __launch_bounds__(kThreads)
-    mxfp4_quantize_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, Pieces pieces,
+    mxfp4_quantize_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, Blocks blocks,
                                uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, int* err) {
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const uint32_t warps = gridDim.x * (kThreads / 32);
-    const int sf_cols = static_cast<int>(mx_sf_tiles(cols)) * kMxTileCols;
-    for (uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w * kPieces < pieces.count; w += warps) {
-        MxHeld<T, kVec> held[kPieces];
-        uint32_t r, at;
-        pieces.place(w * kPieces, r, at);
-        uint32_t r_of[kPieces], at_of[kPieces];
+    const uint32_t step = gridDim.x * kThreads;
+    for (uint32_t first = blockIdx.x * kThreads + threadIdx.x; first < blocks.count; first += kHeld * step) {
+        MxBlock<T, kAlign> held[kHeld];
+        uint32_t r[kHeld], at[kHeld];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            r_of[i] = r;
-            at_of[i] = at;
-            const int c = static_cast<int>(at) * 256 + 8 * lane;
-            held[i].load(x + r * ld + c, r < rows && c < cols);
-            if (++at == pieces.per_row) {
-                at = 0;
-                ++r;
-            }
+        for (int i = 0; i < kHeld; ++i) {
+            const uint32_t b = first + i * step;
+            r[i] = b / blocks.per_row;
+            at[i] = b - r[i] * blocks.per_row;
+            held[i].load(x + r[i] * ld + at[i] * kMxBlock, b < blocks.count && r[i] < rows && at[i] < blocks.live);
         }
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            if (w * kPieces + i >= pieces.count) break;
-            const int c = static_cast<int>(at_of[i]) * 256 + 8 * lane;
-            uint32_t word, scale;
-            held[i].quantise(word, scale, err);
-            uint32_t scales = scale;                                 // 16 lanes' four scales, in the first of them
-            scales |= __shfl_down_sync(0xFFFFFFFFu, scale, 4) << 8;
-            scales |= __shfl_down_sync(0xFFFFFFFFu, scale, 8) << 16;
-            scales |= __shfl_down_sync(0xFFFFFFFFu, scale, 12) << 24;
-            if (c < cols) *reinterpret_cast<uint32_t*>(codes + r_of[i] * (cols / 2) + c / 2) = word;
-            if ((lane & 15) == 0 && c < sf_cols)
-                *reinterpret_cast<uint32_t*>(sf + mx_sf_offset(r_of[i], c / kMxBlock, cols)) = scales;
+        for (int i = 0; i < kHeld; ++i) {
+            if (first + i * step >= blocks.count) break;
+            uint4 c;
+            uint32_t scale;
+            held[i].quantise(c, scale, err);
+            if (at[i] < blocks.live) *reinterpret_cast<uint4*>(codes + r[i] * (cols / 2) + at[i] * (kMxBlock / 2)) = c;
+            sf[mx_sf_offset(r[i], at[i], cols)] = static_cast<uint8_t>(scale);
         }
     }
 }
@@ -88,95 +70,101 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Eight values to a lane: one word of codes in, 16 (BF16) or 32 (FP32) bytes out.  The product with a
-// power of two is exact in BF16 (its smallest subnormal is 2^-133, the smallest product 2^-128).
-template <typename T>
-__device__ __forceinline__ void store8(T* p, uint32_t c, uint32_t scale, bool vec) {
+// One block of 32 values to a lane: 16 bytes of codes in, 64 (BF16) or 128 (FP32) bytes out.  The product
+// with a power of two is exact in BF16 (its smallest subnormal is 2^-133, the smallest product 2^-128).
+template <typename T, int kAlign>
+__device__ __forceinline__ void store_block(T* p, const uint4& codes, uint32_t scale) {
     const uint32_t s16 = __float_as_uint(e8m0_value(scale)) >> 16;
     const uint32_t s2 = s16 | (s16 << 16);
-    uint32_t w[4];
-    e2m1x4_bf16(c, w[0], w[1]);
-    e2m1x4_bf16(c >> 16, w[2], w[3]);
+    const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
+    constexpr int kWords = 8 * sizeof(T);
+    uint32_t w[kWords];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = bf16x2_mul(w[i], s2);
-    if constexpr (sizeof(T) == 2) {
-        if (vec) {
-            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            uint16_t* q = reinterpret_cast<uint16_t*>(p);
+    for (int i = 0; i < 8; ++i) {
+        uint32_t v[2];
+        e2m1x4_bf16(c[i >> 1] >> (16 * (i & 1)), v[0], v[1]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+        for (int j = 0; j < 2; ++j) {
+            v[j] = bf16x2_mul(v[j], s2);
+            if constexpr (sizeof(T) == 2) w[2 * i + j] = v[j];
+            else w[4 * i + 2 * j] = v[j] << 16, w[4 * i + 2 * j + 1] = v[j] & 0xFFFF0000u;
         }
+    }
+    if constexpr (kAlign == 2) {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint32_t*>(p) + i),
+                         "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
+                         "r"(w[i + 7])
+                         : "memory");
+    } else if constexpr (kAlign == 1) {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4)
+            *(reinterpret_cast<uint4*>(p) + i / 4) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
     } else {
-        float v[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-        if (vec) {
-            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = v[i];
-        }
+        for (int i = 0; i < 32; ++i) reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
     }
 }
 
-template <typename T>
+template <typename T, int kAlign>
 __global__ void __launch_bounds__(kThreads)
-    mxfp4_dequantize_rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ sf, int64_t rows,
-                                 int64_t cols, Pieces pieces, T* __restrict__ out, int64_t ld, bool vec) {
-    const int lane = threadIdx.x & 31;
-    const uint32_t warps = gridDim.x * (kThreads / 32);
-    for (uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w * kPieces < pieces.count; w += warps) {
-        uint32_t r, at, c[kPieces], scale[kPieces], r_of[kPieces], at_of[kPieces];
-        pieces.place(w * kPieces, r, at);
+    mxfp4_dequantize_rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ sf, int64_t cols,
+                                 Blocks blocks, T* __restrict__ out, int64_t ld) {
+    const uint32_t step = gridDim.x * kThreads;
+    for (uint32_t first = blockIdx.x * kThreads + threadIdx.x; first < blocks.count; first += kHeld * step) {
+        uint4 c[kHeld];
+        uint32_t scale[kHeld], r[kHeld], at[kHeld];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            r_of[i] = r;
-            at_of[i] = at;
-            const int k = static_cast<int>(at) * 256 + 8 * lane;
-            c[i] = scale[i] = 0u;
-            if (r < rows && k < cols) {
-                c[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + r * (cols / 2) + k / 2));
-                scale[i] = __ldg(sf + mx_sf_offset(r, k / kMxBlock, cols));
-            }
-            if (++at == pieces.per_row) {
-                at = 0;
-                ++r;
+        for (int i = 0; i < kHeld; ++i) {
+            const uint32_t b = first + i * step;
+            r[i] = b / blocks.per_row;
+            at[i] = b - r[i] * blocks.per_row;
+            if (b < blocks.count) {
+                c[i] = __ldg(reinterpret_cast<const uint4*>(codes + r[i] * (cols / 2)) + at[i]);
+                scale[i] = __ldg(sf + mx_sf_offset(r[i], at[i], cols));
             }
         }
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int k = static_cast<int>(at_of[i]) * 256 + 8 * lane;
-            if (r_of[i] < rows && k < cols) store8(out + r_of[i] * ld + k, c[i], scale[i], vec);
+        for (int i = 0; i < kHeld; ++i) {
+            if (first + i * step < blocks.count) store_block<T, kAlign>(out + r[i] * ld + at[i] * kMxBlock, c[i], scale[i]);
         }
     }
 }
 
-// Pieces of `rows` rows (fewer than 2^31, as the entry points see to), and enough blocks to fill the SMs.
-void split(int64_t rows, int64_t cols, Pieces& p, unsigned& grid) {
-    const int64_t per_row = (cols + 255) / 256, count = rows * per_row;
-    p = {static_cast<uint32_t>(per_row), static_cast<uint32_t>(count)};
-    const int64_t blocks = (count + kPieces * (kThreads / 32) - 1) / (kPieces * (kThreads / 32));
-    const int64_t most = static_cast<int64_t>(device_sm_count()) * 8;
-    grid = static_cast<unsigned>(blocks < most ? blocks : most);
-}
-
-bool aligned16(const void* p, int64_t ld, int size) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * size) % 16 == 0;
+// Thread blocks that fill the SMs.
+unsigned grid_for(uint32_t count) {
+    const uint32_t blocks = (count + kThreads - 1) / kThreads, most = static_cast<uint32_t>(device_sm_count()) * 8;
+    return blocks < most ? blocks : most;
 }
 
 template <typename T>
 cudaError_t quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes, uint8_t* sf, int* err,
                      cudaStream_t st) {
-    Pieces p;
-    unsigned grid;
-    split((rows + kTileM - 1) / kTileM * kTileM, cols, p, grid);
-    auto k = aligned16(x, ld, sizeof(T)) ? mxfp4_quantize_rows_kernel<T, true> : mxfp4_quantize_rows_kernel<T, false>;
-    return launch_pdl(false, k, grid, kThreads, 0, st, static_cast<const T*>(x), rows, cols, ld, p, codes, sf, err);
+    const int64_t rows_pad = (rows + kTileM - 1) / kTileM * kTileM;
+    const uint32_t per_row = static_cast<uint32_t>(4 * mx_sf_tiles(cols));
+    const Blocks b = {per_row, static_cast<uint32_t>(cols / kMxBlock), static_cast<uint32_t>(rows_pad * per_row)};
+    const int align = mx_align(x, ld, sizeof(T));
+    auto k = align == 2   ? mxfp4_quantize_rows_kernel<T, 2>
+             : align == 1 ? mxfp4_quantize_rows_kernel<T, 1>
+                          : mxfp4_quantize_rows_kernel<T, 0>;
+    return launch_pdl(false, k, grid_for(b.count), kThreads, 0, st, static_cast<const T*>(x), rows, cols, ld, b, codes, sf,
+                      err);
+}
+
+template <typename T>
+cudaError_t dequantize(const uint8_t* codes, const uint8_t* sf, int64_t rows, int64_t cols, void* out, int64_t ld,
+                       cudaStream_t st) {
+    const uint32_t per_row = static_cast<uint32_t>(cols / kMxBlock);
+    const Blocks b = {per_row, per_row, static_cast<uint32_t>(rows * per_row)};
+    const int align = mx_align(out, ld, sizeof(T));
+    auto k = align == 2   ? mxfp4_dequantize_rows_kernel<T, 2>
+             : align == 1 ? mxfp4_dequantize_rows_kernel<T, 1>
+                          : mxfp4_dequantize_rows_kernel<T, 0>;
+    return launch_pdl(false, k, grid_for(b.count), kThreads, 0, st, codes, sf, cols, b, static_cast<T*>(out), ld);
 }
 
 }  // namespace
@@ -192,14 +180,8 @@ cudaError_t launch_mxfp4_quantize_rows(const void* x, int type, int64_t rows, in
 
 cudaError_t launch_mxfp4_dequantize_rows(const uint8_t* codes, const uint8_t* sf, int64_t rows, int64_t cols,
                                          void* out, int type, int64_t ld, cudaStream_t st) {
-    Pieces p;
-    unsigned grid;
-    split(rows, cols, p, grid);
-    if (type == NVFP4_TYPE_F32)
-        return launch_pdl(false, mxfp4_dequantize_rows_kernel<float>, grid, kThreads, 0, st, codes, sf, rows, cols, p,
-                          static_cast<float*>(out), ld, aligned16(out, ld, 4));
-    return launch_pdl(false, mxfp4_dequantize_rows_kernel<__nv_bfloat16>, grid, kThreads, 0, st, codes, sf, rows, cols, p,
-                      static_cast<__nv_bfloat16*>(out), ld, aligned16(out, ld, 2));
+    return type == NVFP4_TYPE_F32 ? dequantize<float>(codes, sf, rows, cols, out, ld, st)
+                                  : dequantize<__nv_bfloat16>(codes, sf, rows, cols, out, ld, st);
 }
 
 }  // namespace nvfp4
