@@ -9,6 +9,9 @@ namespace nvfp4 {
 struct RouteParams {
     int score, k, n_group, topk_group, group_score, renormalize;
     float scale;
+    // set by the launcher
+    int group_lanes;   // lanes of a group, 0 if a group is no power of two of whole lanes
+    int bias_wide;     // bias lies on a 16-byte boundary
 };
 
 // logits [T][ld] of NVFP4_TYPE_*; ids, weights [T][k]

@@ -12,6 +12,7 @@
 // All sums and scores are FP32, taken in one fixed order, so a token's result does not depend on
 // the batch it is in.
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -25,200 +26,383 @@ namespace {
 constexpr int kWarps = 8;                 // tokens (one per warp) of a block
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 template <typename T>
-__device__ __forceinline__ float load_f32(const T* p);
+__device__ __forceinline__ T from_f32(float v);
 template <>
-__device__ __forceinline__ float load_f32<float>(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
-__device__ __forceinline__ float load_f32<__nv_bfloat16>(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <>
-__device__ __forceinline__ float load_f32<__half>(const __half* p) { return __half2float(*p); }
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
+// kN consecutive elements (kN * sizeof(T) <= 16, a power of two, and the address a multiple of it).
+template <int kBytes>
+struct Word;
+template <>
+struct Word<2> { using type = unsigned short; };
+template <>
+struct Word<4> { using type = uint32_t; };
+template <>
+struct Word<8> { using type = uint2; };
+template <>
+struct Word<16> { using type = uint4; };
+template <typename T, int kN>
+struct Vec {
+    union {
+        typename Word<kN * sizeof(T)>::type word;
+        T e[kN];
+    };
+    __device__ Vec() {}
+};
+template <typename T, int kN>
+__device__ __forceinline__ void load_vec(const T* p, float (&v)[kN]) {
+    Vec<T, kN> w;
+    w.word = __ldg(reinterpret_cast<const decltype(w.word)*>(p));
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = to_f32(w.e[i]);
+}
+template <typename T, int kN>
+__device__ __forceinline__ void store_vec(T* p, const float (&v)[kN]) {
+    Vec<T, kN> w;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) w.e[i] = from_f32<T>(v[i]);
+    *reinterpret_cast<decltype(w.word)*>(p) = w.word;
+}
 template <typename T>
-__device__ __forceinline__ void store_f32(T* p, float v);
-template <>
-__device__ __forceinline__ void store_f32<float>(float* p, float v) { *p = v; }
-template <>
-__device__ __forceinline__ void store_f32<__nv_bfloat16>(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ void store_f32<__half>(__half* p, float v) { *p = __float2half_rn(v); }
+__device__ __forceinline__ float load_one(const T* p) {
+    float v[1];
+    load_vec<T, 1>(p, v);
+    return v[0];
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
+// Order-preserving bits of a float: larger first as unsigned, +-0 equal; all above 0, which stands for no value.
+__device__ __forceinline__ uint32_t ordered(float o) {
+    const uint32_t b = __float_as_uint(o + 0.0f);          // -0 + 0 = +0
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float unordered(uint32_t k) {
+    return __uint_as_float(k ^ (~static_cast<uint32_t>(static_cast<int32_t>(k) >> 31) | 0x80000000u));
+}
+__device__ __forceinline__ float warp_max(float v) { return unordered(__reduce_max_sync(kAll, ordered(v))); }
 
 // A logit with NaN replaced by the mask.
 __device__ __forceinline__ float masked_nan(float l) { return l != l ? -INFINITY : l; }
 
-// e^(l - m) of a softmax whose largest logit is m: 1 where l = m (also for m = +inf), 0 where l is
-// masked (also where every logit is, m = -inf).
-__device__ __forceinline__ float softmax_term(float l, float m) {
-    if (l == -INFINITY) return 0.0f;
-    return l == m ? 1.0f : expf(l - m);
-}
-__device__ __forceinline__ float sigmoid(float l) { return l == -INFINITY ? 0.0f : __fdiv_rn(1.0f, 1.0f + expf(-l)); }
+// The terms of a softmax with largest logit m are expf(l - m), 0 where l is masked.  Where m is infinite l and m
+// are replaced by what gives them: all masked (m = -inf), or the +inf ones equal and the others 0.
+__device__ __forceinline__ float softmax_shift(float m) { return m == INFINITY || m == -INFINITY ? 0.0f : m; }
+__device__ __forceinline__ float softmax_logit(float l, float m) { return m == INFINITY ? (l == INFINITY ? 0.0f : -INFINITY) : l; }
+__device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(1.0f + expf(-l)); }   // 0 at -inf, 1 at +inf
 
-// Order-preserving key of an order value: larger first as unsigned; +-0 equal.  Masked: kMasked;
-// an expert outside the kept groups, one already chosen, or none: 0.
-constexpr uint32_t kMasked = 1u;
-__device__ __forceinline__ uint32_t order_key(float o) {
-    const uint32_t b = __float_as_uint(o + 0.0f);          // -0 + 0 = +0
-    if (!(o > -INFINITY)) return kMasked;                  // -inf and NaN
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);     // finite values and +inf: all above kMasked
+// The scores the order goes by, every expert's, come from the hardware's base-2 exponential and reciprocal
+// (2 units of the last place, and that of the argument's rounding): sigmoid(l) and a softmax's terms, at most 1,
+// are within 1e-7 of theirs.  The weights come from expf.
+__device__ __forceinline__ float fast_exp(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+    return y;
+}
+__device__ __forceinline__ float order_sigmoid(float l) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + fast_exp(-l)));
+    return y;
 }
 
-// One warp per token; lane holds experts lane + 32 i, i < V.
-template <typename T, int V>
+// The groups to keep: the topk_group largest keys, the lower group first on equal ones.  Every lane has its
+// own group's key gk; `group` is the lane's group.  Returns whether the lane's group is kept.
+__device__ __forceinline__ bool keep_group(uint32_t gk, int group, int topk_group) {
+    bool kept = false;
+    for (int j = 0; j < topk_group; ++j) {
+        const uint32_t top = __reduce_max_sync(kAll, gk);
+        const int first = __ffs(static_cast<int>(__ballot_sync(kAll, gk == top))) - 1;
+        if (group == __shfl_sync(kAll, group, first)) {
+            kept = true;
+            gk = 0u;
+        }
+    }
+    return kept;
+}
+
+// The k largest of the lanes' keys (lane order, then i, is id order; at least k are not 0), larger first, the lower
+// id first on equal ones: lane c gets a candidate's id and its place, kNone if it is not among the k.
+//
+// The k-th largest of the lanes' maxima is a lower bound of the k-th largest key, which about k + 2 of 256 keys
+// reach; those are put side by side in shared memory and each is ranked against the others.  Where more than 32
+// reach it (many equal keys, few lanes with keys), the picks are taken one by one.
+constexpr int kNone = 32;
+template <int V>
+__device__ __forceinline__ void select(uint32_t (&key)[V], int k, unsigned long long* cand, int lane, int& id, int& place) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = max(m, key[i]);
+    uint32_t bound = 0u;
+    for (int j = 0; j < k; ++j) {
+        bound = __reduce_max_sync(kAll, m);
+        m = m == bound ? 0u : m;
+    }
+    bound = max(bound, 1u);                                // keys of 0 take no part
+    cand[lane] = 0ull;
+    __syncwarp();
+    int n = 0;
+    const uint32_t before = (1u << lane) - 1u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const bool in = key[i] >= bound;
+        const uint32_t who = __ballot_sync(kAll, in);
+        const int at = n + __popc(who & before);
+        if (in && at < 32) cand[at] = (static_cast<unsigned long long>(key[i]) << 32) | static_cast<uint32_t>(~(V * lane + i));
+        n += __popc(who);
+    }
+    __syncwarp();
+    if (n <= 32) {
+        const unsigned long long mine = cand[lane];
+        int rank = 0;
+#pragma unroll
+        for (int c = 0; c < 32; c += 8) {
+            if (c >= n) break;
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const ulonglong2 other = *reinterpret_cast<const ulonglong2*>(cand + c + i);
+                rank += (other.x > mine ? 1 : 0) + (other.y > mine ? 1 : 0);
+            }
+        }
+        id = static_cast<int>(~static_cast<uint32_t>(mine));
+        place = lane < n && rank < k ? rank : kNone;
+        return;
+    }
+    id = 0;
+    place = lane < k ? lane : kNone;
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = key[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < V; ++i) {
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        }
+        const uint32_t top = __reduce_max_sync(kAll, best);
+        const int win = __ffs(static_cast<int>(__ballot_sync(kAll, best == top))) - 1;
+        const int pick = __shfl_sync(kAll, V * lane + at, win);
+        if (lane == j) id = pick;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (pick == V * lane + i) key[i] = 0u;
+        }
+    }
+}
+
+// One warp per token; lane holds experts V * lane + i, i < V, so lane order is id order.  kN: elements of a
+// load (rows aligned to them).
+//
+// Bound by instructions: beside the 1 KB that is read, a token of 256 experts in 8 groups takes a warp some hundreds of
+// them.  What took more: the two largest of a group by one lane per group, a second reduction and a search of
+// every lane's keys for each pick's id (1050 in all, 121 us for 65537 tokens), sorting each lane's keys (1065, 70 us).
+template <typename T, int V, int kN>
 __global__ void __launch_bounds__(32 * kWarps)
     route_topk_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, RouteParams p,
                       const float* __restrict__ bias, int32_t* __restrict__ ids, float* __restrict__ weights,
                       int* err) {
-    extern __shared__ float s_row[];                       // [kWarps][E]: group score inputs
+    extern __shared__ float s_row[];                       // [kWarps][E], only for groups that lanes share
+    __shared__ __align__(16) unsigned long long s_cand[kWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     if (t >= tokens) return;
     const T* row = logits + t * ld;
+    const int e0 = V * lane;
 
-    float l[V];
-    bool finite = true;
+    // the logits, -inf where there is no expert; a row of finite ones needs none of the checks for masks
+    float l[V], probe = 0.0f;
+    if (e0 + V <= E) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane + 32 * i;
-        const float v = e < E ? load_f32(row + e) : -INFINITY;
-        finite = finite && !(v != v || v == INFINITY);
-        l[i] = masked_nan(v);
+        for (int i = 0; i < V; i += kN) load_vec<T, kN>(row + e0 + i, *reinterpret_cast<float(*)[kN]>(l + i));
+#pragma unroll
+        for (int i = 0; i < V; ++i) probe = fmaf(l[i], 0.0f, probe);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            l[i] = e0 + i < E ? load_one(row + e0 + i) : -INFINITY;
+            probe = fmaf(e0 + i < E ? l[i] : 0.0f, 0.0f, probe);
+        }
     }
-    if (!finite) set_device_error(err, NVFP4_ERR_NONFINITE);
+    const bool clean = __all_sync(kAll, probe == 0.0f);
+    if (!clean) {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            bad = bad || !(l[i] < INFINITY);               // +inf and NaN
+            l[i] = masked_nan(l[i]);
+        }
+        if (bad) set_device_error(err, NVFP4_ERR_NONFINITE);
+    }
 
+    // order values: the logits, or the scores plus the bias; the scores are also what "top2" adds up
     const bool top2 = p.n_group > 1 && p.group_score == MOE_GROUP_TOP2;
-    const bool need_scores = bias != nullptr || top2;
-    float s[V];
-    if (need_scores) {
+    const bool scored = bias != nullptr || top2;
+    float o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = l[i];
+    if (scored) {
         if (p.score == MOE_SCORE_SOFTMAX) {
             float m = l[0];
 #pragma unroll
             for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
             m = warp_max(m);
+            if (!clean) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] = softmax_logit(o[i], m);
+                m = softmax_shift(m);
+            }
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                s[i] = softmax_term(l[i], m);
-                sum += s[i];
+                o[i] = fast_exp(o[i] - m);
+                sum += o[i];
             }
             sum = warp_sum(sum);
+            const float r = sum > 0.0f ? __frcp_rn(sum) : 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) s[i] = sum > 0.0f ? __fdiv_rn(s[i], sum) : 0.0f;
+            for (int i = 0; i < V; ++i) o[i] *= r;
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) s[i] = sigmoid(l[i]);
+            for (int i = 0; i < V; ++i) o[i] = order_sigmoid(o[i]);
         }
         if (bias != nullptr) {
+            if (e0 + V <= E) {
+                float b[V];
+                if (p.bias_wide) {
+#pragma unroll
+                    for (int i = 0; i < V; i += V < 4 ? V : 4)
+                        load_vec<float, V < 4 ? V : 4>(bias + e0 + i, *reinterpret_cast<float(*)[V < 4 ? V : 4]>(b + i));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) b[i] = __ldg(bias + e0 + i);
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] = fmaxf(o[i] + b[i], -INFINITY);   // a NaN bias: -inf
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (e0 + i < E) o[i] = fmaxf(o[i] + __ldg(bias + e0 + i), -INFINITY);
+                }
+            }
+        }
+        if (!clean) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int e = lane + 32 * i;
-                s[i] = e < E && l[i] > -INFINITY ? s[i] + __ldg(bias + e) : -INFINITY;
+                if (!(l[i] > -INFINITY)) o[i] = -INFINITY;
             }
         }
     }
     uint32_t key[V];
+    const bool by_logit = bias == nullptr;
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = lane + 32 * i < E ? order_key(bias != nullptr ? s[i] : l[i]) : 0u;
+    for (int i = 0; i < V; ++i) key[i] = ordered(by_logit ? l[i] : o[i]);
+    if (e0 + V > E) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = e0 + i < E ? key[i] : 0u;
+    }
 
     if (p.n_group > 1) {
-        float* sr = s_row + warp * E;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            if (e < E) sr[e] = top2 ? (l[i] > -INFINITY ? s[i] : -INFINITY) : __uint_as_float(key[i]);
-        }
-        __syncwarp();
         const int size = E / p.n_group;
-        uint32_t gk = 0u;                                   // lane g < n_group: key of group g
-        if (lane < p.n_group) {
-            const float* g = sr + lane * size;
+        if (p.group_lanes > 0) {
+            // a group is group_lanes whole lanes (a power of two of them)
+            uint32_t gk;
             if (top2) {
-                float a = -INFINITY, b = -INFINITY;         // the two largest, masked ones left out
-                for (int i = 0; i < size; ++i) {
-                    const float v = g[i];
-                    if (v > a) {
-                        b = a;
-                        a = v;
-                    } else if (v > b) {
-                        b = v;
-                    }
+                float a = -INFINITY, b = -INFINITY;         // the two largest; masked values stay out
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    b = fmaxf(b, fminf(a, o[i]));
+                    a = fmaxf(a, o[i]);
                 }
-                gk = order_key(b > -INFINITY ? a + b : a);
+                for (int x = 1; x < p.group_lanes; x <<= 1) {
+                    const float a2 = __shfl_xor_sync(kAll, a, x), b2 = __shfl_xor_sync(kAll, b, x);
+                    b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+                    a = fmaxf(a, a2);
+                }
+                gk = ordered(b > -INFINITY ? a + b : a);
             } else {
-                for (int i = 0; i < size; ++i) gk = max(gk, __float_as_uint(g[i]));
-            }
-        }
-        int ahead = 0;
-        for (int g = 0; g < p.n_group; ++g) {
-            const uint32_t o = __shfl_sync(kAll, gk, g);
-            ahead += (o > gk || (o == gk && g < lane)) ? 1 : 0;
-        }
-        const uint32_t kept = __ballot_sync(kAll, lane < p.n_group && ahead < p.topk_group);
+                gk = key[0];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            if (e < E && !((kept >> (e / size)) & 1u)) key[i] = 0u;
+                for (int i = 1; i < V; ++i) gk = max(gk, key[i]);
+                for (int x = 1; x < p.group_lanes; x <<= 1) gk = max(gk, __shfl_xor_sync(kAll, gk, x));
+            }
+            if (e0 >= E) gk = 0u;
+            const bool kept = keep_group(gk, lane / p.group_lanes, p.topk_group);
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] = kept ? key[i] : 0u;
+        } else {
+            // any group size: through shared memory, one lane per group
+            float* sr = s_row + warp * E;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (e0 + i < E) sr[e0 + i] = top2 ? o[i] : __uint_as_float(key[i]);
+            }
+            __syncwarp();
+            uint32_t gk = 0u;
+            if (lane < p.n_group) {
+                const float* g = sr + lane * size;
+                if (top2) {
+                    float a = -INFINITY, b = -INFINITY;
+                    for (int i = 0; i < size; ++i) {
+                        b = fmaxf(b, fminf(a, g[i]));
+                        a = fmaxf(a, g[i]);
+                    }
+                    gk = ordered(b > -INFINITY ? a + b : a);
+                } else {
+                    for (int i = 0; i < size; ++i) gk = max(gk, __float_as_uint(g[i]));
+                }
+            }
+            const uint32_t kept = __ballot_sync(kAll, keep_group(gk, lane, p.topk_group));
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (e0 + i < E && !((kept >> ((e0 + i) / size)) & 1u)) key[i] = 0u;
+            }
         }
     }
 
-    // k rounds: the largest key, then the lowest id that has it
-    int my_id = 0;
-    for (int j = 0; j < p.k; ++j) {
-        uint32_t best = key[0];
-        int at = lane;
-#pragma unroll
-        for (int i = 1; i < V; ++i) {
-            if (key[i] > best) {
-                best = key[i];
-                at = lane + 32 * i;
-            }
-        }
-        const uint32_t top = __reduce_max_sync(kAll, best);
-        const int id = static_cast<int>(__reduce_min_sync(kAll, best == top ? static_cast<uint32_t>(at) : kAll));
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (id == lane + 32 * i) key[i] = 0u;
-        }
-        if (lane == j) my_id = id;
-    }
+    int id, place;
+    select<V>(key, p.k, s_cand[warp], lane, id, place);
 
-    // the chosen experts' scores, lane j < k holding slot j
-    const bool slot = lane < p.k;
-    const float lj = slot ? masked_nan(load_f32(row + my_id)) : -INFINITY;
+    // the chosen experts' scores, each in the lane that has it
+    const bool chosen = place < kNone;
+    float lj = chosen ? masked_nan(load_one(row + id)) : -INFINITY;
     float w;
     if (p.score == MOE_SCORE_SIGMOID) {
         w = sigmoid(lj);
-    } else if (p.renormalize) {
-        w = softmax_term(lj, warp_max(lj));                 // the softmax over the chosen
     } else {
-        float m = l[0];
+        float m = lj;
+        if (!p.renormalize) {
 #pragma unroll
-        for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+            for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+        }
         m = warp_max(m);
-        float sum = 0.0f;
+        const float shift = softmax_shift(m);
+        w = expf(softmax_logit(lj, m) - shift);             // renormalised: the softmax over the chosen
+        if (!p.renormalize) {
+            float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum += softmax_term(l[i], m);
-        sum = warp_sum(sum);
-        w = sum > 0.0f ? __fdiv_rn(softmax_term(lj, m), sum) : 0.0f;
+            for (int i = 0; i < V; ++i) sum += expf(softmax_logit(l[i], m) - shift);
+            sum = warp_sum(sum);
+            w = sum > 0.0f ? __fdiv_rn(w, sum) : 0.0f;
+        }
     }
     if (p.renormalize) {
-        const float sum = warp_sum(w);
+        const float sum = warp_sum(chosen ? w : 0.0f);
         w = sum > 0.0f ? __fdiv_rn(w, sum) : 0.0f;
     }
-    if (slot) {
-        ids[t * p.k + lane] = my_id;
-        weights[t * p.k + lane] = w * p.scale;
+    if (chosen) {
+        ids[t * p.k + place] = id;
+        weights[t * p.k + place] = w * p.scale;
     }
 }
 
@@ -228,8 +412,12 @@ __global__ void __launch_bounds__(32 * kWarps)
 //   sigmoid, renormalised:  dl_c = q_c (1 - s_c) (g_c - sum_j g_j q_j),  q_c = s_c / sum_j s_j
 //   sigmoid:                dl_c = g_c s_c (1 - s_c)
 //   softmax:                dl_e = s_e ([e chosen] g_e - sum_j g_j s_j), every expert
-// One warp per token; lane holds experts lane + 32 i of the output row, and slot `lane`.
-template <typename T, int V>
+// One warp per token, lane j < k holding slot j.  Of the row, lane `lane` has the words of four experts at
+// 4 (lane + 32 i), i < kWords, whatever the alignment (kN elements to a load and store), so sums are taken in one
+// order.  The row is written with what an expert that was not chosen gets, then the chosen ones over it.
+//
+// Bound by memory: the row written (and, for the softmax over all experts, read).
+template <typename T, int kWords, int kN>
 __global__ void __launch_bounds__(32 * kWarps)
     route_topk_backward_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, RouteParams p,
                                const int32_t* __restrict__ ids, const float* __restrict__ dw, T* __restrict__ dl,
@@ -238,6 +426,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     if (t >= tokens) return;
     const T* row = logits + t * ld;
+    T* out = dl + t * ld_out;
     int id = -1;
     float g = 0.0f, lj = -INFINITY;
     if (lane < p.k) {
@@ -247,39 +436,80 @@ __global__ void __launch_bounds__(32 * kWarps)
             id = -1;
         } else {
             g = p.scale * __ldg(dw + t * p.k + lane);
-            lj = masked_nan(load_f32(row + id));
+            lj = masked_nan(load_one(row + id));
         }
     }
-    float v[V];
+    auto store4 = [&](int e, const float (&v)[4]) {
+        if (e + 4 <= E) {
+#pragma unroll
+            for (int i = 0; i < 4; i += kN) store_vec<T, kN>(out + e + i, *reinterpret_cast<const float(*)[kN]>(v + i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (e + i < E) out[e + i] = from_f32<T>(v[i]);
+            }
+        }
+    };
     float d;
     if (p.score == MOE_SCORE_SOFTMAX && !p.renormalize) {
-        float m = -INFINITY;
+        float v[kWords][4];
+        float m = -INFINITY, probe = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            v[i] = e < E ? masked_nan(load_f32(row + e)) : -INFINITY;
-            m = fmaxf(m, v[i]);
+        for (int j = 0; j < kWords; ++j) {
+            const int e = 4 * (lane + 32 * j);
+            if (e + 4 <= E) {
+#pragma unroll
+                for (int i = 0; i < 4; i += kN) load_vec<T, kN>(row + e + i, *reinterpret_cast<float(*)[kN]>(v[j] + i));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) probe = fmaf(v[j][i], 0.0f, probe);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[j][i] = e + i < E ? load_one(row + e + i) : -INFINITY;
+                    probe = fmaf(e + i < E ? v[j][i] : 0.0f, 0.0f, probe);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = fmaxf(m, v[j][i]);   // passes NaN over
         }
         m = warp_max(m);
+        const float shift = softmax_shift(m);
+        if (!__all_sync(kAll, probe == 0.0f)) {             // masks, infinities or NaN
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[j][i] = softmax_logit(masked_nan(v[j][i]), m);
+            }
+        }
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            v[i] = softmax_term(v[i], m);
-            sum += v[i];
+        for (int j = 0; j < kWords; ++j) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[j][i] = expf(v[j][i] - shift);
+                sum += v[j][i];
+            }
         }
         sum = warp_sum(sum);
         const float r = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-        d = g * (softmax_term(lj, m) * r);
-        const float c = -warp_sum(d) * r;
+        const float s = expf(softmax_logit(lj, m) - shift);
+        const float own = g * (s * r);
+        const float c = -warp_sum(own) * r;
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= c;
+        for (int j = 0; j < kWords; ++j) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[j][i] *= c;
+            store4(4 * (lane + 32 * j), v[j]);
+        }
+        d = s * c + own;
     } else {
         float s, rest = 1.0f;                               // rest = 1 - s
         if (p.score == MOE_SCORE_SOFTMAX) {
-            s = softmax_term(lj, warp_max(lj));
+            const float m = warp_max(lj);
+            s = expf(softmax_logit(lj, m) - softmax_shift(m));
         } else {
             s = sigmoid(lj);
-            rest = lj == -INFINITY ? 1.0f : __fdiv_rn(1.0f, 1.0f + expf(lj));
+            rest = __frcp_rn(1.0f + expf(lj));
         }
         float dot = 0.0f;
         if (p.renormalize) {
@@ -288,66 +518,90 @@ __global__ void __launch_bounds__(32 * kWarps)
             dot = warp_sum(g * s);
         }
         d = s * rest * (g - dot);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 0.0f;
+        const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int e = 4 * lane; e < E; e += 128) store4(e, zero);
     }
-    for (int j = 0; j < p.k; ++j) {
-        const int e = __shfl_sync(kAll, id, j);
-        const float dj = __shfl_sync(kAll, d, j);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (e == lane + 32 * i) v[i] += dj;
-        }
-    }
-    T* out = dl + t * ld_out;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane + 32 * i;
-        if (e < E) store_f32(out + e, v[i]);
-    }
+    __syncwarp();                                           // orders the warp's writes
+    if (id >= 0) out[id] = from_f32<T>(d);
 }
 
-// f(type tag, lane width) for the logits' type and the experts per lane.
-template <typename T, typename F>
-cudaError_t by_width(int E, F f) {
-    if (E <= 32) return f(T{}, std::integral_constant<int, 1>{});
-    if (E <= 64) return f(T{}, std::integral_constant<int, 2>{});
-    if (E <= 128) return f(T{}, std::integral_constant<int, 4>{});
-    if (E <= 256) return f(T{}, std::integral_constant<int, 8>{});
-    if (E <= 512) return f(T{}, std::integral_constant<int, 16>{});
-    return f(T{}, std::integral_constant<int, 32>{});
+template <typename T, int V, int kN>
+cudaError_t launch_route(const void* logits, int64_t tokens, int E, int64_t ld, RouteParams p, const float* bias,
+                         int32_t* ids, float* weights, int* err, cudaStream_t st) {
+    // a group of whole lanes, a power of two of them
+    const int size = E / p.n_group, lanes = size / V;
+    p.group_lanes = size % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    p.bias_wide = (reinterpret_cast<uintptr_t>(bias) & 15) == 0;
+    const unsigned grid = static_cast<unsigned>((tokens + kWarps - 1) / kWarps);
+    const size_t smem = p.n_group > 1 && p.group_lanes == 0 ? static_cast<size_t>(kWarps) * E * 4 : 0;
+    return launch_pdl(false, route_topk_kernel<T, V, kN>, grid, 32 * kWarps, smem, st, static_cast<const T*>(logits),
+                      tokens, E, ld, p, bias, ids, weights, err);
 }
-template <typename F>
-cudaError_t by_type(int type, int E, F f) {
-    switch (type) {
-        case NVFP4_TYPE_F32: return by_width<float>(E, f);
-        case NVFP4_TYPE_BF16: return by_width<__nv_bfloat16>(E, f);
-        default: return by_width<__half>(E, f);
-    }
+template <typename T, int V>
+cudaError_t route_by_word(const void* logits, int64_t tokens, int E, int64_t ld, const RouteParams& p, const float* bias,
+                          int32_t* ids, float* weights, int* err, cudaStream_t st) {
+    constexpr int kWide = V * sizeof(T) < 16 ? V : 16 / static_cast<int>(sizeof(T));
+    const int64_t bits = static_cast<int64_t>(reinterpret_cast<uintptr_t>(logits)) | (ld * static_cast<int64_t>(sizeof(T)));
+    if (bits % (kWide * static_cast<int64_t>(sizeof(T))) == 0)
+        return launch_route<T, V, kWide>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+    return launch_route<T, V, 1>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+}
+template <typename T>
+cudaError_t route_by_width(const void* logits, int64_t tokens, int E, int64_t ld, const RouteParams& p, const float* bias,
+                           int32_t* ids, float* weights, int* err, cudaStream_t st) {
+    if (E <= 32) return route_by_word<T, 1>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+    if (E <= 64) return route_by_word<T, 2>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+    if (E <= 128) return route_by_word<T, 4>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+    if (E <= 256) return route_by_word<T, 8>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+    if (E <= 512) return route_by_word<T, 16>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+    return route_by_word<T, 32>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+}
+
+template <typename T, int kWords, int kN>
+cudaError_t launch_backward(const void* logits, int64_t tokens, int E, int64_t ld, const RouteParams& p, const int32_t* ids,
+                            const float* dw, void* dl, int64_t ld_out, int* err, cudaStream_t st) {
+    const unsigned grid = static_cast<unsigned>((tokens + kWarps - 1) / kWarps);
+    return launch_pdl(false, route_topk_backward_kernel<T, kWords, kN>, grid, 32 * kWarps, 0, st,
+                      static_cast<const T*>(logits), tokens, E, ld, p, ids, dw, static_cast<T*>(dl), ld_out, err);
+}
+template <typename T, int kWords>
+cudaError_t backward_by_word(const void* logits, int64_t tokens, int E, int64_t ld, const RouteParams& p, const int32_t* ids,
+                             const float* dw, void* dl, int64_t ld_out, int* err, cudaStream_t st) {
+    constexpr int64_t kSize = sizeof(T);
+    const int64_t bits = static_cast<int64_t>(reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dl)) |
+                         (ld * kSize) | (ld_out * kSize);
+    if (bits % (4 * kSize) == 0) return launch_backward<T, kWords, 4>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
+    if (bits % (2 * kSize) == 0) return launch_backward<T, kWords, 2>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
+    return launch_backward<T, kWords, 1>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
+}
+template <typename T>
+cudaError_t backward_by_width(const void* logits, int64_t tokens, int E, int64_t ld, const RouteParams& p, const int32_t* ids,
+                              const float* dw, void* dl, int64_t ld_out, int* err, cudaStream_t st) {
+    if (E <= 128) return backward_by_word<T, 1>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
+    if (E <= 256) return backward_by_word<T, 2>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
+    if (E <= 512) return backward_by_word<T, 4>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
+    return backward_by_word<T, 8>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
 }
 
 }  // namespace
 
 cudaError_t launch_route_topk(const void* logits, int type, int64_t T, int E, int64_t ld, const RouteParams& p,
                               const float* bias, int32_t* ids, float* weights, int* err, cudaStream_t st) {
-    const unsigned grid = static_cast<unsigned>((T + kWarps - 1) / kWarps);
-    const size_t smem = p.n_group > 1 ? static_cast<size_t>(kWarps) * E * 4 : 0;
-    return by_type(type, E, [&](auto tag, auto v) {
-        using L = decltype(tag);
-        return launch_pdl(false, route_topk_kernel<L, decltype(v)::value>, grid, 32 * kWarps, smem, st,
-                          static_cast<const L*>(logits), T, E, ld, p, bias, ids, weights, err);
-    });
+    switch (type) {
+        case NVFP4_TYPE_F32: return route_by_width<float>(logits, T, E, ld, p, bias, ids, weights, err, st);
+        case NVFP4_TYPE_BF16: return route_by_width<__nv_bfloat16>(logits, T, E, ld, p, bias, ids, weights, err, st);
+        default: return route_by_width<__half>(logits, T, E, ld, p, bias, ids, weights, err, st);
+    }
 }
 
 cudaError_t launch_route_topk_backward(const void* logits, int type, int64_t T, int E, int64_t ld,
                                        const RouteParams& p, const int32_t* ids, const float* dw, void* dl,
                                        int64_t ld_out, int* err, cudaStream_t st) {
-    const unsigned grid = static_cast<unsigned>((T + kWarps - 1) / kWarps);
-    return by_type(type, E, [&](auto tag, auto v) {
-        using L = decltype(tag);
-        return launch_pdl(false, route_topk_backward_kernel<L, decltype(v)::value>, grid, 32 * kWarps, 0, st,
-                          static_cast<const L*>(logits), T, E, ld, p, ids, dw, static_cast<L*>(dl), ld_out, err);
-    });
+    switch (type) {
+        case NVFP4_TYPE_F32: return backward_by_width<float>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
+        case NVFP4_TYPE_BF16: return backward_by_width<__nv_bfloat16>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
+        default: return backward_by_width<__half>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
+    }
 }
 
 }  // namespace nvfp4
