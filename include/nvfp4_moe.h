@@ -546,7 +546,8 @@ typedef struct {
  *  0 <= T < 2^31 - 256; 1 <= N < 2^31 - 256
  *  bias_dev   float [N] or NULL
  *  out_dev    [T][ldo] of out_type, element aligned, ldo >= N
- *  ws_dev     *_linear_workspace_bytes(T, K) bytes, 256-byte aligned
+ *  ws_dev     *_linear_workspace_bytes(T, K) bytes, 256-byte aligned; NULL where that is 0 (few
+ *             tokens, whose rows are quantised in shared memory; also 0 for a T or K that is refused)
  * Device errors: NVFP4_ERR_NONFINITE (a row of x with Inf or NaN), NVFP4_ERR_DEVICE_TIMEOUT. */
 size_t nvfp4_linear_workspace_bytes(int64_t T, int64_t K);
 size_t mxfp4_linear_workspace_bytes(int64_t T, int64_t K);

@@ -512,16 +512,23 @@ def mxfp4_sf_bytes(rows, cols):
     return lib().mxfp4_sf_bytes(rows, cols)
 
 
+def _codes_shape(rows, cols):
+    return (rows + 127) // 128 * 128, cols // 2
+
+
+def _mx_sf_shape(rows, cols):
+    return ((rows + 127) // 128 * ((cols + 127) // 128) * 512,)
+
+
 def mxfp4_quantize_rows(x, stream=None):
     """MXFP4-quantise each row of a float32, bfloat16 or float16 CUDA matrix [rows, cols]
     (cols % 32 == 0): (codes uint8 [rows rounded up to 128, cols / 2], sf uint8)."""
     code, rows, cols, ld = _rows("x", x, _TYPES)
     device = x.device
-    L = lib()
-    codes = _empty((L.nvfp4_rows_padded(rows), cols // 2), torch.uint8, device, stream)
-    sf = _empty((L.mxfp4_sf_bytes(rows, cols),), torch.uint8, device, stream)
-    status = L.mxfp4_quantize_rows(x.data_ptr(), code, rows, cols, ld, codes.data_ptr(), sf.data_ptr(),
-                                   _raw_stream(stream, x))
+    codes = _empty(_codes_shape(rows, cols), torch.uint8, device, stream)
+    sf = _empty(_mx_sf_shape(rows, cols), torch.uint8, device, stream)
+    status = lib().mxfp4_quantize_rows(x.data_ptr(), code, rows, cols, ld, codes.data_ptr(), sf.data_ptr(),
+                                       _raw_stream(stream, x))
     if status:
         _check("mxfp4_quantize_rows", status)
     return codes, sf
@@ -531,15 +538,14 @@ def mxfp4_dequantize_rows(codes, sf, rows, cols, dtype=torch.bfloat16, stream=No
     """The values of MXFP4 rows, [rows, cols] bfloat16 or float32 (both exact)."""
     if dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("dtype must be torch.bfloat16 or torch.float32")
-    L = lib()
     device = codes.device
-    _need("codes", codes, torch.uint8, (L.nvfp4_rows_padded(rows), cols // 2), device)
-    _need("sf", sf, torch.uint8, (L.mxfp4_sf_bytes(rows, cols),), device)
+    _need("codes", codes, torch.uint8, _codes_shape(rows, cols), device)
+    _need("sf", sf, torch.uint8, _mx_sf_shape(rows, cols), device)
     if not codes.is_cuda:
         raise ValueError("codes must be a CUDA tensor")
     out = _empty((rows, cols), dtype, device, stream)
-    status = L.mxfp4_dequantize_rows(codes.data_ptr(), sf.data_ptr(), rows, cols, out.data_ptr(), _TYPES[dtype], cols,
-                                     _raw_stream(stream, codes))
+    status = lib().mxfp4_dequantize_rows(codes.data_ptr(), sf.data_ptr(), rows, cols, out.data_ptr(), _TYPES[dtype],
+                                         cols, _raw_stream(stream, codes))
     if status:
         _check("mxfp4_dequantize_rows", status)
     return out
@@ -609,14 +615,15 @@ def _linear(name, mx, x, weight, bias, out, out_dtype, stream):
             raise ValueError(f"out must be [{T}, {N}] on {device}")
     L = lib()
     need = L.mxfp4_linear_workspace_bytes(T, K) if mx else L.nvfp4_linear_workspace_bytes(T, K)
-    ws = _empty((need,), torch.uint8, device, stream)
+    ws = _empty((need,), torch.uint8, device, stream) if need else None
+    ws_ptr = ws.data_ptr() if need else None
     b = None if bias is None else bias.data_ptr()
     if mx:
         status = L.mxfp4_linear(weight.struct, x.data_ptr(), code, T, ldx, b, out.data_ptr(), out_code, ldo,
-                                ws.data_ptr(), need, _raw_stream(stream, x))
+                                ws_ptr, need, _raw_stream(stream, x))
     else:
-        status = L.nvfp4_linear(weight.struct, x.data_ptr(), T, ldx, b, out.data_ptr(), out_code, ldo, ws.data_ptr(),
-                                need, _raw_stream(stream, x))
+        status = L.nvfp4_linear(weight.struct, x.data_ptr(), T, ldx, b, out.data_ptr(), out_code, ldo, ws_ptr, need,
+                                _raw_stream(stream, x))
     if status:
         _check(name, status)
     return out

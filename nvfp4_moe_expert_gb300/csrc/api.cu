@@ -688,7 +688,8 @@ struct LinearLayout {
 };
 LinearLayout linear_layout(bool mx, int64_t T, int64_t K) {
     const size_t rows = static_cast<size_t>(nvfp4_rows_padded(T));
-    LinearLayout L;
+    LinearLayout L = {};
+    if (linear_quantises_x(mx, T, K)) return L;   // x is quantised in shared memory
     L.codes = 0;
     L.sf = align_up(rows * (K / 2), 256);
     L.g = align_up(L.sf + (mx ? mxfp4_sf_bytes(T, K) : nvfp4_sf_bytes(T, K)), 256);
@@ -706,10 +707,10 @@ nvfp4_status linear_impl(bool mx, const fp4_linear_weights* w, const void* x, in
     if (!w->codes || !w->sf || (!mx && !w->g) || !aligned(w->codes, 16) || !aligned(w->sf, 16) || !aligned(w->g, 4))
         return NVFP4_ERR_INVALID_ARG;
     if (T == 0) return NVFP4_OK;
-    if (!x || !out || !ws || !aligned(x, mx ? type_size(x_type) : 16) || !aligned(out, type_size(out_type)) ||
+    const LinearLayout L = linear_layout(mx, T, w->K);
+    if (!x || !out || (!ws && L.total) || !aligned(x, mx ? type_size(x_type) : 16) || !aligned(out, type_size(out_type)) ||
         !aligned(bias, 4) || !aligned(ws, 256))
         return NVFP4_ERR_INVALID_ARG;
-    const LinearLayout L = linear_layout(mx, T, w->K);
     if (ws_bytes < L.total) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
     int* err = device_error_ptr();
     if (!err) return NVFP4_ERR_CUDA;
@@ -729,11 +730,11 @@ nvfp4_status linear_impl(bool mx, const fp4_linear_weights* w, const void* x, in
     a.out_type = out_type;
     a.ldo = ldo;
     a.err = err;
-    if (linear_quantises_x(a)) return from_cuda(launch_linear_x({x, x_type, ldx}, a, st));
+    if (L.total == 0) return from_cuda(launch_linear_x({x, x_type, ldx}, a, st));
     const cudaError_t e =
         mx ? launch_mxfp4_quantize_rows(x, x_type, T, w->K, ldx, at<uint8_t>(ws, L.codes), at<uint8_t>(ws, L.sf), err, st)
-           : launch_quantize_rows(static_cast<const uint16_t*>(x), T, w->K, ldx, at<uint8_t>(ws, L.codes),
-                                  at<uint8_t>(ws, L.sf), at<float>(ws, L.g), err, st);
+           : launch_nvfp4_quantize_x(static_cast<const uint16_t*>(x), T, a.K, ldx, at<uint8_t>(ws, L.codes),
+                                     at<uint8_t>(ws, L.sf), at<float>(ws, L.g), err, st);
     if (e != cudaSuccess) return from_cuda(e);
     return from_cuda(launch_linear(a, st, true));
 }

@@ -3,13 +3,16 @@
 //   NVFP4: acc = sum_k (qa*sa)[t,k] (qb*sb)[n,k] (E4M3 scales per 16), out = (acc*ga[t])*gb[n] + bias
 //   MXFP4: acc = the same with E8M0 scales per 32 and no outer scales
 //
-// Kernel (sm_103a): one CTA per SM walks the (128 tokens x BN outputs) tiles.  Warp 0 loads a
-// stage of 256 K-elements through TMA (128B swizzle) with its 512-byte scale tiles; warp 1 copies
-// the scales to TMEM and issues the K=64 MMAs (M=128, N=BN) into an FP32 TMEM accumulator; warps
-// 2-5 apply the outer scales and the bias and write their rows.  All waits are bounded
-// (NVFP4_ERR_DEVICE_TIMEOUT, then a clean exit).
+// Three kernels, by the number of tokens and the tiles they make (launch_linear): for few tokens one that
+// quantises x itself, below; for many a pair of CTAs per tile (linear_pair.cu); between them the general one here.
 //
-// K is walked 0..K-1 in 64-wide steps into one accumulator whatever the tile, so a token's output
+// General kernel (sm_103a): one CTA per SM walks the (128 tokens x BN outputs) tiles.  Warps 0 and 6 load the
+// stages' 512 K-elements of A and B through TMA (128B swizzle) with their 512-byte scale tiles; warp 1 copies the scales to
+// TMEM and issues the K=64 MMAs (M=128, N=BN) into one of two FP32 TMEM accumulators; warps 2-5 apply
+// the outer scales and the bias and write their rows.  All waits are bounded (NVFP4_ERR_DEVICE_TIMEOUT, then a
+// clean exit).
+//
+// K is walked 0..K-1 in 64-wide steps into one accumulator whatever the kernel and the tile, so a token's output
 // does not depend on how many tokens there are.
 #include "linear.cuh"
 #include "mxfp4_quant.cuh"
@@ -18,9 +21,11 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 8;
+constexpr int kPer = 2;                              // chunks of 256 K-elements per stage
 constexpr int kEpiWarps = 4;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kWarpB = 2 + kEpiWarps;                // the producer of B
+constexpr int kThreads = 32 * (kWarpB + 1);
 
 struct Params {
     int64_t T;
@@ -34,7 +39,7 @@ struct Params {
     int out_type;
     int64_t ldo;
     int align;            // of out's rows: out_align()
-    int a_rows;           // rows of A loaded per tile (a multiple of 8, at most 128)
+    int a_rows;           // rows of A loaded per tile (a multiple of 16, at most 128)
     int stages, stage_bytes;
     int n_tiles;
     int64_t tiles;
@@ -66,10 +71,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     linear_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const Params p) {
     using F = Format<kMx>;
-    constexpr int kSfbSets = BN > 128 ? 2 : 1;                     // 128-row sets of B scale tiles
-    constexpr int kSfSet = F::tiles * kSfAtomBytes;
-    constexpr uint32_t kSfCols = 4 * F::tiles * (1 + kSfbSets);    // TMEM columns of a stage's scales
-    constexpr int kAcc = BN <= 128 ? 2 : 1;                        // accumulators
+    constexpr int kSfBytes = F::tiles * kSfAtomBytes;              // scale tiles of a chunk
+    constexpr uint32_t kSfCols = 8 * F::tiles;                     // TMEM columns of a chunk's scales
     constexpr int kN = mma_n(BN);
     constexpr int kBBytes = kN * kRowBytes;
     extern __shared__ uint8_t smem_raw[];
@@ -80,26 +83,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) float s_col[kEpiWarps][2][32];
     volatile int* abort_flag = &abort_word;
     const int warp = warp_index(), lane = threadIdx.x & 31;
+    // a stage: A's chunks, B's chunks, then their scale tiles
     const int a_bytes = p.a_rows * kRowBytes;
+    const int b_off = kPer * a_bytes, sfa_off = b_off + kPer * kBBytes, sfb_off = sfa_off + kPer * kSfBytes;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+    if (warp == 0) {
+        if (lane < kMaxStages) {
+            mbar_init(&full[lane], 2);                             // both producers
+            mbar_init(&empty[lane], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&tmem_full[i], 1);
-            mbar_init(&tmem_empty[i], 32 * kEpiWarps);
+        if (lane < 2) {
+            mbar_init(&tmem_full[lane], 1);
+            mbar_init(&tmem_empty[lane], 32 * kEpiWarps);
         }
-        mbar_init(&drain, 1);
-        abort_word = 0;
+        if (lane == 0) {
+            mbar_init(&drain, 1);
+            abort_word = 0;
+            prefetch_tensormap(&tmA);
+            prefetch_tensormap(&tmB);
+        }
         fence_barrier_init();
-    }
-    if (warp == 0 && lane == 0) {
-        prefetch_tensormap(&tmA);
-        prefetch_tensormap(&tmB);
-    }
-    if (warp == 1) {
+    } else if (warp == 1) {
         tmem_alloc(&tmem_slot, kTmemCols);
         tmem_relinquish();
     }
@@ -107,56 +111,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(tmem_slot);
-    const int num_ks = (p.K + kStageK - 1) / kStageK;
+    const int num_ks = (p.K + kStageK - 1) / kStageK, num_st = (num_ks + kPer - 1) / kPer;
     const int sf_tiles = (p.K + F::tile_k - 1) / F::tile_k;        // scale tiles of a 128-row set, all of K
     bool failed = false;
 
-    if (warp == 0) {
-        const uint64_t pol_a = policy_evict_last(), pol_b = policy_evict_normal();
+    if (warp == 0 || warp == kWarpB) {
+        const bool is_a = warp == 0;
+        const uint64_t pol = is_a ? policy_evict_last() : policy_evict_normal();
+        const CUtensorMap* map = is_a ? &tmA : &tmB;
+        const uint8_t* sf = is_a ? p.a_sf : p.b_sf;
+        const int box = is_a ? a_bytes : BN * kRowBytes, pitch = is_a ? a_bytes : kBBytes;
+        const int off = is_a ? 0 : b_off, sf_at = is_a ? sfa_off : sfb_off;
         int stage = 0;
         uint32_t phase = 0, issued = 0, issued_parity = 0;
-        auto load_b = [&](int n0, int ks) {
-            uint8_t* b = smem + stage * p.stage_bytes + a_bytes;
-            const uint32_t sf_bytes = static_cast<uint32_t>(min(F::tiles, sf_tiles - F::tiles * ks)) * kSfAtomBytes;
-            // the second set of a BN = 256 tile is past the end of B when N has none
-            const int sets = kSfbSets == 2 && n0 + 128 < p.N ? 2 : 1;
-            mbar_arrive_expect_tx_elect(&full[stage], a_bytes + BN * kRowBytes + (1 + sets) * sf_bytes);
-            tma_load_2d_elect(b + (n0 & (kN - BN)) * kRowBytes, &tmB, &full[stage], ks * kRowBytes, n0, pol_b);
-            for (int i = 0; i < sets; ++i)
-                bulk_load_elect(b + kBBytes + (1 + i) * kSfSet,
-                                p.b_sf + (static_cast<int64_t>(n0 / 128 + i) * sf_tiles + F::tiles * ks) * kSfAtomBytes,
-                                sf_bytes, &full[stage], pol_b);
-            issued |= 1u << stage;
-            issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-        };
-        auto load_a = [&](int64_t mt, int ks) {
-            uint8_t* a = smem + stage * p.stage_bytes;
-            const uint32_t sf_bytes = static_cast<uint32_t>(min(F::tiles, sf_tiles - F::tiles * ks)) * kSfAtomBytes;
-            tma_load_2d_elect(a, &tmA, &full[stage], ks * kRowBytes, static_cast<int>(mt * kBM), pol_a);
-            bulk_load_elect(a + a_bytes + kBBytes, p.a_sf + (mt * sf_tiles + F::tiles * ks) * kSfAtomBytes, sf_bytes,
-                            &full[stage], pol_a);
-        };
-        // the weights are the call's input: their first stages load while x is still being quantised
-        const int early = min(p.stages, num_ks);
-        for (int ks = 0; ks < early; ++ks) {
-            load_b(static_cast<int>(blockIdx.x % p.n_tiles) * BN, ks);
-            ++stage;
-        }
-        stage = 0;
-        pdl_wait();
+        if (is_a) pdl_wait();                         // A is what the kernel before writes; B is the call's input
         for (int64_t t = blockIdx.x; t < p.tiles && !failed; t += gridDim.x) {
-            const int64_t mt = t / p.n_tiles;
-            const int n0 = static_cast<int>(t % p.n_tiles) * BN;
-            for (int ks = 0; ks < num_ks; ++ks) {
-                if (t != blockIdx.x || ks >= early) {
-                    const bool ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, kWaitBudgetCycles);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        failed = true;
-                        break;
-                    }
-                    load_b(n0, ks);
+            const int nt = static_cast<int>(t % p.n_tiles);
+            const int row = is_a ? static_cast<int>(t / p.n_tiles * kBM) : nt * BN;
+            const uint8_t* tile_sf = sf + static_cast<int64_t>(row / 128) * sf_tiles * kSfAtomBytes;
+            const int skip = is_a ? 0 : (row & (kN - BN)) * kRowBytes;
+            for (int st = 0; st < num_st; ++st) {
+                const bool ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, kWaitBudgetCycles);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    failed = true;
+                    break;
                 }
-                load_a(mt, ks);
+                uint8_t* base = smem + stage * p.stage_bytes;
+                const int chunks = min(kPer, num_ks - kPer * st);
+                const uint32_t sf_bytes =
+                    static_cast<uint32_t>(min(kPer * F::tiles, sf_tiles - kPer * F::tiles * st)) * kSfAtomBytes;
+                load_operand_elect(&full[stage], chunks * box + sf_bytes, base + off + skip, map, kPer * st * kRowBytes, row,
+                                   base + sf_at, tile_sf + kPer * F::tiles * st * kSfAtomBytes, sf_bytes, pol);
+                if (chunks == 2)
+                    tma_load_2d_elect(base + off + skip + pitch, map, &full[stage], (kPer * st + 1) * kRowBytes, row, pol);
+                issued |= 1u << stage;
+                issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
                 if (++stage == p.stages) {
                     stage = 0;
                     phase ^= 1u;
@@ -166,13 +155,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (failed) {
             if (lane == 0) set_device_error(p.err, NVFP4_ERR_DEVICE_TIMEOUT);
             *abort_flag = 1;
+            // let the copies in flight land before the CTA's shared memory goes away (a stage that the other
+            // producer never filled runs out its bounded wait)
             for (int s = 0; s < p.stages; ++s) {
                 if (issued & (1u << s)) mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, nullptr, kWaitBudgetCycles);
             }
         }
     } else if (warp == 1) {
         const uint32_t idesc = idesc_fp4(kMx, kBM, kN);
-        const uint32_t sf0 = tmem + kAcc * kN;
+        const uint32_t sf0 = tmem + 2 * kN, base = smem_u32(smem);
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool issued_any = false;
@@ -186,20 +177,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-            for (int ks = 0; ks < num_ks; ++ks) {
+            for (int st = 0; st < num_st; ++st) {
                 const bool okf = mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitBudgetCycles);
                 if (!__all_sync(0xFFFFFFFFu, okf)) {
                     failed = true;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t st = smem_u32(smem + stage * p.stage_bytes);
-                const uint32_t sf = st + a_bytes + kBBytes;
-                const int nk = min(kStageK / 64, (p.K - kStageK * ks + 63) / 64);
-                issue_stage<kMx, kSfbSets, 1>(tmem + acc * kN, sdesc_k_swizzled<kRowBytes>(st),
-                                           sdesc_k_swizzled<kRowBytes>(st + a_bytes), idesc, sdesc_sf(sf),
-                                           sdesc_sf(sf + kSfSet), sdesc_sf(sf + kSfbSets * kSfSet), sf0 + stage * kSfCols,
-                                           sfb_col, nk, ks != 0);
+                const uint32_t at = base + stage * p.stage_bytes;
+                const int chunks = min(kPer, num_ks - kPer * st);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    if (i >= chunks) break;
+                    const int ks = kPer * st + i;
+                    issue_stage<kMx, 1, 1>(tmem + acc * kN, sdesc_k_swizzled<kRowBytes>(at + i * a_bytes),
+                                           sdesc_k_swizzled<kRowBytes>(at + b_off + i * kBBytes), idesc,
+                                           sdesc_sf(at + sfa_off + i * kSfBytes), sdesc_sf(at + sfb_off + i * kSfBytes), 0,
+                                           sf0 + (kPer * stage + i) * kSfCols, sfb_col,
+                                           min(kStageK / 64, (p.K - kStageK * ks + 63) / 64), ks != 0);
+                }
                 issued_any = true;
                 tc_commit_elect(&empty[stage]);
                 if (++stage == p.stages) {
@@ -209,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (failed) break;
             tc_commit_elect(&tmem_full[acc]);
-            if (++acc == kAcc) {
+            if (++acc == 2) {
                 acc = 0;
                 acc_phase ^= 1u;
             }
@@ -243,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             epilogue_row<kMx, BN>(taddr, live, r, n0, ga, p, s_col[warp - 2][0], s_col[warp - 2][1]);
             tc_fence_before();
             mbar_arrive(&tmem_empty[acc]);
-            if (++acc == kAcc) {
+            if (++acc == 2) {
                 acc = 0;
                 acc_phase ^= 1u;
             }
@@ -258,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// ---------------------------------------------------------------- at most 16 tokens: one kernel
+// ---------------------------------------------------------------- few tokens: one kernel
 // The work is the weights' bytes, so a kernel of its own for quantising x would cost more than it
 // does: every CTA quantises the few rows of x itself into shared memory, in the layout a TMA load of
 // quantised rows would give (bit-equal to the row quantisers), while its weights stream in, and
@@ -274,19 +270,16 @@ constexpr int kThreadsD = 32 * (2 + kQuantWarps);
 constexpr int kEpiWarp = 4;
 constexpr int kMaxK = 8192;
 constexpr int kChunkBytes = kMaxT * kRowBytes;       // one 256-element chunk of the 16 rows
-constexpr int kPer = 4;                              // chunks of the weights per stage: 1024 K-elements
+constexpr int kPerD = 4;                              // chunks of the weights per stage: 1024 K-elements
 // A quantiser warp takes pieces of one row: 1024 columns (MXFP4, one block of 32 to a lane) or 512 (NVFP4,
-// one of 16), several loaded before the first is used.  The pieces are ordered by columns, then rows, and a
-// batch (all warps' pieces of one turn) becomes ready as a whole.
+// one of 16), all of them loaded before the first is used: 32768 elements of x at most (few_tokens).
 template <bool kMx>
 __host__ __device__ constexpr int piece_cols() { return kMx ? 1024 : 512; }
 template <bool kMx>
-__host__ __device__ constexpr int pieces_held() { return kMx ? 1 : 4; }
+__host__ __device__ constexpr int pieces_held() { return kMx ? 2 : 4; }
 template <bool kMx>
-__host__ __device__ constexpr int batch_size() { return pieces_held<kMx>() * kQuantWarps; }
-constexpr int kMaxBatches = 8;                       // 16 rows of 8192
-static_assert(kMaxT * (kMaxK / piece_cols<true>()) <= kMaxBatches * batch_size<true>(), "batches");
-static_assert(kMaxT * (kMaxK / piece_cols<false>()) <= kMaxBatches * batch_size<false>(), "batches");
+__host__ __device__ constexpr int max_pieces() { return pieces_held<kMx>() * kQuantWarps; }
+
 constexpr int kMaxStagesD = 8;
 
 struct DecodeParams {
@@ -295,7 +288,7 @@ struct DecodeParams {
     int64_t ldx;
     int x_align;          // of x's rows: mx_align()
     int T, N, K;
-    uint32_t t_magic;     // ceil(2^16 / T): q / T = q * t_magic >> 16 for q < 4096
+    uint32_t t_magic;     // ceil(2^16 / T): q / T = q * t_magic >> 16 for q < 4096 (at most 64 pieces)
     const uint8_t* b_sf;
     const float* b_g;
     const float* bias;
@@ -306,8 +299,6 @@ struct DecodeParams {
     int stages, n_tiles;
     int* err;
 };
-static_assert(kMaxT * (kMaxK / piece_cols<false>()) + batch_size<false>() <= 4096, "t_magic's range (a turn may pass the last piece)");
-
 // Piece q: its row and its place among the row's pieces.
 __device__ __forceinline__ void piece(const DecodeParams& p, int q, int& r, int& i) {
     i = static_cast<int>(static_cast<uint32_t>(q) * p.t_magic >> 16);
@@ -329,32 +320,31 @@ __device__ __forceinline__ void quantise_mx(const DecodeParams& p, int warp, int
     const X* x = static_cast<const X*>(p.x);
     const int pieces = p.T * ((p.K + kCols - 1) / kCols);
     const int sf_cols = (p.K + kMxTileCols - 1) / kMxTileCols * kMxTileCols;   // the blocks past K get zero scales
-    MxBlock<X, kAlign> held, next;
-    auto load = [&](MxBlock<X, kAlign>& h, int q) {
+    MxBlock<X, kAlign> held[pieces_held<true>()];
+#pragma unroll
+    for (int i = 0; i < pieces_held<true>(); ++i) {
+        const int q = i * kQuantWarps + warp;
         int r, at;
         piece(p, q, r, at);
         const int c = at * kCols + kMxBlock * lane;
-        h.load(x + r * p.ldx + c, q < pieces && c < p.K);
-    };
-    load(held, warp);
-    start_wait();                                     // the first loads are on their way before the CTA is set up
-    for (int first = 0, batch = 0; first < pieces; first += kQuantWarps, ++batch) {
-        const int q = first + warp;
-        load(next, q + kQuantWarps);
-        if (q < pieces) {
-            int r, at;
-            piece(p, q, r, at);
-            const int c = at * kCols + kMxBlock * lane;
-            uint4 word;
-            uint32_t scale;
-            held.quantise(word, scale, p.err);
-            if (c < p.K) *reinterpret_cast<uint4*>(codes + c / kStageK * kChunkBytes + swizzled(r, 4 * (lane & 7))) = word;
-            if (c < sf_cols) sf[c / kMxTileCols * kSfAtomBytes + r * 16 + (lane & 3)] = static_cast<uint8_t>(scale);
-        }
-        fence_proxy_async_shared();
-        mbar_arrive(&a_full[batch]);
-        held = next;
+        held[i].load(x + r * p.ldx + c, q < pieces && c < p.K);
     }
+    start_wait();                                     // the loads are on their way before the CTA is set up
+#pragma unroll
+    for (int i = 0; i < pieces_held<true>(); ++i) {
+        const int q = i * kQuantWarps + warp;
+        if (q >= pieces) break;                       // the whole warp
+        int r, at;
+        piece(p, q, r, at);
+        const int c = at * kCols + kMxBlock * lane;
+        uint4 word;
+        uint32_t scale;
+        held[i].quantise(word, scale, p.err);
+        if (c < p.K) *reinterpret_cast<uint4*>(codes + c / kStageK * kChunkBytes + swizzled(r, 4 * (lane & 7))) = word;
+        if (c < sf_cols) sf[c / kMxTileCols * kSfAtomBytes + r * 16 + (lane & 3)] = static_cast<uint8_t>(scale);
+    }
+    fence_proxy_async_shared();
+    mbar_arrive(a_full);
 }
 
 // The block of 16 this lane has of piece q, or zeros.
@@ -374,25 +364,21 @@ __device__ __forceinline__ bool nv_block(const DecodeParams& p, int q, int piece
 
 __device__ __forceinline__ void quantise_nv(const DecodeParams& p, int warp, int lane, uint8_t* codes, uint8_t* sf,
                                             uint32_t* row_max, float* row_g, uint64_t* a_full) {
-    constexpr int kCols = piece_cols<false>(), kHeld = pieces_held<false>(), kBatch = batch_size<false>();
+    constexpr int kCols = piece_cols<false>(), kHeld = pieces_held<false>();
     const int pieces = p.T * ((p.K + kCols - 1) / kCols);
     uint4 v[kHeld][2];
-    // the rows' maxima, then their outer scales; the last batch comes first, so that the first, which
-    // the second pass starts with, is still held then
-    const int last = (pieces - 1) / kBatch * kBatch;
-    for (int first = last; first >= 0; first -= kBatch) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) nv_block(p, first + i * kQuantWarps + warp, pieces, lane, v[i][0], v[i][1]);
-        if (first == last) start_wait();
+    for (int i = 0; i < kHeld; ++i) nv_block(p, i * kQuantWarps + warp, pieces, lane, v[i][0], v[i][1]);
+    start_wait();
+    // the rows' maxima, then their outer scales
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int q = first + i * kQuantWarps + warp;
-            if (q >= pieces) break;                   // the whole warp
-            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, block_absmax_bits(v[i][0], v[i][1]));
-            int r, at;
-            piece(p, q, r, at);
-            if (lane == 0) atomicMax(&row_max[r], top);
-        }
+    for (int i = 0; i < kHeld; ++i) {
+        const int q = i * kQuantWarps + warp;
+        if (q >= pieces) break;                       // the whole warp
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, block_absmax_bits(v[i][0], v[i][1]));
+        int r, at;
+        piece(p, q, r, at);
+        if (lane == 0) atomicMax(&row_max[r], top);
     }
     sync_quantisers();
     if (warp == 0 && lane < p.T) {
@@ -402,27 +388,21 @@ __device__ __forceinline__ void quantise_nv(const DecodeParams& p, int warp, int
         row_g[lane] = finite ? __fdiv_rn(__uint_as_float(top), kOuterDivisor) : 0.0f;
     }
     sync_quantisers();
-    for (int first = 0, batch = 0; first < pieces; first += kBatch, ++batch) {
-        if (first > 0) {
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) nv_block(p, first + i * kQuantWarps + warp, pieces, lane, v[i][0], v[i][1]);
-        }
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int q = first + i * kQuantWarps + warp;
-            int r, at;
-            piece(p, q, r, at);
-            const int c = at * kCols + 16 * lane;
-            if (q >= pieces || c >= p.K) continue;
-            uint32_t w0, w1, scale;
-            nv_quantize16(v[i][0], v[i][1], row_g[r], w0, w1, scale);
-            uint8_t* d = codes + c / kStageK * kChunkBytes + swizzled(r, (c & (kStageK - 1)) >> 3);
-            *reinterpret_cast<uint2*>(d) = make_uint2(w0, w1);
-            sf[c / 64 * kSfAtomBytes + r * 16 + ((c & 63) >> 4)] = static_cast<uint8_t>(scale);
-        }
-        fence_proxy_async_shared();
-        mbar_arrive(&a_full[batch]);
+    for (int i = 0; i < kHeld; ++i) {
+        const int q = i * kQuantWarps + warp;
+        int r, at;
+        piece(p, q, r, at);
+        const int c = at * kCols + 16 * lane;
+        if (q >= pieces || c >= p.K) continue;
+        uint32_t w0, w1, scale;
+        nv_quantize16(v[i][0], v[i][1], row_g[r], w0, w1, scale);
+        uint8_t* d = codes + c / kStageK * kChunkBytes + swizzled(r, (c & (kStageK - 1)) >> 3);
+        *reinterpret_cast<uint2*>(d) = make_uint2(w0, w1);
+        sf[c / 64 * kSfAtomBytes + r * 16 + ((c & 63) >> 4)] = static_cast<uint8_t>(scale);
     }
+    fence_proxy_async_shared();
+    mbar_arrive(a_full);
 }
 
 template <typename X>
@@ -455,11 +435,11 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     constexpr int kN = mma_n(BN);
     constexpr int kBBytes = kN * kRowBytes;                        // codes of one chunk
     constexpr int kSfBytes = F::tiles * kSfAtomBytes;              // its scale tiles
-    constexpr int kStageBytes = kPer * (kBBytes + kSfBytes);       // codes chunk by chunk, then scales
+    constexpr int kStageBytes = kPerD * (kBBytes + kSfBytes);       // codes chunk by chunk, then scales
     constexpr uint32_t kSfCols = 8 * F::tiles;                     // TMEM columns of a chunk's scales
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t full[kMaxStagesD], empty[kMaxStagesD], a_full[kMaxBatches], tmem_full[2], tmem_empty[2], drain;
+    __shared__ uint64_t full[kMaxStagesD], empty[kMaxStagesD], a_full, tmem_full[2], tmem_empty[2], drain;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
     __shared__ uint32_t row_max[kMaxT];
@@ -468,7 +448,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     volatile int* abort_flag = &abort_word;
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int num_ks = (p.K + kStageK - 1) / kStageK;              // chunks of 256
-    const int num_st = (num_ks + kPer - 1) / kPer;                 // stages of the weights
+    const int num_st = (num_ks + kPerD - 1) / kPerD;                 // stages of the weights
     const int sf_tiles = (p.K + F::tile_k - 1) / F::tile_k;
     // x: chunks of codes, then its scale tiles; the weights' stages follow, so the 128 rows an MMA
     // reads from a chunk of 16 stay inside the allocation
@@ -479,18 +459,18 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 
     if (warp == 0) {
         // one barrier of each kind to a lane: one after the other they took 1000 cycles
-        static_assert(kMaxStagesD <= 32 && kMaxBatches <= 32 && kMaxT <= 32, "a lane each");
+        static_assert(kMaxStagesD <= 32 && kMaxT <= 32, "a lane each");
         if (lane < kMaxStagesD) {
             mbar_init(&full[lane], 1);
             mbar_init(&empty[lane], 1);
         }
-        if (lane < kMaxBatches) mbar_init(&a_full[lane], kQuantThreads);
         if (lane < 2) {
             mbar_init(&tmem_full[lane], 1);
             mbar_init(&tmem_empty[lane], 32);
         }
         if (lane < kMaxT) row_max[lane] = 0u;
         if (lane == 0) {
+            mbar_init(&a_full, kQuantThreads);
             mbar_init(&drain, 1);
             abort_word = 0;
         }
@@ -511,12 +491,12 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 }
                 uint8_t* b = stages + stage * kStageBytes;
                 uint8_t* box = b + (n0 & (kN - BN)) * kRowBytes;
-                const int chunks = min(kPer, num_ks - kPer * st);
-                const uint32_t sf_bytes = static_cast<uint32_t>(min(kPer * F::tiles, sf_tiles - kPer * F::tiles * st)) * kSfAtomBytes;
-                load_operand_elect(&full[stage], chunks * BN * kRowBytes + sf_bytes, box, &tmB, kPer * st * kRowBytes, n0,
-                                   b + kPer * kBBytes, bsf + kPer * F::tiles * st * kSfAtomBytes, sf_bytes, pol);
+                const int chunks = min(kPerD, num_ks - kPerD * st);
+                const uint32_t sf_bytes = static_cast<uint32_t>(min(kPerD * F::tiles, sf_tiles - kPerD * F::tiles * st)) * kSfAtomBytes;
+                load_operand_elect(&full[stage], chunks * BN * kRowBytes + sf_bytes, box, &tmB, kPerD * st * kRowBytes, n0,
+                                   b + kPerD * kBBytes, bsf + kPerD * F::tiles * st * kSfAtomBytes, sf_bytes, pol);
                 for (int i = 1; i < chunks; ++i)
-                    tma_load_2d_elect(box + i * kBBytes, &tmB, &full[stage], (kPer * st + i) * kRowBytes, n0, pol);
+                    tma_load_2d_elect(box + i * kBBytes, &tmB, &full[stage], (kPerD * st + i) * kRowBytes, n0, pol);
                 issued |= 1u << stage;
                 issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
                 if (++stage == p.stages) {
@@ -545,7 +525,6 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool issued_any = false;
-        int batch = 0;                                   // batches of x known to be ready
         const bool reused = p.stages < num_st || p.n_tiles > static_cast<int>(gridDim.x);   // stages are filled again
         for (int t = blockIdx.x; t < p.n_tiles && !failed; t += gridDim.x) {
             const uint32_t sfb_col = kN == 64 ? static_cast<uint32_t>((t * BN) & 64) / 32 : 0u;
@@ -555,14 +534,10 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 break;
             }
             for (int st = 0; st < num_st; ++st) {
-                const int chunks = min(kPer, num_ks - kPer * st);
+                const int chunks = min(kPerD, num_ks - kPerD * st);
                 bool okf = true;
-                if (t == static_cast<int>(blockIdx.x)) {   // the batches that complete x's columns of this stage
-                    const int whole = (kPer * st + chunks + piece_cols<kMx>() / kStageK - 1) / (piece_cols<kMx>() / kStageK);
-                    const int need = (whole * p.T - 1) / batch_size<kMx>() + 1;
-                    while (okf && batch < need)
-                        okf = mbar_wait_bounded(&a_full[batch++], 0, abort_flag, kWaitBudgetCycles);
-                }
+                if (st == 0 && t == static_cast<int>(blockIdx.x))   // x
+                    okf = mbar_wait_bounded(&a_full, 0, abort_flag, kWaitBudgetCycles);
                 okf = okf && mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitBudgetCycles);
                 if (!__all_sync(0xFFFFFFFFu, okf)) {
                     failed = true;
@@ -571,13 +546,13 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 tc_fence_after();
                 const uint32_t b = b_base + stage * kStageBytes;
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
+                for (int i = 0; i < kPerD; ++i) {
                     if (i >= chunks) break;
-                    const int ks = kPer * st + i;
+                    const int ks = kPerD * st + i;
                     issue_stage<kMx, 1, 1>(tmem + acc * kN, sdesc_k_swizzled<kRowBytes>(a_base + ks * kChunkBytes),
                                         sdesc_k_swizzled<kRowBytes>(b + i * kBBytes), idesc,
-                                        sdesc_sf(a_sf_base + ks * kSfBytes), sdesc_sf(b + kPer * kBBytes + i * kSfBytes), 0,
-                                        sf0 + (kPer * stage + i) * kSfCols, sfb_col, min(kStageK / 64, (p.K - kStageK * ks + 63) / 64),
+                                        sdesc_sf(a_sf_base + ks * kSfBytes), sdesc_sf(b + kPerD * kBBytes + i * kSfBytes), 0,
+                                        sf0 + (kPerD * stage + i) * kSfCols, sfb_col, min(kStageK / 64, (p.K - kStageK * ks + 63) / 64),
                                         ks != 0);
                 }
                 issued_any = true;
@@ -603,7 +578,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
             }
         }
     } else {
-        quantise_x<kMx>(p, warp - 2, lane, a_codes, a_sf, row_max, row_g, a_full);
+        quantise_x<kMx>(p, warp - 2, lane, a_codes, a_sf, row_max, row_g, &a_full);
         if (warp == kEpiWarp) {
             tc_fence_after();
             const uint32_t tmem = uniform(tmem_slot);                   // written before the CTA's start
@@ -663,17 +638,17 @@ cudaError_t launch_decode(const LinearInput& x, const LinearArgs& a, cudaStream_
     p.ldo = a.ldo;
     p.align = out_align(a);
     p.err = a.err;
-    const int num_ks = (a.K + kStageK - 1) / kStageK, num_st = (num_ks + kPer - 1) / kPer;
+    const int num_ks = (a.K + kStageK - 1) / kStageK, num_st = (num_ks + kPerD - 1) / kPerD;
     const int sf_bytes = (a.K + F::tile_k - 1) / F::tile_k * kSfAtomBytes;
     const int x_bytes = num_ks * kChunkBytes + (sf_bytes + 1023) / 1024 * 1024;
-    const int stage_bytes = kPer * (mma_n(BN) * kRowBytes + F::tiles * kSfAtomBytes);
+    const int stage_bytes = kPerD * (mma_n(BN) * kRowBytes + F::tiles * kSfAtomBytes);
     // an MMA reads 128 rows from x's last chunk: a stage lies behind it
-    static_assert(kPer * mma_n(BN) * kRowBytes >= kBM * kRowBytes, "rows an MMA reads past x");
+    static_assert(kPerD * mma_n(BN) * kRowBytes >= kBM * kRowBytes, "rows an MMA reads past x");
     p.n_tiles = (a.N + BN - 1) / BN;
     const int sms = device_sm_count();
     const int grid = p.n_tiles < sms ? p.n_tiles : sms;
     p.stages = (kSmemLimit - kFixedBytes - 1024 - x_bytes) / stage_bytes;
-    const int by_tmem = static_cast<int>(kTmemCols - 2 * mma_n(BN)) / (8 * kPer * F::tiles);
+    const int by_tmem = static_cast<int>(kTmemCols - 2 * mma_n(BN)) / (8 * kPerD * F::tiles);
     if (p.stages > kMaxStagesD) p.stages = kMaxStagesD;
     if (p.stages > by_tmem) p.stages = by_tmem;
     if (p.n_tiles <= sms && p.stages > num_st) p.stages = num_st;
@@ -683,13 +658,15 @@ cudaError_t launch_decode(const LinearInput& x, const LinearArgs& a, cudaStream_
     return launch_pdl(false, linear_decode_kernel<kMx, BN>, grid, kThreadsD, smem, st, mb, p);
 }
 
+// Rows of A in a tile.
+int rows_of_a(int64_t T) { return T >= kBM ? kBM : static_cast<int>((T + 15) / 16 * 16); }
+
 template <bool kMx, int BN>
 cudaError_t launch(const LinearArgs& a, cudaStream_t st, bool pdl) {
+    using F = Format<kMx>;
     static bool ready[kMaxDevices];
     cudaError_t e = prepare(linear_fp4_kernel<kMx, BN>, kSmemLimit - kFixedBytes, ready);
     if (e != cudaSuccess) return e;
-    using F = Format<kMx>;
-    constexpr int sets = BN > 128 ? 2 : 1;
     Params p{};
     p.T = a.T;
     p.N = a.N;
@@ -703,43 +680,40 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t st, bool pdl) {
     p.out_type = a.out_type;
     p.ldo = a.ldo;
     p.align = out_align(a);
-    p.a_rows = a.T >= kBM ? kBM : static_cast<int>((a.T + 15) / 16 * 16);
-    p.stage_bytes = p.a_rows * kRowBytes + mma_n(BN) * kRowBytes + (1 + sets) * F::tiles * kSfAtomBytes;
-    p.stage_bytes = (p.stage_bytes + 1023) / 1024 * 1024;
-    // An MMA reads 128 rows of A whatever a_rows is (the rows past it give results nobody reads):
-    // 16 KB past the last stage's start stay inside the allocation.
-    const int room = kSmemLimit - kFixedBytes - 1024 - (kBM - p.a_rows) * kRowBytes;
-    p.stages = room / p.stage_bytes;
+    p.a_rows = rows_of_a(a.T);
+    p.stage_bytes = kPer * ((p.a_rows + mma_n(BN)) * kRowBytes + 2 * F::tiles * kSfAtomBytes);
+    // An MMA reads 128 rows of A whatever a_rows is (the rows past it give results nobody reads): 16 KB past
+    // the start of the last stage's last chunk of A stay inside the allocation.
+    const int past = (kBM - p.a_rows) * kRowBytes;
+    p.stages = (kSmemLimit - kFixedBytes - 1024 - past) / p.stage_bytes;
+    const int by_tmem = static_cast<int>(kTmemCols - 2 * mma_n(BN)) / (8 * kPer * F::tiles);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
-    const int by_tmem = static_cast<int>(kTmemCols - (BN <= 128 ? 2 : 1) * mma_n(BN)) / (4 * F::tiles * (1 + sets));
     if (p.stages > by_tmem) p.stages = by_tmem;
-    const int num_ks = (a.K + kStageK - 1) / kStageK;
+    const int num_st = (a.K + kPer * kStageK - 1) / (kPer * kStageK);
     p.n_tiles = (a.N + BN - 1) / BN;
     p.tiles = (a.T + kBM - 1) / kBM * p.n_tiles;
     p.err = a.err;
     const int sms = device_sm_count();
     const unsigned grid = static_cast<unsigned>(p.tiles < sms ? p.tiles : sms);
-    if (p.tiles <= sms && p.stages > num_ks) p.stages = num_ks;
-    const size_t smem = static_cast<size_t>(p.stages) * p.stage_bytes + (kBM - p.a_rows) * kRowBytes + 1024;
+    if (p.tiles <= sms && p.stages > num_st) p.stages = num_st;
+    const size_t smem = static_cast<size_t>(p.stages) * p.stage_bytes + past + 1024;
     CUtensorMap ma, mb;
     if (!make_map(&ma, a.a_codes, a.T, a.K / 2, p.a_rows) || !make_map(&mb, a.b_codes, a.N, a.K / 2, BN))
         return cudaErrorInvalidValue;
     return launch_pdl(pdl, linear_fp4_kernel<kMx, BN>, grid, kThreads, smem, st, ma, mb, p);
 }
 
-template <bool kMx>
-cudaError_t by_tile(const LinearArgs& a, cudaStream_t st, bool pdl) {
-    // the widest tile that still gives every SM one
-    const int64_t m = (a.T + kBM - 1) / kBM, sms = device_sm_count();
-    if (m * ((a.N + 255) / 256) >= sms) return launch<kMx, 256>(a, st, pdl);
-    if (m * ((a.N + 127) / 128) >= sms) return launch<kMx, 128>(a, st, pdl);
-    if (m * ((a.N + 63) / 64) >= sms) return launch<kMx, 64>(a, st, pdl);
-    return launch<kMx, 32>(a, st, pdl);
-}
-
 }  // namespace
 
-bool linear_quantises_x(const LinearArgs& a) { return a.T <= decode::kMaxT && a.K <= decode::kMaxK; }
+// Whether one kernel quantises x and multiplies: as many elements as its quantisers hold.  At that limit it takes as
+// long on the device as two kernels (16 x 1536 x 2048: MXFP4 4.9 and 5.6 us, NVFP4 7.8 and 6.7) and saves the caller
+// a launch and a workspace; twice as many elements take it longer (16 x 4096 x 4096 NVFP4 11.7 and 8.6 us).
+bool linear_quantises_x(bool mx, int64_t T, int64_t K) {
+    using namespace decode;
+    return T <= kMaxT && K <= kMaxK &&
+           (mx ? T * ((K + piece_cols<true>() - 1) / piece_cols<true>()) <= max_pieces<true>()
+               : T * ((K + piece_cols<false>() - 1) / piece_cols<false>()) <= max_pieces<false>());
+}
 
 cudaError_t launch_linear_x(const LinearInput& x, const LinearArgs& a, cudaStream_t st) {
     // a tile takes the time of its MMAs' issue, about the same for 32 and 64 outputs and a fifth more
@@ -751,8 +725,21 @@ cudaError_t launch_linear_x(const LinearInput& x, const LinearArgs& a, cudaStrea
 }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st, bool pdl) {
-    if ((a.T + 255) / 256 * ((a.N + 255) / 256) >= linear_pair_count()) return launch_linear_pair(a, st, pdl);
-    return a.mx ? by_tile<true>(a, st, pdl) : by_tile<false>(a, st, pdl);
+    // The kernel and tile with the least time: rounds over the SMs (or pairs of them) times the cycles of a
+    // 256-element chunk of K, which is the larger of its MMAs (240 cycles for N = 64, 310 for 128) and its
+    // operands' way into the SM (about 2.4 cycles a row of 128 bytes); a pair's chunk takes 560.
+    const int64_t sms = device_sm_count(), m = (a.T + kBM - 1) / kBM;
+    const int rows = rows_of_a(a.T);
+    auto cost = [&](int64_t tiles, int64_t at_once, int chunk) { return (tiles + at_once - 1) / at_once * chunk; };
+    auto chunk = [&](int bn, int mma) { return 12 * (rows + bn) / 5 > mma ? 12 * (rows + bn) / 5 : mma; };
+    const int64_t c32 = cost(m * ((a.N + 31) / 32), sms, chunk(32, 240));
+    const int64_t c64 = cost(m * ((a.N + 63) / 64), sms, chunk(64, 240));
+    const int64_t c128 = cost(m * ((a.N + 127) / 128), sms, chunk(128, 310));
+    const int64_t cpair = cost((a.T + 255) / 256 * ((a.N + 255) / 256), linear_pair_count(), 560);
+    if (cpair <= c32 && cpair <= c64 && cpair <= c128) return launch_linear_pair(a, st, pdl);
+    if (c128 <= c64 && c128 <= c32) return a.mx ? launch<true, 128>(a, st, pdl) : launch<false, 128>(a, st, pdl);
+    if (c64 <= c32) return a.mx ? launch<true, 64>(a, st, pdl) : launch<false, 64>(a, st, pdl);
+    return a.mx ? launch<true, 32>(a, st, pdl) : launch<false, 32>(a, st, pdl);
 }
 
 }  // namespace nvfp4

@@ -1,0 +1,92 @@
+// The NVFP4 quantisation of a dense product's x: bit for bit what nvfp4_quantize_rows gives for its rows (the
+// arithmetic is nvfp4_quant.cuh's), laid out for few rows as well as many.
+//
+// A row is taken by 1, 2 or 4 warps, each lane holding at most four blocks of 16 elements (32 consecutive bytes
+// each, a warp's side by side), so the row is read once, the maximum found and the codes made from the
+// registers.  The rows kernel of quant.cu has whole 64-element groups to a lane, up to 256 elements one after
+// the other: 6 us for one row of 4096 to 16 of them, where this one takes 2.
+//
+// The rows past T of the last 128-row tile are not written: what the tensor cores make of them is not read.
+#include "nvfp4_quant.cuh"
+#include "ops.cuh"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kHeld = 4;                             // blocks of 16 to a lane
+constexpr int kWarpCols = 32 * kHeld * kBlock;       // columns of a warp: 2048
+constexpr int kWarpsQ = 4;                           // warps of a thread block
+
+template <int kWarpsPerRow>
+__global__ void __launch_bounds__(32 * kWarpsQ)
+    quantize_x_kernel(const uint16_t* __restrict__ x, int64_t rows, int cols, int64_t ld, uint8_t* __restrict__ codes,
+                      uint8_t* __restrict__ sf, float* __restrict__ g, int* err) {
+    constexpr int kRows = kWarpsQ / kWarpsPerRow;    // rows of a thread block
+    __shared__ uint32_t s_top[2][kWarpsQ];
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = warp % kWarpsPerRow, slot = warp / kWarpsPerRow;
+    int turn = 0;
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kRows; base < rows; base += static_cast<int64_t>(gridDim.x) * kRows) {
+        const int64_t r = base + slot;
+        uint4 v[kHeld][2];
+        uint32_t top = 0u;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int c = kBlock * (32 * (i * kWarpsPerRow + part) + lane);
+            v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows && c < cols) {
+                const uint4* s = reinterpret_cast<const uint4*>(x + r * ld + c);
+                v[i][0] = __ldg(s);
+                v[i][1] = __ldg(s + 1);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) top = max(top, block_absmax_bits(v[i][0], v[i][1]));
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        if (kWarpsPerRow > 1) {
+            if (lane == 0) s_top[turn][warp] = top;
+            __syncthreads();                          // the other turn's values are read before the next one's
+#pragma unroll
+            for (int i = 0; i < kWarpsPerRow; ++i) top = max(top, s_top[turn][slot * kWarpsPerRow + i]);
+            turn ^= 1;
+        }
+        if (r >= rows) continue;                      // past the last row: nothing to write
+        const bool finite = top < 0x7F800000u;
+        const float gr = finite ? __fdiv_rn(__uint_as_float(top), kOuterDivisor) : 0.0f;
+        if (part == 0 && lane == 0) {
+            g[r] = gr;
+            if (!finite) set_device_error(err, NVFP4_ERR_NONFINITE);
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int c = kBlock * (32 * (i * kWarpsPerRow + part) + lane);
+            if (c >= cols) continue;
+            uint32_t w0, w1, scale;
+            nv_quantize16(v[i][0], v[i][1], gr, w0, w1, scale);
+            *reinterpret_cast<uint2*>(codes + r * (cols / 2) + c / 2) = make_uint2(w0, w1);
+            sf[sf_offset(r, c / kBlock, cols)] = static_cast<uint8_t>(scale);
+        }
+    }
+}
+
+template <int kWarpsPerRow>
+cudaError_t launch(const uint16_t* x, int64_t rows, int cols, int64_t ld, uint8_t* codes, uint8_t* sf, float* g, int* err,
+                   cudaStream_t st) {
+    const int64_t blocks = (rows + kWarpsQ / kWarpsPerRow - 1) / (kWarpsQ / kWarpsPerRow);
+    const int64_t most = static_cast<int64_t>(device_sm_count()) * 8;
+    return launch_pdl(false, quantize_x_kernel<kWarpsPerRow>, static_cast<unsigned>(blocks < most ? blocks : most),
+                      32 * kWarpsQ, 0, st, x, rows, cols, ld, codes, sf, g, err);
+}
+
+}  // namespace
+
+cudaError_t launch_nvfp4_quantize_x(const uint16_t* x, int64_t rows, int cols, int64_t ld, uint8_t* codes, uint8_t* sf,
+                                    float* g, int* err, cudaStream_t st) {
+    static_assert(4 * kWarpCols >= 8192, "the widest row");
+    if (cols <= kWarpCols) return launch<1>(x, rows, cols, ld, codes, sf, g, err, st);
+    if (cols <= 2 * kWarpCols) return launch<2>(x, rows, cols, ld, codes, sf, g, err, st);
+    return launch<4>(x, rows, cols, ld, codes, sf, g, err, st);
+}
+
+}  // namespace nvfp4

@@ -56,14 +56,18 @@ struct LinearArgs {
     int* err;
 };
 // The same with x not quantised yet, [T][ld] of NVFP4_TYPE_* (a's operand pointers unused): for the
-// few tokens linear_quantises_x(a) takes, which one kernel serves.
+// few tokens linear_quantises_x takes, which one kernel serves.
 struct LinearInput {
     const void* x;
     int type;
     int64_t ld;
 };
-bool linear_quantises_x(const LinearArgs& a);
+bool linear_quantises_x(bool mx, int64_t T, int64_t K);
 cudaError_t launch_linear_x(const LinearInput& x, const LinearArgs& a, cudaStream_t st);
+
+// x [rows][ld] BF16 (cols % 64 == 0, at most 8192) to NVFP4 rows for a_codes, a_sf and a_g.
+cudaError_t launch_nvfp4_quantize_x(const uint16_t* x, int64_t rows, int cols, int64_t ld, uint8_t* codes, uint8_t* sf,
+                                    float* g, int* err, cudaStream_t st);
 
 // pdl: launched as a programmatic dependent of the kernel that quantises a
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st, bool pdl);

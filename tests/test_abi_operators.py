@@ -77,7 +77,7 @@ def test_mxfp4_rows(lib):
 
 @pytest.mark.parametrize("mx", [True, False])
 def test_linear_refusals(lib, mx):
-    def call(T=4, K=128, N=100, ldx=128, ldo=100, x=P, x_type=1, bias=None, out=P, out_type=1, ws=P, nbytes=1 << 20,
+    def call(T=17, K=128, N=100, ldx=128, ldo=100, x=P, x_type=1, bias=None, out=P, out_type=1, ws=P, nbytes=1 << 20,
              codes=4096, sf=4096, g=4096):
         w = M.fp4_linear_weights(codes, sf, None if mx else g, N, K)
         if mx:
@@ -94,12 +94,16 @@ def test_linear_refusals(lib, mx):
     for kw in (dict(x=None), dict(out=None), dict(ws=None), dict(x=ODD), dict(out=ODD), dict(bias=ODD),
                dict(ws=ctypes.c_void_p(4112)), dict(codes=None), dict(sf=None), dict(codes=4104), dict(sf=4104)):
         assert call(**kw) == ARG, kw
-    need = (lib.mxfp4_linear_workspace_bytes if mx else lib.nvfp4_linear_workspace_bytes)(4, 128)
+    size = lib.mxfp4_linear_workspace_bytes if mx else lib.nvfp4_linear_workspace_bytes
+    need = size(17, 128)
     assert need >= 128 * 64 + (512 if mx else 1024) and need % 256 == 0
     assert call(nbytes=need - 1) == WS
+    # few tokens need none
+    assert size(1, 8192) == 0 and size(16, 2048) == 0 and size(16, 4096) > 0
+    assert call(T=4, ws=ctypes.c_void_p(4112)) == ARG
     assert lib.mxfp4_linear_workspace_bytes(4, 48) == 0 and lib.nvfp4_linear_workspace_bytes(4, 96) == 0
     f = lib.mxfp4_linear if mx else lib.nvfp4_linear
-    args = (P, 1, 4, 128) if mx else (P, 4, 128)
+    args = (P, 1, 17, 128) if mx else (P, 17, 128)
     assert f(None, *args, None, P, 1, 100, P, 1 << 20, None) == ARG
 
 
