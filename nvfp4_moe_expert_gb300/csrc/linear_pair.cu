@@ -343,6 +343,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (lane == 0) arrive_leader(empty_bar);
             if (p.staged) {
                 if (r - lane >= p.T) continue;         // the whole warp
+                // the column quarters' stores spread over the next tile's main loop (about half of it): all at
+                // once, in every SM at about the same time, they hold its loads up (8192^3 MXFP4 189 -> 185 us,
+                // 32768 x 4096 x 1536 NVFP4 121 -> 115.5 us; spread over all of it 190 and 115.4)
+                const long long until = clock64() + static_cast<long long>(sub) * num_ks * 64;
+                while (clock64() < until) __nanosleep(64);
                 const int row0 = static_cast<int>(r - lane);
                 if (p.out_type == NVFP4_TYPE_BF16) outputs_staged<kMx, __nv_bfloat16>(v, ga, gcol, bcol, buf, &tmOut, n0, row0, p);
                 else if (p.out_type == NVFP4_TYPE_F32) outputs_staged<kMx, float>(v, ga, gcol, bcol, buf, &tmOut, n0, row0, p);

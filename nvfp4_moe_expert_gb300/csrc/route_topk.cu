@@ -116,109 +116,56 @@ __device__ __forceinline__ float order_sigmoid(float l) {
     return y;
 }
 
-// The groups to keep: the topk_group largest keys, the lower group first on equal ones.  Every lane has its
-// own group's key gk; `group` is the lane's group.  Returns whether the lane's group is kept.
-__device__ __forceinline__ bool keep_group(uint32_t gk, int group, int topk_group) {
-    bool kept = false;
-    for (int j = 0; j < topk_group; ++j) {
-        const uint32_t top = __reduce_max_sync(kAll, gk);
-        const int first = __ffs(static_cast<int>(__ballot_sync(kAll, gk == top))) - 1;
-        if (group == __shfl_sync(kAll, group, first)) {
-            kept = true;
-            gk = 0u;
-        }
-    }
-    return kept;
+// Routing.  A token is taken by 8, 16 or 32 lanes (kLanes), so that a lane has at most 16 experts (32 of more than 512)
+// and what a token needs whatever E is, its addresses, the bound, the candidates' ranks and the weights, is shared by the
+// warp's four, two or one.  Lane s of a token holds experts V s + i, i < V; kN: elements of a load (rows aligned to them).
+//
+// The k largest keys: the k-th largest of the two largest of each half of the lanes' keys is a lower bound of the k-th
+// largest, which about k + 2 of 256 keys reach; those are put side by side in shared memory (a lane finds its own
+// by a bit mask) and each is ranked against the others.  Where more than 32 reach it (many equal keys, few lanes with
+// keys), the picks are taken one by one.
+//
+// Bound by instructions: 525 to a token of 256 experts in 8 groups with a bias, beside the 1 KB that is read (65537 of
+// them take 40 us; 121 at first, with one reduction and a search of all keys for each pick; 70 with each lane's keys sorted; 47
+// with one token to a warp; 52 with 8 lanes and 32 experts to a lane, whose registers leave too few warps).
+template <int V, int kLanes>
+struct Shared {
+    static constexpr int tokens = 32 / kLanes;
+    static constexpr int pitch = V + 4;                        // words of a lane's keys: 16-byte words without bank conflicts
+    __align__(16) uint32_t key[tokens][kLanes * pitch];
+    __align__(16) unsigned long long cand[tokens][32];
+    int id[tokens][32];
+};
+
+template <int kLanes>
+__device__ __forceinline__ float token_sum(float v) {
+#pragma unroll
+    for (int x = 1; x < kLanes; x <<= 1) v += __shfl_xor_sync(kAll, v, x);
+    return v;
+}
+template <int kLanes, typename U>
+__device__ __forceinline__ U token_max(U v) {
+#pragma unroll
+    for (int x = 1; x < kLanes; x <<= 1) v = max(v, __shfl_xor_sync(kAll, v, x));
+    return v;
 }
 
-// The k largest of the lanes' keys (lane order, then i, is id order; at least k are not 0), larger first, the lower
-// id first on equal ones: lane c gets a candidate's id and its place, kNone if it is not among the k.
-//
-// The k-th largest of the lanes' maxima is a lower bound of the k-th largest key, which about k + 2 of 256 keys
-// reach; those are put side by side in shared memory and each is ranked against the others.  Where more than 32
-// reach it (many equal keys, few lanes with keys), the picks are taken one by one.
-constexpr int kNone = 32;
-template <int V>
-__device__ __forceinline__ void select(uint32_t (&key)[V], int k, unsigned long long* cand, int lane, int& id, int& place) {
-    uint32_t m = key[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) m = max(m, key[i]);
-    uint32_t bound = 0u;
-    for (int j = 0; j < k; ++j) {
-        bound = __reduce_max_sync(kAll, m);
-        m = m == bound ? 0u : m;
-    }
-    bound = max(bound, 1u);                                // keys of 0 take no part
-    cand[lane] = 0ull;
-    __syncwarp();
-    int n = 0;
-    const uint32_t before = (1u << lane) - 1u;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const bool in = key[i] >= bound;
-        const uint32_t who = __ballot_sync(kAll, in);
-        const int at = n + __popc(who & before);
-        if (in && at < 32) cand[at] = (static_cast<unsigned long long>(key[i]) << 32) | static_cast<uint32_t>(~(V * lane + i));
-        n += __popc(who);
-    }
-    __syncwarp();
-    if (n <= 32) {
-        const unsigned long long mine = cand[lane];
-        int rank = 0;
-#pragma unroll
-        for (int c = 0; c < 32; c += 8) {
-            if (c >= n) break;
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const ulonglong2 other = *reinterpret_cast<const ulonglong2*>(cand + c + i);
-                rank += (other.x > mine ? 1 : 0) + (other.y > mine ? 1 : 0);
-            }
-        }
-        id = static_cast<int>(~static_cast<uint32_t>(mine));
-        place = lane < n && rank < k ? rank : kNone;
-        return;
-    }
-    id = 0;
-    place = lane < k ? lane : kNone;
-    for (int j = 0; j < k; ++j) {
-        uint32_t best = key[0];
-        int at = 0;
-#pragma unroll
-        for (int i = 1; i < V; ++i) {
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-            }
-        }
-        const uint32_t top = __reduce_max_sync(kAll, best);
-        const int win = __ffs(static_cast<int>(__ballot_sync(kAll, best == top))) - 1;
-        const int pick = __shfl_sync(kAll, V * lane + at, win);
-        if (lane == j) id = pick;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (pick == V * lane + i) key[i] = 0u;
-        }
-    }
-}
-
-// One warp per token; lane holds experts V * lane + i, i < V, so lane order is id order.  kN: elements of a
-// load (rows aligned to them).
-//
-// Bound by instructions: beside the 1 KB that is read, a token of 256 experts in 8 groups takes a warp some hundreds of
-// them.  What took more: the two largest of a group by one lane per group, a second reduction and a search of
-// every lane's keys for each pick's id (1050 in all, 121 us for 65537 tokens), sorting each lane's keys (1065, 70 us).
-template <typename T, int V, int kN>
+template <typename T, int V, int kLanes, int kN>
 __global__ void __launch_bounds__(32 * kWarps)
     route_topk_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, RouteParams p,
-                      const float* __restrict__ bias, int32_t* __restrict__ ids, float* __restrict__ weights,
-                      int* err) {
-    extern __shared__ float s_row[];                       // [kWarps][E], only for groups that lanes share
-    __shared__ __align__(16) unsigned long long s_cand[kWarps][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    if (t >= tokens) return;
+                            const float* __restrict__ bias, int32_t* __restrict__ ids, float* __restrict__ weights,
+                            int* err) {
+    using S = Shared<V, kLanes>;
+    __shared__ S s_warps[kWarps];
+    constexpr int kPitch = S::pitch, kTokens = S::tokens;
+    const int lane = threadIdx.x & 31, slot = lane / kLanes, sub = lane % kLanes;
+    S& sh = s_warps[threadIdx.x >> 5];
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kTokens;
+    if (first >= tokens) return;
+    const bool real = first + slot < tokens;                   // a warp's last tokens may be one that is there, again
+    const int64_t t = real ? first + slot : tokens - 1;
     const T* row = logits + t * ld;
-    const int e0 = V * lane;
+    const int e0 = V * sub;
 
     // the logits, -inf where there is no expert; a row of finite ones needs none of the checks for masks
     float l[V], probe = 0.0f;
@@ -239,24 +186,38 @@ __global__ void __launch_bounds__(32 * kWarps)
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            bad = bad || !(l[i] < INFINITY);               // +inf and NaN
+            bad = bad || !(l[i] < INFINITY);                   // +inf and NaN
             l[i] = masked_nan(l[i]);
         }
         if (bad) set_device_error(err, NVFP4_ERR_NONFINITE);
     }
 
-    // order values: the logits, or the scores plus the bias; the scores are also what "top2" adds up
+    // a softmax over all experts: its largest logit and the sum of its terms, where the weights need them
     const bool top2 = p.n_group > 1 && p.group_score == MOE_GROUP_TOP2;
     const bool scored = bias != nullptr || top2;
+    const bool softmax = p.score == MOE_SCORE_SOFTMAX;
+    const bool full = softmax && !p.renormalize;
+    float all_max = 0.0f, all_sum = 0.0f;
+    if (softmax && (scored || full)) {
+        float m = l[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+        all_max = token_max<kLanes>(m);
+    }
+    if (full) {
+        const float shift = softmax_shift(all_max);
+#pragma unroll
+        for (int i = 0; i < V; ++i) all_sum += expf(softmax_logit(l[i], all_max) - shift);
+        all_sum = token_sum<kLanes>(all_sum);
+    }
+
+    // order values o: the logits, or the scores plus the bias; the scores are also what "top2" adds up
     float o[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = l[i];
     if (scored) {
-        if (p.score == MOE_SCORE_SOFTMAX) {
-            float m = l[0];
-#pragma unroll
-            for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
-            m = warp_max(m);
+        if (softmax) {
+            float m = all_max;
             if (!clean) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) o[i] = softmax_logit(o[i], m);
@@ -268,7 +229,7 @@ __global__ void __launch_bounds__(32 * kWarps)
                 o[i] = fast_exp(o[i] - m);
                 sum += o[i];
             }
-            sum = warp_sum(sum);
+            sum = token_sum<kLanes>(sum);
             const float r = sum > 0.0f ? __frcp_rn(sum) : 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) o[i] *= r;
@@ -277,18 +238,14 @@ __global__ void __launch_bounds__(32 * kWarps)
             for (int i = 0; i < V; ++i) o[i] = order_sigmoid(o[i]);
         }
         if (bias != nullptr) {
-            if (e0 + V <= E) {
-                float b[V];
-                if (p.bias_wide) {
+            if (e0 + V <= E && p.bias_wide) {
 #pragma unroll
-                    for (int i = 0; i < V; i += V < 4 ? V : 4)
-                        load_vec<float, V < 4 ? V : 4>(bias + e0 + i, *reinterpret_cast<float(*)[V < 4 ? V : 4]>(b + i));
-                } else {
+                for (int i = 0; i < V; i += 4) {
+                    float b[4];
+                    load_vec<float, 4>(bias + e0 + i, b);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) b[i] = __ldg(bias + e0 + i);
+                    for (int j = 0; j < 4; ++j) o[i + j] = fmaxf(o[i + j] + b[j], -INFINITY);   // a NaN bias: -inf
                 }
-#pragma unroll
-                for (int i = 0; i < V; ++i) o[i] = fmaxf(o[i] + b[i], -INFINITY);   // a NaN bias: -inf
             } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
@@ -299,7 +256,7 @@ __global__ void __launch_bounds__(32 * kWarps)
         if (!clean) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (!(l[i] > -INFINITY)) o[i] = -INFINITY;
+                if (!(l[i] > -INFINITY)) o[i] = -INFINITY;     // masked
             }
         }
     }
@@ -312,13 +269,14 @@ __global__ void __launch_bounds__(32 * kWarps)
         for (int i = 0; i < V; ++i) key[i] = e0 + i < E ? key[i] : 0u;
     }
 
+    uint32_t* my_keys = sh.key[slot] + sub * kPitch;
     if (p.n_group > 1) {
         const int size = E / p.n_group;
         if (p.group_lanes > 0) {
             // a group is group_lanes whole lanes (a power of two of them)
             uint32_t gk;
             if (top2) {
-                float a = -INFINITY, b = -INFINITY;         // the two largest; masked values stay out
+                float a = -INFINITY, b = -INFINITY;            // the two largest; masked values stay out
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     b = fmaxf(b, fminf(a, o[i]));
@@ -337,72 +295,177 @@ __global__ void __launch_bounds__(32 * kWarps)
                 for (int x = 1; x < p.group_lanes; x <<= 1) gk = max(gk, __shfl_xor_sync(kAll, gk, x));
             }
             if (e0 >= E) gk = 0u;
-            const bool kept = keep_group(gk, lane / p.group_lanes, p.topk_group);
+            // kept if fewer than topk_group groups come before it
+            const int group = sub / p.group_lanes;
+            int ahead = 0;
+            for (int g = 0; g < p.n_group; ++g) {
+                const uint32_t other = __shfl_sync(kAll, gk, g * p.group_lanes, kLanes);
+                ahead += other > gk || (other == gk && g < group) ? 1 : 0;
+            }
 #pragma unroll
-            for (int i = 0; i < V; ++i) key[i] = kept ? key[i] : 0u;
+            for (int i = 0; i < V; ++i) key[i] = ahead < p.topk_group ? key[i] : 0u;
         } else {
-            // any group size: through shared memory, one lane per group
-            float* sr = s_row + warp * E;
+            // any group size: the values through shared memory, group sub, sub + kLanes, ... in lane sub; each group's
+            // key then lies in sh.id
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (e0 + i < E) sr[e0 + i] = top2 ? o[i] : __uint_as_float(key[i]);
+            for (int i = 0; i < V; ++i) my_keys[i] = top2 ? __float_as_uint(o[i]) : key[i];
+            __syncwarp();
+            for (int g = sub; g < p.n_group; g += kLanes) {
+                uint32_t gk = 0u;
+                float a = -INFINITY, b = -INFINITY;
+                for (int e = g * size; e < (g + 1) * size; ++e) {
+                    const uint32_t v = sh.key[slot][e / V * kPitch + e % V];
+                    gk = max(gk, v);
+                    const float f = __uint_as_float(v);
+                    b = fmaxf(b, fminf(a, f));
+                    a = fmaxf(a, f);
+                }
+                sh.id[slot][g] = static_cast<int>(top2 ? ordered(b > -INFINITY ? a + b : a) : gk);
             }
             __syncwarp();
-            uint32_t gk = 0u;
-            if (lane < p.n_group) {
-                const float* g = sr + lane * size;
-                if (top2) {
-                    float a = -INFINITY, b = -INFINITY;
-                    for (int i = 0; i < size; ++i) {
-                        b = fmaxf(b, fminf(a, g[i]));
-                        a = fmaxf(a, g[i]);
-                    }
-                    gk = ordered(b > -INFINITY ? a + b : a);
-                } else {
-                    for (int i = 0; i < size; ++i) gk = max(gk, __float_as_uint(g[i]));
+            uint32_t kept = 0u;                                // bit g: group g
+            for (int g = 0; g < p.n_group; ++g) {
+                const uint32_t gk = static_cast<uint32_t>(sh.id[slot][g]);
+                int ahead = 0;
+                for (int h = 0; h < p.n_group; ++h) {
+                    const uint32_t other = static_cast<uint32_t>(sh.id[slot][h]);
+                    ahead += other > gk || (other == gk && h < g) ? 1 : 0;
                 }
+                kept |= (ahead < p.topk_group ? 1u : 0u) << g;
             }
-            const uint32_t kept = __ballot_sync(kAll, keep_group(gk, lane, p.topk_group));
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 if (e0 + i < E && !((kept >> ((e0 + i) / size)) & 1u)) key[i] = 0u;
             }
+            __syncwarp();
         }
     }
 
-    int id, place;
-    select<V>(key, p.k, s_cand[warp], lane, id, place);
-
-    // the chosen experts' scores, each in the lane that has it
-    const bool chosen = place < kNone;
-    float lj = chosen ? masked_nan(load_one(row + id)) : -INFINITY;
-    float w;
-    if (p.score == MOE_SCORE_SIGMOID) {
-        w = sigmoid(lj);
+    // the bound: the k-th largest of the two largest keys of each half of the lanes' (equal ones together)
+    uint32_t m[2] = {0u, 0u}, m2[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int h = 2 * i / V;
+        m2[h] = max(m2[h], min(m[h], key[i]));
+        m[h] = max(m[h], key[i]);
+    }
+    uint32_t bound = 0u;
+    for (int j = 0; j < p.k; ++j) {
+        bound = token_max<kLanes>(max(m[0], m[1]));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool gone = m[h] == bound;
+            m[h] = gone ? m2[h] : m[h];
+            m2[h] = gone ? 0u : m2[h];
+        }
+    }
+    bound = max(bound, 1u);                                    // keys of 0 take no part
+    // the keys that reach it, side by side
+    uint32_t hits = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) hits |= key[i] >= bound ? 1u << i : 0u;
+#pragma unroll
+    for (int i = 0; i < V; i += 4) *reinterpret_cast<uint4*>(my_keys + i) = make_uint4(key[i], key[i + 1], key[i + 2], key[i + 3]);
+    unsigned long long* cand = sh.cand[slot];
+#pragma unroll
+    for (int i = 0; i < 32 / kLanes; ++i) cand[sub + kLanes * i] = 0ull;
+    const int count = __popc(hits);
+    int at = count;
+#pragma unroll
+    for (int x = 1; x < kLanes; x <<= 1) {
+        const int below = __shfl_up_sync(kAll, at, x, kLanes);
+        at += sub >= x ? below : 0;
+    }
+    const int n = __shfl_sync(kAll, at, kLanes - 1, kLanes);
+    at -= count;
+    const int most = __reduce_max_sync(kAll, n);
+    __syncwarp();
+    if (most <= 32) {
+        while (hits) {
+            const int i = __ffs(static_cast<int>(hits)) - 1;
+            hits &= hits - 1u;
+            cand[at++] = (static_cast<unsigned long long>(my_keys[i]) << 32) | static_cast<uint32_t>(~(e0 + i));
+        }
+        __syncwarp();
+        for (int c = sub; c < most; c += kLanes) {
+            const unsigned long long mine = cand[c];
+            int rank = 0;
+            for (int d = 0; d < most; d += 4) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(cand + d);
+                const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(cand + d + 2);
+                rank += (x.x > mine ? 1 : 0) + (x.y > mine ? 1 : 0) + (y.x > mine ? 1 : 0) + (y.y > mine ? 1 : 0);
+            }
+            if (mine != 0ull && rank < p.k) sh.id[slot][rank] = static_cast<int>(~static_cast<uint32_t>(mine));
+        }
     } else {
-        float m = lj;
-        if (!p.renormalize) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
-        }
-        m = warp_max(m);
-        const float shift = softmax_shift(m);
-        w = expf(softmax_logit(lj, m) - shift);             // renormalised: the softmax over the chosen
-        if (!p.renormalize) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) sum += expf(softmax_logit(l[i], m) - shift);
-            sum = warp_sum(sum);
-            w = sum > 0.0f ? __fdiv_rn(w, sum) : 0.0f;
+        // many equal keys, or few lanes with keys: one pick after the other
+        for (int j = 0; j < p.k; ++j) {
+            unsigned long long best = 0ull;
+            for (int i = 0; i < V; ++i) {
+                const unsigned long long v = (static_cast<unsigned long long>(my_keys[i]) << 32) | static_cast<uint32_t>(~(e0 + i));
+                best = v > best ? v : best;
+            }
+            const unsigned long long top = token_max<kLanes>(best);
+            if (best == top) {
+                my_keys[~static_cast<uint32_t>(top) - e0] = 0u;
+                sh.id[slot][j] = static_cast<int>(~static_cast<uint32_t>(top));
+            }
         }
     }
+    __syncwarp();
+
+    // the chosen experts' scores, slot j in lane j % kLanes
+    constexpr int kSlots = 32 / kLanes;
+    float w[kSlots];
+    int id[kSlots];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+        const int j = sub + kLanes * i;
+        id[i] = 0;
+        w[i] = -INFINITY;
+        if (j < p.k) {
+            id[i] = sh.id[slot][j];
+            w[i] = masked_nan(load_one(row + id[i]));
+        }
+        top = fmaxf(top, w[i]);
+    }
+    if (softmax) {
+        const float mx = full ? all_max : token_max<kLanes>(top);      // renormalised: the softmax over the chosen
+        const float shift = softmax_shift(mx);
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            if (kLanes * i < p.k) w[i] = expf(softmax_logit(w[i], mx) - shift);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            if (kLanes * i < p.k) w[i] = sigmoid(w[i]);
+        }
+    }
+    float sum = all_sum;
     if (p.renormalize) {
-        const float sum = warp_sum(chosen ? w : 0.0f);
-        w = sum > 0.0f ? __fdiv_rn(w, sum) : 0.0f;
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            if (kLanes * i < p.k) sum += sub + kLanes * i < p.k ? w[i] : 0.0f;
+        }
+        sum = token_sum<kLanes>(sum);
     }
-    if (chosen) {
-        ids[t * p.k + place] = id;
-        weights[t * p.k + place] = w * p.scale;
+    if (p.renormalize || full) {
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            if (kLanes * i < p.k) w[i] = sum > 0.0f ? __fdiv_rn(w[i], sum) : 0.0f;
+        }
+    }
+    if (!real) return;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+        const int j = sub + kLanes * i;
+        if (j < p.k) {
+            ids[t * p.k + j] = id[i];
+            weights[t * p.k + j] = w[i] * p.scale;
+        }
     }
 }
 
@@ -525,36 +588,36 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (id >= 0) out[id] = from_f32<T>(d);
 }
 
-template <typename T, int V, int kN>
+template <typename T, int V, int kLanes, int kN>
 cudaError_t launch_route(const void* logits, int64_t tokens, int E, int64_t ld, RouteParams p, const float* bias,
                          int32_t* ids, float* weights, int* err, cudaStream_t st) {
     // a group of whole lanes, a power of two of them
     const int size = E / p.n_group, lanes = size / V;
     p.group_lanes = size % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     p.bias_wide = (reinterpret_cast<uintptr_t>(bias) & 15) == 0;
-    const unsigned grid = static_cast<unsigned>((tokens + kWarps - 1) / kWarps);
-    const size_t smem = p.n_group > 1 && p.group_lanes == 0 ? static_cast<size_t>(kWarps) * E * 4 : 0;
-    return launch_pdl(false, route_topk_kernel<T, V, kN>, grid, 32 * kWarps, smem, st, static_cast<const T*>(logits),
-                      tokens, E, ld, p, bias, ids, weights, err);
+    constexpr int kPerBlock = kWarps * 32 / kLanes;
+    return launch_pdl(false, route_topk_kernel<T, V, kLanes, kN>, static_cast<unsigned>((tokens + kPerBlock - 1) / kPerBlock),
+                      32 * kWarps, 0, st, static_cast<const T*>(logits), tokens, E, ld, p, bias, ids, weights, err);
 }
-template <typename T, int V>
+template <typename T, int V, int kLanes>
 cudaError_t route_by_word(const void* logits, int64_t tokens, int E, int64_t ld, const RouteParams& p, const float* bias,
                           int32_t* ids, float* weights, int* err, cudaStream_t st) {
     constexpr int kWide = V * sizeof(T) < 16 ? V : 16 / static_cast<int>(sizeof(T));
     const int64_t bits = static_cast<int64_t>(reinterpret_cast<uintptr_t>(logits)) | (ld * static_cast<int64_t>(sizeof(T)));
     if (bits % (kWide * static_cast<int64_t>(sizeof(T))) == 0)
-        return launch_route<T, V, kWide>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
-    return launch_route<T, V, 1>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+        return launch_route<T, V, kLanes, kWide>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+    return launch_route<T, V, kLanes, 1>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
 }
+// The kernel goes by E alone, so a token's result does not depend on how many there are.
 template <typename T>
 cudaError_t route_by_width(const void* logits, int64_t tokens, int E, int64_t ld, const RouteParams& p, const float* bias,
                            int32_t* ids, float* weights, int* err, cudaStream_t st) {
-    if (E <= 32) return route_by_word<T, 1>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
-    if (E <= 64) return route_by_word<T, 2>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
-    if (E <= 128) return route_by_word<T, 4>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
-    if (E <= 256) return route_by_word<T, 8>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
-    if (E <= 512) return route_by_word<T, 16>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
-    return route_by_word<T, 32>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+    if (E <= 32) return route_by_word<T, 4, 8>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+    if (E <= 64) return route_by_word<T, 8, 8>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+    if (E <= 128) return route_by_word<T, 16, 8>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+    if (E <= 256) return route_by_word<T, 16, 16>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+    if (E <= 512) return route_by_word<T, 16, 32>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
+    return route_by_word<T, 32, 32>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
 }
 
 template <typename T, int kWords, int kN>
