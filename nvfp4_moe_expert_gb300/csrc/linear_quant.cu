@@ -13,12 +13,12 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kHeld = 4;                             // blocks of 16 to a lane
-constexpr int kWarpCols = 32 * kHeld * kBlock;       // columns of a warp: 2048
+constexpr int kMaxHeld = 4;                          // blocks of 16 to a lane
+constexpr int kPassCols = 32 * kBlock;               // columns of a warp's pass: one block to a lane
 constexpr int kWarpsQ = 4;                           // warps of a thread block
 
-template <int kWarpsPerRow>
-__global__ void __launch_bounds__(32 * kWarpsQ)
+template <int kWarpsPerRow, int kHeld>
+__global__ void __launch_bounds__(32 * kWarpsQ, 8)
     quantize_x_kernel(const uint16_t* __restrict__ x, int64_t rows, int cols, int64_t ld, uint8_t* __restrict__ codes,
                       uint8_t* __restrict__ sf, float* __restrict__ g, int* err) {
     constexpr int kRows = kWarpsQ / kWarpsPerRow;    // rows of a thread block
@@ -70,12 +70,12 @@ __global__ void __launch_bounds__(32 * kWarpsQ)
     }
 }
 
-template <int kWarpsPerRow>
+template <int kWarpsPerRow, int kHeld>
 cudaError_t launch(const uint16_t* x, int64_t rows, int cols, int64_t ld, uint8_t* codes, uint8_t* sf, float* g, int* err,
                    cudaStream_t st) {
     const int64_t blocks = (rows + kWarpsQ / kWarpsPerRow - 1) / (kWarpsQ / kWarpsPerRow);
     const int64_t most = static_cast<int64_t>(device_sm_count()) * 8;
-    return launch_pdl(false, quantize_x_kernel<kWarpsPerRow>, static_cast<unsigned>(blocks < most ? blocks : most),
+    return launch_pdl(false, quantize_x_kernel<kWarpsPerRow, kHeld>, static_cast<unsigned>(blocks < most ? blocks : most),
                       32 * kWarpsQ, 0, st, x, rows, cols, ld, codes, sf, g, err);
 }
 
@@ -83,10 +83,16 @@ cudaError_t launch(const uint16_t* x, int64_t rows, int cols, int64_t ld, uint8_
 
 cudaError_t launch_nvfp4_quantize_x(const uint16_t* x, int64_t rows, int cols, int64_t ld, uint8_t* codes, uint8_t* sf,
                                     float* g, int* err, cudaStream_t st) {
-    static_assert(4 * kWarpCols >= 8192, "the widest row");
-    if (cols <= kWarpCols) return launch<1>(x, rows, cols, ld, codes, sf, g, err, st);
-    if (cols <= 2 * kWarpCols) return launch<2>(x, rows, cols, ld, codes, sf, g, err, st);
-    return launch<4>(x, rows, cols, ld, codes, sf, g, err, st);
+    static_assert(4 * kMaxHeld * kPassCols >= 8192, "the widest row");
+    const int passes = (cols + kPassCols - 1) / kPassCols;
+    if (passes <= 1) return launch<1, 1>(x, rows, cols, ld, codes, sf, g, err, st);
+    if (passes <= 2) return launch<1, 2>(x, rows, cols, ld, codes, sf, g, err, st);
+    if (passes <= 3) return launch<1, 3>(x, rows, cols, ld, codes, sf, g, err, st);
+    if (passes <= 4) return launch<1, 4>(x, rows, cols, ld, codes, sf, g, err, st);
+    if (passes <= 6) return launch<2, 3>(x, rows, cols, ld, codes, sf, g, err, st);
+    if (passes <= 8) return launch<2, 4>(x, rows, cols, ld, codes, sf, g, err, st);
+    if (passes <= 12) return launch<4, 3>(x, rows, cols, ld, codes, sf, g, err, st);
+    return launch<4, 4>(x, rows, cols, ld, codes, sf, g, err, st);
 }
 
 }  // namespace nvfp4

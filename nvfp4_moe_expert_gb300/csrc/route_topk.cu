@@ -475,117 +475,148 @@ __global__ void __launch_bounds__(32 * kWarps)
 //   sigmoid, renormalised:  dl_c = q_c (1 - s_c) (g_c - sum_j g_j q_j),  q_c = s_c / sum_j s_j
 //   sigmoid:                dl_c = g_c s_c (1 - s_c)
 //   softmax:                dl_e = s_e ([e chosen] g_e - sum_j g_j s_j), every expert
-// One warp per token, lane j < k holding slot j.  Of the row, lane `lane` has the words of four experts at
-// 4 (lane + 32 i), i < kWords, whatever the alignment (kN elements to a load and store), so sums are taken in one
-// order.  The row is written with what an expert that was not chosen gets, then the chosen ones over it.
+// The row is written with what an expert that was not chosen gets, in words of four experts side by side (kN elements to
+// a load and store), and the chosen ones over it.
 //
 // Bound by memory: the row written (and, for the softmax over all experts, read).
-template <typename T, int kWords, int kN>
+
+// Slot j's expert, g = scale * dw and logit; -1, 0 and -inf where there is none.
+template <typename T>
+__device__ __forceinline__ void load_slot(const T* row, const int32_t* ids, const float* dw, bool live, int E, float scale,
+                                          int& id, float& g, float& lj, int* err) {
+    id = live ? __ldg(ids) : -1;
+    g = live ? scale * __ldg(dw) : 0.0f;
+    lj = -INFINITY;
+    if (live && (id < 0 || id >= E)) {
+        set_device_error(err, NVFP4_ERR_BAD_EXPERT_ID);
+        id = -1;
+        g = 0.0f;
+    }
+    if (id >= 0) lj = masked_nan(load_one(row + id));
+}
+
+// Four experts' values at e of a row of E.
+template <typename T, int kN>
+__device__ __forceinline__ void store4(T* out, int e, int E, const float (&v)[4]) {
+    if (e + 4 <= E) {
+#pragma unroll
+        for (int i = 0; i < 4; i += kN) store_vec<T, kN>(out + e + i, *reinterpret_cast<const float(*)[kN]>(v + i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (e + i < E) out[e + i] = from_f32<T>(v[i]);
+        }
+    }
+}
+
+// Every weight but the softmax's over all experts: only the chosen logits take part.  A token is taken by kLanes >= k
+// lanes, slot j in lane j; the warp writes its tokens' zeros first, which waits for nothing.  (With one token to a
+// warp 65537 x 256 took 21.4 us.)
+template <typename T, int kLanes, int kN>
 __global__ void __launch_bounds__(32 * kWarps)
     route_topk_backward_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, RouteParams p,
                                const int32_t* __restrict__ ids, const float* __restrict__ dw, T* __restrict__ dl,
                                int64_t ld_out, int* err) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    constexpr int kTokens = 32 / kLanes;
+    const int lane = threadIdx.x & 31, sub = lane % kLanes;
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kTokens;
+    if (first >= tokens) return;
+    const int64_t t = first + lane / kLanes;
+    const bool live = t < tokens && sub < p.k;
+    int id;
+    float g, lj;
+    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        if (first + i >= tokens) break;
+        for (int e = 4 * lane; e < E; e += 128) store4<T, kN>(dl + (first + i) * ld_out, e, E, zero);
+    }
+    load_slot(logits + t * ld, ids + t * p.k + sub, dw + t * p.k + sub, live, E, p.scale, id, g, lj, err);
+    float s, rest = 1.0f;                                       // rest = 1 - s
+    if (p.score == MOE_SCORE_SOFTMAX) {
+        const float m = token_max<kLanes>(lj);
+        s = expf(softmax_logit(lj, m) - softmax_shift(m));
+    } else {
+        s = sigmoid(lj);
+        rest = __frcp_rn(1.0f + expf(lj));
+    }
+    float dot = 0.0f;
+    if (p.renormalize) {
+        const float sum = token_sum<kLanes>(s);
+        s = sum > 0.0f ? __fdiv_rn(s, sum) : 0.0f;
+        dot = token_sum<kLanes>(g * s);
+    }
+    __syncwarp();                                               // orders the warp's writes
+    if (id >= 0) dl[t * ld_out + id] = from_f32<T>(s * rest * (g - dot));
+}
+
+// The softmax over all experts.  One warp per token; lane `lane` has the words of four experts at 4 (lane + 32 i), i <
+// kWords, whatever the alignment, so sums are taken in one order.
+template <typename T, int kWords, int kN>
+__global__ void __launch_bounds__(32 * kWarps)
+    route_topk_backward_full_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, RouteParams p,
+                                    const int32_t* __restrict__ ids, const float* __restrict__ dw, T* __restrict__ dl,
+                                    int64_t ld_out, int* err) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     if (t >= tokens) return;
     const T* row = logits + t * ld;
     T* out = dl + t * ld_out;
-    int id = -1;
-    float g = 0.0f, lj = -INFINITY;
-    if (lane < p.k) {
-        id = __ldg(ids + t * p.k + lane);
-        if (id < 0 || id >= E) {
-            set_device_error(err, NVFP4_ERR_BAD_EXPERT_ID);
-            id = -1;
-        } else {
-            g = p.scale * __ldg(dw + t * p.k + lane);
-            lj = masked_nan(load_one(row + id));
-        }
-    }
-    auto store4 = [&](int e, const float (&v)[4]) {
+    float v[kWords][4];
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+        const int e = 4 * (lane + 32 * j);
         if (e + 4 <= E) {
 #pragma unroll
-            for (int i = 0; i < 4; i += kN) store_vec<T, kN>(out + e + i, *reinterpret_cast<const float(*)[kN]>(v + i));
+            for (int i = 0; i < 4; i += kN) load_vec<T, kN>(row + e + i, *reinterpret_cast<float(*)[kN]>(v[j] + i));
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (e + i < E) out[e + i] = from_f32<T>(v[i]);
-            }
+            for (int i = 0; i < 4; ++i) v[j][i] = e + i < E ? load_one(row + e + i) : -INFINITY;
         }
-    };
-    float d;
-    if (p.score == MOE_SCORE_SOFTMAX && !p.renormalize) {
-        float v[kWords][4];
-        float m = -INFINITY, probe = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kWords; ++j) {
-            const int e = 4 * (lane + 32 * j);
-            if (e + 4 <= E) {
-#pragma unroll
-                for (int i = 0; i < 4; i += kN) load_vec<T, kN>(row + e + i, *reinterpret_cast<float(*)[kN]>(v[j] + i));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) probe = fmaf(v[j][i], 0.0f, probe);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[j][i] = e + i < E ? load_one(row + e + i) : -INFINITY;
-                    probe = fmaf(e + i < E ? v[j][i] : 0.0f, 0.0f, probe);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m = fmaxf(m, v[j][i]);   // passes NaN over
-        }
-        m = warp_max(m);
-        const float shift = softmax_shift(m);
-        if (!__all_sync(kAll, probe == 0.0f)) {             // masks, infinities or NaN
-#pragma unroll
-            for (int j = 0; j < kWords; ++j) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[j][i] = softmax_logit(masked_nan(v[j][i]), m);
-            }
-        }
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kWords; ++j) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[j][i] = expf(v[j][i] - shift);
-                sum += v[j][i];
-            }
-        }
-        sum = warp_sum(sum);
-        const float r = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-        const float s = expf(softmax_logit(lj, m) - shift);
-        const float own = g * (s * r);
-        const float c = -warp_sum(own) * r;
-#pragma unroll
-        for (int j = 0; j < kWords; ++j) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[j][i] *= c;
-            store4(4 * (lane + 32 * j), v[j]);
-        }
-        d = s * c + own;
-    } else {
-        float s, rest = 1.0f;                               // rest = 1 - s
-        if (p.score == MOE_SCORE_SOFTMAX) {
-            const float m = warp_max(lj);
-            s = expf(softmax_logit(lj, m) - softmax_shift(m));
-        } else {
-            s = sigmoid(lj);
-            rest = __frcp_rn(1.0f + expf(lj));
-        }
-        float dot = 0.0f;
-        if (p.renormalize) {
-            const float sum = warp_sum(s);
-            s = sum > 0.0f ? __fdiv_rn(s, sum) : 0.0f;
-            dot = warp_sum(g * s);
-        }
-        d = s * rest * (g - dot);
-        const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int e = 4 * lane; e < E; e += 128) store4(e, zero);
     }
-    __syncwarp();                                           // orders the warp's writes
-    if (id >= 0) out[id] = from_f32<T>(d);
+    int id;
+    float g, lj;
+    load_slot(row, ids + t * p.k + lane, dw + t * p.k + lane, lane < p.k, E, p.scale, id, g, lj, err);
+    float m = -INFINITY, probe = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m = fmaxf(m, v[j][i]);                              // passes NaN over
+            probe = fmaf(4 * (lane + 32 * j) + i < E ? v[j][i] : 0.0f, 0.0f, probe);
+        }
+    }
+    m = warp_max(m);
+    const float shift = softmax_shift(m);
+    if (!__all_sync(kAll, probe == 0.0f)) {                     // masks, infinities or NaN
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[j][i] = softmax_logit(masked_nan(v[j][i]), m);
+        }
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[j][i] = expf(v[j][i] - shift);
+            sum += v[j][i];
+        }
+    }
+    sum = warp_sum(sum);
+    const float r = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+    const float s = expf(softmax_logit(lj, m) - shift);
+    const float own = g * (s * r);
+    const float c = -warp_sum(own) * r;
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] *= c;
+        store4<T, kN>(out, 4 * (lane + 32 * j), E, v[j]);
+    }
+    __syncwarp();                                               // orders the warp's writes
+    if (id >= 0) out[id] = from_f32<T>(s * c + own);
 }
 
 template <typename T, int V, int kLanes, int kN>
@@ -620,30 +651,34 @@ cudaError_t route_by_width(const void* logits, int64_t tokens, int E, int64_t ld
     return route_by_word<T, 32, 32>(logits, tokens, E, ld, p, bias, ids, weights, err, st);
 }
 
-template <typename T, int kWords, int kN>
+// By the experts (of a softmax over all of them) or the slots.
+template <typename T, int kN>
 cudaError_t launch_backward(const void* logits, int64_t tokens, int E, int64_t ld, const RouteParams& p, const int32_t* ids,
                             const float* dw, void* dl, int64_t ld_out, int* err, cudaStream_t st) {
-    const unsigned grid = static_cast<unsigned>((tokens + kWarps - 1) / kWarps);
-    return launch_pdl(false, route_topk_backward_kernel<T, kWords, kN>, grid, 32 * kWarps, 0, st,
-                      static_cast<const T*>(logits), tokens, E, ld, p, ids, dw, static_cast<T*>(dl), ld_out, err);
+    auto run = [&](auto kernel, int per_warp) {
+        const int per_block = kWarps * per_warp;
+        return launch_pdl(false, kernel, static_cast<unsigned>((tokens + per_block - 1) / per_block), 32 * kWarps, 0, st,
+                          static_cast<const T*>(logits), tokens, E, ld, p, ids, dw, static_cast<T*>(dl), ld_out, err);
+    };
+    if (p.score == MOE_SCORE_SOFTMAX && !p.renormalize) {
+        if (E <= 128) return run(route_topk_backward_full_kernel<T, 1, kN>, 1);
+        if (E <= 256) return run(route_topk_backward_full_kernel<T, 2, kN>, 1);
+        if (E <= 512) return run(route_topk_backward_full_kernel<T, 4, kN>, 1);
+        return run(route_topk_backward_full_kernel<T, 8, kN>, 1);
+    }
+    if (p.k <= 8) return run(route_topk_backward_kernel<T, 8, kN>, 4);
+    if (p.k <= 16) return run(route_topk_backward_kernel<T, 16, kN>, 2);
+    return run(route_topk_backward_kernel<T, 32, kN>, 1);
 }
-template <typename T, int kWords>
+template <typename T>
 cudaError_t backward_by_word(const void* logits, int64_t tokens, int E, int64_t ld, const RouteParams& p, const int32_t* ids,
                              const float* dw, void* dl, int64_t ld_out, int* err, cudaStream_t st) {
     constexpr int64_t kSize = sizeof(T);
     const int64_t bits = static_cast<int64_t>(reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dl)) |
                          (ld * kSize) | (ld_out * kSize);
-    if (bits % (4 * kSize) == 0) return launch_backward<T, kWords, 4>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
-    if (bits % (2 * kSize) == 0) return launch_backward<T, kWords, 2>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
-    return launch_backward<T, kWords, 1>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
-}
-template <typename T>
-cudaError_t backward_by_width(const void* logits, int64_t tokens, int E, int64_t ld, const RouteParams& p, const int32_t* ids,
-                              const float* dw, void* dl, int64_t ld_out, int* err, cudaStream_t st) {
-    if (E <= 128) return backward_by_word<T, 1>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
-    if (E <= 256) return backward_by_word<T, 2>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
-    if (E <= 512) return backward_by_word<T, 4>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
-    return backward_by_word<T, 8>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
+    if (bits % (4 * kSize) == 0) return launch_backward<T, 4>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
+    if (bits % (2 * kSize) == 0) return launch_backward<T, 2>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
+    return launch_backward<T, 1>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
 }
 
 }  // namespace
@@ -661,9 +696,9 @@ cudaError_t launch_route_topk_backward(const void* logits, int type, int64_t T, 
                                        const RouteParams& p, const int32_t* ids, const float* dw, void* dl,
                                        int64_t ld_out, int* err, cudaStream_t st) {
     switch (type) {
-        case NVFP4_TYPE_F32: return backward_by_width<float>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
-        case NVFP4_TYPE_BF16: return backward_by_width<__nv_bfloat16>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
-        default: return backward_by_width<__half>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
+        case NVFP4_TYPE_F32: return backward_by_word<float>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
+        case NVFP4_TYPE_BF16: return backward_by_word<__nv_bfloat16>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
+        default: return backward_by_word<__half>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
     }
 }
 
