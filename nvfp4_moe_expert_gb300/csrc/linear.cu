@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kPer; ++i) {
                     if (i >= chunks) break;
                     const int ks = kPer * st + i;
-                    issue_stage<kMx, 1, 1>(tmem + acc * kN, sdesc_k_swizzled<kRowBytes>(at + i * a_bytes),
+                    issue_stage<kMx, false>(tmem + acc * kN, sdesc_k_swizzled<kRowBytes>(at + i * a_bytes),
                                            sdesc_k_swizzled<kRowBytes>(at + b_off + i * kBBytes), idesc,
                                            sdesc_sf(at + sfa_off + i * kSfBytes), sdesc_sf(at + sfb_off + i * kSfBytes), 0,
                                            sf0 + (kPer * stage + i) * kSfCols, sfb_col,
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 for (int i = 0; i < kPerD; ++i) {
                     if (i >= chunks) break;
                     const int ks = kPerD * st + i;
-                    issue_stage<kMx, 1, 1>(tmem + acc * kN, sdesc_k_swizzled<kRowBytes>(a_base + ks * kChunkBytes),
+                    issue_stage<kMx, false>(tmem + acc * kN, sdesc_k_swizzled<kRowBytes>(a_base + ks * kChunkBytes),
                                         sdesc_k_swizzled<kRowBytes>(b + i * kBBytes), idesc,
                                         sdesc_sf(a_sf_base + ks * kSfBytes), sdesc_sf(b + kPerD * kBBytes + i * kSfBytes), 0,
                                         sf0 + (kPerD * stage + i) * kSfCols, sfb_col, min(kStageK / 64, (p.K - kStageK * ks + 63) / 64),

@@ -49,10 +49,9 @@ __host__ __device__ constexpr uint32_t idesc_fp4(bool mx, int M, int N) {
 __host__ __device__ constexpr uint32_t idesc_sf_id(uint32_t id) { return (id << 4) | (id << 29); }
 
 // One stage of the main loop, in one block of PTX with one elect.sync: the scale tiles go to TMEM
-// (columns sf .. , A's first, then B's kSets per tile), then nk <= 4 K=64 MMAs accumulate into d.
+// (columns sf .. , A's first, then B's, one set of 128 rows or, by a pair of CTAs, two), then nk <= 4 K=64 MMAs accumulate into d.
 // sa, sb, sb2: descriptors of the scale tiles of A and of B's first and second 128 rows (the next tile
-// 512 bytes, 32 units, further); a K step is 32 bytes (2 units) of the operands' rows.  kGroup: the
-// CTAs of the MMA.  (As twelve separately elected instructions a stage took 730-800 cycles to issue.)
+// 512 bytes, 32 units, further); a K step is 32 bytes (2 units) of the operands' rows.  (As twelve separately elected instructions a stage took 730-800 cycles to issue.)
 #define LINEAR_CP(G, P, dst, src) "@" P " tcgen05.cp.cta_group::" G ".32x128b.warpx4 [" dst "], " src ";\n\t"
 #define LINEAR_MMA_NV(G, P, acc, sfb)                                                                        \
     "@" P " tcgen05.mma.cta_group::" G ".kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %3, [ca], [" sfb "], " acc ";\n\t"
@@ -72,41 +71,36 @@ __host__ __device__ constexpr uint32_t idesc_sf_id(uint32_t id) { return (id << 
         "r"(accumulate ? 1u : 0u), "r"(nk), "n"(4 * Format<kMx>::tiles) : "memory"
 // one 128-row set of B: its MMA's scales may start at the tile's third column
 #define LINEAR_NV1(P, acc) LINEAR_CP("1", P, "ca", "s0") LINEAR_CP("1", P, "cb", "s1") "add.u32 cc, cb, %8;\n\t" LINEAR_MMA_NV("1", P, acc, "cc")
-#define LINEAR_NV2(G, P, acc)                                                                                \
-    LINEAR_CP(G, P, "ca", "s0") LINEAR_CP(G, P, "cb", "s1") "add.u32 cc, cb, 4;\n\t" LINEAR_CP(G, P, "cc", "s2") LINEAR_MMA_NV(G, P, acc, "cb")
+// a pair of CTAs, two sets
+#define LINEAR_NV2(P, acc)                                                                                   \
+    LINEAR_CP("2", P, "ca", "s0") LINEAR_CP("2", P, "cb", "s1") "add.u32 cc, cb, 4;\n\t" LINEAR_CP("2", P, "cc", "s2") \
+        LINEAR_MMA_NV("2", P, acc, "cb")
 #define LINEAR_MX1(P, Q, acc)                                                                                \
     LINEAR_CP("1", P, "ca", "s0") LINEAR_CP("1", P, "cb", "s1") "add.u32 cc, cb, %8;\n\t"                       \
         LINEAR_MMA_MX("1", P, acc, "%3", "cc") LINEAR_STEP LINEAR_MMA_MX("1", Q, "p1", "i2", "cc")
-#define LINEAR_MX2(G, P, Q, acc)                                                                             \
-    LINEAR_CP(G, P, "ca", "s0") LINEAR_CP(G, P, "cb", "s1") "add.u32 cc, cb, 4;\n\t" LINEAR_CP(G, P, "cc", "s2")  \
-        LINEAR_MMA_MX(G, P, acc, "%3", "cb") LINEAR_STEP LINEAR_MMA_MX(G, Q, "p1", "i2", "cb")
-#define LINEAR_NV2_STAGE(G)                                                                                  \
-    LINEAR_BEGIN LINEAR_NV2(G, "ep", "p0") LINEAR_STEP LINEAR_NEXT("8") LINEAR_NV2(G, "e1", "p1") LINEAR_STEP    \
-        LINEAR_NEXT("8") LINEAR_NV2(G, "e2", "p1") LINEAR_STEP LINEAR_NEXT("8") LINEAR_NV2(G, "e3", "p1") "}"
-#define LINEAR_MX2_STAGE(G)                                                                                  \
-    LINEAR_BEGIN "or.b32 i2, %3, 0x40000020;\n\t" LINEAR_MX2(G, "ep", "e1", "p0") LINEAR_STEP LINEAR_NEXT("8")   \
-        LINEAR_MX2(G, "e2", "e3", "p1") "}"
+#define LINEAR_MX2(P, Q, acc)                                                                                \
+    LINEAR_CP("2", P, "ca", "s0") LINEAR_CP("2", P, "cb", "s1") "add.u32 cc, cb, 4;\n\t" LINEAR_CP("2", P, "cc", "s2") \
+        LINEAR_MMA_MX("2", P, acc, "%3", "cb") LINEAR_STEP LINEAR_MMA_MX("2", Q, "p1", "i2", "cb")
+#define LINEAR_ID2 "or.b32 i2, %3, 0x40000020;\n\t"
 
-template <bool kMx, int kSets, int kGroup>
+template <bool kMx, bool kPair>
 __device__ __forceinline__ void issue_stage(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint64_t sa, uint64_t sb,
                                             uint64_t sb2, uint32_t sf, uint32_t sfb_col, int nk, bool accumulate) {
     static_assert(idesc_sf_id(2) == 0x40000020u, "scale-factor id of the second half of a word");
-    static_assert(kGroup == 1 || kSets == 2, "variants");
-    if constexpr (!kMx && kSets == 1)
+    if constexpr (!kMx && !kPair)
         asm volatile(LINEAR_BEGIN LINEAR_NV1("ep", "p0") LINEAR_STEP LINEAR_NEXT("4") LINEAR_NV1("e1", "p1") LINEAR_STEP
                          LINEAR_NEXT("4") LINEAR_NV1("e2", "p1") LINEAR_STEP LINEAR_NEXT("4") LINEAR_NV1("e3", "p1") "}"
                      LINEAR_OPERANDS);
-    else if constexpr (kSets == 1)
-        asm volatile(LINEAR_BEGIN "or.b32 i2, %3, 0x40000020;\n\t" LINEAR_MX1("ep", "e1", "p0") LINEAR_STEP LINEAR_NEXT("4")
+    else if constexpr (!kPair)
+        asm volatile(LINEAR_BEGIN LINEAR_ID2 LINEAR_MX1("ep", "e1", "p0") LINEAR_STEP LINEAR_NEXT("4")
                          LINEAR_MX1("e2", "e3", "p1") "}" LINEAR_OPERANDS);
-    else if constexpr (!kMx && kGroup == 1)
-        asm volatile(LINEAR_NV2_STAGE("1") LINEAR_OPERANDS);
     else if constexpr (!kMx)
-        asm volatile(LINEAR_NV2_STAGE("2") LINEAR_OPERANDS);
-    else if constexpr (kGroup == 1)
-        asm volatile(LINEAR_MX2_STAGE("1") LINEAR_OPERANDS);
+        asm volatile(LINEAR_BEGIN LINEAR_NV2("ep", "p0") LINEAR_STEP LINEAR_NEXT("8") LINEAR_NV2("e1", "p1") LINEAR_STEP
+                         LINEAR_NEXT("8") LINEAR_NV2("e2", "p1") LINEAR_STEP LINEAR_NEXT("8") LINEAR_NV2("e3", "p1") "}"
+                     LINEAR_OPERANDS);
     else
-        asm volatile(LINEAR_MX2_STAGE("2") LINEAR_OPERANDS);
+        asm volatile(LINEAR_BEGIN LINEAR_ID2 LINEAR_MX2("ep", "e1", "p0") LINEAR_STEP LINEAR_NEXT("8")
+                         LINEAR_MX2("e2", "e3", "p1") "}" LINEAR_OPERANDS);
 }
 #undef LINEAR_CP
 #undef LINEAR_MMA_NV
@@ -119,8 +113,7 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint64_t a, uint64_t b, 
 #undef LINEAR_NV2
 #undef LINEAR_MX1
 #undef LINEAR_MX2
-#undef LINEAR_NV2_STAGE
-#undef LINEAR_MX2_STAGE
+#undef LINEAR_ID2
 
 // ---- outputs
 

@@ -280,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t st = base + stage * S::bytes;
-                    issue_stage<kMx, 2, 2>(tmem, sdesc_k_swizzled<kRowBytes>(st), sdesc_k_swizzled<kRowBytes>(st + kHalfBytes),
+                    issue_stage<kMx, true>(tmem, sdesc_k_swizzled<kRowBytes>(st), sdesc_k_swizzled<kRowBytes>(st + kHalfBytes),
                                            idesc, sdesc_sf(st + S::sfa), sdesc_sf(st + S::sfb),
                                            sdesc_sf(st + S::sfb + S::tiles * kSfAtomBytes), tmem + kAccCols + stage * S::sf_cols, 0,
                                            min(kStageK / 64, (p.K - kStageK * ks + 63) / 64), ks != 0);

@@ -66,14 +66,19 @@ def check(x, w, mx, out_dtype=torch.float32, bias=None):
 
 @pytest.mark.parametrize("T,N,K", [(1, 1, 32), (1, 128, 64), (2, 31, 96), (16, 64, 128), (17, 33, 160), (31, 257, 288),
                                    (128, 256, 256), (129, 100, 512), (130, 1000, 320), (300, 520, 1056), (1, 5000, 2048),
-                                   (64, 2000, 4096), (700, 4100, 256), (2500, 2100, 192), (40, 9, 16384)])
+                                   (64, 2000, 4096), (700, 4100, 256), (2500, 2100, 192), (40, 9, 16384),
+                                   # few tokens, several tiles to an SM and more stages than fit; the same for many
+                                   (3, 33000, 544), (1, 12000, 8192), (2, 300, 8160), (16, 20000, 96), (4, 100, 8192),
+                                   (200, 20000, 288), (1000, 8200, 352), (3000, 5000, 1056)])
 def test_mxfp4_shapes(T, N, K):
     check(*make(T, N, K), True)
 
 
 @pytest.mark.parametrize("T,N,K", [(1, 1, 64), (1, 128, 128), (2, 31, 192), (16, 64, 256), (17, 33, 320), (31, 257, 448),
                                    (129, 100, 512), (130, 1000, 320), (300, 520, 1088), (1, 5000, 2048), (64, 2000, 4096),
-                                   (700, 4100, 256), (2500, 2100, 192), (40, 9, 8192)])
+                                   (700, 4100, 256), (2500, 2100, 192), (40, 9, 8192),
+                                   (3, 33000, 576), (1, 12000, 8192), (2, 300, 8128), (16, 20000, 128), (4, 100, 8192),
+                                   (200, 20000, 320), (1000, 8200, 320), (3000, 5000, 1088), (50, 70, 3136), (33, 64, 6080)])
 def test_nvfp4_shapes(T, N, K):
     check(*make(T, N, K), False)
 
@@ -88,9 +93,22 @@ def test_output_types_and_bias(mx, out_dtype, N):
     check(x, w, mx, out_dtype)
 
 
-@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
-def test_mxfp4_input_types(dtype):
-    check(*make(33, 200, 416, dtype), True)
+@pytest.mark.parametrize("mx", [True, False])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N", [2104, 2101, 2052])              # rows on 16-byte boundaries or not, ends inside a tile
+def test_output_types_of_many_tokens(mx, out_dtype, N):
+    x, w = make(2350, N, 320)
+    check(x, w, mx, out_dtype, torch.randn(N, device="cuda", generator=torch.Generator("cuda").manual_seed(N)))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T", [1, 9, 33])
+@pytest.mark.parametrize("offset,pitch", [(0, 2080), (8, 2104), (4, 2084), (3, 2085)])   # 32-, 16- and 8-byte aligned rows, odd ones
+def test_mxfp4_input_types(dtype, T, offset, pitch):
+    x, w = make(T, 200, 2080, dtype)
+    wide = torch.zeros((T, pitch + offset), dtype=dtype, device="cuda")
+    wide[:, offset:offset + 2080] = x
+    check(wide[:, offset:offset + 2080], w, True)
 
 
 @pytest.mark.parametrize("mx", [True, False])
@@ -104,13 +122,14 @@ def test_zero_rows_and_channels(mx):
 
 
 @pytest.mark.parametrize("mx", [True, False])
-def test_a_non_finite_row_stays_its_own(mx):
-    x, w = make(40, 96, 256)
+@pytest.mark.parametrize("T,N", [(9, 96), (40, 96), (2400, 2100)])      # each of the kernels
+def test_a_non_finite_row_stays_its_own(mx, T, N):
+    x, w = make(T, N, 256)
     want = linear(mx)(x, weight(w, mx))
     x[7, 100] = float("inf")
     got = linear(mx)(x, weight(w, mx))
     assert M.nvfp4_get_device_error() == 6
-    keep = [t for t in range(40) if t != 7]
+    keep = [t for t in range(T) if t != 7]
     assert torch.equal(got[keep], want[keep])
     if mx:
         assert bool(torch.isnan(got[7]).all())
