@@ -396,7 +396,7 @@ __device__ __forceinline__ void quantise_nv(const DecodeParams& p, int warp, int
         const int c = at * kCols + 16 * lane;
         if (q >= pieces || c >= p.K) continue;
         uint32_t w0, w1, scale;
-        nv_quantize16(v[i][0], v[i][1], row_g[r], w0, w1, scale);
+        nv_quantize16(v[i][0], v[i][1], __uint_as_float(block_absmax_bits(v[i][0], v[i][1])), nv_row(row_g[r]), w0, w1, scale);
         uint8_t* d = codes + c / kStageK * kChunkBytes + swizzled(r, (c & (kStageK - 1)) >> 3);
         *reinterpret_cast<uint2*>(d) = make_uint2(w0, w1);
         sf[c / 64 * kSfAtomBytes + r * 16 + ((c & 63) >> 4)] = static_cast<uint8_t>(scale);

@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(32 * kWarpsQ, 8)
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * kRows; base < rows; base += static_cast<int64_t>(gridDim.x) * kRows) {
         const int64_t r = base + slot;
         uint4 v[kHeld][2];
-        uint32_t top = 0u;
+        uint32_t top = 0u, block_top[kHeld];
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
             const int c = kBlock * (32 * (i * kWarpsPerRow + part) + lane);
@@ -42,7 +42,10 @@ __global__ void __launch_bounds__(32 * kWarpsQ, 8)
             }
         }
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) top = max(top, block_absmax_bits(v[i][0], v[i][1]));
+        for (int i = 0; i < kHeld; ++i) {
+            block_top[i] = block_absmax_bits(v[i][0], v[i][1]);
+            top = max(top, block_top[i]);
+        }
         top = __reduce_max_sync(0xFFFFFFFFu, top);
         if (kWarpsPerRow > 1) {
             if (lane == 0) s_top[turn][warp] = top;
@@ -58,12 +61,13 @@ __global__ void __launch_bounds__(32 * kWarpsQ, 8)
             g[r] = gr;
             if (!finite) set_device_error(err, NVFP4_ERR_NONFINITE);
         }
+        const NvRow row = nv_row(gr);
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
             const int c = kBlock * (32 * (i * kWarpsPerRow + part) + lane);
             if (c >= cols) continue;
             uint32_t w0, w1, scale;
-            nv_quantize16(v[i][0], v[i][1], gr, w0, w1, scale);
+            nv_quantize16(v[i][0], v[i][1], __uint_as_float(block_top[i]), row, w0, w1, scale);
             *reinterpret_cast<uint2*>(codes + r * (cols / 2) + c / 2) = make_uint2(w0, w1);
             sf[sf_offset(r, c / kBlock, cols)] = static_cast<uint8_t>(scale);
         }
