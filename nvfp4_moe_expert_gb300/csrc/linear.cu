@@ -3,14 +3,16 @@
 //   NVFP4: acc = sum_k (qa*sa)[t,k] (qb*sb)[n,k] (E4M3 scales per 16), out = (acc*ga[t])*gb[n] + bias
 //   MXFP4: acc = the same with E8M0 scales per 32 and no outer scales
 //
-// Three kernels, by the number of tokens and the tiles they make (launch_linear): for few tokens one that
-// quantises x itself, below; for many a pair of CTAs per tile (linear_pair.cu); between them the general one here.
+// Three kernels: for few elements of x one that quantises them itself, below (linear_quantises_x); for many tiles
+// a pair of CTAs to each (linear_pair.cu); between them the general one here (launch_linear chooses by time).
 //
-// General kernel (sm_103a): one CTA per SM walks the (128 tokens x BN outputs) tiles.  Warps 0 and 6 load the
-// stages' 512 K-elements of A and B through TMA (128B swizzle) with their 512-byte scale tiles; warp 1 copies the scales to
-// TMEM and issues the K=64 MMAs (M=128, N=BN) into one of two FP32 TMEM accumulators; warps 2-5 apply
-// the outer scales and the bias and write their rows.  All waits are bounded (NVFP4_ERR_DEVICE_TIMEOUT, then a
-// clean exit).
+// General kernel (sm_103a): one CTA per SM walks the (128 tokens x BN outputs) tiles.  Warps 0 and 6 load the stages'
+// 512 K-elements of A and B through TMA (128B swizzle) with their 512-byte scale tiles; warp 1 copies the scales to
+// TMEM and issues the K=64 MMAs (M=128, N=BN) into one of two FP32 TMEM accumulators; warps 2-5 apply the outer scales
+// and the bias and write their rows.  All waits are bounded (NVFP4_ERR_DEVICE_TIMEOUT, then a clean exit).
+//
+// What bounds it: the weights' bytes for few tokens (64 x 8192 x 8192 MXFP4, 37 MB: 10.1 us with the quantisation of
+// x, 3.7 TB/s), the way of the operands into the SM for more (512 x 4096 x 8192: 13.1 us, 2.6 PFLOP/s).
 //
 // K is walked 0..K-1 in 64-wide steps into one accumulator whatever the kernel and the tile, so a token's output
 // does not depend on how many tokens there are.
@@ -24,6 +26,7 @@ namespace {
 constexpr int kMaxStages = 8;
 constexpr int kPer = 2;                              // chunks of 256 K-elements per stage
 constexpr int kEpiWarps = 4;
+constexpr int kOutBuf = 2048;                        // an epilogue warp's 32 rows of 16 outputs
 constexpr int kWarpB = 2 + kEpiWarps;                // the producer of B
 constexpr int kThreads = 32 * (kWarpB + 1);
 
@@ -46,11 +49,13 @@ struct Params {
     int* err;
 };
 
-// BN outputs of row r from the accumulator's columns at taddr (this warp's lanes): outer scales
-// (ga: the row's), bias, one rounding.  gcol, bcol: the warp's 32 column values in shared memory.
+// BN outputs of `rows` rows from row0 on, a lane each, from the accumulator's columns at taddr: outer scales (ga: this
+// lane's row's), bias, one rounding.  gcol, bcol: the warp's 32 column values, in shared memory.  buf: 2 KB of it for
+// outputs row by row where rows lie on no 16-byte boundary; nullptr: each lane its own row all the same, which is
+// faster for the few rows of linear_decode_kernel (16 x 8191 x 2048 6.4 and 7.5 us).
 template <bool kMx, int BN, typename P>
-__device__ __forceinline__ void epilogue_row(uint32_t taddr, bool live, int64_t r, int n0, float ga, const P& p, float* gcol,
-                                             float* bcol) {
+__device__ __forceinline__ void epilogue_rows(uint32_t taddr, int64_t row0, int rows, int n0, float ga, const P& p,
+                                              float* gcol, float* bcol, uint8_t* buf) {
     const int lane = threadIdx.x & 31;
 #pragma unroll 1
     for (int c = 0; c < BN; c += 32) {
@@ -62,7 +67,16 @@ __device__ __forceinline__ void epilogue_row(uint32_t taddr, bool live, int64_t 
         bcol[lane] = p.bias != nullptr && n < p.N ? __ldg(p.bias + n) : 0.0f;
         __syncwarp();
         tmem_ld_wait();
-        if (live && n0 + c < p.N) write_outputs<kMx, 32>(v, ga, gcol, bcol, r, n0 + c, p);
+        if (n0 + c >= p.N || rows <= 0) continue;     // the whole warp
+        if (p.align > 0 || buf == nullptr) {
+            if (lane < rows) write_outputs<kMx, 32>(v, ga, gcol, bcol, row0 + lane, n0 + c, p);
+        } else if (p.out_type == NVFP4_TYPE_BF16) {
+            write_by_row<kMx, __nv_bfloat16, 32, 16>(v, ga, gcol, bcol, buf, row0, n0 + c, rows, p);
+        } else if (p.out_type == NVFP4_TYPE_F32) {
+            write_by_row<kMx, float, 32, 16>(v, ga, gcol, bcol, buf, row0, n0 + c, rows, p);
+        } else {
+            write_by_row<kMx, __half, 32, 16>(v, ga, gcol, bcol, buf, row0, n0 + c, rows, p);
+        }
     }
 }
 
@@ -81,6 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
     __shared__ __align__(8) float s_col[kEpiWarps][2][32];
+    __shared__ __align__(16) uint8_t s_out[kEpiWarps][kOutBuf];
     volatile int* abort_flag = &abort_word;
     const int warp = warp_index(), lane = threadIdx.x & 31;
     // a stage: A's chunks, B's chunks, then their scale tiles
@@ -224,10 +239,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x) {
-            const int64_t r = t / p.n_tiles * kBM + q * 32 + lane;
+            const int64_t row0 = t / p.n_tiles * kBM + q * 32;
             const int n0 = static_cast<int>(t % p.n_tiles) * BN;
-            const bool live = r < p.T;
-            const float ga = !kMx && live ? __ldg(p.a_g + r) : 1.0f;
+            const int rows = static_cast<int>(min(p.T - row0, static_cast<int64_t>(32)));
+            const float ga = !kMx && lane < rows ? __ldg(p.a_g + row0 + lane) : 1.0f;
             const bool ok = mbar_wait_bounded(&tmem_full[acc], acc_phase, abort_flag, kWaitBudgetCycles);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 if (lane == 0) set_device_error(p.err, NVFP4_ERR_DEVICE_TIMEOUT);
@@ -236,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const uint32_t taddr = tmem + acc * kN + (n0 & (kN - BN)) + (static_cast<uint32_t>(q * 32) << 16);
-            epilogue_row<kMx, BN>(taddr, live, r, n0, ga, p, s_col[warp - 2][0], s_col[warp - 2][1]);
+            epilogue_rows<kMx, BN>(taddr, row0, rows, n0, ga, p, s_col[warp - 2][0], s_col[warp - 2][1], s_out[warp - 2]);
             tc_fence_before();
             mbar_arrive(&tmem_empty[acc]);
             if (++acc == 2) {
@@ -492,7 +507,8 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 uint8_t* b = stages + stage * kStageBytes;
                 uint8_t* box = b + (n0 & (kN - BN)) * kRowBytes;
                 const int chunks = min(kPerD, num_ks - kPerD * st);
-                const uint32_t sf_bytes = static_cast<uint32_t>(min(kPerD * F::tiles, sf_tiles - kPerD * F::tiles * st)) * kSfAtomBytes;
+                const uint32_t sf_bytes =
+                    static_cast<uint32_t>(min(kPerD * F::tiles, sf_tiles - kPerD * F::tiles * st)) * kSfAtomBytes;
                 load_operand_elect(&full[stage], chunks * BN * kRowBytes + sf_bytes, box, &tmB, kPerD * st * kRowBytes, n0,
                                    b + kPerD * kBBytes, bsf + kPerD * F::tiles * st * kSfAtomBytes, sf_bytes, pol);
                 for (int i = 1; i < chunks; ++i)
@@ -552,8 +568,8 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                     issue_stage<kMx, false>(tmem + acc * kN, sdesc_k_swizzled<kRowBytes>(a_base + ks * kChunkBytes),
                                         sdesc_k_swizzled<kRowBytes>(b + i * kBBytes), idesc,
                                         sdesc_sf(a_sf_base + ks * kSfBytes), sdesc_sf(b + kPerD * kBBytes + i * kSfBytes), 0,
-                                        sf0 + (kPerD * stage + i) * kSfCols, sfb_col, min(kStageK / 64, (p.K - kStageK * ks + 63) / 64),
-                                        ks != 0);
+                                        sf0 + (kPerD * stage + i) * kSfCols, sfb_col,
+                                        min(kStageK / 64, (p.K - kStageK * ks + 63) / 64), ks != 0);
                 }
                 issued_any = true;
                 if (reused) tc_commit_elect(&empty[stage]);
@@ -594,7 +610,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                     break;
                 }
                 tc_fence_after();
-                epilogue_row<kMx, BN>(tmem + acc * kN + (n0 & (kN - BN)), lane < p.T, lane, n0, ga, p, s_col[0], s_col[1]);
+                epilogue_rows<kMx, BN>(tmem + acc * kN + (n0 & (kN - BN)), 0, p.T, n0, ga, p, s_col[0], s_col[1], nullptr);
                 tc_fence_before();
                 mbar_arrive(&tmem_empty[acc]);
                 if (++acc == 2) {
@@ -716,8 +732,9 @@ bool linear_quantises_x(bool mx, int64_t T, int64_t K) {
 }
 
 cudaError_t launch_linear_x(const LinearInput& x, const LinearArgs& a, cudaStream_t st) {
-    // a tile takes the time of its MMAs' issue, about the same for 32 and 64 outputs and a fifth more
-    // for 128: the narrowest tile that needs the fewest rounds over the SMs
+    // A tile takes the time of its MMAs' issue, about the same for 32 and 64 outputs and a fifth more for 128: the
+    // narrowest tile that needs one round over the SMs, or the widest.  One token MXFP4, tiles 32, 64 and 128 wide:
+    // 4096 x 4096 5.3, 5.5 and 6.5 us, 8192 x 4096 8.4, 5.9 and 6.6, 20000 x 2048 9.7, 7.1 and 6.7.
     const int sms = device_sm_count();
     if (a.N <= 32 * sms) return a.mx ? launch_decode<true, 32>(x, a, st) : launch_decode<false, 32>(x, a, st);
     if (a.N <= 64 * sms) return a.mx ? launch_decode<true, 64>(x, a, st) : launch_decode<false, 64>(x, a, st);
@@ -725,17 +742,33 @@ cudaError_t launch_linear_x(const LinearInput& x, const LinearArgs& a, cudaStrea
 }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st, bool pdl) {
-    // The kernel and tile with the least time: rounds over the SMs (or pairs of them) times the cycles of a
-    // 256-element chunk of K, which is the larger of its MMAs (240 cycles for N = 64, 310 for 128) and its
-    // operands' way into the SM (about 2.4 cycles a row of 128 bytes); a pair's chunk takes 560.
-    const int64_t sms = device_sm_count(), m = (a.T + kBM - 1) / kBM;
+    // The kernel and tile with the least time, in cycles: over the SMs (or pairs of them) a round of tiles takes the
+    // longer of its main loop and its outputs, and one of each is left at the ends.  A 256-element chunk of K takes the
+    // larger of its MMAs (240 for N = 64, 310 for 128) and its operands' way into the SM (about 2.4 a row of 128
+    // bytes), in a pair 560; a tile's outputs 700 and 22 a column, 93 row by row, a pair's 4500 or 9600.  Both sides,
+    // us of MXFP4 with the quantisation of x (* the rule's):
+    //                         32      64      128     pair
+    //   300 x 1536 x 2048     6.1 *   6.1     6.8     8.6
+    //   256 x 4096 x 4096    10.7     7.7 *   8.8    10.7
+    //   512 x 4096 x 4096    17.3    10.9     9.2 *  10.9
+    //   700 x 4096 x 4096    23.6    14.3    13.0    11.2 *
+    //   4096 x 4096 x 4096   94.1    51.8    36.4    29.9 *
+    //   5000 x 2048 x 512    14.7    11.9    11.2     9.4 *
+    //   300 x 1533 x 2048     7.0 *   8.3    11.1    10.8     rows on no 16-byte boundary
+    //   8192 x 1999 x 2048   58.2    54.9    51.9    28.1 *   the same
+    const int64_t sms = device_sm_count(), m = (a.T + kBM - 1) / kBM, num_ks = (a.K + kStageK - 1) / kStageK;
     const int rows = rows_of_a(a.T);
-    auto cost = [&](int64_t tiles, int64_t at_once, int chunk) { return (tiles + at_once - 1) / at_once * chunk; };
-    auto chunk = [&](int bn, int mma) { return 12 * (rows + bn) / 5 > mma ? 12 * (rows + bn) / 5 : mma; };
-    const int64_t c32 = cost(m * ((a.N + 31) / 32), sms, chunk(32, 240));
-    const int64_t c64 = cost(m * ((a.N + 63) / 64), sms, chunk(64, 240));
-    const int64_t c128 = cost(m * ((a.N + 127) / 128), sms, chunk(128, 310));
-    const int64_t cpair = cost((a.T + 255) / 256 * ((a.N + 255) / 256), linear_pair_count(), 560);
+    const bool wide = out_align(a) > 0;
+    auto cost = [](int64_t tiles, int64_t at_once, int64_t main, int64_t out) {
+        return (tiles + at_once - 1) / at_once * (main > out ? main : out) + (main > out ? out : main);
+    };
+    auto one = [&](int bn, int mma) {
+        const int load = 12 * (rows + bn) / 5;
+        return cost(m * ((a.N + bn - 1) / bn), sms, num_ks * (load > mma ? load : mma), 700 + bn * (wide ? 22 : 93));
+    };
+    const int64_t c32 = one(32, 240), c64 = one(64, 240), c128 = one(128, 310);
+    const int64_t pair_tiles = (a.T + 255) / 256 * ((a.N + 255) / 256);
+    const int64_t cpair = cost(pair_tiles, linear_pair_count(), num_ks * 560 + 800, wide ? 4500 : 9600);
     if (cpair <= c32 && cpair <= c64 && cpair <= c128) return launch_linear_pair(a, st, pdl);
     if (c128 <= c64 && c128 <= c32) return a.mx ? launch<true, 128>(a, st, pdl) : launch<false, 128>(a, st, pdl);
     if (c64 <= c32) return a.mx ? launch<true, 64>(a, st, pdl) : launch<false, 64>(a, st, pdl);

@@ -19,7 +19,7 @@ constexpr int kRowBytes = 128;                       // bytes of K per row and s
 constexpr int kStageK = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemLimit = 227 * 1024;
-constexpr int kFixedBytes = 4096;                    // column data, barriers, alignment slack
+constexpr int kFixedBytes = 10240;                   // room left for static shared memory
 
 // A value all lanes hold, taken from lane 0: the compiler then knows that it is the same in all of them.
 // Roles chosen by such a warp index, and descriptors made of such values, stay on the uniform
@@ -48,10 +48,11 @@ __host__ __device__ constexpr uint32_t idesc_fp4(bool mx, int M, int N) {
 // Scale-factor ids: which byte pair of a 4-byte scale word an MXFP4 MMA uses (0 or 2).
 __host__ __device__ constexpr uint32_t idesc_sf_id(uint32_t id) { return (id << 4) | (id << 29); }
 
-// One stage of the main loop, in one block of PTX with one elect.sync: the scale tiles go to TMEM
-// (columns sf .. , A's first, then B's, one set of 128 rows or, by a pair of CTAs, two), then nk <= 4 K=64 MMAs accumulate into d.
-// sa, sb, sb2: descriptors of the scale tiles of A and of B's first and second 128 rows (the next tile
-// 512 bytes, 32 units, further); a K step is 32 bytes (2 units) of the operands' rows.  (As twelve separately elected instructions a stage took 730-800 cycles to issue.)
+// One stage of the main loop, in one block of PTX with one elect.sync: the scale tiles go to TMEM (from column sf on,
+// A's first, then B's, one set of 128 rows or, by a pair of CTAs, two), then nk <= 4 K=64 MMAs accumulate into d.
+// sa, sb, sb2: descriptors of the scale tiles of A and of B's first and second 128 rows (the next tile 512 bytes, 32
+// units, further); a K step is 32 bytes (2 units) of the operands' rows.  (As twelve separately elected instructions
+// a stage took 730-800 cycles to issue, so 260.)
 #define LINEAR_CP(G, P, dst, src) "@" P " tcgen05.cp.cta_group::" G ".32x128b.warpx4 [" dst "], " src ";\n\t"
 #define LINEAR_MMA_NV(G, P, acc, sfb)                                                                        \
     "@" P " tcgen05.mma.cta_group::" G ".kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %3, [ca], [" sfb "], " acc ";\n\t"
@@ -156,20 +157,20 @@ __device__ __forceinline__ void pack16(const uint64_t (&v)[8], uint32_t (&w)[4 *
 }
 
 // 16 consecutive outputs of a row, of which the first `n` exist.  align: 2 where rows lie on 32-byte
-// boundaries (whole sectors in one store), 1 on 16-byte ones, 0 otherwise.
+// boundaries (whole sectors in one store), 1 on 16-byte ones, less otherwise.
 template <typename T>
 __device__ __forceinline__ void store16(T* p, const uint64_t (&v)[8], int n, int align) {
     constexpr int kWords = 4 * sizeof(T);
     uint32_t w[kWords];
     pack16<T>(v, w);
-    if (n >= 16 && align == 2) {
+    if (n >= 16 && align > 1) {
 #pragma unroll
         for (int i = 0; i < kWords; i += 8)
             asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint32_t*>(p) + i),
                          "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
                          "r"(w[i + 7])
                          : "memory");
-    } else if (n >= 16 && align == 1) {
+    } else if (n >= 16 && align > 0) {
 #pragma unroll
         for (int i = 0; i < kWords; i += 4)
             *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
@@ -182,6 +183,11 @@ __device__ __forceinline__ void store16(T* p, const uint64_t (&v)[8], int n, int
         }
     }
 }
+
+// Byte of 16-byte chunk c of row r among rows of kRow bytes in shared memory: eight rows' same chunk lie in eight
+// different banks' groups.
+template <int kRow>
+__device__ __forceinline__ int row_chunk(int r, int c) { return (c ^ (r / (128 / kRow) & (kRow / 16 - 1))) << 4; }
 
 // 16 outputs from a lane's accumulator values: NVFP4 outer scales (g2: the row's twice, gcol: the
 // columns'), the bias (bcol) if there is one.  gcol, bcol: 8-byte aligned shared memory.
@@ -208,6 +214,59 @@ __device__ __forceinline__ void outputs(const uint32_t* v, float ga, const float
         store16<T>(row + h, o, left - h, align);
     }
 }
+// The same for a warp's `rows` rows (this lane's: v) where rows lie on no 16-byte boundary: kPass columns at a time
+// through the warp's shared memory (buf, 32 rows of kPass outputs in swizzled 16-byte chunks) and from there row by
+// row, in 4-byte words where rows lie on such boundaries.  (With each lane storing its own row, 32 sectors to an
+// instruction, the MXFP4 product of 8192 x 1999 x 2048 took 173 us instead of 28.)  left: columns that exist.
+template <typename U, typename T, int kPass>
+__device__ __forceinline__ void copy_rows(const uint8_t* buf, T* out, int64_t ldo, int rows, int left) {
+    constexpr int kRow = kPass * sizeof(T), kUnits = kRow / sizeof(U), kEach = sizeof(U) / sizeof(T);
+    const int lane = threadIdx.x & 31;
+#pragma unroll 4
+    for (int i = lane; i < rows * kUnits; i += 32) {
+        const int r = i / kUnits, u = i % kUnits, at = u * sizeof(U), col = u * kEach;
+        const U v = *reinterpret_cast<const U*>(buf + r * kRow + row_chunk<kRow>(r, at / 16) + at % 16);
+        T* dst = out + r * ldo + col;
+        if (col + kEach <= left) *reinterpret_cast<U*>(dst) = v;
+        else if (kEach > 1 && col < left) *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(v);
+    }
+}
+template <bool kMx, bool kBias, typename T, int kCols, int kPass>
+__device__ __forceinline__ void outputs_by_row(const uint32_t* v, float ga, const float* gcol, const float* bcol, uint8_t* buf,
+                                               T* out, int64_t ldo, int rows, int left, bool words) {
+    constexpr int kRow = kPass * sizeof(T), kChunks = sizeof(T);   // 16-byte chunks of 16 columns
+    const int lane = threadIdx.x & 31;
+    const uint64_t g2 = pair(ga, ga);
+#pragma unroll
+    for (int c = 0; c < kCols; c += kPass) {
+        if (left <= c) break;
+        __syncwarp();                                 // the last columns have been read
+#pragma unroll
+        for (int h = 0; h < kPass; h += 16) {
+            uint64_t o[8];
+            scale16<kMx, kBias>(v + c + h, g2, gcol + c + h, bcol + c + h, o);
+            uint32_t w[4 * kChunks];
+            pack16<T>(o, w);
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i)
+                *reinterpret_cast<uint4*>(buf + lane * kRow + row_chunk<kRow>(lane, h / 16 * kChunks + i)) =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+        __syncwarp();
+        if (sizeof(T) == 4 || words) copy_rows<uint32_t, T, kPass>(buf, out + c, ldo, rows, left - c);
+        else copy_rows<uint16_t, T, kPass>(buf, out + c, ldo, rows, left - c);
+    }
+}
+template <bool kMx, typename T, int kCols, int kPass, typename P>
+__device__ __forceinline__ void write_by_row(const uint32_t* v, float ga, const float* gcol, const float* bcol, uint8_t* buf,
+                                             int64_t row0, int n0, int rows, const P& p) {
+    T* out = static_cast<T*>(p.out) + row0 * p.ldo + n0;
+    if (p.bias)
+        outputs_by_row<kMx, true, T, kCols, kPass>(v, ga, gcol, bcol, buf, out, p.ldo, rows, p.N - n0, p.align >= 0);
+    else
+        outputs_by_row<kMx, false, T, kCols, kPass>(v, ga, gcol, bcol, buf, out, p.ldo, rows, p.N - n0, p.align >= 0);
+}
+
 template <bool kMx, int kCols, typename P>
 __device__ __forceinline__ void write_outputs(const uint32_t* v, float ga, const float* gcol, const float* bcol, int64_t r,
                                               int n0, const P& p) {
@@ -309,10 +368,10 @@ cudaError_t prepare(void (*kernel)(A...), int bytes, bool (&ready)[kMaxDevices])
     return cudaSuccess;
 }
 
-// Rows of out lie on 32-byte (2) or 16-byte (1) boundaries, or neither (0).
+// Rows of out lie on 32-byte (2), 16-byte (1), 4-byte (0) or 2-byte (-1) boundaries.
 int out_align(const LinearArgs& a) {
     const int64_t bits = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.out)) | (a.ldo * (a.out_type == NVFP4_TYPE_F32 ? 4 : 2));
-    return bits % 32 == 0 ? 2 : bits % 16 == 0 ? 1 : 0;
+    return bits % 32 == 0 ? 2 : bits % 16 == 0 ? 1 : bits % 4 == 0 ? 0 : -1;
 }
 
 }  // namespace

@@ -50,12 +50,16 @@ struct PairParams {
     int out_type;
     int64_t ldo;
     int align;            // of out's rows: out_align()
-    int staged;           // outputs go through the tensor map tmOut
     int n_tiles;
     int64_t tiles;
     int* err;
 };
 
+__device__ __forceinline__ uint32_t cycles32() {
+    uint32_t c;
+    asm volatile("mov.u32 %0, %%clock;" : "=r"(c));
+    return c;
+}
 __device__ __forceinline__ uint32_t cta_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -120,8 +124,7 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar) {
 }
 
 // A warp's 64 columns at n0 of the 32 rows at row0 (this lane's: accumulator values v) through its
-// shared-memory buffer: rows of 128 bytes, 128B swizzle, one TMA store for 64 16-bit or 32 FP32 columns;
-// what lies past T or N is not written.
+// shared-memory buffer: rows of 128 bytes, 128B swizzle, one TMA store for 64 16-bit or 32 FP32 columns.
 template <bool kMx, bool kBias, typename T>
 __device__ __forceinline__ void outputs_staged(const uint32_t* v, float ga, const float* gcol, const float* bcol, uint8_t* buf,
                                                const CUtensorMap* map, int n0, int row0, int N) {
@@ -163,7 +166,8 @@ __device__ __forceinline__ void outputs_staged(const uint32_t* v, float ga, cons
     else outputs_staged<kMx, false, T>(v, ga, gcol, bcol, buf, map, n0, row0, p.N);
 }
 
-template <bool kMx>
+// kStaged: outputs go through the tensor map tmOut, otherwise row by row (write_by_row).
+template <bool kMx, bool kStaged>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmSfa, const __grid_constant__ CUtensorMap tmSfb,
@@ -310,14 +314,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint32_t taddr = tmem + 64 * sub + (static_cast<uint32_t>(q * 32) << 16);
         const uint32_t empty_bar = leader_addr(&tmem_empty);
         float* gcol = s_col[warp - 4][0];
-        float* bcol = s_col[warp - 4][1];
+        float* bcol = gcol + 64;
         uint8_t* buf = smem + S::out + (warp - 4) * kOutBytes;
         uint32_t acc_phase = 0;
         for (int64_t t = first; t < p.tiles; t += step) {
-            const int64_t r = t / p.n_tiles * 256 + 128 * rank + q * 32 + lane;
+            const int row0 = static_cast<int>(t / p.n_tiles) * 256 + 128 * static_cast<int>(rank) + q * 32;
             const int n0 = static_cast<int>(t % p.n_tiles) * kPairN + 64 * sub;
-            const bool live = r < p.T;
-            const float ga = !kMx && live ? __ldg(p.a_g + r) : 1.0f;
+            const float ga = !kMx && row0 + lane < p.T ? __ldg(p.a_g + row0 + lane) : 1.0f;
             __syncwarp();
 #pragma unroll
             for (int h = 0; h < 64; h += 32) {
@@ -341,19 +344,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_leader(empty_bar);
-            if (p.staged) {
-                if (r - lane >= p.T) continue;         // the whole warp
-                // the column quarters' stores spread over the next tile's main loop (about half of it): all at
-                // once, in every SM at about the same time, they hold its loads up (8192^3 MXFP4 189 -> 185 us,
-                // 32768 x 4096 x 1536 NVFP4 121 -> 115.5 us; spread over all of it 190 and 115.4)
-                const long long until = clock64() + static_cast<long long>(sub) * num_ks * 64;
-                while (clock64() < until) __nanosleep(64);
-                const int row0 = static_cast<int>(r - lane);
+            if (row0 >= p.T || n0 >= p.N) continue;    // the whole warp
+            // the column quarters' stores spread over the next tile's main loop (about half of it), if there is one:
+            // all at once, in every SM at about the same time, they hold its loads up (8192^3 MXFP4 189 -> 185 us,
+            // 32768 x 4096 x 1536 NVFP4 121 -> 115.5 us; spread over all of it 190 and 115.4)
+            if (t + step < p.tiles) {
+                const uint32_t start = cycles32();
+                while (cycles32() - start < static_cast<uint32_t>(sub * num_ks * 64)) __nanosleep(64);
+            }
+            if constexpr (kStaged) {
                 if (p.out_type == NVFP4_TYPE_BF16) outputs_staged<kMx, __nv_bfloat16>(v, ga, gcol, bcol, buf, &tmOut, n0, row0, p);
                 else if (p.out_type == NVFP4_TYPE_F32) outputs_staged<kMx, float>(v, ga, gcol, bcol, buf, &tmOut, n0, row0, p);
                 else outputs_staged<kMx, __half>(v, ga, gcol, bcol, buf, &tmOut, n0, row0, p);
-            } else if (live && n0 < p.N) {
-                write_outputs<kMx, 64>(v, ga, gcol, bcol, r, n0, p);
+            } else {
+                const int rows = static_cast<int>(min(p.T - row0, static_cast<int64_t>(32)));
+                if (p.out_type == NVFP4_TYPE_BF16)
+                    write_by_row<kMx, __nv_bfloat16, 64, 64>(v, ga, gcol, bcol, buf, row0, n0, rows, p);
+                else if (p.out_type == NVFP4_TYPE_F32)
+                    write_by_row<kMx, float, 64, 32>(v, ga, gcol, bcol, buf, row0, n0, rows, p);
+                else
+                    write_by_row<kMx, __half, 64, 64>(v, ga, gcol, bcol, buf, row0, n0, rows, p);
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -384,11 +394,11 @@ bool make_out_map(CUtensorMap* m, const LinearArgs& a) {
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kMx>
+template <bool kMx, bool kStaged>
 cudaError_t launch_pair(const LinearArgs& a, cudaStream_t st, bool pdl) {
     using S = PairStage<kMx>;
     static bool ready[kMaxDevices];
-    cudaError_t e = prepare(linear_pair_kernel<kMx>, S::dynamic, ready);
+    cudaError_t e = prepare(linear_pair_kernel<kMx, kStaged>, S::dynamic, ready);
     if (e != cudaSuccess) return e;
     PairParams p{};
     p.T = a.T;
@@ -406,15 +416,14 @@ cudaError_t launch_pair(const LinearArgs& a, cudaStream_t st, bool pdl) {
     p.tiles = (a.T + 255) / 256 * p.n_tiles;
     const int64_t sf_tiles = (a.K + Format<kMx>::tile_k - 1) / Format<kMx>::tile_k;
     CUtensorMap ma, mb, msa, msb, mo = {};
-    p.staged = p.align != 0;
-    if (p.staged && !make_out_map(&mo, a)) return cudaErrorInvalidValue;
+    if (kStaged && !make_out_map(&mo, a)) return cudaErrorInvalidValue;
     if (!make_map(&ma, a.a_codes, a.T, a.K / 2, 128) || !make_map(&mb, a.b_codes, a.N, a.K / 2, 128) ||
         !make_sf_map(&msa, a.a_sf, (a.T + 127) / 128, sf_tiles, S::tiles, 1) ||
         !make_sf_map(&msb, a.b_sf, (a.N + 127) / 128, sf_tiles, S::tiles, 2))
         return cudaErrorInvalidValue;
     const int64_t pairs = linear_pair_count();
     const unsigned grid = static_cast<unsigned>(2 * (p.tiles < pairs ? p.tiles : pairs));
-    return launch_pdl(pdl, linear_pair_kernel<kMx>, grid, kPairThreads, S::dynamic, st, ma, mb, msa, msb, mo, p);
+    return launch_pdl(pdl, linear_pair_kernel<kMx, kStaged>, grid, kPairThreads, S::dynamic, st, ma, mb, msa, msb, mo, p);
 }
 
 }  // namespace
@@ -425,7 +434,7 @@ int linear_pair_count() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 1;
     static bool ready[kMaxDevices];
-    if (prepare(linear_pair_kernel<false>, PairStage<false>::dynamic, ready) != cudaSuccess) return 1;
+    if (prepare(linear_pair_kernel<false, true>, PairStage<false>::dynamic, ready) != cudaSuccess) return 1;
     std::lock_guard<std::mutex> lock(g_linear_mutex);
     if (!count[dev]) {
         cudaLaunchConfig_t cfg = {};
@@ -433,14 +442,17 @@ int linear_pair_count() {
         cfg.blockDim = kPairThreads;
         cfg.dynamicSmemBytes = PairStage<false>::dynamic;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel<false>, &cfg) != cudaSuccess || n < 1) n = device_sm_count() / 2;
+        if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel<false, true>, &cfg) != cudaSuccess || n < 1) n = device_sm_count() / 2;
         count[dev] = n < 1 ? 1 : n;
     }
     return count[dev];
 }
 
 cudaError_t launch_linear_pair(const LinearArgs& a, cudaStream_t st, bool pdl) {
-    return a.mx ? launch_pair<true>(a, st, pdl) : launch_pair<false>(a, st, pdl);
+    // A TMA store writes whole 16-byte units: of a row that ends inside one it would also write what lies behind.
+    const bool staged = out_align(a) > 0 && static_cast<int64_t>(a.N) * (a.out_type == NVFP4_TYPE_F32 ? 4 : 2) % 16 == 0;
+    if (staged) return a.mx ? launch_pair<true, true>(a, st, pdl) : launch_pair<false, true>(a, st, pdl);
+    return a.mx ? launch_pair<true, false>(a, st, pdl) : launch_pair<false, false>(a, st, pdl);
 }
 
 }  // namespace nvfp4

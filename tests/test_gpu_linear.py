@@ -173,6 +173,23 @@ def test_strides_and_given_output(mx):
 
 
 @pytest.mark.parametrize("mx", [True, False])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,N", [(5, 95), (40, 95), (300, 77), (2350, 2051)])          # each of the kernels
+def test_output_rows_on_every_boundary(mx, out_dtype, T, N):
+    x, w = make(T, N, 256)
+    wq = weight(w, mx)
+    bias = torch.randn(N, device="cuda", generator=torch.Generator("cuda").manual_seed(N))
+    want = linear(mx)(x, wq, bias=bias, out_dtype=out_dtype)
+    # row pitches and starts of an odd number of elements, of two, of four, of eight and sixteen
+    for lo, pitch in ((0, N + 4 - N % 4), (1, N + 2), (2, N + 4 - N % 2), (3, N + 9), (4, N + 24 - N % 8), (16, N + 48 - N % 16)):
+        out = torch.full((T, pitch), 7.0, dtype=out_dtype, device="cuda")
+        assert torch.equal(linear(mx)(x, wq, bias=bias, out=out[:, lo:lo + N]), want)
+        rest = torch.ones(pitch, dtype=torch.bool, device="cuda")
+        rest[lo:lo + N] = False
+        assert bool((out[:, rest] == 7.0).all())
+
+
+@pytest.mark.parametrize("mx", [True, False])
 def test_refusals(mx):
     x, w = make(4, 32, 128)
     wq = weight(w, mx)
