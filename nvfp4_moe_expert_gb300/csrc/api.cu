@@ -668,7 +668,7 @@ bool route_params_ok(const moe_route_params& p, int E) {
 }
 
 RouteParams route_params(const moe_route_params& p) {
-    return {p.score, p.k, p.n_group, p.topk_group, p.group_score, p.renormalize, p.scale, 0, 0};
+    return {p.score, p.k, p.n_group, p.topk_group, p.group_score, p.renormalize, p.scale, 0, 0, 0};
 }
 
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 256;

@@ -11,6 +11,7 @@ struct RouteParams {
     float scale;
     // set by the launcher
     int group_lanes;   // lanes of a group, 0 if a group is no power of two of whole lanes
+    int group_share;   // log2 of the lanes that search a group of any other size
     int bias_wide;     // bias lies on a 16-byte boundary
 };
 

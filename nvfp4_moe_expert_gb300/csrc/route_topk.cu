@@ -117,13 +117,15 @@ __device__ __forceinline__ float order_sigmoid(float l) {
 // keys), the picks are taken one by one.
 //
 // Bound by instructions: 525 to a token of 256 experts in 8 groups with a bias, beside the 1 KB that is read (65537 of
-// them take 40 us; 121 at first, with one reduction and a search of all keys for each pick; 70 with each lane's keys sorted; 47
-// with one token to a warp; 52 with 8 lanes and 32 experts to a lane, whose registers leave too few warps).
+// them take 40 us; 121 at first, with one reduction and a search of all keys for each pick; 70 with each lane's keys
+// sorted; 47 with one token to a warp; 52 with 8 lanes and 32 experts to a lane, whose registers leave too few warps).
+// Groups that are not whole lanes cost a third more (8 of 31: 54 us; 84 with a lane to a group).
 template <int V, int kLanes>
 struct Shared {
     static constexpr int tokens = 32 / kLanes;
     static constexpr int pitch = V + 4;                        // words of a lane's keys: 16-byte words without bank conflicts
-    __align__(16) uint32_t key[tokens][kLanes * pitch];
+    static constexpr int pad = kLanes < 32 ? kLanes : 0;       // and the tokens' consecutive words
+    __align__(16) uint32_t key[tokens][kLanes * pitch + pad];
     __align__(16) unsigned long long cand[tokens][32];
     int id[tokens][32];
 };
@@ -160,17 +162,38 @@ __global__ void __launch_bounds__(32 * kWarps)
 
     // the logits, -inf where there is no expert; a row of finite ones needs none of the checks for masks
     float l[V], probe = 0.0f;
-    if (e0 + V <= E) {
+    uint32_t* my_keys = sh.key[slot] + sub * kPitch;
+    if constexpr (kN > 1) {
 #pragma unroll
-        for (int i = 0; i < V; i += kN) load_vec<T, kN>(row + e0 + i, *reinterpret_cast<float(*)[kN]>(l + i));
+        for (int i = 0; i < V; i += kN) {
+            if (e0 + i + kN <= E) {
+                load_vec<T, kN>(row + e0 + i, *reinterpret_cast<float(*)[kN]>(l + i));
+            } else {
+#pragma unroll
+                for (int j = i; j < i + kN; ++j) l[j] = e0 + j < E ? load_one(row + e0 + j) : -INFINITY;
+            }
+        }
+    } else {
+        // rows on no such boundary: side by side from memory, each lane's own from shared memory (65537 x 251 in FP32
+        // 33 us, 48 with each lane's own from memory)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = sub + kLanes * i;
+            sh.key[slot][e / V * kPitch + e % V] = __float_as_uint(e < E ? load_one(row + e) : -INFINITY);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(my_keys + i);
+            l[i] = w.x, l[i + 1] = w.y, l[i + 2] = w.z, l[i + 3] = w.w;
+        }
+    }
+    if (e0 + V <= E) {
 #pragma unroll
         for (int i = 0; i < V; ++i) probe = fmaf(l[i], 0.0f, probe);
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            l[i] = e0 + i < E ? load_one(row + e0 + i) : -INFINITY;
-            probe = fmaf(e0 + i < E ? l[i] : 0.0f, 0.0f, probe);
-        }
+        for (int i = 0; i < V; ++i) probe = fmaf(e0 + i < E ? l[i] : 0.0f, 0.0f, probe);
     }
     const bool clean = __all_sync(kAll, probe == 0.0f);
     if (!clean) {
@@ -229,19 +252,17 @@ __global__ void __launch_bounds__(32 * kWarps)
             for (int i = 0; i < V; ++i) o[i] = order_sigmoid(o[i]);
         }
         if (bias != nullptr) {
-            if (e0 + V <= E && p.bias_wide) {
 #pragma unroll
-                for (int i = 0; i < V; i += 4) {
-                    float b[4];
+            for (int i = 0; i < V; i += 4) {
+                float b[4];
+                if (p.bias_wide && e0 + i + 4 <= E) {
                     load_vec<float, 4>(bias + e0 + i, b);
+                } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[i + j] = fmaxf(o[i + j] + b[j], -INFINITY);   // a NaN bias: -inf
+                    for (int j = 0; j < 4; ++j) b[j] = e0 + i + j < E ? __ldg(bias + e0 + i + j) : 0.0f;
                 }
-            } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    if (e0 + i < E) o[i] = fmaxf(o[i] + __ldg(bias + e0 + i), -INFINITY);
-                }
+                for (int j = 0; j < 4; ++j) o[i + j] = fmaxf(o[i + j] + b[j], -INFINITY);   // a NaN bias: -inf
             }
         }
         if (!clean) {
@@ -260,7 +281,6 @@ __global__ void __launch_bounds__(32 * kWarps)
         for (int i = 0; i < V; ++i) key[i] = e0 + i < E ? key[i] : 0u;
     }
 
-    uint32_t* my_keys = sh.key[slot] + sub * kPitch;
     if (p.n_group > 1) {
         const int size = E / p.n_group;
         if (p.group_lanes > 0) {
@@ -296,26 +316,42 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
             for (int i = 0; i < V; ++i) key[i] = ahead < p.topk_group ? key[i] : 0u;
         } else {
-            // any group size: the values through shared memory, group sub, sub + kLanes, ... in lane sub; each group's
-            // key then lies in sh.id
+            // any group size: the values through shared memory, a power of two of lanes to a group (one if there are
+            // more groups than lanes); each group's key then lies in sh.id
 #pragma unroll
-            for (int i = 0; i < V; ++i) my_keys[i] = top2 ? __float_as_uint(o[i]) : key[i];
+            for (int i = 0; i < V; i += 4) {
+                *reinterpret_cast<uint4*>(my_keys + i) =
+                    top2 ? make_uint4(__float_as_uint(o[i]), __float_as_uint(o[i + 1]), __float_as_uint(o[i + 2]),
+                                      __float_as_uint(o[i + 3]))
+                         : make_uint4(key[i], key[i + 1], key[i + 2], key[i + 3]);
+            }
             __syncwarp();
-            for (int g = sub; g < p.n_group; g += kLanes) {
+            const int share = 1 << p.group_share, at_once = kLanes >> p.group_share, part = sub & (share - 1);
+            for (int base = 0; base < p.n_group; base += at_once) {
+                const int g = base + (sub >> p.group_share), end = g < p.n_group ? (g + 1) * size : 0;
                 uint32_t gk = 0u;
-                float a = -INFINITY, b = -INFINITY;
-                for (int e = g * size; e < (g + 1) * size; ++e) {
-                    const uint32_t v = sh.key[slot][e / V * kPitch + e % V];
-                    gk = max(gk, v);
-                    const float f = __uint_as_float(v);
-                    b = fmaxf(b, fminf(a, f));
-                    a = fmaxf(a, f);
+                if (top2) {
+                    float a = -INFINITY, b = -INFINITY;
+                    for (int e = g * size + part; e < end; e += share) {
+                        const float f = __uint_as_float(sh.key[slot][e / V * kPitch + e % V]);
+                        b = fmaxf(b, fminf(a, f));
+                        a = fmaxf(a, f);
+                    }
+                    for (int x = 1; x < share; x <<= 1) {
+                        const float a2 = __shfl_xor_sync(kAll, a, x), b2 = __shfl_xor_sync(kAll, b, x);
+                        b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+                        a = fmaxf(a, a2);
+                    }
+                    gk = ordered(b > -INFINITY ? a + b : a);
+                } else {
+                    for (int e = g * size + part; e < end; e += share) gk = max(gk, sh.key[slot][e / V * kPitch + e % V]);
+                    for (int x = 1; x < share; x <<= 1) gk = max(gk, __shfl_xor_sync(kAll, gk, x));
                 }
-                sh.id[slot][g] = static_cast<int>(top2 ? ordered(b > -INFINITY ? a + b : a) : gk);
+                if (end > 0 && part == 0) sh.id[slot][g] = static_cast<int>(gk);
             }
             __syncwarp();
             uint32_t kept = 0u;                                // bit g: group g
-            for (int g = 0; g < p.n_group; ++g) {
+            for (int g = sub; g < p.n_group; g += kLanes) {
                 const uint32_t gk = static_cast<uint32_t>(sh.id[slot][g]);
                 int ahead = 0;
                 for (int h = 0; h < p.n_group; ++h) {
@@ -324,11 +360,15 @@ __global__ void __launch_bounds__(32 * kWarps)
                 }
                 kept |= (ahead < p.topk_group ? 1u : 0u) << g;
             }
+            __syncwarp();
+#pragma unroll
+            for (int x = 1; x < kLanes; x <<= 1) kept |= __shfl_xor_sync(kAll, kept, x);
+            int group = e0 / size, left = (group + 1) * size - e0;   // this expert's; past E the keys are 0
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (e0 + i < E && !((kept >> ((e0 + i) / size)) & 1u)) key[i] = 0u;
+                key[i] = (kept >> (group & 31)) & 1u ? key[i] : 0u;
+                if (--left == 0) ++group, left = size;
             }
-            __syncwarp();
         }
     }
 
@@ -487,24 +527,23 @@ __device__ __forceinline__ void load_slot(const T* row, const int32_t* ids, cons
     if (id >= 0) lj = masked_nan(load_one(row + id));
 }
 
-// Four experts' values at e of a row of E.
-template <typename T, int kN>
-__device__ __forceinline__ void store4(T* out, int e, int E, const float (&v)[4]) {
-    if (e + 4 <= E) {
-#pragma unroll
-        for (int i = 0; i < 4; i += kN) store_vec<T, kN>(out + e + i, *reinterpret_cast<const float(*)[kN]>(v + i));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (e + i < E) out[e + i] = from_f32<T>(v[i]);
-        }
-    }
+// Zeros at p, `bytes` of them (elements of kSize bytes), by a warp: whole 16-byte words but for the ends.
+template <int kSize>
+__device__ __forceinline__ void zero_span(uint8_t* p, int bytes) {
+    using U = typename Word<kSize>::type;
+    const int lane = threadIdx.x & 31, head = min(bytes, static_cast<int>(-reinterpret_cast<uintptr_t>(p) & 15));
+    uint4* words = reinterpret_cast<uint4*>(p + head);
+    const int n = (bytes - head) / 16, tail = (bytes - head) % 16;
+    for (int i = lane; i < n; i += 32) words[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (lane * kSize < head) *reinterpret_cast<U*>(p + lane * kSize) = 0;
+    if (lane * kSize < tail) *reinterpret_cast<U*>(p + bytes - tail + lane * kSize) = 0;
 }
 
 // Every weight but the softmax's over all experts: only the chosen logits take part.  A token is taken by kLanes >= k
 // lanes, slot j in lane j; the warp writes its tokens' zeros first, which waits for nothing.  (With one token to a
-// warp 65537 x 256 took 21.4 us.)
-template <typename T, int kLanes, int kN>
+// warp 65537 x 256 took 21.4 us instead of 16.0, with the zeros of odd rows element by element 65537 x 251 in BF16 21.5
+// instead of 9.1.)
+template <typename T, int kLanes>
 __global__ void __launch_bounds__(32 * kWarps)
     route_topk_backward_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, RouteParams p,
                                const int32_t* __restrict__ ids, const float* __restrict__ dw, T* __restrict__ dl,
@@ -517,11 +556,13 @@ __global__ void __launch_bounds__(32 * kWarps)
     const bool live = t < tokens && sub < p.k;
     int id;
     float g, lj;
-    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-        if (first + i >= tokens) break;
-        for (int e = 4 * lane; e < E; e += 128) store4<T, kN>(dl + (first + i) * ld_out, e, E, zero);
+    const int here = static_cast<int>(min(tokens - first, static_cast<int64_t>(kTokens)));
+    uint8_t* rows = reinterpret_cast<uint8_t*>(dl + first * ld_out);
+    constexpr int kSize = sizeof(T);
+    if (ld_out == E) {
+        zero_span<kSize>(rows, here * E * kSize);
+    } else {
+        for (int i = 0; i < here; ++i) zero_span<kSize>(rows + i * ld_out * kSize, E * kSize);
     }
     load_slot(logits + t * ld, ids + t * p.k + sub, dw + t * p.k + sub, live, E, p.scale, id, g, lj, err);
     float s, rest = 1.0f;                                       // rest = 1 - s
@@ -542,8 +583,24 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (id >= 0) dl[t * ld_out + id] = from_f32<T>(s * rest * (g - dot));
 }
 
+// Four experts' values at e of a row of E.
+template <typename T, int kN>
+__device__ __forceinline__ void store4(T* out, int e, int E, const float (&v)[4]) {
+    if (e + 4 <= E) {
+#pragma unroll
+        for (int i = 0; i < 4; i += kN) store_vec<T, kN>(out + e + i, *reinterpret_cast<const float(*)[kN]>(v + i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (e + i < E) out[e + i] = from_f32<T>(v[i]);
+        }
+    }
+}
+
 // The softmax over all experts.  A token is taken by kLanes lanes; lane s of them has the words of four experts at
-// 4 (s + kLanes i), i < kWords, whatever the alignment, so sums are taken in one order, and slots s + kLanes i.
+// 4 (s + kLanes i), i < kWords, whatever the alignment, so sums are taken in one order, and slots s + kLanes i.  Rows
+// of 16-bit logits on odd boundaries go through shared memory, side by side from and to memory (65537 x 251 in BF16 27.3 us
+// without, 23.4 with it; in FP32, element by element, 26.3 and 31.2).
 //
 // Bound by memory, the row read and written: 65537 x 250 in FP32 take 23.9 us, 131 MB at 5.5 TB/s (25.2 us, bound by
 // instructions, with one token to a warp whatever E).
@@ -560,11 +617,23 @@ __global__ void __launch_bounds__(32 * kWarps)
     const int64_t t = real ? first + lane / kLanes : tokens - 1;
     const T* row = logits + t * ld;
     T* out = dl + t * ld_out;
+    constexpr bool kShared = kN == 1 && sizeof(T) == 2;
+    constexpr int kCols = 4 * kWords * kLanes, kPitch = kCols + (kLanes < 32 ? kLanes : 0);
+    __shared__ __align__(16) float s_rows[kShared ? kWarps : 1][kTokens * kPitch];
+    float* staged = s_rows[kShared ? threadIdx.x >> 5 : 0] + lane / kLanes * kPitch;
     float v[kWords][4], probe = 0.0f;
+    if (kShared) {
+#pragma unroll
+        for (int e = sub; e < kCols; e += kLanes) staged[e] = e < E ? load_one(row + e) : -INFINITY;
+        __syncwarp();
+    }
 #pragma unroll
     for (int j = 0; j < kWords; ++j) {
         const int e = 4 * (sub + kLanes * j);
-        if (e + 4 <= E) {
+        if (kShared) {
+            const float4 w = *reinterpret_cast<const float4*>(staged + e);
+            v[j][0] = w.x, v[j][1] = w.y, v[j][2] = w.z, v[j][3] = w.w;
+        } else if (e + 4 <= E) {
 #pragma unroll
             for (int i = 0; i < 4; i += kN) load_vec<T, kN>(row + e + i, *reinterpret_cast<float(*)[kN]>(v[j] + i));
         } else {
@@ -622,12 +691,19 @@ __global__ void __launch_bounds__(32 * kWarps)
         dot += own[i];
     }
     const float c = -token_sum<kLanes>(dot) * r;
-    if (real) {
 #pragma unroll
-        for (int j = 0; j < kWords; ++j) {
+    for (int j = 0; j < kWords; ++j) {
+        const int e = 4 * (sub + kLanes * j);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[j][i] *= c;
-            store4<T, kN>(out, 4 * (sub + kLanes * j), E, v[j]);
+        for (int i = 0; i < 4; ++i) v[j][i] *= c;
+        if (kShared) *reinterpret_cast<float4*>(staged + e) = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
+        else if (real) store4<T, kN>(out, e, E, v[j]);
+    }
+    if (kShared) {
+        __syncwarp();
+#pragma unroll
+        for (int e = sub; e < kCols; e += kLanes) {
+            if (real && e < E) out[e] = from_f32<T>(staged[e]);
         }
     }
     __syncwarp();                                               // orders the warp's writes
@@ -643,6 +719,8 @@ cudaError_t launch_route(const void* logits, int64_t tokens, int E, int64_t ld, 
     // a group of whole lanes, a power of two of them
     const int size = E / p.n_group, lanes = size / V;
     p.group_lanes = size % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    p.group_share = 0;
+    while ((2 << p.group_share) * p.n_group <= kLanes) ++p.group_share;
     p.bias_wide = (reinterpret_cast<uintptr_t>(bias) & 15) == 0;
     constexpr int kPerBlock = kWarps * 32 / kLanes;
     return launch_pdl(false, route_topk_kernel<T, V, kLanes, kN>, static_cast<unsigned>((tokens + kPerBlock - 1) / kPerBlock),
@@ -670,33 +748,51 @@ cudaError_t route_by_width(const void* logits, int64_t tokens, int E, int64_t ld
 }
 
 // By the experts (of a softmax over all of them) or the slots.
-template <typename T, int kN>
-cudaError_t launch_backward(const void* logits, int64_t tokens, int E, int64_t ld, const RouteParams& p, const int32_t* ids,
-                            const float* dw, void* dl, int64_t ld_out, int* err, cudaStream_t st) {
-    auto run = [&](auto kernel, int per_warp) {
+template <typename T>
+struct Backward {
+    const T* logits;
+    int64_t tokens;
+    int E;
+    int64_t ld;
+    const RouteParams& p;
+    const int32_t* ids;
+    const float* dw;
+    T* dl;
+    int64_t ld_out;
+    int* err;
+    cudaStream_t st;
+
+    template <typename Kernel>
+    cudaError_t run(Kernel kernel, int per_warp) const {
         const int per_block = kWarps * per_warp;
-        return launch_pdl(false, kernel, static_cast<unsigned>((tokens + per_block - 1) / per_block), 32 * kWarps, 0, st,
-                          static_cast<const T*>(logits), tokens, E, ld, p, ids, dw, static_cast<T*>(dl), ld_out, err);
-    };
-    if (p.score == MOE_SCORE_SOFTMAX && !p.renormalize) {
+        return launch_pdl(false, kernel, static_cast<unsigned>((tokens + per_block - 1) / per_block), 32 * kWarps, 0, st, logits,
+                          tokens, E, ld, p, ids, dw, dl, ld_out, err);
+    }
+    template <int kN>
+    cudaError_t full() const {
         if (E <= 128) return run(route_topk_backward_full_kernel<T, 4, 8, kN>, 4);
         if (E <= 256) return run(route_topk_backward_full_kernel<T, 4, 16, kN>, 2);
         if (E <= 512) return run(route_topk_backward_full_kernel<T, 4, 32, kN>, 1);
         return run(route_topk_backward_full_kernel<T, 8, 32, kN>, 1);
     }
-    if (p.k <= 8) return run(route_topk_backward_kernel<T, 8, kN>, 4);
-    if (p.k <= 16) return run(route_topk_backward_kernel<T, 16, kN>, 2);
-    return run(route_topk_backward_kernel<T, 32, kN>, 1);
-}
+    cudaError_t operator()() const {
+        if (p.score != MOE_SCORE_SOFTMAX || p.renormalize) {
+            if (p.k <= 8) return run(route_topk_backward_kernel<T, 8>, 4);
+            if (p.k <= 16) return run(route_topk_backward_kernel<T, 16>, 2);
+            return run(route_topk_backward_kernel<T, 32>, 1);
+        }
+        constexpr int64_t kSize = sizeof(T);
+        const int64_t bits = static_cast<int64_t>(reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dl)) |
+                             (ld * kSize) | (ld_out * kSize);
+        if (bits % (4 * kSize) == 0) return full<4>();
+        if (bits % (2 * kSize) == 0) return full<2>();
+        return full<1>();
+    }
+};
 template <typename T>
-cudaError_t backward_by_word(const void* logits, int64_t tokens, int E, int64_t ld, const RouteParams& p, const int32_t* ids,
-                             const float* dw, void* dl, int64_t ld_out, int* err, cudaStream_t st) {
-    constexpr int64_t kSize = sizeof(T);
-    const int64_t bits = static_cast<int64_t>(reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dl)) |
-                         (ld * kSize) | (ld_out * kSize);
-    if (bits % (4 * kSize) == 0) return launch_backward<T, 4>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
-    if (bits % (2 * kSize) == 0) return launch_backward<T, 2>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
-    return launch_backward<T, 1>(logits, tokens, E, ld, p, ids, dw, dl, ld_out, err, st);
+cudaError_t backward(const void* logits, int64_t tokens, int E, int64_t ld, const RouteParams& p, const int32_t* ids,
+                     const float* dw, void* dl, int64_t ld_out, int* err, cudaStream_t st) {
+    return Backward<T>{static_cast<const T*>(logits), tokens, E, ld, p, ids, dw, static_cast<T*>(dl), ld_out, err, st}();
 }
 
 }  // namespace
@@ -714,9 +810,9 @@ cudaError_t launch_route_topk_backward(const void* logits, int type, int64_t T, 
                                        const RouteParams& p, const int32_t* ids, const float* dw, void* dl,
                                        int64_t ld_out, int* err, cudaStream_t st) {
     switch (type) {
-        case NVFP4_TYPE_F32: return backward_by_word<float>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
-        case NVFP4_TYPE_BF16: return backward_by_word<__nv_bfloat16>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
-        default: return backward_by_word<__half>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
+        case NVFP4_TYPE_F32: return backward<float>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
+        case NVFP4_TYPE_BF16: return backward<__nv_bfloat16>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
+        default: return backward<__half>(logits, T, E, ld, p, ids, dw, dl, ld_out, err, st);
     }
 }
 

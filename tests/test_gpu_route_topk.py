@@ -113,6 +113,18 @@ def test_groups(E, n_group, topk_group, k, group_score, score, with_bias):
           n_group=n_group, topk_group=topk_group, group_score=group_score)
 
 
+@pytest.mark.parametrize("E,n_group,topk_group,k", [(248, 8, 4, 8), (136, 8, 3, 9), (200, 2, 1, 8), (80, 16, 3, 4),
+                                                    (93, 31, 7, 5), (510, 30, 4, 11), (29, 29, 9, 9), (1023, 11, 2, 6)])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_groups_of_any_size(E, n_group, topk_group, k, group_score, dtype):
+    bias = 0.05 * np.random.default_rng(E).standard_normal(E).astype(np.float32)
+    for b in (None, bias):
+        # of hundreds of scores one pair in most rows lies within 2e-6 (BF16 logits: also of equal scores plus a bias)
+        check(make(70, E, dtype, seed=k), k, least=0.5 if b is None and group_score == "max" else 0.0, score="sigmoid", bias=b,
+              n_group=n_group, topk_group=topk_group, group_score=group_score)
+
+
 def test_ties_take_the_lower_id():
     l = torch.zeros((3, 64), device="cuda")
     ids, w = M.moe_route_topk(l, 5)
@@ -246,6 +258,29 @@ def test_gradient(dtype, score, renorm, T, E, k):
     tol = G_REL * gradient_bound(l64, i, d64, score, renorm, 2.5, dtype) + UNIT[dtype] * np.abs(want) + TINY[dtype]
     assert np.all(np.abs(values(got) - want) <= tol)
     assert M.nvfp4_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,k", [(41, 251, 6), (9, 127, 8), (5, 501, 12), (33, 63, 5), (3, 1023, 32), (6, 254, 20)])
+def test_gradient_of_odd_rows(dtype, renorm, T, E, k):
+    l = make(T, E, dtype, seed=9)
+    l[1, 3: E // 2] = -float("inf")
+    ids, _ = M.moe_route_topk(l, k, renormalize=renorm)
+    dw = torch.randn(T, k, device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+    got = M.moe_route_topk_backward(l, ids, dw, renormalize=renorm)
+    l64, i, d64 = values(l), ids.cpu().numpy(), values(dw)
+    want = R.backward(l64, i, d64, "softmax", renorm, 1.0)
+    tol = G_REL * gradient_bound(l64, i, d64, "softmax", renorm, 1.0, dtype) + UNIT[dtype] * np.abs(want) + TINY[dtype]
+    assert np.all(np.abs(values(got) - want) <= tol)
+    # into rows of another pitch on any boundary, nothing beside them written
+    p = M.moe_route_params(0, k, 1, 1, 0, 1 if renorm else 0, 1.0)
+    for lo, pitch in ((0, E + 5), (1, E + 1), (2, E + 2), (3, E + 4), (8, E + 24 - E % 8)):
+        out = torch.full((T, pitch), 7.0, dtype=dtype, device="cuda")
+        status = M.lib().moe_route_topk_backward(l.data_ptr(), M._TYPES[dtype], T, E, E, p, ids.data_ptr(), dw.data_ptr(),
+                                                 out[:, lo:].data_ptr(), pitch, torch.cuda.current_stream().cuda_stream)
+        assert status == 0 and torch.equal(out[:, lo:lo + E], got)
+        assert bool((out[:, :lo] == 7.0).all()) and bool((out[:, lo + E:] == 7.0).all())
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
