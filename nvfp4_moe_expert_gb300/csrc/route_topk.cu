@@ -163,14 +163,20 @@ __global__ void __launch_bounds__(32 * kWarps)
     // the logits, -inf where there is no expert; a row of finite ones needs none of the checks for masks
     float l[V], probe = 0.0f;
     uint32_t* my_keys = sh.key[slot] + sub * kPitch;
+    const bool whole = e0 + V <= E;
     if constexpr (kN > 1) {
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < V; i += kN) {
-            if (e0 + i + kN <= E) {
-                load_vec<T, kN>(row + e0 + i, *reinterpret_cast<float(*)[kN]>(l + i));
-            } else {
+            for (int i = 0; i < V; i += kN) load_vec<T, kN>(row + e0 + i, *reinterpret_cast<float(*)[kN]>(l + i));
+        } else {
 #pragma unroll
-                for (int j = i; j < i + kN; ++j) l[j] = e0 + j < E ? load_one(row + e0 + j) : -INFINITY;
+            for (int i = 0; i < V; i += kN) {
+                if (e0 + i + kN <= E) {
+                    load_vec<T, kN>(row + e0 + i, *reinterpret_cast<float(*)[kN]>(l + i));
+                } else {
+#pragma unroll
+                    for (int j = i; j < i + kN; ++j) l[j] = e0 + j < E ? load_one(row + e0 + j) : -INFINITY;
+                }
             }
         }
     } else {
@@ -188,7 +194,7 @@ __global__ void __launch_bounds__(32 * kWarps)
             l[i] = w.x, l[i + 1] = w.y, l[i + 2] = w.z, l[i + 3] = w.w;
         }
     }
-    if (e0 + V <= E) {
+    if (whole) {
 #pragma unroll
         for (int i = 0; i < V; ++i) probe = fmaf(l[i], 0.0f, probe);
     } else {
@@ -252,18 +258,23 @@ __global__ void __launch_bounds__(32 * kWarps)
             for (int i = 0; i < V; ++i) o[i] = order_sigmoid(o[i]);
         }
         if (bias != nullptr) {
+            float b[V];
+            if (whole && p.bias_wide) {
 #pragma unroll
-            for (int i = 0; i < V; i += 4) {
-                float b[4];
-                if (p.bias_wide && e0 + i + 4 <= E) {
-                    load_vec<float, 4>(bias + e0 + i, b);
-                } else {
+                for (int i = 0; i < V; i += 4) load_vec<float, 4>(bias + e0 + i, *reinterpret_cast<float(*)[4]>(b + i));
+            } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) b[j] = e0 + i + j < E ? __ldg(bias + e0 + i + j) : 0.0f;
+                for (int i = 0; i < V; i += 4) {
+                    if (p.bias_wide && e0 + i + 4 <= E) {
+                        load_vec<float, 4>(bias + e0 + i, *reinterpret_cast<float(*)[4]>(b + i));
+                    } else {
+#pragma unroll
+                        for (int j = i; j < i + 4; ++j) b[j] = e0 + j < E ? __ldg(bias + e0 + j) : 0.0f;
+                    }
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[i + j] = fmaxf(o[i + j] + b[j], -INFINITY);   // a NaN bias: -inf
             }
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = fmaxf(o[i] + b[i], -INFINITY);   // a NaN bias: -inf
         }
         if (!clean) {
 #pragma unroll
@@ -276,7 +287,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     const bool by_logit = bias == nullptr;
 #pragma unroll
     for (int i = 0; i < V; ++i) key[i] = ordered(by_logit ? l[i] : o[i]);
-    if (e0 + V > E) {
+    if (!whole) {
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = e0 + i < E ? key[i] : 0u;
     }
