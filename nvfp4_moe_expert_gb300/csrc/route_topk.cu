@@ -258,23 +258,18 @@ __global__ void __launch_bounds__(32 * kWarps)
             for (int i = 0; i < V; ++i) o[i] = order_sigmoid(o[i]);
         }
         if (bias != nullptr) {
-            float b[V];
-            if (whole && p.bias_wide) {
 #pragma unroll
-                for (int i = 0; i < V; i += 4) load_vec<float, 4>(bias + e0 + i, *reinterpret_cast<float(*)[4]>(b + i));
-            } else {
+            for (int i = 0; i < V; i += 4) {
+                float b[4];
+                if (p.bias_wide && e0 + i + 4 <= E) {
+                    load_vec<float, 4>(bias + e0 + i, b);
+                } else {
 #pragma unroll
-                for (int i = 0; i < V; i += 4) {
-                    if (p.bias_wide && e0 + i + 4 <= E) {
-                        load_vec<float, 4>(bias + e0 + i, *reinterpret_cast<float(*)[4]>(b + i));
-                    } else {
-#pragma unroll
-                        for (int j = i; j < i + 4; ++j) b[j] = e0 + j < E ? __ldg(bias + e0 + j) : 0.0f;
-                    }
+                    for (int j = 0; j < 4; ++j) b[j] = e0 + i + j < E ? __ldg(bias + e0 + i + j) : 0.0f;
                 }
-            }
 #pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = fmaxf(o[i] + b[i], -INFINITY);   // a NaN bias: -inf
+                for (int j = 0; j < 4; ++j) o[i + j] = fmaxf(o[i + j] + b[j], -INFINITY);   // a NaN bias: -inf
+            }
         }
         if (!clean) {
 #pragma unroll
