@@ -143,6 +143,13 @@ __device__ __forceinline__ U token_max(U v) {
     return v;
 }
 
+// The largest of a token's keys: one instruction where the token has the warp (65536 x 512 57.1 -> 48.2 us); several
+// tokens' would go one after the other (65536 x 128 17.2 us by shuffles, 20.4).
+template <int kLanes>
+__device__ __forceinline__ uint32_t key_max(uint32_t v) {
+    return kLanes == 32 ? __reduce_max_sync(kAll, v) : token_max<kLanes>(v);
+}
+
 template <typename T, int V, int kLanes, int kN>
 __global__ void __launch_bounds__(32 * kWarps)
     route_topk_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, RouteParams p,
@@ -280,8 +287,13 @@ __global__ void __launch_bounds__(32 * kWarps)
     }
     uint32_t key[V];
     const bool by_logit = bias == nullptr;
+    if (by_logit) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = ordered(by_logit ? l[i] : o[i]);
+        for (int i = 0; i < V; ++i) key[i] = ordered(l[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = ordered(o[i]);
+    }
     if (!whole) {
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = e0 + i < E ? key[i] : 0u;
@@ -388,7 +400,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     }
     uint32_t bound = 0u;
     for (int j = 0; j < p.k; ++j) {
-        bound = token_max<kLanes>(max(m[0], m[1]));
+        bound = key_max<kLanes>(max(m[0], m[1]));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const bool gone = m[h] == bound;
