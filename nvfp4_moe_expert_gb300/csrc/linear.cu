@@ -277,6 +277,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // which T rows are real), K in the same order.
 // Warps: 0 loads weights, 1 issues the MMAs, 2-17 quantise x, then warp 4 (TMEM lanes 0-31) writes
 // the outputs.
+//
+// Bound by latency, one thing after the other: the CTA's start, the first loads, the quantisation, the MMAs, the
+// outputs.  One token through 4096 x 4096 MXFP4 (8.9 MB) 5.3 us, 16 through 1536 x 2048 NVFP4 6.6 us.
 namespace decode {
 constexpr int kMaxT = 16;
 constexpr int kQuantWarps = 16;

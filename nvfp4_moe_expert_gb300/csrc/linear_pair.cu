@@ -12,6 +12,9 @@
 // back, and put their 32 rows x 64 columns in shared memory for a TMA store while the next tile's MMAs
 // run.  (Stores straight from the lanes, 32 rows to an instruction, slowed the loads down: a tile of K = 8192
 // took 19700 cycles instead of 17200 without any stores, one of K = 1536 6300 instead of 3900.)
+//
+// 8192 x 8192 x 8192 MXFP4 149 us, 7.4 PFLOP/s: the tensor pipe is active for 78% of them, at the power limit.  32768 x
+// 4096 x 1536 NVFP4 85 us, bound by the operands' way into the SMs beside 268 MB of stores.
 #include "linear.cuh"
 
 namespace nvfp4 {
