@@ -19,7 +19,9 @@ exception is raised.
 """
 
 import ctypes
+import functools
 import os
+from operator import index
 
 import torch
 
@@ -462,6 +464,17 @@ def _choice(name, value, table):
     return code
 
 
+@functools.lru_cache(maxsize=256)
+def _route_struct(score, k, n_group, topk_group, group_score, renormalize, scale):
+    return moe_route_params(_choice("score", score, _SCORES), k, n_group, topk_group,
+                            _choice("group_score", group_score, _GROUP_SCORES), renormalize, scale)
+
+
+def _route_params(score, k, n_group, topk_group, group_score, renormalize, scale):
+    """The parameters as the C call takes them; made once for the same values (0.5 to 1 us of a call's 10)."""
+    return _route_struct(score, index(k), index(n_group), index(topk_group), group_score, 1 if renormalize else 0, float(scale))
+
+
 def moe_route_topk(logits, k, score="softmax", bias=None, n_group=1, topk_group=1, group_score="max",
                    renormalize=True, scale=1.0, stream=None):
     """Routing of given router logits: (topk_ids int32 [T, k], topk_w float32 [T, k]).
@@ -476,8 +489,7 @@ def moe_route_topk(logits, k, score="softmax", bias=None, n_group=1, topk_group=
     device = logits.device
     if bias is not None:
         _need("bias", bias, torch.float32, (E,), device)
-    p = moe_route_params(_choice("score", score, _SCORES), k, n_group, topk_group,
-                         _choice("group_score", group_score, _GROUP_SCORES), 1 if renormalize else 0, scale)
+    p = _route_params(score, k, n_group, topk_group, group_score, renormalize, scale)
     shape = (T, k if k > 0 else 0)
     ids = _empty(shape, torch.int32, device, stream)
     w = _empty(shape, torch.float32, device, stream)
@@ -498,7 +510,7 @@ def moe_route_topk_backward(logits, topk_ids, dw, score="softmax", renormalize=T
     k = topk_ids.shape[1]
     _need("topk_ids", topk_ids, torch.int32, (T, k), device)
     _need("dw", dw, torch.float32, (T, k), device)
-    p = moe_route_params(_choice("score", score, _SCORES), k, 1, 1, 0, 1 if renormalize else 0, scale)
+    p = _route_params(score, k, 1, 1, "max", renormalize, scale)
     dlogits = _empty((T, E), logits.dtype, device, stream)
     status = lib().moe_route_topk_backward(logits.data_ptr(), code, T, E, ld, p, topk_ids.data_ptr(), dw.data_ptr(),
                                            dlogits.data_ptr(), E, _raw_stream(stream, logits))
@@ -595,6 +607,11 @@ def mxfp4_weight_from_codes(codes, scales):
     return FP4Weight(padded, sf.contiguous(), None, N, K)
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(mx, T, K):
+    return (lib().mxfp4_linear_workspace_bytes if mx else lib().nvfp4_linear_workspace_bytes)(T, K)
+
+
 def _linear(name, mx, x, weight, bias, out, out_dtype, stream):
     code, T, K, ldx = _rows("x", x, _TYPES if mx else _BF16)
     N, device = weight.N, x.device
@@ -614,7 +631,7 @@ def _linear(name, mx, x, weight, bias, out, out_dtype, stream):
         if rows != T or cols != N or out.device != device:
             raise ValueError(f"out must be [{T}, {N}] on {device}")
     L = lib()
-    need = L.mxfp4_linear_workspace_bytes(T, K) if mx else L.nvfp4_linear_workspace_bytes(T, K)
+    need = _workspace_bytes(mx, T, K)
     ws = _empty((need,), torch.uint8, device, stream) if need else None
     ws_ptr = ws.data_ptr() if need else None
     b = None if bias is None else bias.data_ptr()

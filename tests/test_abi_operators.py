@@ -120,3 +120,18 @@ def test_python_checks():
                                                    torch.zeros((4, 3), dtype=torch.uint8))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_routing_parameters_are_those_of_the_call():
+    scale = torch.tensor(2.5)
+    p = M._route_params("sigmoid", 8, 4, 2, "top2", True, scale)
+    assert (p.score, p.k, p.n_group, p.topk_group, p.group_score, p.renormalize, p.scale) == (1, 8, 4, 2, 1, 1, 2.5)
+    scale += 1.0                                             # a parameter is its value, not its object
+    assert M._route_params("sigmoid", 8, 4, 2, "top2", True, scale).scale == 3.5 and p.scale == 2.5
+    assert M._route_params("softmax", 8, 1, 1, "max", 0, 1).renormalize == 0
+    with pytest.raises(ValueError):
+        M._route_params("relu", 8, 1, 1, "max", True, 1.0)
+    with pytest.raises(ValueError):
+        M._route_params("softmax", 8, 1, 1, "mean", True, 1.0)
+    with pytest.raises(TypeError):
+        M._route_params("softmax", 2.5, 1, 1, "max", True, 1.0)
