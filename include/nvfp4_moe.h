@@ -29,7 +29,8 @@
  *    every buffer.  The library never allocates or frees memory.
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream).  All GPU work is enqueued on it; no entry point synchronises
- *    except nvfp4_get_device_error.
+ *    except nvfp4_get_device_error.  Kernels run on the calling thread's
+ *    current device: the stream and every buffer have to belong to it.
  *  - Arguments are validated on the host before anything is launched; an
  *    invalid call returns an error and enqueues nothing.  A failed launch
  *    returns NVFP4_ERR_CUDA.  Conditions only the GPU can see (an expert id

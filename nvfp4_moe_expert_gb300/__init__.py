@@ -15,7 +15,7 @@ entry points have the names of the C ABI in ``include/nvfp4_moe.h``:
     mxfp4_quantize_rows, mxfp4_dequantize_rows, mxfp4_linear, nvfp4_linear
 
 There is no CPU fallback: if the library is missing or a call fails, an
-exception is raised.
+exception is raised.  Tensors and streams have to belong to the current device.
 """
 
 import ctypes
@@ -166,15 +166,38 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _current_device():
+    return torch._C._cuda_getDevice()
+
+
+# The library launches on the current device: on memory or a stream of another one a kernel would fault, or run
+# unordered beside that device's own work.
+
+def _on_device(*ts):
+    """Refuses CUDA tensors of any but the current device."""
+    here = _current_device()
+    for t in ts:
+        if t.get_device() != here:
+            raise ValueError(f"tensors must be on the current device (cuda:{here}), not on {t.device}: "
+                             "call under torch.cuda.device(...)")
+
+
+def _stream_handle(stream):
+    here = _current_device()
+    if stream.device_index != here:
+        raise ValueError(f"the stream must be one of the current device (cuda:{here}), not of cuda:{stream.device_index}")
+    return stream.cuda_stream
+
+
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream if stream is None else _stream_handle(stream))
 
 
 def _need_cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous CUDA tensors")
+    _on_device(*[t for t in ts if t is not None])
 
 
 # ---------------------------------------------------------------- host queries
@@ -207,6 +230,7 @@ def nvfp4_quantize_rows(x, codes=None, sf=None, g=None, stream=None):
         raise ValueError("x must be a 2-D bfloat16 tensor")
     if not x.is_cuda or (x.shape[0] > 0 and x.stride(1) != 1):
         raise ValueError("x must be a CUDA tensor with contiguous rows")
+    _on_device(x, *[t for t in (codes, sf, g) if t is not None])
     rows, cols = x.shape
     rp = nvfp4_rows_padded(rows)
     dev = x.device
@@ -250,6 +274,7 @@ class MoEWeights:
         self.struct = moe_nvfp4_weights(*[t.data_ptr() for t in self.tensors], E, H, I)
 
     def ref(self):
+        _on_device(*self.tensors)
         return ctypes.byref(self.struct)
 
 
@@ -429,7 +454,7 @@ _GROUP_SCORES = {"max": 0, "top2": 1}
 # look at each property, and the current stream's handle without a Stream object around it.
 
 def _raw_stream(stream, t):
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream_handle(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _empty(shape, dtype, device, stream):
@@ -449,6 +474,7 @@ def _rows(name, t, types):
     ld, step = t.stride()
     if not t.is_cuda or (step != 1 and rows and cols > 1):
         raise ValueError(f"{name} must be a CUDA tensor with contiguous rows")
+    _on_device(t)
     return code, rows, cols, ld if rows > 1 else cols
 
 
@@ -555,6 +581,7 @@ def mxfp4_dequantize_rows(codes, sf, rows, cols, dtype=torch.bfloat16, stream=No
     _need("sf", sf, torch.uint8, _mx_sf_shape(rows, cols), device)
     if not codes.is_cuda:
         raise ValueError("codes must be a CUDA tensor")
+    _on_device(codes)
     out = _empty((rows, cols), dtype, device, stream)
     status = lib().mxfp4_dequantize_rows(codes.data_ptr(), sf.data_ptr(), rows, cols, out.data_ptr(), _TYPES[dtype],
                                          cols, _raw_stream(stream, codes))
@@ -678,6 +705,7 @@ class MoEWeightsBF16:
         self.struct = moe_bf16_weights_t(self.w1.data_ptr(), self.w2.data_ptr(), self.E, self.H, self.I)
 
     def ref(self):
+        _on_device(self.w1, self.w2)
         return ctypes.byref(self.struct)
 
 
