@@ -546,7 +546,9 @@ typedef struct {
  *             takes
  *  0 <= T < 2^31 - 256; 1 <= N < 2^31 - 256
  *  bias_dev   float [N] or NULL
- *  out_dev    [T][ldo] of out_type, element aligned, ldo >= N
+ *  out_dev    [T][ldo] of out_type, element aligned, ldo >= N; its rows may be x's own memory where there
+ *             is a workspace (x is quantised before the first output), and share no byte with x's where
+ *             there is none (NVFP4_ERR_INVALID_ARG)
  *  ws_dev     *_linear_workspace_bytes(T, K) bytes, 256-byte aligned; NULL where that is 0 (few
  *             tokens, whose rows are quantised in shared memory; also 0 for a T or K that is refused)
  * Device errors: NVFP4_ERR_NONFINITE (a row of x with Inf or NaN), NVFP4_ERR_DEVICE_TIMEOUT. */

@@ -639,6 +639,17 @@ def _workspace_bytes(mx, T, K):
     return (lib().mxfp4_linear_workspace_bytes if mx else lib().nvfp4_linear_workspace_bytes)(T, K)
 
 
+def _share_memory(x, out):
+    """Whether rows of x and out, as many, share memory; exact for rows of one pitch (column blocks of one buffer)."""
+    a, b = x.data_ptr(), out.data_ptr()
+    pa, pb = x.stride(0) * x.element_size(), out.stride(0) * out.element_size()
+    na, nb, last = x.shape[1] * x.element_size(), out.shape[1] * out.element_size(), x.shape[0] - 1
+    if last < 0 or a + last * pa + na <= b or b + last * pb + nb <= a:
+        return False
+    d = (b - a) % pa if pa else 0
+    return last == 0 or pa != pb or d < na or d + nb > pa
+
+
 def _linear(name, mx, x, weight, bias, out, out_dtype, stream):
     code, T, K, ldx = _rows("x", x, _TYPES if mx else _BF16)
     N, device = weight.N, x.device
@@ -648,7 +659,8 @@ def _linear(name, mx, x, weight, bias, out, out_dtype, stream):
         raise ValueError(f"x must be [T, {weight.K}] on {weight.device}")
     if bias is not None:
         _need("bias", bias, torch.float32, (N,), device)
-    if out is None:
+    caller_out = out is not None
+    if not caller_out:
         out_code, ldo = _TYPES.get(out_dtype), N
         if out_code is None:
             raise ValueError("out_dtype must be torch.float32, torch.bfloat16 or torch.float16")
@@ -659,6 +671,9 @@ def _linear(name, mx, x, weight, bias, out, out_dtype, stream):
             raise ValueError(f"out must be [{T}, {N}] on {device}")
     L = lib()
     need = _workspace_bytes(mx, T, K)
+    if need == 0 and caller_out and _share_memory(x, out):   # few tokens: one kernel reads x and writes out
+        with torch.cuda.stream(stream):
+            x, ldx = x.clone(memory_format=torch.contiguous_format), K
     ws = _empty((need,), torch.uint8, device, stream) if need else None
     ws_ptr = ws.data_ptr() if need else None
     b = None if bias is None else bias.data_ptr()
@@ -676,13 +691,14 @@ def _linear(name, mx, x, weight, bias, out, out_dtype, stream):
 def mxfp4_linear(x, weight, bias=None, out=None, out_dtype=torch.bfloat16, stream=None):
     """x [T, K] float32, bfloat16 or float16 times the MXFP4 weight's transpose (plus bias
     float32 [N]): x is quantised to MXFP4 rows, the products accumulate in FP32 and are rounded
-    once.  Returns out [T, N] (of out_dtype if not given)."""
+    once.  Returns out [T, N] (of out_dtype if not given); out may lie in x's memory."""
     return _linear("mxfp4_linear", True, x, weight, bias, out, out_dtype, stream)
 
 
 def nvfp4_linear(x, weight, bias=None, out=None, out_dtype=torch.bfloat16, stream=None):
     """x bfloat16 [T, K] times the NVFP4 weight's transpose (plus bias float32 [N]): x is quantised
-    to NVFP4 rows as nvfp4_quantize_rows does.  Returns out [T, N] (of out_dtype if not given)."""
+    to NVFP4 rows as nvfp4_quantize_rows does.  Returns out [T, N] (of out_dtype if not given); out may
+    lie in x's memory."""
     return _linear("nvfp4_linear", False, x, weight, bias, out, out_dtype, stream)
 
 

@@ -661,6 +661,25 @@ bool type_ok(int type) { return type == NVFP4_TYPE_F32 || type == NVFP4_TYPE_BF1
 // Every row start rows are read or written at stays inside 63-bit byte offsets.
 bool rows_ok(int64_t rows, int64_t ld) { return ld <= 0 || rows <= (int64_t(1) << 60) / ld; }
 
+// Whether two sets of `rows` rows share a byte: of bytes_a and bytes_b bytes each, pitch_a and pitch_b (at least as many)
+// apart.  Rows side by side in one buffer do not.
+bool rows_overlap(const void* a, int64_t pitch_a, int64_t bytes_a, const void* b, int64_t pitch_b, int64_t bytes_b,
+                  int64_t rows) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    const uintptr_t pa = pitch_a, pb = pitch_b, na = bytes_a, nb = bytes_b, last = rows - 1;
+    if (a0 + last * pa + na <= b0 || b0 + last * pb + nb <= a0) return false;
+    if (pa == pb) {                                   // b's rows start d bytes behind a's
+        const uintptr_t d = b0 >= a0 ? (b0 - a0) % pa : (pa - (a0 - b0) % pa) % pa;
+        return rows == 1 || d < na || d + nb > pa;
+    }
+    for (uintptr_t i = 0, j = 0; i <= last && j <= last;) {
+        if (a0 + i * pa + na <= b0 + j * pb) ++i;
+        else if (b0 + j * pb + nb <= a0 + i * pa) ++j;
+        else return true;
+    }
+    return false;
+}
+
 // The parameters both routing calls use.
 bool route_params_ok(const moe_route_params& p, int E) {
     return (p.score == MOE_SCORE_SOFTMAX || p.score == MOE_SCORE_SIGMOID) && (p.renormalize == 0 || p.renormalize == 1) &&
@@ -712,6 +731,10 @@ nvfp4_status linear_impl(bool mx, const fp4_linear_weights* w, const void* x, in
         !aligned(bias, 4) || !aligned(ws, 256))
         return NVFP4_ERR_INVALID_ARG;
     if (ws_bytes < L.total) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
+    // one kernel reads x and stores outputs: a thread block's outputs must not be what another still reads
+    const int64_t x_size = type_size(x_type), out_size = type_size(out_type);
+    if (L.total == 0 && rows_overlap(x, ldx * x_size, w->K * x_size, out, ldo * out_size, w->N * out_size, T))
+        return NVFP4_ERR_INVALID_ARG;
     int* err = device_error_ptr();
     if (!err) return NVFP4_ERR_CUDA;
     LinearArgs a{};
