@@ -551,7 +551,9 @@ typedef struct {
  *             there is none (NVFP4_ERR_INVALID_ARG)
  *  ws_dev     *_linear_workspace_bytes(T, K) bytes, 256-byte aligned; NULL where that is 0 (few
  *             tokens, whose rows are quantised in shared memory; also 0 for a T or K that is refused)
- * Device errors: NVFP4_ERR_NONFINITE (a row of x with Inf or NaN), NVFP4_ERR_DEVICE_TIMEOUT. */
+ * Device errors: NVFP4_ERR_NONFINITE (a row of x with Inf or NaN: its outputs are NaN),
+ * NVFP4_ERR_DEVICE_TIMEOUT.  A weight row that nvfp4_quantize_rows reported has zero codes and g and gives its
+ * outputs the bias alone; one that mxfp4_quantize_rows reported gives NaN. */
 size_t nvfp4_linear_workspace_bytes(int64_t T, int64_t K);
 size_t mxfp4_linear_workspace_bytes(int64_t T, int64_t K);
 nvfp4_status nvfp4_linear(const fp4_linear_weights* w, const void* x_dev, int64_t T, int64_t ldx,

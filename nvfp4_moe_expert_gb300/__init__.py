@@ -691,14 +691,15 @@ def _linear(name, mx, x, weight, bias, out, out_dtype, stream):
 def mxfp4_linear(x, weight, bias=None, out=None, out_dtype=torch.bfloat16, stream=None):
     """x [T, K] float32, bfloat16 or float16 times the MXFP4 weight's transpose (plus bias
     float32 [N]): x is quantised to MXFP4 rows, the products accumulate in FP32 and are rounded
-    once.  Returns out [T, N] (of out_dtype if not given); out may lie in x's memory."""
+    once; a row with an Inf or NaN gives NaN.  Returns out [T, N] (of out_dtype if not given); out may lie in x's
+    memory."""
     return _linear("mxfp4_linear", True, x, weight, bias, out, out_dtype, stream)
 
 
 def nvfp4_linear(x, weight, bias=None, out=None, out_dtype=torch.bfloat16, stream=None):
     """x bfloat16 [T, K] times the NVFP4 weight's transpose (plus bias float32 [N]): x is quantised
-    to NVFP4 rows as nvfp4_quantize_rows does.  Returns out [T, N] (of out_dtype if not given); out may
-    lie in x's memory."""
+    to NVFP4 rows as nvfp4_quantize_rows does; a row with an Inf or NaN gives NaN.  Returns out [T, N] (of
+    out_dtype if not given); out may lie in x's memory."""
     return _linear("nvfp4_linear", False, x, weight, bias, out, out_dtype, stream)
 
 

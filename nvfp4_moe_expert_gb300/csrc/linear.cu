@@ -399,12 +399,7 @@ __device__ __forceinline__ void quantise_nv(const DecodeParams& p, int warp, int
         if (lane == 0) atomicMax(&row_max[r], top);
     }
     sync_quantisers();
-    if (warp == 0 && lane < p.T) {
-        const uint32_t top = row_max[lane];
-        const bool finite = top < 0x7F800000u;
-        if (!finite) set_device_error(p.err, NVFP4_ERR_NONFINITE);
-        row_g[lane] = finite ? __fdiv_rn(__uint_as_float(top), kOuterDivisor) : 0.0f;
-    }
+    if (warp == 0 && lane < p.T) row_g[lane] = nv_outer_scale(row_max[lane], p.err);
     sync_quantisers();
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {

@@ -1,5 +1,6 @@
 // The NVFP4 quantisation of a dense product's x: bit for bit what nvfp4_quantize_rows gives for its rows (the
-// arithmetic is nvfp4_quant.cuh's), laid out for few rows as well as many.
+// arithmetic is nvfp4_quant.cuh's) but for the NaN outer scale of a row with an Inf or NaN, laid out for few rows as
+// well as many.
 //
 // A row is taken by 1, 2 or 4 warps, each lane holding at most four blocks of 16 elements (32 consecutive bytes
 // each, a warp's side by side), so the row is read once, the maximum found and the codes made from the
@@ -55,12 +56,9 @@ __global__ void __launch_bounds__(32 * kWarpsQ, 8)
             turn ^= 1;
         }
         if (r >= rows) continue;                      // past the last row: nothing to write
-        const bool finite = top < 0x7F800000u;
-        const float gr = finite ? __fdiv_rn(__uint_as_float(top), kOuterDivisor) : 0.0f;
-        if (part == 0 && lane == 0) {
-            g[r] = gr;
-            if (!finite) set_device_error(err, NVFP4_ERR_NONFINITE);
-        }
+        const bool first = part == 0 && lane == 0;
+        const float gr = nv_outer_scale(top, first ? err : nullptr);
+        if (first) g[r] = gr;
         const NvRow row = nv_row(gr);
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {

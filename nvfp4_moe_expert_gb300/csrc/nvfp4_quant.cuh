@@ -168,6 +168,14 @@ __device__ __noinline__ uint3 nv_quantize16_any(uint4 v0, uint4 v1, float bmx, f
     return make_uint3(codes8_fdiv(v0.x, v0.y, v0.z, v0.w, d2), codes8_fdiv(v1.x, v1.y, v1.z, v1.w, d2), scale);
 }
 
+// Outer scale of a dense product's row of x whose largest magnitude has the FP32 bits `top`: NaN for a row with an Inf or
+// NaN, whose codes and block scales are then zero, so that its outputs are NaN and not the bias alone.
+__device__ __forceinline__ float nv_outer_scale(uint32_t top, int* err) {
+    if (top < 0x7F800000u) return __fdiv_rn(__uint_as_float(top), kOuterDivisor);
+    set_device_error(err, NVFP4_ERR_NONFINITE);
+    return __uint_as_float(0x7FC00000u);
+}
+
 // What a row's blocks share.  From g = 2^-51 on every divisor, 6g or g times a block scale (2^-9 at least, if it
 // is not 0), is in the Markstein step's range, and a block needs no checks of its own (32768 x 1536 BF16: 27.0 to
 // 25.5 us).
