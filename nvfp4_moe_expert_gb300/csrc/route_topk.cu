@@ -10,7 +10,9 @@
 //   w_j  = scale * s_j / sum of the chosen s (renormalised; 0 where the sum is 0), or scale * s_j
 //
 // All sums and scores are FP32, taken in one fixed order, so a token's result does not depend on
-// the batch it is in.
+// the batch it is in.  The order and the weights go by the same s_e, bit for bit: expf, IEEE reciprocals and
+// quotients (with the hardware's approximate exponential and reciprocal for the order experts and groups a few units
+// in the last place apart changed places; 65537 x 256, sigmoid + bias, 8 groups: 43.5 us a call, 58.4 so).
 #include <cmath>
 #include <type_traits>
 
@@ -92,20 +94,6 @@ __device__ __forceinline__ float masked_nan(float l) { return l != l ? -INFINITY
 __device__ __forceinline__ float softmax_shift(float m) { return m == INFINITY || m == -INFINITY ? 0.0f : m; }
 __device__ __forceinline__ float softmax_logit(float l, float m) { return m == INFINITY ? (l == INFINITY ? 0.0f : -INFINITY) : l; }
 __device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(1.0f + expf(-l)); }   // 0 at -inf, 1 at +inf
-
-// The scores the order goes by, every expert's, come from the hardware's base-2 exponential and reciprocal
-// (2 units of the last place, and that of the argument's rounding): sigmoid(l) and a softmax's terms, at most 1,
-// are within 1e-7 of theirs.  The weights come from expf.
-__device__ __forceinline__ float fast_exp(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
-    return y;
-}
-__device__ __forceinline__ float order_sigmoid(float l) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + fast_exp(-l)));
-    return y;
-}
 
 // Routing.  A token is taken by 8, 16 or 32 lanes (kLanes), so that a lane has at most 16 experts (32 of more than 512)
 // and what a token needs whatever E is, its addresses, the bound, the candidates' ranks and the weights, is shared by the
@@ -219,50 +207,37 @@ __global__ void __launch_bounds__(32 * kWarps)
         if (bad) set_device_error(err, NVFP4_ERR_NONFINITE);
     }
 
-    // a softmax over all experts: its largest logit and the sum of its terms, where the weights need them
+    // a softmax over all experts: its largest logit, its terms (in o) and their sum, where the order or the weights
+    // need them
     const bool top2 = p.n_group > 1 && p.group_score == MOE_GROUP_TOP2;
     const bool scored = bias != nullptr || top2;
     const bool softmax = p.score == MOE_SCORE_SOFTMAX;
     const bool full = softmax && !p.renormalize;
     float all_max = 0.0f, all_sum = 0.0f;
+    float o[V];
     if (softmax && (scored || full)) {
         float m = l[0];
 #pragma unroll
         for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
         all_max = token_max<kLanes>(m);
-    }
-    if (full) {
         const float shift = softmax_shift(all_max);
 #pragma unroll
-        for (int i = 0; i < V; ++i) all_sum += expf(softmax_logit(l[i], all_max) - shift);
+        for (int i = 0; i < V; ++i) {
+            o[i] = expf(softmax_logit(l[i], all_max) - shift);
+            all_sum += o[i];
+        }
         all_sum = token_sum<kLanes>(all_sum);
     }
 
-    // order values o: the logits, or the scores plus the bias; the scores are also what "top2" adds up
-    float o[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = l[i];
+    // order values o where they are not the logits: the scores, computed as the weights are, plus the bias; the scores
+    // are also what "top2" adds up
     if (scored) {
         if (softmax) {
-            float m = all_max;
-            if (!clean) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) o[i] = softmax_logit(o[i], m);
-                m = softmax_shift(m);
-            }
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                o[i] = fast_exp(o[i] - m);
-                sum += o[i];
-            }
-            sum = token_sum<kLanes>(sum);
-            const float r = sum > 0.0f ? __frcp_rn(sum) : 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) o[i] *= r;
+            for (int i = 0; i < V; ++i) o[i] = all_sum > 0.0f ? __fdiv_rn(o[i], all_sum) : 0.0f;
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = order_sigmoid(o[i]);
+            for (int i = 0; i < V; ++i) o[i] = sigmoid(l[i]);
         }
         if (bias != nullptr) {
 #pragma unroll
