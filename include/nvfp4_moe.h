@@ -463,7 +463,9 @@ nvfp4_status moe_expert_backward_ste(const moe_bf16_weights_t* w, int64_t T, int
  *          consecutive experts) with the largest group score, the lower group first on equal scores:
  *          max o (MOE_GROUP_MAX) or the sum of the two largest s_e (+ bias_e) of the unmasked
  *          (MOE_GROUP_TOP2)
- *   w_j  = scale * s_j / sum of the k chosen s if renormalize (0 if that sum is 0), else scale * s_j
+ *   w_j  = scale * s_j / sum of the k chosen s if renormalize, else scale * s_j.  The ratios hold where the
+ *          scores themselves underflow; they are 0 if all k chosen are masked or, of sigmoids, all their
+ *          logits lie below -709 (a mask by the type's lowest value)
  * Every row gives k different ids in [0, E).  A token's ids and weights do not depend on T or on
  * the other tokens. */
 typedef enum { NVFP4_TYPE_F32 = 0, NVFP4_TYPE_BF16 = 1, NVFP4_TYPE_F16 = 2 } nvfp4_type;

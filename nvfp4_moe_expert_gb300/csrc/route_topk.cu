@@ -7,12 +7,13 @@
 //          masked experts last
 //   groups of E / n_group consecutive experts: the topk_group groups with the largest score stay,
 //          score = max o, or the sum of the two largest s_e (+ b_e)
-//   w_j  = scale * s_j / sum of the chosen s (renormalised; 0 where the sum is 0), or scale * s_j
+//   w_j  = scale * s_j / sum of the chosen s (renormalised; 0 where the sum is 0), or scale * s_j; the ratios are taken
+//          of scores relative to the largest chosen one, which do not underflow
 //
 // All sums and scores are FP32, taken in one fixed order, so a token's result does not depend on
-// the batch it is in.  The order and the weights go by the same s_e, bit for bit: expf, IEEE reciprocals and
-// quotients (with the hardware's approximate exponential and reciprocal for the order experts and groups a few units
-// in the last place apart changed places; 65537 x 256, sigmoid + bias, 8 groups: 43.5 us a call, 58.4 so).
+// the batch it is in.  The order and the weights go by the same s_e, bit for bit (with the hardware's approximate
+// exponential and reciprocal for the order, experts and groups a few units in the last place apart changed places;
+// 65537 x 256, sigmoid + bias, 8 groups: 43.5 us a call, 51.2 so).
 #include <cmath>
 #include <type_traits>
 
@@ -93,7 +94,28 @@ __device__ __forceinline__ float masked_nan(float l) { return l != l ? -INFINITY
 // are replaced by what gives them: all masked (m = -inf), or the +inf ones equal and the others 0.
 __device__ __forceinline__ float softmax_shift(float m) { return m == INFINITY || m == -INFINITY ? 0.0f : m; }
 __device__ __forceinline__ float softmax_logit(float l, float m) { return m == INFINITY ? (l == INFINITY ? 0.0f : -INFINITY) : l; }
-__device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(1.0f + expf(-l)); }   // 0 at -inf, 1 at +inf
+
+// A sigmoid by t = e^-|l|, which does not overflow: s = y where l >= 0 and t y below, y = 1 / (1 + t); 0 at -inf, 1 at +inf.
+// 1 - s is the sigmoid of -l.  (By 1 / (1 + e^-l) scores below e^-88, in FP32's range, were 0.)
+// y: 1 <= d <= 2, so one Newton-Raphson step, y + y (1 - d y), takes the hardware's reciprocal (2^-23) to within rounding
+// (65537 x 256 in 8 groups 59.4 us a call with __frcp_rn, whose range every d is checked for, 51.2 so).
+__device__ __forceinline__ float reciprocal_1_2(float d) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));
+    return __fmaf_rn(y, __fmaf_rn(-d, y, 1.0f), y);
+}
+__device__ __forceinline__ float sigmoid(float l) {
+    const float t = expf(-fabsf(l)), y = reciprocal_1_2(1.0f + t);
+    return l < 0.0f ? t * y : y;
+}
+// Sigmoids relative to that of the largest chosen logit, m: e^(min(l, 0) - min(m, 0)) y(l), a common factor of e^-min(m, 0)
+// more than the sigmoids, so their ratios do not underflow with them.  All 0 where every chosen logit is masked or lies
+// below -709 (a mask by the type's lowest value), where a score is 0 in 64 bits too.
+constexpr float kLowestLogit = -709.0f;
+__device__ __forceinline__ float sigmoid_ratio(float l, float m) {
+    const float y = reciprocal_1_2(1.0f + expf(-fabsf(l)));
+    return m < kLowestLogit ? 0.0f : expf(fminf(l, 0.0f) - fminf(m, 0.0f)) * y;
+}
 
 // Routing.  A token is taken by 8, 16 or 32 lanes (kLanes), so that a lane has at most 16 experts (32 of more than 512)
 // and what a token needs whatever E is, its addresses, the bound, the candidates' ranks and the weights, is shared by the
@@ -461,6 +483,12 @@ __global__ void __launch_bounds__(32 * kWarps)
         for (int i = 0; i < kSlots; ++i) {
             if (kLanes * i < p.k) w[i] = expf(softmax_logit(w[i], mx) - shift);
         }
+    } else if (p.renormalize) {
+        const float mx = token_max<kLanes>(top);
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            if (kLanes * i < p.k) w[i] = sigmoid_ratio(w[i], mx);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
@@ -563,8 +591,8 @@ __global__ void __launch_bounds__(32 * kWarps)
         const float m = token_max<kLanes>(lj);
         s = expf(softmax_logit(lj, m) - softmax_shift(m));
     } else {
-        s = sigmoid(lj);
-        rest = __frcp_rn(1.0f + expf(lj));
+        s = p.renormalize ? sigmoid_ratio(lj, token_max<kLanes>(lj)) : sigmoid(lj);
+        rest = sigmoid(-lj);
     }
     float dot = 0.0f;
     if (p.renormalize) {
