@@ -502,7 +502,8 @@ nvfp4_status moe_route_topk(const void* logits_dev, int type, int64_t T, int E, 
  * and 0 for every other expert.
  *  topk_ids_dev   int32 [T][k], different ids, as moe_route_topk wrote them
  *  dw_dev         float [T][k]
- *  dlogits_dev    [T][ld_out] of `type` out, the first E of each row written; ld_out >= E
+ *  dlogits_dev    [T][ld_out] of `type` out, the first E of each row written; ld_out >= E; its rows share no
+ *                 byte with the logits' (NVFP4_ERR_INVALID_ARG)
  * Device error: NVFP4_ERR_BAD_EXPERT_ID (an id outside [0, E); its slot is left out). */
 nvfp4_status moe_route_topk_backward(const void* logits_dev, int type, int64_t T, int E, int64_t ld,
                                      const moe_route_params* params, const int32_t* topk_ids_dev,

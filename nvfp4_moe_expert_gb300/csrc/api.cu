@@ -795,6 +795,9 @@ nvfp4_status moe_route_topk_backward(const void* logits_dev, int type, int64_t T
     if (!logits_dev || !topk_ids_dev || !dw_dev || !dlogits_dev || !aligned(logits_dev, type_size(type)) ||
         !aligned(dlogits_dev, type_size(type)) || !aligned(topk_ids_dev, 4) || !aligned(dw_dev, 4))
         return NVFP4_ERR_INVALID_ARG;
+    // a row's zeros go out before its logits come in
+    const int64_t size = type_size(type);
+    if (rows_overlap(logits_dev, ld * size, E * size, dlogits_dev, ld_out * size, E * size, T)) return NVFP4_ERR_INVALID_ARG;
     int* err = device_error_ptr();
     if (!err) return NVFP4_ERR_CUDA;
     return from_cuda(launch_route_topk_backward(logits_dev, type, T, E, ld, route_params(*params), topk_ids_dev, dw_dev,

@@ -1,6 +1,6 @@
 """Outputs in the memory of the input they are computed from.
 
-The product of few tokens reads x and writes its outputs in one kernel, so through the C ABI their rows have to lie
+The routing's gradient writes a row's zeros before it reads the logits, so it cannot be taken in place.  The product of few tokens reads x and writes its outputs in one kernel, so through the C ABI their rows have to lie
 apart; the Python calls take a copy of x where they do not."""
 
 import ctypes
@@ -51,6 +51,39 @@ def test_share_memory():
     assert not share(rows(0, 256), rows(640, 256)) and share(rows(0, 256), rows(641, 256))
     assert share(rows(0, 200, T=1), rows(127, 300, T=1)) and not share(rows(0, 200, T=1), rows(128, 300, T=1))
     assert not share(rows(0, 128, T=0), rows(0, 128, T=0))
+
+
+def test_routing_gradient_refuses_its_logits_memory(lib):
+    p = M.moe_route_params(0, 4, 1, 1, 0, 1, 1.0)
+    base = 1 << 20
+
+    def call(x, out, T=8, E=64, ld=64, ldo=64):
+        x, out = ctypes.c_void_p(x), ctypes.c_void_p(out)
+        return lib.moe_route_topk_backward(x, 0, T, E, ld, p, ctypes.c_void_p(4096), ctypes.c_void_p(4096), out, ldo, None)
+    for score in (0, 1):
+        for renormalize in (0, 1):
+            p.score, p.renormalize = score, renormalize
+            assert call(base, base) == ARG and call(base, base, T=1) == ARG
+            assert call(base, base + 252, ld=128, ldo=128) == ARG and call(base, base + 8 * 256 - 4) == ARG
+            assert call(base, base + 4096, T=64, ld=64, ldo=128) == ARG
+
+
+@pytest.mark.gpu
+def test_routing_gradient_beside_its_logits(lib):
+    # logits and gradient as column blocks of one buffer
+    both = torch.zeros(300, 256, device="cuda")
+    l = torch.randn(300, 128, device="cuda", generator=torch.Generator("cuda").manual_seed(5))
+    both[:, :128] = l
+    dw = torch.randn(300, 8, device="cuda", generator=torch.Generator("cuda").manual_seed(6))
+    for score in (0, 1):
+        for renormalize in (0, 1):
+            name = "sigmoid" if score else "softmax"
+            ids, _ = M.moe_route_topk(l, 8, score=name, renormalize=bool(renormalize))
+            want = M.moe_route_topk_backward(l, ids, dw, score=name, renormalize=bool(renormalize))
+            p = M.moe_route_params(score, 8, 1, 1, 0, renormalize, 1.0)
+            status = lib.moe_route_topk_backward(both.data_ptr(), 0, 300, 128, 256, p, ids.data_ptr(), dw.data_ptr(),
+                                                 both[:, 128:].data_ptr(), 256, torch.cuda.current_stream().cuda_stream)
+            assert status == OK and torch.equal(both[:, 128:], want) and torch.equal(both[:, :128], l)
 
 
 @pytest.mark.gpu
