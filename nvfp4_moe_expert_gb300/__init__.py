@@ -490,8 +490,17 @@ def _choice(name, value, table):
     return code
 
 
+def _int32(name, value):
+    """ctypes would take the low 32 bits of any whole number."""
+    if not -(1 << 31) <= value < 1 << 31:
+        raise ValueError(f"{name} must be a 32-bit number, not {value}")
+    return value
+
+
 @functools.lru_cache(maxsize=256)
 def _route_struct(score, k, n_group, topk_group, group_score, renormalize, scale):
+    for name, value in (("k", k), ("n_group", n_group), ("topk_group", topk_group)):
+        _int32(name, value)
     return moe_route_params(_choice("score", score, _SCORES), k, n_group, topk_group,
                             _choice("group_score", group_score, _GROUP_SCORES), renormalize, scale)
 
@@ -512,6 +521,7 @@ def moe_route_topk(logits, k, score="softmax", bias=None, n_group=1, topk_group=
     are divided by their sum; then multiplied by scale.  The larger first, the lower id first on
     equal values; experts with a logit of -inf are masked."""
     code, T, E, ld = _rows("logits", logits, _TYPES)
+    _int32("the number of experts", E)
     device = logits.device
     if bias is not None:
         _need("bias", bias, torch.float32, (E,), device)
@@ -530,6 +540,7 @@ def moe_route_topk_backward(logits, topk_ids, dw, score="softmax", renormalize=T
     """Gradient of moe_route_topk's weights with respect to the logits: [T, E] of the logits' type,
     from the ids it returned and dw float32 [T, k], the gradient of the weights."""
     code, T, E, ld = _rows("logits", logits, _TYPES)
+    _int32("the number of experts", E)
     device = logits.device
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids must be a 2-D tensor")
