@@ -628,10 +628,28 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 }
 }  // namespace decode
 
+// Shared memory of x and of a stage of the weights, and the stages that fit.
+template <bool kMx>
+int decode_x_bytes(int K) {
+    using F = Format<kMx>;
+    const int sf_bytes = (K + F::tile_k - 1) / F::tile_k * kSfAtomBytes;
+    return (K + kStageK - 1) / kStageK * decode::kChunkBytes + (sf_bytes + 1023) / 1024 * 1024;
+}
+template <bool kMx, int BN>
+constexpr int decode_stage_bytes() {
+    return decode::kPerD * (mma_n(BN) * kRowBytes + Format<kMx>::tiles * kSfAtomBytes);
+}
+template <bool kMx, int BN>
+int decode_stages(int K) {
+    constexpr int by_tmem = static_cast<int>(kTmemCols - 2 * mma_n(BN)) / (8 * decode::kPerD * Format<kMx>::tiles);
+    constexpr int most = by_tmem < decode::kMaxStagesD ? by_tmem : decode::kMaxStagesD;
+    const int fit = (kSmemLimit - kFixedBytes - 1024 - decode_x_bytes<kMx>(K)) / decode_stage_bytes<kMx, BN>();
+    return fit < most ? fit : most;
+}
+
 template <bool kMx, int BN>
 cudaError_t launch_decode(const LinearInput& x, const LinearArgs& a, cudaStream_t st) {
     using namespace decode;
-    using F = Format<kMx>;
     static bool ready[kMaxDevices];
     cudaError_t e = prepare(linear_decode_kernel<kMx, BN>, kSmemLimit - kFixedBytes, ready);
     if (e != cudaSuccess) return e;
@@ -652,19 +670,14 @@ cudaError_t launch_decode(const LinearInput& x, const LinearArgs& a, cudaStream_
     p.ldo = a.ldo;
     p.align = out_align(a);
     p.err = a.err;
-    const int num_ks = (a.K + kStageK - 1) / kStageK, num_st = (num_ks + kPerD - 1) / kPerD;
-    const int sf_bytes = (a.K + F::tile_k - 1) / F::tile_k * kSfAtomBytes;
-    const int x_bytes = num_ks * kChunkBytes + (sf_bytes + 1023) / 1024 * 1024;
-    const int stage_bytes = kPerD * (mma_n(BN) * kRowBytes + F::tiles * kSfAtomBytes);
+    const int num_st = (a.K + kPerD * kStageK - 1) / (kPerD * kStageK);
+    const int x_bytes = decode_x_bytes<kMx>(a.K), stage_bytes = decode_stage_bytes<kMx, BN>();
     // an MMA reads 128 rows from x's last chunk: a stage lies behind it
     static_assert(kPerD * mma_n(BN) * kRowBytes >= kBM * kRowBytes, "rows an MMA reads past x");
     p.n_tiles = (a.N + BN - 1) / BN;
     const int sms = device_sm_count();
     const int grid = p.n_tiles < sms ? p.n_tiles : sms;
-    p.stages = (kSmemLimit - kFixedBytes - 1024 - x_bytes) / stage_bytes;
-    const int by_tmem = static_cast<int>(kTmemCols - 2 * mma_n(BN)) / (8 * kPerD * F::tiles);
-    if (p.stages > kMaxStagesD) p.stages = kMaxStagesD;
-    if (p.stages > by_tmem) p.stages = by_tmem;
+    p.stages = decode_stages<kMx, BN>(a.K);
     if (p.n_tiles <= sms && p.stages > num_st) p.stages = num_st;
     const size_t smem = static_cast<size_t>(x_bytes) + static_cast<size_t>(p.stages) * stage_bytes + 1024;
     CUtensorMap mb;
@@ -733,9 +746,13 @@ cudaError_t launch_linear_x(const LinearInput& x, const LinearArgs& a, cudaStrea
     // A tile takes the time of its MMAs' issue, about the same for 32 and 64 outputs and a fifth more for 128: the
     // narrowest tile that needs one round over the SMs, or the widest.  One token MXFP4, tiles 32, 64 and 128 wide:
     // 4096 x 4096 5.3, 5.5 and 6.5 us, 8192 x 4096 8.4, 5.9 and 6.6, 20000 x 2048 9.7, 7.1 and 6.7.
+    // The widest only where two stages of its weights fit beside x: with one (MXFP4 above K = 6656, NVFP4 above 4608)
+    // each load waits for the last one's MMAs.  One token, 64 and 128 wide, MXFP4 and NVFP4: 28672 x 8192 24.7 and 41.5 us,
+    // 30.6 and 46.0; 12000 x 8192 16.7 and 20.8, 21.0 and 24.3; with two stages 28672 x 4096 14.3 and 15.8, 16.8 and 18.6.
     const int sms = device_sm_count();
     if (a.N <= 32 * sms) return a.mx ? launch_decode<true, 32>(x, a, st) : launch_decode<false, 32>(x, a, st);
-    if (a.N <= 64 * sms) return a.mx ? launch_decode<true, 64>(x, a, st) : launch_decode<false, 64>(x, a, st);
+    if (a.N <= 64 * sms || (a.mx ? decode_stages<true, 128>(a.K) : decode_stages<false, 128>(a.K)) < 2)
+        return a.mx ? launch_decode<true, 64>(x, a, st) : launch_decode<false, 64>(x, a, st);
     return a.mx ? launch_decode<true, 128>(x, a, st) : launch_decode<false, 128>(x, a, st);
 }
 
