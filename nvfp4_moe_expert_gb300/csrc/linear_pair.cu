@@ -349,9 +349,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (lane == 0) arrive_leader(empty_bar);
             if (row0 >= p.T || n0 >= p.N) continue;    // the whole warp
             // the column quarters' stores spread over the next tile's main loop (about half of it), if there is one:
-            // all at once, in every SM at about the same time, they hold its loads up (8192^3 MXFP4 189 -> 185 us,
-            // 32768 x 4096 x 1536 NVFP4 121 -> 115.5 us; spread over all of it 190 and 115.4)
-            if (t + step < p.tiles) {
+            // all at once, in every SM at about the same time, they hold its loads up (8192^3 MXFP4 176.5 -> 171 us of a
+            // call on the device, with FP32 outputs 201.5 -> 192.5; 32768 x 4096 x 1536 NVFP4 108.5 -> 106.5 and 142.5 -> 135.5;
+            // 16384 x 4096 x 512 30.7 -> 29.9; 4096 x 4096 x 65536 452 and 454; spread over all of the main loop no
+            // better).  Outputs that go row by row take long enough by themselves (with the delay 8192 x 1999 x 2048 27.2 ->
+            // 28.4 us, 16384 x 4095 x 1024 NVFP4 to FP32 91 -> 103).
+            if (kStaged && t + step < p.tiles) {
                 const uint32_t start = cycles32();
                 while (cycles32() - start < static_cast<uint32_t>(sub * num_ks * 64)) __nanosleep(64);
             }
