@@ -166,8 +166,7 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _current_device():
-    return torch._C._cuda_getDevice()
+_current_device = torch._C._cuda_getDevice
 
 
 # The library launches on the current device: on memory or a stream of another one a kernel would fault, or run
@@ -474,7 +473,8 @@ def _rows(name, t, types):
     ld, step = t.stride()
     if not t.is_cuda or (step != 1 and rows and cols > 1):
         raise ValueError(f"{name} must be a CUDA tensor with contiguous rows")
-    _on_device(t)
+    if t.get_device() != _current_device():
+        _on_device(t)
     return code, rows, cols, ld if rows > 1 else cols
 
 
@@ -521,7 +521,8 @@ def moe_route_topk(logits, k, score="softmax", bias=None, n_group=1, topk_group=
     are divided by their sum; then multiplied by scale.  The larger first, the lower id first on
     equal values; experts with a logit of -inf are masked."""
     code, T, E, ld = _rows("logits", logits, _TYPES)
-    _int32("the number of experts", E)
+    if E > 0x7FFFFFFF:
+        _int32("the number of experts", E)
     device = logits.device
     if bias is not None:
         _need("bias", bias, torch.float32, (E,), device)
@@ -540,7 +541,8 @@ def moe_route_topk_backward(logits, topk_ids, dw, score="softmax", renormalize=T
     """Gradient of moe_route_topk's weights with respect to the logits: [T, E] of the logits' type,
     from the ids it returned and dw float32 [T, k], the gradient of the weights."""
     code, T, E, ld = _rows("logits", logits, _TYPES)
-    _int32("the number of experts", E)
+    if E > 0x7FFFFFFF:
+        _int32("the number of experts", E)
     device = logits.device
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids must be a 2-D tensor")

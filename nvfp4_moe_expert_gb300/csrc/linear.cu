@@ -11,8 +11,9 @@
 // TMEM and issues the K=64 MMAs (M=128, N=BN) into one of two FP32 TMEM accumulators; warps 2-5 apply the outer scales
 // and the bias and write their rows.  All waits are bounded (NVFP4_ERR_DEVICE_TIMEOUT, then a clean exit).
 //
-// What bounds it: the weights' bytes for few tokens (64 x 8192 x 8192 MXFP4, 37 MB: 10.1 us with the quantisation of
-// x, 3.7 TB/s), the way of the operands into the SM for more (512 x 4096 x 8192: 13.1 us, 2.6 PFLOP/s).
+// What bounds it: the way of the operands into the SM.  64 x 8192 x 8192 MXFP4 take 11.9 us on the device, 2.0 of them the
+// quantisation of x, for 37 MB of weights (5.5 us at the copy rate): 128 SMs have a tile each and take in a row of x for
+// every row of the weights.  512 x 4096 x 8192: 14.2 us, 2.9 of them x, 2.4 PFLOP/s.
 //
 // K is walked 0..K-1 in 64-wide steps into one accumulator whatever the kernel and the tile, so a token's output
 // does not depend on how many tokens there are.

@@ -133,10 +133,12 @@ __device__ __forceinline__ float sigmoid_ratio(float l, float m) {
 // by a bit mask) and each is ranked against the others.  Where more than 32 reach it (many equal keys, few lanes with
 // keys), the picks are taken one by one.
 //
-// Bound by instructions: 525 to a token of 256 experts in 8 groups with a bias, beside the 1 KB that is read (65537 of
-// them take 40 us; 121 at first, with one reduction and a search of all keys for each pick; 70 with each lane's keys
-// sorted; 47 with one token to a warp; 52 with 8 lanes and 32 experts to a lane, whose registers leave too few warps).
-// Groups that are not whole lanes cost a third more (8 of 31: 54 us; 84 with a lane to a group).
+// Bound by instructions: 595 to a token of 256 experts in 8 groups with sigmoids and a bias, beside the 1 KB that is read
+// (65537 of them take 44.8 us, 73% of the issue slots; measured against today's form when its scores were approximate and
+// it took 40: 121 with one reduction and a search of all keys for each pick, 70 with each lane's keys sorted, 47 with one
+// token to a warp, 52 with 8 lanes and 32 experts to a lane, whose registers leave too few warps).  Groups that are not
+// whole lanes cost a third more (8 of 31: 60.3 us).  Smaller batches are bound by latency: 16384 x 128 BF16 5.7 us with
+// 3.4 blocks to an SM, 53% of the issue slots.
 template <int V, int kLanes>
 struct Shared {
     static constexpr int tokens = 32 / kLanes;
@@ -541,8 +543,8 @@ __global__ void __launch_bounds__(32 * kWarps)
 // The row is written with what an expert that was not chosen gets, in words of four experts side by side (kN elements to
 // a load and store), and the chosen ones over it.
 //
-// Bound by memory: the row written (and, for the softmax over all experts, read).  4096 x 128 in FP32, 2 MB: 4.5 us,
-// the time of a launch and its three dependent loads.
+// Small batches take the time of a launch and its three dependent loads (4096 x 128 in FP32: 2.4 us); large ones are
+// bound by the row written (and, for the softmax over all experts, read).
 
 // Slot j's expert, g = scale * dw and logit; -1, 0 and -inf where there is none.
 template <typename T>
@@ -572,9 +574,10 @@ __device__ __forceinline__ void zero_span(uint8_t* p, int bytes) {
 }
 
 // Every weight but the softmax's over all experts: only the chosen logits take part.  A token is taken by kLanes >= k
-// lanes, slot j in lane j; the warp writes its tokens' zeros first, which waits for nothing.  (With one token to a
-// warp 65537 x 256 took 21.4 us instead of 16.0, with the zeros of odd rows element by element 65537 x 251 in BF16 21.5
-// instead of 9.1.)
+// lanes, slot j in lane j; the warp writes its tokens' zeros first, which waits for nothing.  65537 x 256 in FP32 take
+// 16.8 us for the 73 MB they cannot do without (4.4 TB/s): without the zeros it is 10.8, without the loads of the logits
+// (a sector each) 11.1, so the one waits for most of the other.  (With one token to a warp 21.4 us, and with the zeros
+// of odd rows element by element 65537 x 251 in BF16 21.5 instead of 10.2.)
 template <typename T, int kLanes>
 __global__ void __launch_bounds__(32 * kWarps)
     route_topk_backward_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, RouteParams p,
