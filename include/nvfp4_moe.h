@@ -509,6 +509,47 @@ nvfp4_status moe_route_topk_backward(const void* logits_dev, int type, int64_t T
                                      const moe_route_params* params, const int32_t* topk_ids_dev,
                                      const float* dw_dev, void* dlogits_dev, int64_t ld_out, void* stream);
 
+/* ---- Balance loss of a router ------------------------------------------------------------
+ * What a trainer of the router needs beside its route: how often each expert was chosen, how much
+ * probability it got, and the loss that pulls the two even, for each of S packed sequences.
+ *   p_te = softmax(l_t)_e, or sigmoid(l_te) / sum_j sigmoid(l_tj); 0 for a masked expert (l_te = -inf or
+ *          NaN); a row whose experts are all masked, or of sigmoids all lie below -709, has p = 0
+ *   of the n tokens of a sequence whose mask is not 0:
+ *   c_e  = the slots j < k with topk_ids[t, j] = e,  P_e = (1/n) sum_t p_te
+ *   loss = E / (k n) sum_e c_e P_e                   (1 where both are even; 0 where n = 0)
+ * The sums are FP32, taken in one order for one batch.  The gradient (the counts have none), with
+ * g_e = dloss E c_e / (k n^2):
+ *   softmax  dl_te = p_te (g_e - sum_j g_j p_tj)
+ *   sigmoid  dl_te = p_te (1 - sigmoid(l_te)) (g_e - sum_j g_j p_tj)
+ * and 0 for masked experts, masked tokens and rows of no sequence.  It takes counts and tokens as
+ * inputs: sums of them over the ranks or micro-batches of a larger batch give this batch's part of
+ * the gradient of the larger one's loss.
+ *  logits_dev       [T][ld] of `type`, the first E of each row used; element aligned; 0 <= T < 2^31 - 256,
+ *                   1 <= E <= 1024, ld >= E
+ *  score            MOE_SCORE_*
+ *  topk_ids_dev     int32 [T][k], 1 <= k <= min(E, 32)
+ *  mask_dev         uint8 [T], or NULL (every token counts); a masked token's logits and ids are not read
+ *  seq_offsets_dev  int32 [S + 1], ascending, inside [0, T]: sequence s has the rows [offset s, offset s + 1);
+ *                   rows in front of the first and behind the last belong to none.  NULL: S = 1, all rows
+ *  S                1 <= S < 2^27
+ *  loss_dev         float [S], counts_dev int32 [S][E], probs_dev float [S][E] (P), tokens_dev int32 [S] (n), out
+ * Device errors: NVFP4_ERR_NONFINITE (a logit is NaN or +inf; +inf as the limit of large logits),
+ * NVFP4_ERR_BAD_EXPERT_ID (an id outside [0, E); it is not counted). */
+nvfp4_status moe_balance_loss(const void* logits_dev, int type, int64_t T, int E, int64_t ld, int score,
+                              const int32_t* topk_ids_dev, int k, const uint8_t* mask_dev,
+                              const int32_t* seq_offsets_dev, int64_t S, float* loss_dev, int32_t* counts_dev,
+                              float* probs_dev, int32_t* tokens_dev, void* stream);
+/*  counts_dev, tokens_dev   int32 [S][E] and [S], as above or sums of several batches'
+ *  dloss_dev                float [S], the gradient of each loss
+ *  dlogits_dev              [T][ld_out] of `type`, ld_out >= E, the first E of each row; its rows share no byte with
+ *                           the logits' (NVFP4_ERR_INVALID_ARG).  accumulate 0: written; 1: added to, in FP32 with
+ *                           one rounding (moe_route_topk_backward's output, for one), rows without a gradient as they were
+ * Device error: NVFP4_ERR_NONFINITE. */
+nvfp4_status moe_balance_loss_backward(const void* logits_dev, int type, int64_t T, int E, int64_t ld, int score, int k,
+                                       const uint8_t* mask_dev, const int32_t* seq_offsets_dev, int64_t S,
+                                       const int32_t* counts_dev, const int32_t* tokens_dev, const float* dloss_dev,
+                                       void* dlogits_dev, int64_t ld_out, int accumulate, void* stream);
+
 /* ---- Dense 4-bit products ----------------------------------------------------------------
  * "MXFP4 rows": E2M1 elements in the code layout above, and one E8M0 scale (value 2^(code - 127),
  * 255 = NaN) per 32 elements: code = clamp(floor(log2 max|x|) - 2 + 127, 0, 254), 0 for a zero

@@ -11,13 +11,15 @@ entry points have the names of the C ABI in ``include/nvfp4_moe.h``:
     moe_router_topk, the fixed-capacity moe_*_masked calls, the
     straight-through backward: moe_backward_layout_query,
     moe_backward_workspace_bytes, moe_expert_backward_ste, routing of given
-    logits: moe_route_topk, moe_route_topk_backward, and dense 4-bit products:
+    logits: moe_route_topk, moe_route_topk_backward, a router's balance loss:
+    moe_balance_loss, moe_balance_loss_backward, and dense 4-bit products:
     mxfp4_quantize_rows, mxfp4_dequantize_rows, mxfp4_linear, nvfp4_linear
 
 There is no CPU fallback: if the library is missing or a call fails, an
 exception is raised.  Tensors and streams have to belong to the current device.
 """
 
+import collections
 import ctypes
 import functools
 import os
@@ -123,6 +125,9 @@ _SIGNATURES = {
     "moe_route_topk": (_I32, [_P, _I32, _I64, _I32, _I64, ctypes.POINTER(moe_route_params), _P, _P, _P, _P]),
     "moe_route_topk_backward": (_I32, [_P, _I32, _I64, _I32, _I64, ctypes.POINTER(moe_route_params), _P, _P, _P, _I64,
                                        _P]),
+    "moe_balance_loss": (_I32, [_P, _I32, _I64, _I32, _I64, _I32, _P, _I32, _P, _P, _I64, _P, _P, _P, _P, _P]),
+    "moe_balance_loss_backward": (_I32, [_P, _I32, _I64, _I32, _I64, _I32, _I32, _P, _P, _I64, _P, _P, _P, _P, _I64, _I32,
+                                         _P]),
     "mxfp4_sf_bytes": (_SZ, [_I64, _I64]),
     "mxfp4_quantize_rows": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _P, _P]),
     "mxfp4_dequantize_rows": (_I32, [_P, _P, _I64, _I64, _P, _I32, _I64, _P]),
@@ -555,6 +560,81 @@ def moe_route_topk_backward(logits, topk_ids, dw, score="softmax", renormalize=T
                                            dlogits.data_ptr(), E, _raw_stream(stream, logits))
     if status:
         _check("moe_route_topk_backward", status)
+    return dlogits
+
+
+# ---------------------------------------------------------------- balance loss of a router
+MoEBalance = collections.namedtuple("MoEBalance", ("loss", "counts", "probs", "tokens"))
+
+
+def _balance_rows(logits, score, mask, seq_offsets):
+    """What both calls take of the logits, the mask and the sequences."""
+    code, T, E, ld = _rows("logits", logits, _TYPES)
+    if E > 0x7FFFFFFF:
+        _int32("the number of experts", E)
+    device = logits.device
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("mask must be a bool or uint8 tensor")
+        _need("mask", mask, mask.dtype, (T,), device)
+    S = 1
+    if seq_offsets is not None:
+        if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+            raise ValueError("seq_offsets must be a 1-D tensor of two offsets at least")
+        S = seq_offsets.shape[0] - 1
+        _need("seq_offsets", seq_offsets, torch.int32, (S + 1,), device)
+    return (code, T, E, ld, _choice("score", score, _SCORES), None if mask is None else mask.data_ptr(),
+            None if seq_offsets is None else seq_offsets.data_ptr(), S)
+
+
+def moe_balance_loss(logits, topk_ids, score="softmax", mask=None, seq_offsets=None, stream=None):
+    """Balance loss of a router: MoEBalance(loss float32 [S], counts int32 [S, E], probs float32
+    [S, E], tokens int32 [S]) of each of S sequences, loss = E / (k n) sum_e counts_e probs_e.
+
+    logits [T, E] float32, bfloat16 or float16, contiguous rows; topk_ids int32 [T, k], the experts
+    chosen; score "softmax" or "sigmoid" (divided by their sum over the experts); probs are their means
+    over the n tokens; mask bool or uint8 [T]: a token of 0 does not count; seq_offsets int32
+    [S + 1], ascending row offsets (None: one sequence of all rows)."""
+    code, T, E, ld, kind, mask_ptr, seq_ptr, S = _balance_rows(logits, score, mask, seq_offsets)
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be a 2-D tensor")
+    k, device = _int32("k", topk_ids.shape[1]), logits.device
+    _need("topk_ids", topk_ids, torch.int32, (T, k), device)
+    loss = _empty((S,), torch.float32, device, stream)
+    counts = _empty((S, E), torch.int32, device, stream)
+    probs = _empty((S, E), torch.float32, device, stream)
+    tokens = _empty((S,), torch.int32, device, stream)
+    status = lib().moe_balance_loss(logits.data_ptr(), code, T, E, ld, kind, topk_ids.data_ptr(), k, mask_ptr, seq_ptr,
+                                    S, loss.data_ptr(), counts.data_ptr(), probs.data_ptr(), tokens.data_ptr(),
+                                    _raw_stream(stream, logits))
+    if status:
+        _check("moe_balance_loss", status)
+    return MoEBalance(loss, counts, probs, tokens)
+
+
+def moe_balance_loss_backward(logits, k, counts, tokens, dloss, score="softmax", mask=None, seq_offsets=None, dlogits=None,
+                              stream=None):
+    """Gradient of moe_balance_loss's losses with respect to the logits, from its counts and tokens
+    (or their sums over the ranks or micro-batches of a larger batch) and dloss float32 [S], the
+    gradient of each loss; rows that do not count get 0.  Returns [T, E] of the logits' type, or
+    adds to dlogits (moe_route_topk_backward's result, for one), in float32 with one rounding."""
+    code, T, E, ld, kind, mask_ptr, seq_ptr, S = _balance_rows(logits, score, mask, seq_offsets)
+    k, device = _int32("k", index(k)), logits.device
+    _need("counts", counts, torch.int32, (S, E), device)
+    _need("tokens", tokens, torch.int32, (S,), device)
+    _need("dloss", dloss, torch.float32, (S,), device)
+    add = dlogits is not None
+    if add:
+        out_code, rows, cols, ldo = _rows("dlogits", dlogits, _TYPES)
+        if out_code != code or rows != T or cols != E or dlogits.device != device:
+            raise ValueError(f"dlogits must be {logits.dtype} [{T}, {E}] on {device}")
+    else:
+        dlogits, ldo = _empty((T, E), logits.dtype, device, stream), E
+    status = lib().moe_balance_loss_backward(logits.data_ptr(), code, T, E, ld, kind, k, mask_ptr, seq_ptr, S,
+                                             counts.data_ptr(), tokens.data_ptr(), dloss.data_ptr(), dlogits.data_ptr(), ldo,
+                                             1 if add else 0, _raw_stream(stream, logits))
+    if status:
+        _check("moe_balance_loss_backward", status)
     return dlogits
 
 

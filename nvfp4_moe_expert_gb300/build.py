@@ -19,6 +19,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libnvfp4moe.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["quant.cu", "gemm.cu", "combine.cu", "router.cu", "api.cu", "route_noalloc.cu", "backward.cu", "route_topk.cu",
+           "balance.cu",
            "mxfp4.cu", "linear.cu", "linear_pair.cu", "linear_quant.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", BUILD_DIR]

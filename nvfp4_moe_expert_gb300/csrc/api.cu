@@ -804,6 +804,56 @@ nvfp4_status moe_route_topk_backward(const void* logits_dev, int type, int64_t T
                                                 dlogits_dev, ld_out, err, static_cast<cudaStream_t>(stream)));
 }
 
+// ---- balance loss of a router
+
+namespace {
+
+// What both calls refuse by shape; T == 0 has its outputs too.
+bool balance_shape_ok(int type, int64_t T, int E, int64_t ld, int score, int k, const int32_t* offsets, int64_t S) {
+    return T >= 0 && T < kMaxTokens && E >= 1 && E <= 1024 && ld >= E && rows_ok(T, ld) && type_ok(type) &&
+           (score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID) && k >= 1 && k <= 32 && k <= E && S >= 1 &&
+           S < (int64_t(1) << 27) && (offsets || S == 1);
+}
+
+}  // namespace
+
+nvfp4_status moe_balance_loss(const void* logits_dev, int type, int64_t T, int E, int64_t ld, int score,
+                              const int32_t* topk_ids_dev, int k, const uint8_t* mask_dev,
+                              const int32_t* seq_offsets_dev, int64_t S, float* loss_dev, int32_t* counts_dev,
+                              float* probs_dev, int32_t* tokens_dev, void* stream) {
+    if (!balance_shape_ok(type, T, E, ld, score, k, seq_offsets_dev, S)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if ((T > 0 && (!logits_dev || !topk_ids_dev)) || !loss_dev || !counts_dev || !probs_dev || !tokens_dev ||
+        !aligned(logits_dev, type_size(type)) || !aligned(topk_ids_dev, 4) || !aligned(seq_offsets_dev, 4) ||
+        !aligned(loss_dev, 4) || !aligned(counts_dev, 4) || !aligned(probs_dev, 4) || !aligned(tokens_dev, 4))
+        return NVFP4_ERR_INVALID_ARG;
+    int* err = device_error_ptr();
+    if (!err) return NVFP4_ERR_CUDA;
+    return from_cuda(launch_balance_loss(logits_dev, type, {T, E, ld, score, k, topk_ids_dev, mask_dev, seq_offsets_dev, S},
+                                         loss_dev, counts_dev, probs_dev, tokens_dev, err,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status moe_balance_loss_backward(const void* logits_dev, int type, int64_t T, int E, int64_t ld, int score, int k,
+                                       const uint8_t* mask_dev, const int32_t* seq_offsets_dev, int64_t S,
+                                       const int32_t* counts_dev, const int32_t* tokens_dev, const float* dloss_dev,
+                                       void* dlogits_dev, int64_t ld_out, int accumulate, void* stream) {
+    if (!balance_shape_ok(type, T, E, ld, score, k, seq_offsets_dev, S) || ld_out < E || !rows_ok(T, ld_out) ||
+        (accumulate != 0 && accumulate != 1))
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return NVFP4_OK;
+    if (!logits_dev || !counts_dev || !tokens_dev || !dloss_dev || !dlogits_dev || !aligned(logits_dev, type_size(type)) ||
+        !aligned(dlogits_dev, type_size(type)) || !aligned(seq_offsets_dev, 4) || !aligned(counts_dev, 4) ||
+        !aligned(tokens_dev, 4) || !aligned(dloss_dev, 4))
+        return NVFP4_ERR_INVALID_ARG;
+    const int64_t size = type_size(type);
+    if (rows_overlap(logits_dev, ld * size, E * size, dlogits_dev, ld_out * size, E * size, T)) return NVFP4_ERR_INVALID_ARG;
+    int* err = device_error_ptr();
+    if (!err) return NVFP4_ERR_CUDA;
+    return from_cuda(launch_balance_loss_backward(logits_dev, type, {T, E, ld, score, k, nullptr, mask_dev, seq_offsets_dev, S},
+                                                  counts_dev, tokens_dev, dloss_dev, dlogits_dev, ld_out, accumulate != 0, err,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
 size_t mxfp4_sf_bytes(int64_t rows, int64_t cols) {
     if (!mx_shape_ok(rows, cols)) return 0;
     return static_cast<size_t>(nvfp4_rows_padded(rows) / kTileM) * mx_sf_tiles(cols) * kSfAtomBytes;

@@ -1,4 +1,4 @@
-// Host launchers of the routing operators and of the dense 4-bit products (each defined in the
+// Host launchers of the routing operators, of the dense 4-bit products and of what stands beside them (each defined in the
 // .cu that holds its kernels).  Arguments have been checked by the C entry points.
 #pragma once
 
@@ -22,6 +22,26 @@ cudaError_t launch_route_topk(const void* logits, int type, int64_t T, int E, in
 cudaError_t launch_route_topk_backward(const void* logits, int type, int64_t T, int E, int64_t ld,
                                        const RouteParams& p, const int32_t* ids, const float* dw, void* dl,
                                        int64_t ld_out, int* err, cudaStream_t st);
+
+// Rows of a balance loss: logits [T][ld] of NVFP4_TYPE_*, ids [T][k], mask [T] or nullptr, offsets [S + 1] or nullptr (one
+// sequence of all rows)
+struct BalanceArgs {
+    int64_t T;
+    int E;
+    int64_t ld;
+    int score, k;
+    const int32_t* ids;
+    const uint8_t* mask;
+    const int32_t* offsets;
+    int64_t S;
+};
+// loss, tokens [S]; counts, probs [S][E]
+cudaError_t launch_balance_loss(const void* logits, int type, const BalanceArgs& a, float* loss, int32_t* counts,
+                                float* probs, int32_t* tokens, int* err, cudaStream_t st);
+// dl [T][ld_out], the logits' type; a.ids unused
+cudaError_t launch_balance_loss_backward(const void* logits, int type, const BalanceArgs& a, const int32_t* counts,
+                                         const int32_t* tokens, const float* dloss, void* dl, int64_t ld_out,
+                                         bool accumulate, int* err, cudaStream_t st);
 
 // Columns of one 512-byte scale tile: 4 scales of 16 (NVFP4) or 32 (MXFP4) elements.
 constexpr int kMxBlock = 32;
