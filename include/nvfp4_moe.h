@@ -607,6 +607,54 @@ nvfp4_status mxfp4_linear(const fp4_linear_weights* w, const void* x_dev, int x_
                           const float* bias_dev, void* out_dev, int out_type, int64_t ldo, void* ws_dev,
                           size_t ws_bytes, void* stream);
 
+/* ---- Low-rank adapters beside a shared projection ------------------------------------------
+ * Adapters of many requests at once, added to the outputs of a projection that all of them share
+ * (nvfp4_linear or mxfp4_linear, whose 4-bit weights stay as they are):
+ *   h_t = A_a x_t,   out_t = y_t + scale_a B_a h_t,   a = adapter_ids[t]; out_t = y_t where a is negative
+ * The products accumulate in FP32, h stays FP32 between them (held as sums of 16-bit terms), y is added
+ * in FP32 and the sum is rounded once to the outputs' type.  K is summed in an order that goes by K alone:
+ * a token's row does not depend on T, on the other tokens or on their order. */
+typedef struct {
+    const void* down;     /* A: [L][R][K] of `type`, 16-byte aligned */
+    const void* up;       /* B: [L][N][R] of `type`, 16-byte aligned */
+    const float* scale;   /* [L], or NULL: 1 */
+    int32_t type;         /* NVFP4_TYPE_BF16 or NVFP4_TYPE_F16 */
+    int32_t L, R;         /* 1 <= L <= 1024 adapters of rank R, a multiple of 8, 8 <= R <= 128 (an adapter of a
+                             lower rank has rows of zeros) */
+    int64_t K, N;         /* K % 8 == 0, 8 <= K <= 2^20; 1 <= N <= 2^20 */
+} lora_adapters;
+
+/*  x_dev            [T][ldx] of the adapters' type, 16-byte aligned, ldx % 8 == 0, ldx >= K; 0 <= T < 2^31 - 256
+ *  adapter_ids_dev  int32 [T]; negative: no adapter
+ *  y_dev            [T][ldy], out_dev [T][ldo], both of out_type (any of NVFP4_TYPE_*), element aligned, ld >= N.
+ *                   out may be y itself (the same pointer and pitch; rows without an adapter stay as they are); otherwise
+ *                   its rows share no byte with y's, and never one with x's (NVFP4_ERR_INVALID_ARG)
+ *  h_dev            float [T][R] out, 16-byte aligned, or NULL: h (zeros where there is no adapter), what
+ *                   lora_add_backward takes
+ *  ws_dev           lora_add_workspace_bytes(T, L) bytes, 256-byte aligned; NULL where that is 0 (few tokens)
+ * Device error: NVFP4_ERR_BAD_EXPERT_ID (an adapter id of L or more; its row is as without an adapter). */
+size_t lora_add_workspace_bytes(int64_t T, int L);
+nvfp4_status lora_add(const lora_adapters* adapters, const void* x_dev, int64_t T, int64_t ldx,
+                      const int32_t* adapter_ids_dev, const void* y_dev, int64_t ldy, void* out_dev, int64_t ldo,
+                      int out_type, float* h_dev, void* ws_dev, size_t ws_bytes, void* stream);
+
+/* The gradient of lora_add (with respect to y it is dy itself):
+ *   dh_t = scale_a B_a^T dy_t,  dx_t (+)= A_a^T dh_t,  ddown_a = sum_t dh_t x_t^T,  dup_a = sum_t scale_a dy_t h_t^T
+ * over the tokens of adapter a, in their order; FP32 sums, no atomics: the same bits for the same call.
+ *  adapters       of NVFP4_TYPE_BF16
+ *  dy_dev         BF16 [T][lddy], element aligned, lddy >= N;  x_dev, adapter_ids_dev as above, BF16
+ *  h_dev          float [T][R] as lora_add wrote it, 16-byte aligned
+ *  dx_dev         [T][lddx] of dx_type, element aligned, lddx >= K; shares no byte with dy or x.  accumulate 0:
+ *                 written (zeros where there is no adapter); 1: added to, in FP32 with one rounding
+ *  ddown_dev      float [L][R][K], dup_dev float [L][N][R], written whole (zeros for adapters without tokens)
+ *  ws_dev         lora_add_backward_workspace_bytes(T, L, R) bytes, 256-byte aligned
+ * Device error: NVFP4_ERR_BAD_EXPERT_ID. */
+size_t lora_add_backward_workspace_bytes(int64_t T, int L, int R);
+nvfp4_status lora_add_backward(const lora_adapters* adapters, const void* dy_dev, int64_t lddy, const void* x_dev,
+                               int64_t ldx, const float* h_dev, const int32_t* adapter_ids_dev, int64_t T, void* dx_dev,
+                               int64_t lddx, int dx_type, int accumulate, float* ddown_dev, float* dup_dev, void* ws_dev,
+                               size_t ws_bytes, void* stream);
+
 /* nvfp4_silu_table -- the SiLU that the FC1 epilogue applies to its BF16 gate values
  * ([RL/4.4]: SiLU(gate)*up in FP32), evaluated by the epilogue's own code for every input:
  * out_dev float [65536], entry i = silu(a) for the BF16 value a whose bit pattern is i, where

@@ -12,8 +12,9 @@ entry points have the names of the C ABI in ``include/nvfp4_moe.h``:
     straight-through backward: moe_backward_layout_query,
     moe_backward_workspace_bytes, moe_expert_backward_ste, routing of given
     logits: moe_route_topk, moe_route_topk_backward, a router's balance loss:
-    moe_balance_loss, moe_balance_loss_backward, and dense 4-bit products:
-    mxfp4_quantize_rows, mxfp4_dequantize_rows, mxfp4_linear, nvfp4_linear
+    moe_balance_loss, moe_balance_loss_backward, dense 4-bit products:
+    mxfp4_quantize_rows, mxfp4_dequantize_rows, mxfp4_linear, nvfp4_linear,
+    and low-rank adapters beside them: lora_add, lora_add_backward
 
 There is no CPU fallback: if the library is missing or a call fails, an
 exception is raised.  Tensors and streams have to belong to the current device.
@@ -70,6 +71,11 @@ class moe_route_params(ctypes.Structure):
 class fp4_linear_weights(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("sf", ctypes.c_void_p), ("g", ctypes.c_void_p),
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class lora_adapters(ctypes.Structure):
+    _fields_ = [("down", ctypes.c_void_p), ("up", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("type", ctypes.c_int32),
+                ("L", ctypes.c_int32), ("R", ctypes.c_int32), ("K", ctypes.c_int64), ("N", ctypes.c_int64)]
 
 
 class moe_bf16_weights_t(ctypes.Structure):
@@ -136,6 +142,11 @@ _SIGNATURES = {
     "nvfp4_linear": (_I32, [ctypes.POINTER(fp4_linear_weights), _P, _I64, _I64, _P, _P, _I32, _I64, _P, _SZ, _P]),
     "mxfp4_linear": (_I32, [ctypes.POINTER(fp4_linear_weights), _P, _I32, _I64, _I64, _P, _P, _I32, _I64, _P, _SZ,
                             _P]),
+    "lora_add_workspace_bytes": (_SZ, [_I64, _I32]),
+    "lora_add": (_I32, [ctypes.POINTER(lora_adapters), _P, _I64, _I64, _P, _P, _I64, _P, _I64, _I32, _P, _P, _SZ, _P]),
+    "lora_add_backward_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
+    "lora_add_backward": (_I32, [ctypes.POINTER(lora_adapters), _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I32, _I32, _P, _P,
+                                 _P, _SZ, _P]),
 }
 
 _lib = None
@@ -794,6 +805,103 @@ def nvfp4_linear(x, weight, bias=None, out=None, out_dtype=torch.bfloat16, strea
     to NVFP4 rows as nvfp4_quantize_rows does; a row with an Inf or NaN gives NaN.  Returns out [T, N] (of
     out_dtype if not given); out may lie in x's memory."""
     return _linear("nvfp4_linear", False, x, weight, bias, out, out_dtype, stream)
+
+
+# ---------------------------------------------------------------- low-rank adapters
+_HALVES = {torch.bfloat16: 1, torch.float16: 2}
+
+
+class LoRAAdapters:
+    """Low-rank adapters of one projection (device tensors) and the C struct pointing at them: down
+    [L, R, K] and up [L, N, R], bfloat16 or float16, contiguous (R a multiple of 8 up to 128; an adapter of a
+    lower rank has zeros behind it), scale float32 [L] (None: 1).  The tensors are used as they are at each
+    call, so in-place changes of them count."""
+
+    def __init__(self, down, up, scale=None):
+        code = _HALVES.get(down.dtype)
+        if code is None or down.dim() != 3 or not down.is_cuda:
+            raise ValueError("down must be a 3-D CUDA tensor of torch.bfloat16 or torch.float16")
+        L, R, K = down.shape
+        if up.dim() != 3:
+            raise ValueError("up must be a 3-D tensor")
+        N, device = up.shape[1], down.device
+        _need("down", down, down.dtype, (L, R, K), device)
+        _need("up", up, down.dtype, (L, N, R), device)
+        if scale is not None:
+            _need("scale", scale, torch.float32, (L,), device)
+        self.tensors = (down, up, scale)
+        self.L, self.R, self.K, self.N, self.dtype, self.device = _int32("L", L), _int32("R", R), K, N, down.dtype, device
+        self.struct = lora_adapters(down.data_ptr(), up.data_ptr(), None if scale is None else scale.data_ptr(), code, L, R, K, N)
+
+
+@functools.lru_cache(maxsize=1024)
+def _lora_workspace_bytes(T, L):
+    return lib().lora_add_workspace_bytes(T, L)
+
+
+def _lora_rows(name, t, types, T, cols, device):
+    code, rows, n, ld = _rows(name, t, types)
+    if rows != T or n != cols or t.device != device:
+        raise ValueError(f"{name} must be [{T}, {cols}] on {device}")
+    return code, ld
+
+
+def lora_add(y, x, adapters, adapter_ids, out=None, save_for_backward=False, stream=None):
+    """y + scale_a (x A_a^T) B_a^T for each row, a its adapter (adapter_ids int32 [T], negative: none, the row is y's):
+    low-rank adapters of many requests beside a shared projection's outputs y [T, N] (float32, bfloat16 or
+    float16), x [T, K] of the adapters' type, rows on 16-byte boundaries.  Returns out (of y's type;
+    out=y adds in place), and with save_for_backward h float32 [T, R] beside it, which
+    lora_add_backward takes.  A row does not depend on the others."""
+    _, T, K, ldx = _rows("x", x, _HALVES)
+    device = x.device
+    if x.dtype != adapters.dtype or K != adapters.K or device != adapters.device:
+        raise ValueError(f"x must be {adapters.dtype} [T, {adapters.K}] on {adapters.device}")
+    code, ldy = _lora_rows("y", y, _TYPES, T, adapters.N, device)
+    _need("adapter_ids", adapter_ids, torch.int32, (T,), device)
+    if out is None:
+        out, ldo = _empty((T, adapters.N), y.dtype, device, stream), adapters.N
+    else:
+        out_code, ldo = _lora_rows("out", out, _TYPES, T, adapters.N, device)
+        if out_code != code:
+            raise ValueError(f"out must be {y.dtype}")
+    h = _empty((T, adapters.R), torch.float32, device, stream) if save_for_backward else None
+    need = _lora_workspace_bytes(T, adapters.L)
+    ws = _empty((need,), torch.uint8, device, stream) if need else None
+    status = lib().lora_add(adapters.struct, x.data_ptr(), T, ldx, adapter_ids.data_ptr(), y.data_ptr(), ldy, out.data_ptr(),
+                            ldo, code, None if h is None else h.data_ptr(), ws.data_ptr() if need else None, need,
+                            _raw_stream(stream, x))
+    if status:
+        _check("lora_add", status)
+    return (out, h) if save_for_backward else out
+
+
+def lora_add_backward(dy, x, h, adapters, adapter_ids, dx=None, stream=None):
+    """Gradient of lora_add: (dx [T, K], ddown float32 [L, R, K], dup float32 [L, N, R]) from dy
+    [T, N], x and the adapters in bfloat16 and the h that lora_add returned.  dx is bfloat16 (zeros for rows
+    without an adapter), or the tensor given (float32, bfloat16 or float16), to which it is added in
+    float32 with one rounding: the shared projection's own gradient."""
+    _, T, K, ldx = _rows("x", x, _BF16)
+    device = x.device
+    if adapters.dtype != torch.bfloat16 or K != adapters.K or device != adapters.device:
+        raise ValueError(f"adapters and x must be torch.bfloat16, x [T, {adapters.K}] on {adapters.device}")
+    _, lddy = _lora_rows("dy", dy, _BF16, T, adapters.N, device)
+    _need("h", h, torch.float32, (T, adapters.R), device)
+    _need("adapter_ids", adapter_ids, torch.int32, (T,), device)
+    add = dx is not None
+    if add:
+        code, lddx = _lora_rows("dx", dx, _TYPES, T, K, device)
+    else:
+        dx, code, lddx = _empty((T, K), torch.bfloat16, device, stream), 1, K
+    ddown = _empty((adapters.L, adapters.R, K), torch.float32, device, stream)
+    dup = _empty((adapters.L, adapters.N, adapters.R), torch.float32, device, stream)
+    need = lib().lora_add_backward_workspace_bytes(T, adapters.L, adapters.R)
+    ws = _empty((need,), torch.uint8, device, stream) if need else None
+    status = lib().lora_add_backward(adapters.struct, dy.data_ptr(), lddy, x.data_ptr(), ldx, h.data_ptr(),
+                                     adapter_ids.data_ptr(), T, dx.data_ptr(), lddx, code, 1 if add else 0, ddown.data_ptr(),
+                                     dup.data_ptr(), ws.data_ptr() if need else None, need, _raw_stream(stream, x))
+    if status:
+        _check("lora_add_backward", status)
+    return dx, ddown, dup
 
 
 # ---------------------------------------------------------------- straight-through backward

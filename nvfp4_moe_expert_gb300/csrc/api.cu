@@ -906,6 +906,89 @@ nvfp4_status mxfp4_linear(const fp4_linear_weights* w, const void* x_dev, int x_
                        static_cast<cudaStream_t>(stream));
 }
 
+// ---- low-rank adapters
+
+namespace {
+
+// What both calls refuse of the adapters, first by shape, then by pointer.
+bool adapters_shape_ok(const lora_adapters& a) {
+    return (a.type == NVFP4_TYPE_BF16 || a.type == NVFP4_TYPE_F16) && a.L >= 1 && a.L <= 1024 && a.R >= 8 && a.R <= 128 &&
+           a.R % 8 == 0 && a.K >= 8 && a.K <= (int64_t(1) << 20) && a.K % 8 == 0 && a.N >= 1 && a.N <= (int64_t(1) << 20);
+}
+bool adapters_ok(const lora_adapters& a) {
+    return a.down && a.up && aligned(a.down, 16) && aligned(a.up, 16) && aligned(a.scale, 4);
+}
+
+}  // namespace
+
+size_t lora_add_workspace_bytes(int64_t T, int L) {
+    return T >= 0 && T < kMaxTokens && L >= 1 && L <= 1024 ? lora_workspace(T, L) : 0;
+}
+size_t lora_add_backward_workspace_bytes(int64_t T, int L, int R) {
+    return T > 0 && T < kMaxTokens && L >= 1 && L <= 1024 && R >= 8 && R <= 128 && R % 8 == 0 ? lora_backward_workspace(T, L, R)
+                                                                                              : 0;
+}
+
+nvfp4_status lora_add(const lora_adapters* adapters, const void* x_dev, int64_t T, int64_t ldx,
+                      const int32_t* adapter_ids_dev, const void* y_dev, int64_t ldy, void* out_dev, int64_t ldo,
+                      int out_type, float* h_dev, void* ws_dev, size_t ws_bytes, void* stream) {
+    if (!adapters) return NVFP4_ERR_INVALID_ARG;
+    const lora_adapters& a = *adapters;
+    if (!adapters_shape_ok(a) || T < 0 || T >= kMaxTokens || ldx < a.K || ldx % 8 || ldy < a.N || ldo < a.N || !type_ok(out_type) ||
+        !rows_ok(T, ldx) || !rows_ok(T, ldy) || !rows_ok(T, ldo))
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!adapters_ok(a)) return NVFP4_ERR_INVALID_ARG;
+    if (T == 0) return NVFP4_OK;
+    const size_t need = lora_workspace(T, a.L);
+    const int64_t out_size = type_size(out_type);
+    if (!x_dev || !adapter_ids_dev || !y_dev || !out_dev || (need && !ws_dev) || !aligned(x_dev, 16) ||
+        !aligned(adapter_ids_dev, 4) || !aligned(y_dev, out_size) || !aligned(out_dev, out_size) || !aligned(h_dev, 16) ||
+        !aligned(ws_dev, 256))
+        return NVFP4_ERR_INVALID_ARG;
+    if (ws_bytes < need) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
+    const bool in_place = y_dev == out_dev && ldy == ldo;
+    if ((!in_place && rows_overlap(y_dev, ldy * out_size, a.N * out_size, out_dev, ldo * out_size, a.N * out_size, T)) ||
+        rows_overlap(x_dev, ldx * 2, a.K * 2, out_dev, ldo * out_size, a.N * out_size, T))
+        return NVFP4_ERR_INVALID_ARG;
+    int* err = device_error_ptr();
+    if (!err) return NVFP4_ERR_CUDA;
+    return from_cuda(launch_lora_add({x_dev, T, ldx, a.type, a.down, a.up, a.scale, adapter_ids_dev, a.L, a.R, a.K, a.N, y_dev, ldy,
+                                      out_dev, ldo, out_type, h_dev, ws_dev, err},
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status lora_add_backward(const lora_adapters* adapters, const void* dy_dev, int64_t lddy, const void* x_dev,
+                               int64_t ldx, const float* h_dev, const int32_t* adapter_ids_dev, int64_t T, void* dx_dev,
+                               int64_t lddx, int dx_type, int accumulate, float* ddown_dev, float* dup_dev, void* ws_dev,
+                               size_t ws_bytes, void* stream) {
+    if (!adapters) return NVFP4_ERR_INVALID_ARG;
+    const lora_adapters& a = *adapters;
+    if (!adapters_shape_ok(a) || a.type != NVFP4_TYPE_BF16 || T < 0 || T >= kMaxTokens || lddy < a.N || ldx < a.K || ldx % 8 ||
+        lddx < a.K || !type_ok(dx_type) || (accumulate != 0 && accumulate != 1) || !rows_ok(T, lddy) || !rows_ok(T, ldx) ||
+        !rows_ok(T, lddx))
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!adapters_ok(a) || !ddown_dev || !dup_dev || !aligned(ddown_dev, 4) || !aligned(dup_dev, 4)) return NVFP4_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        const size_t down = sizeof(float) * a.L * a.R * a.K, up = sizeof(float) * a.L * a.R * a.N;
+        const nvfp4_status s = from_cuda(cudaMemsetAsync(ddown_dev, 0, down, st));
+        return s != NVFP4_OK ? s : from_cuda(cudaMemsetAsync(dup_dev, 0, up, st));
+    }
+    const int64_t dx_size = type_size(dx_type);
+    if (!dy_dev || !x_dev || !h_dev || !adapter_ids_dev || !dx_dev || !ws_dev || !aligned(dy_dev, 2) || !aligned(x_dev, 16) ||
+        !aligned(h_dev, 16) || !aligned(adapter_ids_dev, 4) || !aligned(dx_dev, dx_size) || !aligned(ws_dev, 256))
+        return NVFP4_ERR_INVALID_ARG;
+    if (ws_bytes < lora_backward_workspace(T, a.L, a.R)) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
+    if (rows_overlap(dy_dev, lddy * 2, a.N * 2, dx_dev, lddx * dx_size, a.K * dx_size, T) ||
+        rows_overlap(x_dev, ldx * 2, a.K * 2, dx_dev, lddx * dx_size, a.K * dx_size, T))
+        return NVFP4_ERR_INVALID_ARG;
+    int* err = device_error_ptr();
+    if (!err) return NVFP4_ERR_CUDA;
+    return from_cuda(launch_lora_add_backward({dy_dev, x_dev, T, lddy, ldx, h_dev, a.down, a.up, a.scale, adapter_ids_dev, a.L, a.R,
+                                               a.K, a.N, dx_dev, lddx, dx_type, accumulate != 0, ddown_dev, dup_dev, ws_dev, err},
+                                              st));
+}
+
 int nvfp4_last_cuda_error(void) { return static_cast<int>(t_last_cuda_error); }
 
 const char* nvfp4_cuda_error_name(int error) { return cudaGetErrorName(static_cast<cudaError_t>(error)); }

@@ -1,0 +1,367 @@
+// Low-rank adapters of many requests beside a shared projection: what its kernels share.
+//
+//   forward    h_t = A_a x_t,           y_t += s_a B_a h_t        a = adapter of token t, A [R][K], B [N][R]
+//   backward   dh_t = s_a B_a^T dy_t,   dx_t += A_a^T dh_t,   dA_a = sum_t dh_t x_t^T,  dB_a = sum_t s_a dy_t h_t^T
+//
+// Forward and dx have one shape: a row of C columns shrinks to R and expands to D columns.  Tokens of an adapter are put
+// together in tiles of 16 or 128 rows; a cluster of 8 CTAs takes a tile, each CTA an eighth of C, then an eighth of D.
+//
+// The order of the sum over C goes by C alone, so a token's row does not depend on the batch it is in: C is cut into 64
+// sub-slices of 16 ceil(C / 1024) columns; a sub-slice is one chain of m16n8k16 products from zero, the 8 sub-slices of a
+// CTA are added in order, then the 8 CTAs' sums.  mma.sync serves this better than tcgen05: a tile has as few as one real
+// row and 8 to 128 columns of accumulator, the two products together have 2 R operations to a byte that is moved, and
+// accumulators in registers need no pass through TMEM between the two products (its rate, 600 TFLOP/s measured, is enough
+// for R <= 64 at the memory's rate).
+//
+// Between the products h is FP32; the second product takes it as a sum of 16-bit terms (two for 16-bit outputs, which leaves
+// 2^-17 of h beside the output's own 2^-9; three for FP32 outputs), so h is not rounded to 16 bits.
+#pragma once
+
+#include "cluster.cuh"
+#include "common.cuh"
+#include "ops.cuh"
+#include "scores.cuh"
+
+namespace nvfp4 {
+namespace lora {
+
+constexpr int kThreads = 256, kWarps = 8;
+constexpr int kSplit = 8;                 // CTAs of a cluster
+constexpr int kFewRows = 16, kManyRows = 128;
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+// The tiles that the sort kernel lists, in the workspace.
+struct Tiles {
+    const int32_t* perm;        // [T] rows, adapter by adapter, those without one last
+    const int32_t* adapter;     // [count] -1: rows without an adapter
+    const int32_t* start;       // [count] first row of the tile in perm
+    const int32_t* offsets;     // [L + 2] first row of each adapter in perm
+    const int32_t* count;
+};
+
+struct Params {
+    const void* x;              // [T][ldx], C columns
+    int64_t ldx;
+    int x_wide;                 // rows start on 16-byte boundaries
+    const void* down;           // what x is multiplied with: [L][R][C], or [L][C][R] (transposed)
+    const void* up;             // and h: [L][D][R], or [L][R][D] (transposed)
+    const float* scale;         // [L] or nullptr
+    const int32_t* ids;         // [T]
+    const void* y;              // [T][ldy] of y_type, or nullptr (zeros)
+    void* out;                  // [T][ldo]
+    float* h;                   // [T][R] or nullptr
+    int64_t ldy, ldo;
+    int y_type, out_wide;       // out_wide: y's and out's rows start on 16-byte boundaries
+    int h_scaled;               // h holds s_a h
+    int skip_none;              // rows without an adapter need no work
+    int T, L, R, C, D;
+    Tiles tiles;
+    int* err;
+};
+
+// ------------------------------------------------------------------ pieces of the kernels
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {   // the rest of the 16 are zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma(__nv_bfloat16, float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(__half, float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Tiles of 64 16-bit columns: rows of 128 bytes, their 16-byte chunks exchanged by the row, so that the eight rows of a
+// matrix lie in different banks.
+__device__ __forceinline__ uint32_t swizzled(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+// Tiles of R columns: rows padded by 16 bytes (the eight rows of a matrix in different banks where R is a multiple of 16).
+__host__ __device__ constexpr int padded_pitch(int R) { return 2 * R + 16; }
+__host__ __device__ constexpr int rank_up(int R) { return (R + 15) / 16 * 16; }   // the second product's steps are 16 wide
+
+// Sub-slices of the first product: 64 of them, of as many steps of 16 columns.
+__host__ __device__ inline int sub_steps(int C) { return (C + 1023) / 1024; }
+
+// 16 bytes of a row of 16-bit elements from column c on (zeros from `cols` on) into shared memory.
+__device__ __forceinline__ void copy_chunk(uint32_t dst, const uint16_t* row, int c, int cols, bool wide) {
+    const int left = min(max(cols - c, 0), 8);
+    if (wide) {
+        cp_async16(dst, left ? row + c : row, 2 * left);
+        return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = 2 * i < left ? row[c + 2 * i] : 0, hi = 2 * i + 1 < left ? row[c + 2 * i + 1] : 0;
+        w[i] = lo | hi << 16;
+    }
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+
+// Operand of the first product: `cols` (a multiple of 16, at most 64) columns from c on of the adapter's matrix.
+template <bool kTrans>
+__device__ __forceinline__ void load_down(uint32_t dst, const uint16_t* down, int R, int C, int c, int cols, int thread, int threads) {
+    if (!kTrans) {                        // [R][C]: R rows of 64 columns, swizzled
+        const int q = thread & 7;
+        if (8 * q < cols) {
+            for (int r = thread >> 3; r < R; r += threads >> 3)
+                copy_chunk(dst + swizzled(r, q), down + static_cast<int64_t>(r) * C, c + 8 * q, C, true);
+        }
+    } else {                              // [C][R]: rows of R columns, padded
+        const int per = R / 8;
+        for (int i = thread; i < cols * per; i += threads) {
+            const int n = i / per, q = i % per;
+            const bool real = c + n < C;
+            cp_async16(dst + n * padded_pitch(R) + 16 * q, real ? down + static_cast<int64_t>(c + n) * R + 8 * q : down, real ? 16 : 0);
+        }
+    }
+}
+template <bool kTrans>
+__host__ __device__ constexpr int down_bytes(int R, int cols) { return kTrans ? cols * padded_pitch(R) : rank_up(R) * 128; }
+
+// Products of 16 rows x 16 columns of x (a) with step kk of the operand above: acc[j] gets ranks 8 j to 8 j + 7.
+template <typename T, bool kTrans, int kTiles>
+__device__ __forceinline__ void multiply_down(float (&acc)[kTiles][4], const uint32_t (&a)[4], uint32_t down, int kk, int R, int lane) {
+#pragma unroll
+    for (int j = 0; j < kTiles; j += 2) {
+        if (8 * j >= R) break;
+        uint32_t b[4];
+        if (!kTrans) ldsm4(down + swizzled(8 * (j + (lane >> 4)) + (lane & 7), 2 * kk + ((lane >> 3) & 1)), b);
+        else ldsm4_trans(down + (16 * kk + ((lane >> 3) & 1) * 8 + (lane & 7)) * padded_pitch(R) + 16 * (j + (lane >> 4)), b);
+        mma(T(), acc[j], a, b[0], b[1]);
+        if (8 * (j + 1) < R) mma(T(), acc[j + 1], a, b[2], b[3]);
+    }
+}
+
+// Operand of the second product: outputs [n, n + kCols) of the adapter's matrix; ranks from R to rank_up(R) are zeros.
+// Not transposed, output 8 q + 2 i + l of a group of 32 lies in row 8 i + 2 q + l: the accumulators of a lane are then 8
+// consecutive outputs of a row.
+template <bool kTrans, int kCols>
+__device__ __forceinline__ void load_up(uint32_t dst, const uint16_t* up, int R, int D, int n, int thread, int threads) {
+    const int Rp = rank_up(R);
+    if (!kTrans) {                        // [D][R]
+        const int per = Rp / 8;
+        for (int i = thread; i < kCols * per; i += threads) {
+            const int j = i / per, q = i % per, w = j & 31;
+            const int at = (j & ~31) + 8 * ((w & 7) >> 1) + 2 * (w >> 3) + (w & 1);
+            const bool real = n + j < D && 8 * q < R;
+            cp_async16(dst + at * padded_pitch(Rp) + 16 * q, real ? up + static_cast<int64_t>(n + j) * R + 8 * q : up, real ? 16 : 0);
+        }
+    } else {                              // [R][D]: rows of 64 columns, swizzled
+        for (int i = thread; i < Rp * (kCols / 8); i += threads) {
+            const int r = i / (kCols / 8), q = i % (kCols / 8);
+            if (r < R) copy_chunk(dst + swizzled(r, q), up + static_cast<int64_t>(r) * D, n + 8 * q, D, true);
+            else cp_async16(dst + swizzled(r, q), up, 0);
+        }
+    }
+}
+template <bool kTrans, int kCols>
+__host__ __device__ constexpr int up_bytes(int R) { return kTrans ? rank_up(R) * 128 : kCols * padded_pitch(rank_up(R)); }
+
+// h (16 rows from `h`, `terms` arrays of 16-bit terms that add up to it) times the operand above, group g32 of 32 outputs:
+// o[i] gets the 8 consecutive outputs 8 (lane % 4) of row lane / 4 + 8 i.
+template <typename T, bool kTrans>
+__device__ __forceinline__ void multiply_up(float (&o)[2][8], uint32_t h, int term_bytes, int terms, uint32_t up, int g32, int R, int lane) {
+    const int Rp = rank_up(R);
+    float acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+    }
+    const uint32_t ha = h + ((lane & 7) + ((lane >> 3) & 1) * 8) * padded_pitch(Rp) + 16 * (lane >> 4);
+    for (int kk = 0; kk < Rp / 16; ++kk) {
+        uint32_t b[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {     // two tiles of 8 outputs at once
+            if (!kTrans) ldsm4(up + (32 * g32 + 8 * (2 * i + (lane >> 4)) + (lane & 7)) * padded_pitch(Rp) + 16 * (2 * kk + ((lane >> 3) & 1)), b[i]);
+            else ldsm4_trans(up + swizzled(16 * kk + ((lane >> 3) & 1) * 8 + (lane & 7), 4 * g32 + 2 * i + (lane >> 4)), b[i]);
+        }
+        for (int t = 0; t < terms; ++t) {
+            uint32_t a[4];
+            ldsm4(ha + t * term_bytes + 32 * kk, a);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma(T(), acc[i], a, b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
+        }
+    }
+    if (!kTrans) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[0][2 * i] = acc[i][0], o[0][2 * i + 1] = acc[i][1];
+            o[1][2 * i] = acc[i][2], o[1][2 * i + 1] = acc[i][3];
+        }
+    } else {
+        // lane q of a quad has outputs 2 q, 2 q + 1 of four tiles and gets all 8 of tile q: a transposition in two steps,
+        // with the lane two away, then with the one beside
+        const int q = lane & 3;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float v[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i][0] = acc[i][2 * r], v[i][1] = acc[i][2 * r + 1];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int l = 0; l < 2; ++l) {
+                    const float got = __shfl_xor_sync(kAll, q & 2 ? v[i][l] : v[i + 2][l], 2);
+                    if (q & 2) v[i][l] = got;
+                    else v[i + 2][l] = got;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+#pragma unroll
+                for (int l = 0; l < 2; ++l) {
+                    const float got = __shfl_xor_sync(kAll, q & 1 ? v[i][l] : v[i + 1][l], 1);
+                    if (q & 1) v[i][l] = got;
+                    else v[i + 1][l] = got;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[r][2 * i] = v[i][0], o[r][2 * i + 1] = v[i][1];
+        }
+    }
+}
+
+// 8 consecutive elements of a row of y or out, raw (kept so while they are on their way).
+struct Eight {
+    uint4 a, b;                           // b: FP32 only
+};
+__device__ __forceinline__ uint32_t element(const void* row, int64_t i, int type) {
+    return type == NVFP4_TYPE_F32 ? static_cast<const uint32_t*>(row)[i] : static_cast<const uint16_t*>(row)[i];
+}
+__device__ __forceinline__ Eight load_eight(const void* base, int type, int64_t row, int64_t ld, int n, int D, bool wide) {
+    Eight e = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (n >= D) return e;
+    const int size = type == NVFP4_TYPE_F32 ? 4 : 2;
+    const uint8_t* p = static_cast<const uint8_t*>(base) + (row * ld + n) * size;
+    if (wide && n + 8 <= D) {
+        e.a = *reinterpret_cast<const uint4*>(p);
+        if (size == 4) e.b = *reinterpret_cast<const uint4*>(p + 16);
+        return e;
+    }
+    uint32_t w[8] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (n + i >= D) continue;
+        if (size == 4) w[i] = element(p, i, type);
+        else w[i / 2] |= element(p, i, type) << (16 * (i & 1));
+    }
+    e.a = make_uint4(w[0], w[1], w[2], w[3]);
+    e.b = make_uint4(w[4], w[5], w[6], w[7]);
+    return e;
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, int type) {
+    if (type == NVFP4_TYPE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
+    if (type == NVFP4_TYPE_BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// out = y + o, in FP32 with one rounding.
+__device__ __forceinline__ void store_eight(void* base, int type, int64_t row, int64_t ld, int n, int D, bool wide, const Eight& y,
+                                            const float (&o)[8]) {
+    if (n >= D) return;
+    uint32_t w[8];
+    if (type == NVFP4_TYPE_F32) {
+        const uint32_t v[8] = {y.a.x, y.a.y, y.a.z, y.a.w, y.b.x, y.b.y, y.b.z, y.b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(v[i]) + o[i]);
+    } else {
+        const uint32_t v[4] = {y.a.x, y.a.y, y.a.z, y.a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2(v[i], type);
+            w[i] = pack2(f.x + o[2 * i], f.y + o[2 * i + 1], type);
+        }
+    }
+    const int size = type == NVFP4_TYPE_F32 ? 4 : 2;
+    uint8_t* p = static_cast<uint8_t*>(base) + (row * ld + n) * size;
+    if (wide && n + 8 <= D) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (size == 4) *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (n + i >= D) continue;
+        if (size == 4) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+        else reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// The 16-bit terms of v: v = t0 + t1 (+ t2) but for the last one's rounding.  Where a term is infinite the rest is 0.
+template <typename T>
+__device__ __forceinline__ uint16_t next_term(float& v) {
+    const T t = from_f32<T>(v);
+    const float f = to_f32(t), left = v - f;
+    v = fabsf(f) == INFINITY ? 0.0f : left;
+    return *reinterpret_cast<const uint16_t*>(&t);
+}
+// FP16 has no room for h of any size: its rows are scaled by a power of two that puts their largest value near 2^14
+// (exact, and undone in FP32 behind the product).  The exponent that is taken out of a row whose largest |h| is m.
+__device__ __forceinline__ int row_exponent(float m) {
+    if (!(m > 0.0f) || m == INFINITY) return 0;
+    return max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100) - 14;
+}
+
+// A row of h: lane l of 16 sums the 8 CTAs' parts of columns l, l + 16, ... in their order, and writes the row's terms to
+// `dst` (a shared-memory address in the cluster, or one for every CTA of it).
+template <typename T, int kRank, typename Store>
+__device__ __forceinline__ void finish_row(const float* part, int row, int pitch, int R, float scale, int terms, int term_bytes,
+                                           float* h_out, bool h_scaled, int l, Store&& store, float& undo) {
+    constexpr int kMine = kRank / 16;
+    float v[kMine], m = 0.0f;
+    uint32_t from[kSplit];
+#pragma unroll
+    for (int c = 0; c < kSplit; ++c) from[c] = cluster_addr(part, c) + 4 * row * pitch;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int r = l + 16 * i;
+        v[i] = 0.0f;
+        if (r < R) {
+            v[i] = cluster_load_f32(from[0] + 4 * r);
+#pragma unroll
+            for (int c = 1; c < kSplit; ++c) v[i] += cluster_load_f32(from[c] + 4 * r);
+            const float scaled = v[i] * scale;
+            if (h_out != nullptr) h_out[r] = h_scaled ? scaled : v[i];
+            v[i] = scaled;
+        }
+        m = fmaxf(m, fabsf(v[i]));
+    }
+    undo = 1.0f;
+    if (sizeof(T) == 2 && std::is_same<T, __half>::value) {
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        const int e = row_exponent(m);
+        undo = ldexpf(1.0f, e);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) v[i] = ldexpf(v[i], -e);
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int r = l + 16 * i;
+        if (r >= rank_up(R)) continue;
+        for (int t = 0; t < terms; ++t) store(t * term_bytes + 2 * r, next_term<T>(v[i]));
+    }
+}
+
+}  // namespace lora
+}  // namespace nvfp4

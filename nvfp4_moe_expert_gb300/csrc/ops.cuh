@@ -43,6 +43,53 @@ cudaError_t launch_balance_loss_backward(const void* logits, int type, const Bal
                                          const int32_t* tokens, const float* dloss, void* dl, int64_t ld_out,
                                          bool accumulate, int* err, cudaStream_t st);
 
+// Low-rank adapters: out [T][ldo] = y [T][ldy] + scale_a (x_t A_a^T) B_a^T, a = ids[t] (negative: none); down A [L][R][K],
+// up B [L][N][R], x [T][ldx] of `type` (BF16 or FP16); y, out of y_type; h [T][R] = x_t A_a^T or nullptr
+struct LoraArgs {
+    const void* x;
+    int64_t T, ldx;
+    int type;
+    const void* down;
+    const void* up;
+    const float* scale;
+    const int32_t* ids;
+    int L, R;
+    int64_t K, N;
+    const void* y;
+    int64_t ldy;
+    void* out;
+    int64_t ldo;
+    int y_type;
+    float* h;
+    void* ws;                 // lora_workspace(T, L) bytes
+    int* err;
+};
+size_t lora_workspace(int64_t T, int L);
+cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t st);
+// dx (+)= scale_a (dy_t B_a) A_a, ddown [L][R][K], dup [L][N][R]; BF16 x, dy and adapters
+struct LoraBackwardArgs {
+    const void* dy;
+    const void* x;
+    int64_t T, lddy, ldx;
+    const float* h;
+    const void* down;
+    const void* up;
+    const float* scale;
+    const int32_t* ids;
+    int L, R;
+    int64_t K, N;
+    void* dx;
+    int64_t lddx;
+    int dx_type;
+    bool accumulate;
+    float* ddown;
+    float* dup;
+    void* ws;                 // lora_backward_workspace(T, L, R) bytes
+    int* err;
+};
+size_t lora_backward_workspace(int64_t T, int L, int R);
+cudaError_t launch_lora_add_backward(const LoraBackwardArgs& a, cudaStream_t st);
+
 // Columns of one 512-byte scale tile: 4 scales of 16 (NVFP4) or 32 (MXFP4) elements.
 constexpr int kMxBlock = 32;
 constexpr int kMxTileCols = 128;
