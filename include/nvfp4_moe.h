@@ -533,12 +533,14 @@ nvfp4_status moe_route_topk_backward(const void* logits_dev, int type, int64_t T
  *                   rows in front of the first and behind the last belong to none.  NULL: S = 1, all rows
  *  S                1 <= S < 2^27
  *  loss_dev         float [S], counts_dev int32 [S][E], probs_dev float [S][E] (P), tokens_dev int32 [S] (n), out
+ *  ws_dev           moe_balance_workspace_bytes(T, E, S) bytes, 256-byte aligned; NULL where that is 0 (few tokens)
  * Device errors: NVFP4_ERR_NONFINITE (a logit is NaN or +inf; +inf as the limit of large logits),
  * NVFP4_ERR_BAD_EXPERT_ID (an id outside [0, E); it is not counted). */
+size_t moe_balance_workspace_bytes(int64_t T, int E, int64_t S);
 nvfp4_status moe_balance_loss(const void* logits_dev, int type, int64_t T, int E, int64_t ld, int score,
                               const int32_t* topk_ids_dev, int k, const uint8_t* mask_dev,
                               const int32_t* seq_offsets_dev, int64_t S, float* loss_dev, int32_t* counts_dev,
-                              float* probs_dev, int32_t* tokens_dev, void* stream);
+                              float* probs_dev, int32_t* tokens_dev, void* ws_dev, size_t ws_bytes, void* stream);
 /*  counts_dev, tokens_dev   int32 [S][E] and [S], as above or sums of several batches'
  *  dloss_dev                float [S], the gradient of each loss
  *  dlogits_dev              [T][ld_out] of `type`, ld_out >= E, the first E of each row; its rows share no byte with

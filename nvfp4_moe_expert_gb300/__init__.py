@@ -131,7 +131,8 @@ _SIGNATURES = {
     "moe_route_topk": (_I32, [_P, _I32, _I64, _I32, _I64, ctypes.POINTER(moe_route_params), _P, _P, _P, _P]),
     "moe_route_topk_backward": (_I32, [_P, _I32, _I64, _I32, _I64, ctypes.POINTER(moe_route_params), _P, _P, _P, _I64,
                                        _P]),
-    "moe_balance_loss": (_I32, [_P, _I32, _I64, _I32, _I64, _I32, _P, _I32, _P, _P, _I64, _P, _P, _P, _P, _P]),
+    "moe_balance_workspace_bytes": (_SZ, [_I64, _I32, _I64]),
+    "moe_balance_loss": (_I32, [_P, _I32, _I64, _I32, _I64, _I32, _P, _I32, _P, _P, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_balance_loss_backward": (_I32, [_P, _I32, _I64, _I32, _I64, _I32, _I32, _P, _P, _I64, _P, _P, _P, _P, _I64, _I32,
                                          _P]),
     "mxfp4_sf_bytes": (_SZ, [_I64, _I64]),
@@ -578,6 +579,11 @@ def moe_route_topk_backward(logits, topk_ids, dw, score="softmax", renormalize=T
 MoEBalance = collections.namedtuple("MoEBalance", ("loss", "counts", "probs", "tokens"))
 
 
+@functools.lru_cache(maxsize=1024)
+def _balance_workspace_bytes(T, E, S):
+    return lib().moe_balance_workspace_bytes(T, E, S)
+
+
 def _balance_rows(logits, score, mask, seq_offsets):
     """What both calls take of the logits, the mask and the sequences."""
     code, T, E, ld = _rows("logits", logits, _TYPES)
@@ -615,9 +621,11 @@ def moe_balance_loss(logits, topk_ids, score="softmax", mask=None, seq_offsets=N
     counts = _empty((S, E), torch.int32, device, stream)
     probs = _empty((S, E), torch.float32, device, stream)
     tokens = _empty((S,), torch.int32, device, stream)
+    need = _balance_workspace_bytes(T, E, S)
+    ws = _empty((need,), torch.uint8, device, stream) if need else None
     status = lib().moe_balance_loss(logits.data_ptr(), code, T, E, ld, kind, topk_ids.data_ptr(), k, mask_ptr, seq_ptr,
                                     S, loss.data_ptr(), counts.data_ptr(), probs.data_ptr(), tokens.data_ptr(),
-                                    _raw_stream(stream, logits))
+                                    ws.data_ptr() if need else None, need, _raw_stream(stream, logits))
     if status:
         _check("moe_balance_loss", status)
     return MoEBalance(loss, counts, probs, tokens)

@@ -20,6 +20,7 @@ LIB_NAME = "libnvfp4moe.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["quant.cu", "gemm.cu", "combine.cu", "router.cu", "api.cu", "route_noalloc.cu", "backward.cu", "route_topk.cu",
            "balance.cu",
+           "balance_backward.cu",
            "mxfp4.cu", "linear.cu", "linear_pair.cu", "linear_quant.cu", "lora.cu", "lora_few_forward_bf16.cu",
            "lora_few_forward_f16.cu", "lora_few_backward.cu", "lora_many_forward_bf16.cu", "lora_many_forward_f16.cu",
            "lora_many_backward.cu", "lora_grad.cu"]

@@ -817,19 +817,25 @@ bool balance_shape_ok(int type, int64_t T, int E, int64_t ld, int score, int k, 
 
 }  // namespace
 
+size_t moe_balance_workspace_bytes(int64_t T, int E, int64_t S) {
+    return T >= 0 && T < kMaxTokens && E >= 1 && E <= 1024 && S >= 1 && S < (int64_t(1) << 27) ? balance_workspace(T, E, S) : 0;
+}
+
 nvfp4_status moe_balance_loss(const void* logits_dev, int type, int64_t T, int E, int64_t ld, int score,
                               const int32_t* topk_ids_dev, int k, const uint8_t* mask_dev,
                               const int32_t* seq_offsets_dev, int64_t S, float* loss_dev, int32_t* counts_dev,
-                              float* probs_dev, int32_t* tokens_dev, void* stream) {
+                              float* probs_dev, int32_t* tokens_dev, void* ws_dev, size_t ws_bytes, void* stream) {
     if (!balance_shape_ok(type, T, E, ld, score, k, seq_offsets_dev, S)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-    if ((T > 0 && (!logits_dev || !topk_ids_dev)) || !loss_dev || !counts_dev || !probs_dev || !tokens_dev ||
+    const size_t need = balance_workspace(T, E, S);
+    if ((need && !ws_dev) || !aligned(ws_dev, 256) || (T > 0 && (!logits_dev || !topk_ids_dev)) || !loss_dev || !counts_dev || !probs_dev || !tokens_dev ||
         !aligned(logits_dev, type_size(type)) || !aligned(topk_ids_dev, 4) || !aligned(seq_offsets_dev, 4) ||
         !aligned(loss_dev, 4) || !aligned(counts_dev, 4) || !aligned(probs_dev, 4) || !aligned(tokens_dev, 4))
         return NVFP4_ERR_INVALID_ARG;
+    if (ws_bytes < need) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
     int* err = device_error_ptr();
     if (!err) return NVFP4_ERR_CUDA;
     return from_cuda(launch_balance_loss(logits_dev, type, {T, E, ld, score, k, topk_ids_dev, mask_dev, seq_offsets_dev, S},
-                                         loss_dev, counts_dev, probs_dev, tokens_dev, err,
+                                         loss_dev, counts_dev, probs_dev, tokens_dev, ws_dev, err,
                                          static_cast<cudaStream_t>(stream)));
 }
 

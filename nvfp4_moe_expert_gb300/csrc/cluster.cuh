@@ -37,5 +37,24 @@ __device__ __forceinline__ int cluster_load_s32(uint32_t addr) {
     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
+// Arrive on another CTA's barrier (`addr`: cluster_addr of it): what this thread knows is done is visible to who waits there.
+__device__ __forceinline__ void cluster_arrive(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// Bounded wait on a barrier that CTAs of the cluster arrive on.
+__device__ __forceinline__ bool cluster_wait_bounded(uint64_t* bar, uint32_t parity, const volatile int* abort, long long budget) {
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (abort != nullptr && *abort) return false;
+        if (clock64() - t0 > budget) return false;
+    }
+}
 
 }  // namespace nvfp4

@@ -7,94 +7,159 @@ namespace {
 
 constexpr int kSortThreads = 1024, kSortWarps = 32;
 
-// Rows put in order by adapter (each adapter's in their own order), then cut into tiles of `rows_per_tile`.  One block: a
-// warp takes a stretch of the rows, counts its adapters, and after the sums over adapters and warps puts its rows in place,
-// 32 at a time (match_any gives a row its place among them).  ids are read twice.
-__global__ void __launch_bounds__(kSortThreads)
+// Rows put in order by adapter (each adapter's in their own order), then cut into tiles of `rows_per_tile`.  One cluster of
+// 8 CTAs: a warp takes a stretch of the rows, counts its adapters, and after the sums over warps, CTAs and adapters puts
+// its rows in place, 32 at a time (match_any gives a row its place among them).  The counts need no global memory, so
+// nothing has to be cleared in front.  Bound by latency and by the instructions of each warp: one CTA took 9 us for 8192
+// rows, 10.4 for 16384.
+constexpr int kAhead = 4;                 // loads of ids at a time
+
+__global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kSortThreads, 1)
     sort_kernel(const int32_t* __restrict__ ids, int T, int L, int rows_per_tile, int32_t* __restrict__ perm,
                 int32_t* __restrict__ offsets, int32_t* __restrict__ tile_adapter, int32_t* __restrict__ tile_start,
                 int32_t* __restrict__ tile_count, int* err) {
-    extern __shared__ int s_at[];                           // [kSortWarps][L + 1], first counts, then places
-    __shared__ int s_scan[kSortWarps], s_rows, s_tiles;
+    extern __shared__ int s_at[];                           // [kSortWarps][bins] rows of a warp, then those in front of it
+    __shared__ int s_scan[2][kSortWarps];
     const int bins = L + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_rank());
     int* mine = s_at + warp * bins;
+    int *s_own = s_at + kSortWarps * bins, *s_first = s_own + bins;   // [bins] the CTA's rows; its first place
     for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) s_at[i] = 0;
-    if (threadIdx.x == 0) s_rows = s_tiles = 0;
     __syncthreads();
-    const int stretch = ((T + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
-    const int64_t begin = static_cast<int64_t>(warp) * stretch, end = min(begin + stretch, static_cast<int64_t>(T));
+    constexpr unsigned kAllWarps = kSortWarps * kSplit;
+    const unsigned rows = T, stretch = ((rows + kAllWarps - 1) / kAllWarps + 31) / 32 * 32;   // T < 2^31 - 256: no overflow below
+    const unsigned begin = (rank * kSortWarps + warp) * stretch, end = min(begin + stretch, rows);
+    int id[kAhead];
+    const auto fetch = [&](unsigned base) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const unsigned t = base + 32 * j + lane;
+            id[j] = t < end ? ids[t] : -1;
+        }
+    };
     bool bad = false;
-    for (int64_t t = begin + lane; t < end; t += 32) {
-        const int id = ids[t];
-        bad |= id >= L;
-        atomicAdd(mine + (id < 0 || id >= L ? L : id), 1);
+#pragma unroll 1
+    for (unsigned base = begin; base < end; base += 32 * kAhead) {
+        fetch(base);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (base + 32 * j + lane >= end) continue;
+            bad |= id[j] >= L;
+            atomicAdd(mine + (id[j] < 0 || id[j] >= L ? L : id[j]), 1);
+        }
     }
     if (bad) set_device_error(err, NVFP4_ERR_BAD_EXPERT_ID);
     __syncthreads();
-    // an adapter's rows over the warps, then the adapters one behind the other, 1024 at a time
+    for (int a = warp; a < bins; a += kSortWarps) {         // an adapter's rows over the warps
+        const int c = s_at[lane * bins + a];
+        int v = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(kAll, v, o);
+            if (lane >= o) v += u;
+        }
+        s_at[lane * bins + a] = v - c;
+        if (lane == 31) s_own[a] = v;
+    }
+    cluster_barrier();
+    // the adapters one behind the other, 1024 at a time (L is at most that, and one for the rows without); every CTA
+    // does all of it, each writes the tiles of every eighth adapter
+    int first_row = 0, first_tile = 0;
     for (int base = 0; base < bins; base += kSortThreads) {
         const int a = base + static_cast<int>(threadIdx.x);
-        int rows = 0;
+        int own = 0, front = 0;
         if (a < bins) {
-            for (int w = 0; w < kSortWarps; ++w) {
-                const int c = s_at[w * bins + a];
-                s_at[w * bins + a] = rows;
-                rows += c;
-            }
-        }
-        const int tiles = (rows + rows_per_tile - 1) / rows_per_tile;
-        const int first_row = s_rows, first_tile = s_tiles;
-        int sums[2] = {rows, tiles}, before[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {                       // sums over the adapters in front, in the block
-            int v = sums[k];
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(kAll, v, o);
-                if (lane >= o) v += u;
+            for (int c = 0; c < kSplit; ++c) {
+                const int v = cluster_load_s32(cluster_addr(s_own + a, c));
+                own += v;
+                if (c < rank) front += v;
             }
-            __syncthreads();
-            if (lane == 31) s_scan[warp] = v;
-            __syncthreads();
-            int front = 0;
-            for (int w = 0; w < warp; ++w) front += s_scan[w];
-            before[k] = front + v - sums[k];
         }
-        const int row = first_row + before[0], tile = first_tile + before[1];
+        const int tiles = (own + rows_per_tile - 1) / rows_per_tile;
+        int r = own, n = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int ur = __shfl_up_sync(kAll, r, o), un = __shfl_up_sync(kAll, n, o);
+            if (lane >= o) r += ur, n += un;
+        }
+        if (lane == 31) s_scan[0][warp] = r, s_scan[1][warp] = n;
+        __syncthreads();
+        int wr = s_scan[0][lane], wn = s_scan[1][lane];     // every warp: the warps in front
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int ur = __shfl_up_sync(kAll, wr, o), un = __shfl_up_sync(kAll, wn, o);
+            if (lane >= o) wr += ur, wn += un;
+        }
+        const int row = first_row + r - own + (warp ? __shfl_sync(kAll, wr, (warp - 1) & 31) : 0);
+        const int tile = first_tile + n - tiles + (warp ? __shfl_sync(kAll, wn, (warp - 1) & 31) : 0);
+        first_row += __shfl_sync(kAll, wr, 31);
+        first_tile += __shfl_sync(kAll, wn, 31);
         if (a < bins) {
-            offsets[a] = row;
-            for (int w = 0; w < kSortWarps; ++w) s_at[w * bins + a] += row;
-            for (int i = 0; i < tiles; ++i) {
-                tile_adapter[tile + i] = a < L ? a : -1;
-                tile_start[tile + i] = row + i * rows_per_tile;
+            s_first[a] = row + front;
+            if (a % kSplit == rank) {
+                offsets[a] = row;
+                for (int i = 0; i < tiles; ++i) {
+                    tile_adapter[tile + i] = a < L ? a : -1;
+                    tile_start[tile + i] = row + i * rows_per_tile;
+                }
             }
         }
         __syncthreads();
-        if (threadIdx.x == kSortThreads - 1) {
-            s_rows = row + rows;
-            s_tiles = tile + tiles;
-        }
-        __syncthreads();
     }
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && rank == 0) {
         offsets[bins] = T;
-        *tile_count = s_tiles;
+        *tile_count = first_tile;
     }
-    for (int64_t base = begin; base < end; base += 32) {
-        const int64_t t = base + lane;
-        const unsigned active = __ballot_sync(kAll, t < end);
-        if (t < end) {
-            const int id = ids[t], a = id < 0 || id >= L ? L : id;
-            const unsigned same = __match_any_sync(active, a);
-            const int place = mine[a] + __popc(same & ((1u << lane) - 1));
-            perm[place] = static_cast<int32_t>(t);
-            __syncwarp(active);
-            if ((same >> lane) == 1) mine[a] += __popc(same);   // the last of them
+#pragma unroll 1
+    for (unsigned base = begin; base < end; base += 32 * kAhead) {
+        if (end - begin > 32 * kAhead) fetch(base);         // otherwise they are still here
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const unsigned t = base + 32 * j + lane;
+            if (base + 32 * j >= end) continue;
+            const int a = t >= end ? -1 : id[j] < 0 || id[j] >= L ? L : id[j];
+            const unsigned same = __match_any_sync(kAll, a);
+            if (a >= 0) perm[s_first[a] + mine[a] + __popc(same & ((1u << lane) - 1))] = t;
+            __syncwarp();
+            if (a >= 0 && (same >> lane) == 1) mine[a] += __popc(same);   // the last of them
+            __syncwarp();
         }
-        __syncwarp();
     }
+    cluster_barrier();                                      // no CTA leaves while another reads its counts
 }
 
 }  // namespace
+
+namespace {
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+}  // namespace
+
+bool make_units_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t slices, int64_t slice, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(slices)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(slice) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, slices ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 size_t sort_bytes(int64_t T, int L) {
     const size_t tiles = static_cast<size_t>(tiles_bound(T, L, kFewRows));
@@ -118,12 +183,12 @@ Tiles sort_layout(void* ws, int64_t T, int L) {
 }
 
 cudaError_t launch_sort(const int32_t* ids, int64_t T, int L, int rows_per_tile, const Tiles& t, int* err, cudaStream_t st) {
-    const size_t smem = static_cast<size_t>(kSortWarps) * (L + 1) * sizeof(int);
+    const size_t smem = static_cast<size_t>(kSortWarps + 2) * (L + 1) * sizeof(int);
     static Ready ready;
     const cudaError_t e = allow_shared(reinterpret_cast<const void*>(sort_kernel),
-                                       kSortWarps * (kMaxAdapters + 1) * static_cast<int>(sizeof(int)), ready);
+                                       (kSortWarps + 2) * (kMaxAdapters + 1) * static_cast<int>(sizeof(int)), ready);
     if (e != cudaSuccess) return e;
-    return launch_pdl(false, sort_kernel, dim3(1), dim3(kSortThreads), smem, st, ids, static_cast<int>(T), L, rows_per_tile,
+    return launch_pdl(false, sort_kernel, dim3(kSplit), dim3(kSortThreads), smem, st, ids, static_cast<int>(T), L, rows_per_tile,
                       const_cast<int32_t*>(t.perm), const_cast<int32_t*>(t.offsets), const_cast<int32_t*>(t.adapter),
                       const_cast<int32_t*>(t.start), const_cast<int32_t*>(t.count), err);
 }
@@ -176,7 +241,7 @@ cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t st) {
         const int64_t tiles = tiles_bound(a.T, a.L, kFewRows);
         return bf16 ? launch_few_forward_bf16(p, tiles, false, st) : launch_few_forward_f16(p, tiles, false, st);
     }
-    const int rows = a.T <= kFewTokens ? kFewRows : kManyRows;
+    const int rows = a.T <= kFewTokens || !many_fits(a.R, bf16 && a.y_type == NVFP4_TYPE_F32 ? 3 : 2, false) ? kFewRows : kManyRows;
     p.tiles = sort_layout(a.ws, a.T, a.L);
     const cudaError_t e = launch_sort(a.ids, a.T, a.L, rows, p.tiles, a.err, st);
     if (e != cudaSuccess) return e;
@@ -189,7 +254,7 @@ cudaError_t launch_lora_add_backward(const LoraBackwardArgs& a, cudaStream_t st)
     using namespace lora;
     const Tiles tiles = sort_layout(a.ws, a.T, a.L);
     float* dh = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + align_256(sort_bytes(a.T, a.L)));
-    const int rows = a.T <= kFewTokens ? kFewRows : kManyRows;
+    const int rows = a.T <= kFewTokens || !many_fits(a.R, a.dx_type == NVFP4_TYPE_F32 ? 3 : 2, true) ? kFewRows : kManyRows;
     cudaError_t e = launch_sort(a.ids, a.T, a.L, rows, tiles, a.err, st);
     if (e != cudaSuccess) return e;
     Params p = {};

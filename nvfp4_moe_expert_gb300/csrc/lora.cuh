@@ -63,6 +63,9 @@ struct Params {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {   // the rest of the 16 are zeros
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
@@ -94,22 +97,50 @@ __host__ __device__ constexpr int rank_up(int R) { return (R + 15) / 16 * 16; } 
 // Sub-slices of the first product: 64 of them, of as many steps of 16 columns.
 __host__ __device__ inline int sub_steps(int C) { return (C + 1023) / 1024; }
 
-// 16 bytes of a row of 16-bit elements from column c on (zeros from `cols` on) into shared memory.
-__device__ __forceinline__ void copy_chunk(uint32_t dst, const uint16_t* row, int c, int cols, bool wide) {
-    const int left = min(max(cols - c, 0), 8);
-    if (wide) {
-        cp_async16(dst, left ? row + c : row, 2 * left);
-        return;
+// 16 bytes of a row from 16-bit unit c on (zeros from `units` on) into shared memory.  Rows that do not start on a 16-byte
+// boundary are read in the aligned 16-byte words that hold a unit of theirs, two of them shifted together: with loads of
+// single elements 8191 x 1999 took a CTA eight times the instructions.
+struct Straddle {
+    uint4 lo, hi;
+    int left, off;                        // units that are there, bytes in front of them
+    __device__ __forceinline__ void load(const uint16_t* row, int c, int units) { load(row + c, units - c); }
+    __device__ __forceinline__ void load(const uint16_t* from, int units) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(from);
+        left = min(max(units, 0), 8);
+        off = static_cast<int>(at & 15);
+        const uint4* p = reinterpret_cast<const uint4*>(at & ~uintptr_t(15));
+        lo = hi = make_uint4(0, 0, 0, 0);
+        if (left > 0) lo = __ldg(p);
+        if (2 * left > 16 - off) hi = __ldg(p + 1);
     }
-    uint32_t w[4];
+    __device__ __forceinline__ void store(uint32_t dst) const {
+        uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        if (off & 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = 2 * i < left ? row[c + 2 * i] : 0, hi = 2 * i + 1 < left ? row[c + 2 * i + 1] : 0;
-        w[i] = lo | hi << 16;
+            for (int i = 0; i < 7; ++i) w[i] = w[i + 1];
+        }
+        if (off & 8) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 2];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
+            if (2 * i + 1 >= left) w[i] = 2 * i < left ? w[i] & 0xFFFFu : 0;
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
     }
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+};
+__device__ __forceinline__ void copy_chunk(uint32_t dst, const uint16_t* row, int c, int units, bool wide) {
+    if (wide) {
+        const int left = min(max(units - c, 0), 8);
+        cp_async16(dst, left ? row + c : row, 2 * left);
+    } else {
+        Straddle s;
+        s.load(row, c, units);
+        s.store(dst);
+    }
 }
-
 // Operand of the first product: `cols` (a multiple of 16, at most 64) columns from c on of the adapter's matrix.
 template <bool kTrans>
 __device__ __forceinline__ void load_down(uint32_t dst, const uint16_t* down, int R, int C, int c, int cols, int thread, int threads) {
@@ -120,55 +151,74 @@ __device__ __forceinline__ void load_down(uint32_t dst, const uint16_t* down, in
                 copy_chunk(dst + swizzled(r, q), down + static_cast<int64_t>(r) * C, c + 8 * q, C, true);
         }
     } else {                              // [C][R]: rows of R columns, padded
-        const int per = R / 8;
-        for (int i = thread; i < cols * per; i += threads) {
-            const int n = i / per, q = i % per;
-            const bool real = c + n < C;
-            cp_async16(dst + n * padded_pitch(R) + 16 * q, real ? down + static_cast<int64_t>(c + n) * R + 8 * q : down, real ? 16 : 0);
+        const int per = R / 8, at_once = threads / per, n0 = thread / per, q = thread - n0 * per;
+        if (n0 < at_once) {
+            const uint16_t* src = down + static_cast<int64_t>(c + n0) * R + 8 * q;
+            dst += n0 * padded_pitch(R) + 16 * q;
+            for (int n = n0; n < cols; n += at_once, src += at_once * R, dst += at_once * padded_pitch(R)) {
+                if (c + n < C) cp_async16(dst, src);
+                else cp_async16(dst, down, 0);
+            }
         }
     }
 }
 template <bool kTrans>
 __host__ __device__ constexpr int down_bytes(int R, int cols) { return kTrans ? cols * padded_pitch(R) : rank_up(R) * 128; }
 
-// Products of 16 rows x 16 columns of x (a) with step kk of the operand above: acc[j] gets ranks 8 j to 8 j + 7.
+// A lane's address in a swizzled tile for ldmatrix, of step 0; step kk is at ^ (kk << 5) of it, 8 more rows 1024 further.
+__device__ __forceinline__ uint32_t lane_rows(int lane) {   // matrices: 8 rows, the next 8, then the next 8 columns of both
+    return swizzled((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+}
+template <bool kTrans>
+__device__ __forceinline__ uint32_t lane_down(int lane, int R) {
+    return kTrans ? (((lane >> 3) & 1) * 8 + (lane & 7)) * padded_pitch(R) + 16 * (lane >> 4)
+                  : swizzled(8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1);
+}
+// Products of 16 rows x 16 columns of x (a) with step kk of the operand above (`down`: its address + lane_down): acc[j]
+// gets ranks 8 j to 8 j + 7.
 template <typename T, bool kTrans, int kTiles>
-__device__ __forceinline__ void multiply_down(float (&acc)[kTiles][4], const uint32_t (&a)[4], uint32_t down, int kk, int R, int lane) {
+__device__ __forceinline__ void multiply_down(float (&acc)[kTiles][4], const uint32_t (&a)[4], uint32_t down, int kk, int R) {
+    const uint32_t at = kTrans ? down + 16 * kk * padded_pitch(R) : down ^ (kk << 5);
 #pragma unroll
     for (int j = 0; j < kTiles; j += 2) {
         if (8 * j >= R) break;
         uint32_t b[4];
-        if (!kTrans) ldsm4(down + swizzled(8 * (j + (lane >> 4)) + (lane & 7), 2 * kk + ((lane >> 3) & 1)), b);
-        else ldsm4_trans(down + (16 * kk + ((lane >> 3) & 1) * 8 + (lane & 7)) * padded_pitch(R) + 16 * (j + (lane >> 4)), b);
+        if (!kTrans) ldsm4(at + 1024 * j, b);
+        else ldsm4_trans(at + 16 * j, b);
         mma(T(), acc[j], a, b[0], b[1]);
         if (8 * (j + 1) < R) mma(T(), acc[j + 1], a, b[2], b[3]);
     }
 }
 
-// Operand of the second product: outputs [n, n + kCols) of the adapter's matrix; ranks from R to rank_up(R) are zeros.
+// Operand of the second product: `cols` (32 or 64) outputs from n on of the adapter's matrix; ranks from R to rank_up(R) are zeros.
 // Not transposed, output 8 q + 2 i + l of a group of 32 lies in row 8 i + 2 q + l: the accumulators of a lane are then 8
 // consecutive outputs of a row.
-template <bool kTrans, int kCols>
-__device__ __forceinline__ void load_up(uint32_t dst, const uint16_t* up, int R, int D, int n, int thread, int threads) {
+template <bool kTrans>
+__device__ __forceinline__ void load_up(uint32_t dst, const uint16_t* up, int R, int D, int n, int cols, int thread, int threads) {
     const int Rp = rank_up(R);
     if (!kTrans) {                        // [D][R]
-        const int per = Rp / 8;
-        for (int i = thread; i < kCols * per; i += threads) {
-            const int j = i / per, q = i % per, w = j & 31;
-            const int at = (j & ~31) + 8 * ((w & 7) >> 1) + 2 * (w >> 3) + (w & 1);
-            const bool real = n + j < D && 8 * q < R;
-            cp_async16(dst + at * padded_pitch(Rp) + 16 * q, real ? up + static_cast<int64_t>(n + j) * R + 8 * q : up, real ? 16 : 0);
+        const int per = Rp / 8, at_once = threads / per, j0 = thread / per, q = thread - j0 * per;
+        if (j0 < at_once) {
+            const uint16_t* src = up + static_cast<int64_t>(n + j0) * R + 8 * q;
+            dst += 16 * q;
+            for (int j = j0; j < cols; j += at_once, src += at_once * R) {
+                const int at = (j & ~31) + 8 * ((j & 7) >> 1) + 2 * ((j & 31) >> 3) + (j & 1);
+                if (n + j < D && 8 * q < R) cp_async16(dst + at * padded_pitch(Rp), src);
+                else cp_async16(dst + at * padded_pitch(Rp), up, 0);
+            }
         }
     } else {                              // [R][D]: rows of 64 columns, swizzled
-        for (int i = thread; i < Rp * (kCols / 8); i += threads) {
-            const int r = i / (kCols / 8), q = i % (kCols / 8);
-            if (r < R) copy_chunk(dst + swizzled(r, q), up + static_cast<int64_t>(r) * D, n + 8 * q, D, true);
-            else cp_async16(dst + swizzled(r, q), up, 0);
+        const int q = thread & 7;
+        if (8 * q < cols) {
+            for (int r = thread >> 3; r < Rp; r += threads >> 3) {
+                if (r < R) copy_chunk(dst + swizzled(r, q), up + static_cast<int64_t>(r) * D, n + 8 * q, D, true);
+                else cp_async16(dst + swizzled(r, q), up, 0);
+            }
         }
     }
 }
-template <bool kTrans, int kCols>
-__host__ __device__ constexpr int up_bytes(int R) { return kTrans ? rank_up(R) * 128 : kCols * padded_pitch(rank_up(R)); }
+template <bool kTrans>
+__host__ __device__ constexpr int up_bytes(int R, int cols) { return kTrans ? rank_up(R) * 128 : cols * padded_pitch(rank_up(R)); }
 
 // h (16 rows from `h`, `terms` arrays of 16-bit terms that add up to it) times the operand above, group g32 of 32 outputs:
 // o[i] gets the 8 consecutive outputs 8 (lane % 4) of row lane / 4 + 8 i.
@@ -263,46 +313,40 @@ __device__ __forceinline__ Eight load_eight(const void* base, int type, int64_t 
     e.b = make_uint4(w[4], w[5], w[6], w[7]);
     return e;
 }
-__device__ __forceinline__ float2 unpack2(uint32_t w, int type) {
-    if (type == NVFP4_TYPE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
-    if (type == NVFP4_TYPE_BF16) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
-    const __half2 v = __floats2half2_rn(lo, hi);
+__device__ __forceinline__ uint32_t add2_bf16(uint32_t y, float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(y << 16) + lo, __uint_as_float(y & 0xFFFF0000u) + hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// out = y + o, in FP32 with one rounding.
-__device__ __forceinline__ void store_eight(void* base, int type, int64_t row, int64_t ld, int n, int D, bool wide, const Eight& y,
-                                            const float (&o)[8]) {
-    if (n >= D) return;
-    uint32_t w[8];
-    if (type == NVFP4_TYPE_F32) {
-        const uint32_t v[8] = {y.a.x, y.a.y, y.a.z, y.a.w, y.b.x, y.b.y, y.b.z, y.b.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(v[i]) + o[i]);
+__device__ __forceinline__ uint32_t add2_f16(uint32_t y, float lo, float hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y));
+    const __half2 v = __floats2half2_rn(f.x + lo, f.y + hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// y += o, in FP32 with one rounding.
+__device__ __forceinline__ void add_eight(Eight& y, const float (&o)[8], int type) {
+    if (type == NVFP4_TYPE_BF16) {
+        y.a = make_uint4(add2_bf16(y.a.x, o[0], o[1]), add2_bf16(y.a.y, o[2], o[3]), add2_bf16(y.a.z, o[4], o[5]), add2_bf16(y.a.w, o[6], o[7]));
+    } else if (type == NVFP4_TYPE_F16) {
+        y.a = make_uint4(add2_f16(y.a.x, o[0], o[1]), add2_f16(y.a.y, o[2], o[3]), add2_f16(y.a.z, o[4], o[5]), add2_f16(y.a.w, o[6], o[7]));
     } else {
-        const uint32_t v[4] = {y.a.x, y.a.y, y.a.z, y.a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack2(v[i], type);
-            w[i] = pack2(f.x + o[2 * i], f.y + o[2 * i + 1], type);
-        }
+        const auto add = [](uint32_t w, float v) { return __float_as_uint(__uint_as_float(w) + v); };
+        y.a = make_uint4(add(y.a.x, o[0]), add(y.a.y, o[1]), add(y.a.z, o[2]), add(y.a.w, o[3]));
+        y.b = make_uint4(add(y.b.x, o[4]), add(y.b.y, o[5]), add(y.b.z, o[6]), add(y.b.w, o[7]));
     }
-    const int size = type == NVFP4_TYPE_F32 ? 4 : 2;
-    uint8_t* p = static_cast<uint8_t*>(base) + (row * ld + n) * size;
+}
+// Columns [n, D) of 8 consecutive elements at p.
+__device__ __forceinline__ void store_eight(uint8_t* p, int type, int n, int D, bool wide, const Eight& v) {
+    if (n >= D) return;
     if (wide && n + 8 <= D) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (size == 4) *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+        *reinterpret_cast<uint4*>(p) = v.a;
+        if (type == NVFP4_TYPE_F32) *reinterpret_cast<uint4*>(p + 16) = v.b;
         return;
     }
+    const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if (n + i >= D) continue;
-        if (size == 4) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+        if (type == NVFP4_TYPE_F32) reinterpret_cast<uint32_t*>(p)[i] = w[i];
         else reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
     }
 }
@@ -322,44 +366,57 @@ __device__ __forceinline__ int row_exponent(float m) {
     return max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100) - 14;
 }
 
-// A row of h: lane l of 16 sums the 8 CTAs' parts of columns l, l + 16, ... in their order, and writes the row's terms to
-// `dst` (a shared-memory address in the cluster, or one for every CTA of it).
+// A row of h: lane l of 16 sums the 8 CTAs' parts of columns 2 l, 2 l + 1, 2 l + 32, ... in their order, and hands over the
+// row's terms, two columns (32 bits) at a time.
 template <typename T, int kRank, typename Store>
 __device__ __forceinline__ void finish_row(const float* part, int row, int pitch, int R, float scale, int terms, int term_bytes,
                                            float* h_out, bool h_scaled, int l, Store&& store, float& undo) {
-    constexpr int kMine = kRank / 16;
-    float v[kMine], m = 0.0f;
+    constexpr int kMine = (kRank + 31) / 32;
+    float v[kMine][2], m = 0.0f;
     uint32_t from[kSplit];
 #pragma unroll
     for (int c = 0; c < kSplit; ++c) from[c] = cluster_addr(part, c) + 4 * row * pitch;
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-        const int r = l + 16 * i;
-        v[i] = 0.0f;
+        const int r = 2 * l + 32 * i;
+        v[i][0] = v[i][1] = 0.0f;
         if (r < R) {
-            v[i] = cluster_load_f32(from[0] + 4 * r);
+            float got[kSplit][2];
 #pragma unroll
-            for (int c = 1; c < kSplit; ++c) v[i] += cluster_load_f32(from[c] + 4 * r);
-            const float scaled = v[i] * scale;
-            if (h_out != nullptr) h_out[r] = h_scaled ? scaled : v[i];
-            v[i] = scaled;
+            for (int c = 0; c < kSplit; ++c)
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(got[c][0]), "=f"(got[c][1]) : "r"(from[c] + 4 * r) : "memory");
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float sum = got[0][k];
+#pragma unroll
+                for (int c = 1; c < kSplit; ++c) sum += got[c][k];
+                v[i][k] = sum * scale;
+                got[0][k] = h_scaled ? v[i][k] : sum;
+            }
+            if (h_out != nullptr) *reinterpret_cast<float2*>(h_out + r) = make_float2(got[0][0], got[0][1]);
         }
-        m = fmaxf(m, fabsf(v[i]));
+        m = fmaxf(m, fmaxf(fabsf(v[i][0]), fabsf(v[i][1])));
     }
     undo = 1.0f;
-    if (sizeof(T) == 2 && std::is_same<T, __half>::value) {
+    if (std::is_same<T, __half>::value) {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
         const int e = row_exponent(m);
         undo = ldexpf(1.0f, e);
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) v[i] = ldexpf(v[i], -e);
+        for (int i = 0; i < kMine; ++i) {
+            v[i][0] = ldexpf(v[i][0], -e);
+            v[i][1] = ldexpf(v[i][1], -e);
+        }
     }
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-        const int r = l + 16 * i;
+        const int r = 2 * l + 32 * i;
         if (r >= rank_up(R)) continue;
-        for (int t = 0; t < terms; ++t) store(t * term_bytes + 2 * r, next_term<T>(v[i]));
+        for (int t = 0; t < terms; ++t) {
+            const uint32_t lo = next_term<T>(v[i][0]), hi = next_term<T>(v[i][1]);
+            store(t * term_bytes + 2 * r, lo | hi << 16);
+        }
     }
 }
 

@@ -23,7 +23,7 @@ struct FewLayout {
         buffers = R <= 64 ? 2 : 1;
         x = kFewRows * 128;
         down = (down_bytes<kTrans>(R, cols) + 127) / 128 * 128;
-        up = (up_bytes<kTrans, 32>(R) + 127) / 128 * 128;
+        up = (up_bytes<kTrans>(R, 32) + 127) / 128 * 128;
         const int loads = kWarps * (x + down);
         part = 0;                         // over the loads, which are used up then
         sum = part + kWarps * kFewRows * R * 4;
@@ -148,7 +148,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads) few_k
         cp_commit();
         for (int b = 0; b < lay.buffers; ++b) {
             if (first_group + 8 * b < last_group)
-                load_up<kTrans, 32>(my_up + b * lay.up, up, p.R, p.D, 32 * (first_group + 8 * b), lane, 32);
+                load_up<kTrans>(my_up + b * lay.up, up, p.R, p.D, 32 * (first_group + 8 * b), 32, lane, 32);
             cp_commit();
         }
         if (first_group < last_group) load_y(first_group);
@@ -166,8 +166,8 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads) few_k
             const int n = min(lay.cols, c1 - c);
             for (int kk = 0; 16 * kk < n; ++kk) {
                 uint32_t a[4];
-                ldsm4(sx + swizzled((lane & 7) + ((lane >> 3) & 1) * 8, 2 * kk + (lane >> 4)), a);
-                multiply_down<T, kTrans, kTiles>(acc, a, sd, kk, p.R, lane);
+                ldsm4((sx + lane_rows(lane)) ^ (kk << 5), a);
+                multiply_down<T, kTrans, kTiles>(acc, a, sd + lane_down<kTrans>(lane, p.R), kk, p.R);
             }
         }
         __syncthreads();                                    // every warp's loads are used up
@@ -195,7 +195,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads) few_k
         uint8_t* h = smem + lay.h + row * pitch;
         finish_row<T, kRank>(sum, row, p.R, p.R, p.scale == nullptr ? 1.0f : p.scale[adapter], terms, kFewRows * pitch,
                              keep ? p.h + static_cast<int64_t>(s_row[row]) * p.R : nullptr, p.h_scaled != 0, lane & 15,
-                             [&](int at, uint16_t v) { *reinterpret_cast<uint16_t*>(h + at) = v; }, row_undo);
+                             [&](int at, uint32_t v) { *reinterpret_cast<uint32_t*>(h + at) = v; }, row_undo);
         if ((lane & 15) == 0) s_undo[row] = row_undo;
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // the other CTAs' sums are read
         __syncthreads();
@@ -218,7 +218,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads) few_k
             multiply_up<T, kTrans>(o, smem_u32(smem) + lay.h, kFewRows * padded_pitch(rank_up(p.R)), terms, my_up + b * lay.up, 0, p.R, lane);
             __syncwarp();
             const int next = g + kWarps * lay.buffers;
-            if (next < last_group) load_up<kTrans, 32>(my_up + b * lay.up, up, p.R, p.D, 32 * next, lane, 32);
+            if (next < last_group) load_up<kTrans>(my_up + b * lay.up, up, p.R, p.D, 32 * next, 32, lane, 32);
             cp_commit();
             if (++b == lay.buffers) b = 0;
         }
@@ -226,7 +226,11 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads) few_k
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[i][j] *= undo[i];
-            if (row_of[i] >= 0) store_eight(p.out, p.y_type, row_of[i], p.ldo, 32 * g + 8 * (lane & 3), p.D, p.out_wide, y[i], o[i]);
+            const int n = 32 * g + 8 * (lane & 3);
+            if (row_of[i] < 0) continue;
+            add_eight(y[i], o[i], p.y_type);
+            store_eight(static_cast<uint8_t*>(p.out) + (row_of[i] * p.ldo + n) * (p.y_type == NVFP4_TYPE_F32 ? 4 : 2), p.y_type, n, p.D,
+                        p.out_wide, y[i]);
         }
         if (g + kWarps < last_group) load_y(g + kWarps);
     }

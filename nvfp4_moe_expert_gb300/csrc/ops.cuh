@@ -35,9 +35,10 @@ struct BalanceArgs {
     const int32_t* offsets;
     int64_t S;
 };
-// loss, tokens [S]; counts, probs [S][E]
+// loss, tokens [S]; counts, probs [S][E]; ws: balance_workspace(T, E, S) bytes
+size_t balance_workspace(int64_t T, int E, int64_t S);
 cudaError_t launch_balance_loss(const void* logits, int type, const BalanceArgs& a, float* loss, int32_t* counts,
-                                float* probs, int32_t* tokens, int* err, cudaStream_t st);
+                                float* probs, int32_t* tokens, void* ws, int* err, cudaStream_t st);
 // dl [T][ld_out], the logits' type; a.ids unused
 cudaError_t launch_balance_loss_backward(const void* logits, int type, const BalanceArgs& a, const int32_t* counts,
                                          const int32_t* tokens, const float* dloss, void* dl, int64_t ld_out,

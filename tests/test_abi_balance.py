@@ -10,8 +10,9 @@ from nvfp4_moe_expert_gb300 import build as B
 from test_devices import Tensor, device_0  # noqa: F401
 
 OK, ARG, SHAPE = 0, 1, 2
-P, ODD = ctypes.c_void_p(4096), ctypes.c_void_p(4097)
-FAR = ctypes.c_void_p(1 << 30)
+V = ctypes.c_void_p
+P, ODD = V(4096), V(4097)
+FAR = V(1 << 30)
 
 
 @pytest.fixture(scope="module")
@@ -26,14 +27,21 @@ SHAPES = (dict(T=-1), dict(T=1 << 31), dict(E=0, ld=0), dict(E=1025, ld=1025), d
 
 
 def test_refusals(lib):
-    def call(T=8, E=64, ld=64, type=0, score=0, x=P, ids=P, k=4, mask=None, off=None, S=1, loss=P, counts=P, probs=P, tokens=P):
-        return lib.moe_balance_loss(x, type, T, E, ld, score, ids, k, mask, off, S, loss, counts, probs, tokens, None)
+    def call(T=8, E=64, ld=64, type=0, score=0, x=P, ids=P, k=4, mask=None, off=None, S=1, loss=P, counts=P, probs=P, tokens=P,
+             ws=P, n=1 << 24):
+        return lib.moe_balance_loss(x, type, T, E, ld, score, ids, k, mask, off, S, loss, counts, probs, tokens, ws, n, None)
     for kw in SHAPES:
         assert call(**kw) == SHAPE, kw
     for kw in (dict(x=None), dict(ids=None), dict(loss=None), dict(counts=None), dict(probs=None), dict(tokens=None),
                dict(x=ODD), dict(type=1, x=ODD), dict(ids=ODD), dict(off=ODD), dict(loss=ODD), dict(counts=ODD),
-               dict(probs=ODD), dict(tokens=ODD), dict(T=0, loss=None)):
+               dict(probs=ODD), dict(tokens=ODD), dict(T=0, loss=None), dict(ws=V(4112)),
+               dict(T=5000, ws=None)):
         assert call(**kw) == ARG, kw
+    size = lib.moe_balance_workspace_bytes
+    assert size(1024, 64, 32) == 0 and size(8, 1024, 1) == 0                  # few tokens need none
+    need = size(5000, 64, 3)
+    assert need > 0 and need % 256 == 0 and call(T=5000, S=3, off=P, n=need - 1) == 3
+    assert size(8, 64, 33) > 0 and size(-1, 64, 1) == 0 and size(8, 0, 1) == 0 and size(8, 1025, 1) == 0 and size(8, 64, 0) == 0
 
 
 def test_backward_refusals(lib):
@@ -45,7 +53,7 @@ def test_backward_refusals(lib):
         assert call(**kw) == SHAPE, kw
     for kw in (dict(x=None), dict(counts=None), dict(tokens=None), dict(dloss=None), dict(out=None), dict(x=ODD), dict(out=ODD),
                dict(counts=ODD), dict(tokens=ODD), dict(dloss=ODD), dict(off=ODD), dict(out=P), dict(add=1, out=P),
-               dict(out=ctypes.c_void_p(4096 + 8 * 64 * 4 - 4))):
+               dict(out=V(4096 + 8 * 64 * 4 - 4))):
         assert call(**kw) == ARG, kw
 
 
