@@ -22,8 +22,8 @@ SOURCES = ["quant.cu", "gemm.cu", "combine.cu", "router.cu", "api.cu", "route_no
            "balance.cu",
            "balance_backward.cu",
            "mxfp4.cu", "linear.cu", "linear_pair.cu", "linear_quant.cu", "lora.cu", "lora_few_forward_bf16.cu",
-           "lora_few_forward_f16.cu", "lora_few_backward.cu", "lora_many_forward_bf16.cu", "lora_many_forward_f16.cu",
-           "lora_many_backward.cu", "lora_grad.cu"]
+           "lora_few_forward_f16.cu", "lora_few_backward.cu", "lora_grad.cu"] + [
+    f"lora_many_{what}_to_{out}.cu" for what in ("forward_bf16", "forward_f16", "backward") for out in ("bf16", "f16", "f32")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", BUILD_DIR]
 SILU_GEN = os.path.join(HERE, "silu_table.py")

@@ -247,7 +247,7 @@ cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int64_t tiles = tiles_bound(a.T, a.L, rows);
     if (rows == kFewRows) return bf16 ? launch_few_forward_bf16(p, tiles, true, st) : launch_few_forward_f16(p, tiles, true, st);
-    return bf16 ? launch_many_forward_bf16(p, tiles, true, st) : launch_many_forward_f16(p, tiles, true, st);
+    return bf16 ? launch_many_any<__nv_bfloat16, false>(p, tiles, true, st) : launch_many_any<__half, false>(p, tiles, true, st);
 }
 
 cudaError_t launch_lora_add_backward(const LoraBackwardArgs& a, cudaStream_t st) {
@@ -281,7 +281,7 @@ cudaError_t launch_lora_add_backward(const LoraBackwardArgs& a, cudaStream_t st)
     p.tiles = tiles;
     p.err = a.err;
     const int64_t bound = tiles_bound(a.T, a.L, rows);
-    e = rows == kFewRows ? launch_few_backward(p, bound, true, st) : launch_many_backward(p, bound, true, st);
+    e = rows == kFewRows ? launch_few_backward(p, bound, true, st) : launch_many_any<__nv_bfloat16, true>(p, bound, true, st);
     if (e != cudaSuccess) return e;
     GradParams g = {};
     g.x = static_cast<const uint16_t*>(a.x);

@@ -313,21 +313,30 @@ __device__ __forceinline__ Eight load_eight(const void* base, int type, int64_t 
     e.b = make_uint4(w[4], w[5], w[6], w[7]);
     return e;
 }
-__device__ __forceinline__ uint32_t add2_bf16(uint32_t y, float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(y << 16) + lo, __uint_as_float(y & 0xFFFF0000u) + hi);
+__device__ __forceinline__ float2 unpack2(uint32_t w, int type) {
+    if (type == NVFP4_TYPE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
+    if (type == NVFP4_TYPE_BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t add2_f16(uint32_t y, float lo, float hi) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y));
-    const __half2 v = __floats2half2_rn(f.x + lo, f.y + hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
+__device__ __forceinline__ uint32_t add2(uint32_t y, float lo, float hi, int type) {
+    const float2 f = unpack2(y, type);
+    return pack2(f.x + lo, f.y + hi, type);
 }
 // y += o, in FP32 with one rounding.
 __device__ __forceinline__ void add_eight(Eight& y, const float (&o)[8], int type) {
-    if (type == NVFP4_TYPE_BF16) {
-        y.a = make_uint4(add2_bf16(y.a.x, o[0], o[1]), add2_bf16(y.a.y, o[2], o[3]), add2_bf16(y.a.z, o[4], o[5]), add2_bf16(y.a.w, o[6], o[7]));
+    if (type == NVFP4_TYPE_BF16) {        // one branch for all
+        y.a = make_uint4(add2(y.a.x, o[0], o[1], NVFP4_TYPE_BF16), add2(y.a.y, o[2], o[3], NVFP4_TYPE_BF16),
+                         add2(y.a.z, o[4], o[5], NVFP4_TYPE_BF16), add2(y.a.w, o[6], o[7], NVFP4_TYPE_BF16));
     } else if (type == NVFP4_TYPE_F16) {
-        y.a = make_uint4(add2_f16(y.a.x, o[0], o[1]), add2_f16(y.a.y, o[2], o[3]), add2_f16(y.a.z, o[4], o[5]), add2_f16(y.a.w, o[6], o[7]));
+        y.a = make_uint4(add2(y.a.x, o[0], o[1], NVFP4_TYPE_F16), add2(y.a.y, o[2], o[3], NVFP4_TYPE_F16),
+                         add2(y.a.z, o[4], o[5], NVFP4_TYPE_F16), add2(y.a.w, o[6], o[7], NVFP4_TYPE_F16));
     } else {
         const auto add = [](uint32_t w, float v) { return __float_as_uint(__uint_as_float(w) + v); };
         y.a = make_uint4(add(y.a.x, o[0]), add(y.a.y, o[1]), add(y.a.z, o[2]), add(y.a.w, o[3]));

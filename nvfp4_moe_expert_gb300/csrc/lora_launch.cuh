@@ -23,7 +23,7 @@ inline int64_t tiles_bound(int64_t T, int L, int rows_per_tile) {
 
 // Terms that h is taken as by the second product.
 template <typename T>
-int terms_of(int y_type) {
+__host__ __device__ constexpr int terms_of(int y_type) {
     return std::is_same<T, __nv_bfloat16>::value && y_type == NVFP4_TYPE_F32 ? 3 : 2;
 }
 
@@ -39,7 +39,7 @@ cudaError_t by_rank(int R, F&& f) {
 struct Ready {
     std::mutex mutex;
     bool on[kMaxDevices] = {};
-    int clusters[kMaxDevices][2][kMaxRank / 8 + 1] = {};   // that run at once, by output and rank (0: not asked yet)
+    int clusters[kMaxDevices][kMaxRank / 8 + 1] = {};   // that run at once, by rank (0: not asked yet)
 };
 inline cudaError_t allow_shared(const void* kernel, int bytes, Ready& ready) {
     int dev = 0;
@@ -57,13 +57,13 @@ inline cudaError_t allow_shared(const void* kernel, int bytes, Ready& ready) {
 
 // Clusters of kSplit CTAs of a kernel that run at once on the current device.
 template <typename... A>
-cudaError_t clusters_at_once(void (*kernel)(A...), int threads, int smem, int R, bool out32, Ready& ready, int64_t& clusters) {
+cudaError_t clusters_at_once(void (*kernel)(A...), int threads, int smem, int R, Ready& ready, int64_t& clusters) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(ready.mutex);
-    int& known = ready.clusters[dev][out32][R / 8];
+    int& known = ready.clusters[dev][R / 8];
     if (known == 0) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(kSplit);
@@ -132,9 +132,14 @@ cudaError_t launch_sort(const int32_t* ids, int64_t T, int L, int rows_per_tile,
 cudaError_t launch_few_forward_bf16(const Params& p, int64_t tiles, bool pdl, cudaStream_t st);
 cudaError_t launch_few_forward_f16(const Params& p, int64_t tiles, bool pdl, cudaStream_t st);
 cudaError_t launch_few_backward(const Params& p, int64_t tiles, bool pdl, cudaStream_t st);
-cudaError_t launch_many_forward_bf16(const Params& p, int64_t tiles, bool pdl, cudaStream_t st);
-cudaError_t launch_many_forward_f16(const Params& p, int64_t tiles, bool pdl, cudaStream_t st);
-cudaError_t launch_many_backward(const Params& p, int64_t tiles, bool pdl, cudaStream_t st);
+template <typename T, bool kTrans, int kType>
+cudaError_t launch_many(const Params& p, int64_t tiles, bool pdl, cudaStream_t st);
+template <typename T, bool kTrans>
+cudaError_t launch_many_any(const Params& p, int64_t tiles, bool pdl, cudaStream_t st) {
+    return p.y_type == NVFP4_TYPE_BF16  ? launch_many<T, kTrans, NVFP4_TYPE_BF16>(p, tiles, pdl, st)
+           : p.y_type == NVFP4_TYPE_F16 ? launch_many<T, kTrans, NVFP4_TYPE_F16>(p, tiles, pdl, st)
+                                        : launch_many<T, kTrans, NVFP4_TYPE_F32>(p, tiles, pdl, st);
+}
 
 // Gradients of the adapters.
 struct GradParams {

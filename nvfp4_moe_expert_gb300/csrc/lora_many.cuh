@@ -6,7 +6,7 @@
 // 8 CTAs' sums meet in shared memory over the cluster, each CTA adding 16 rows and handing their terms to all; products of the
 // second phase are added to y where it lies in shared memory, which goes out from there in whole rows of 128 bytes.
 //
-// x and y come by TMA, four rows of any place to an instruction (their tile's rows lie where the sort found them), where
+// x and y come by TMA, 16 rows to an instruction where they lie in a row, four rows of any place otherwise, where
 // rows start on 16-byte boundaries; otherwise four loader warps read aligned words and shift them together.  (With the loads
 // and the products in the same warps, cp.async and a barrier for each stage, 16384 x 4096 -> 4096 of rank 16 took 145 to 199 us:
 // 500 instructions a stage and warp, half of them addresses.)
@@ -24,6 +24,12 @@ __device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, ui
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(at[0]), "r"(at[1]), "r"(at[2]), "r"(at[3]), "r"(bar)
         : "memory");
 }
+// Sixteen rows from `row` on.
+__device__ __forceinline__ void load_rows16(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c, int row) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(row), "r"(bar)
+                 : "memory");
+}
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c, int row, int slice) {
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(row), "r"(slice), "r"(bar)
@@ -32,16 +38,19 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, u
 __device__ __forceinline__ void consumer_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 struct ManyMaps {
-    CUtensorMap x, y, down, up;
+    CUtensorMap x, y, x16, y16, down, up;   // of x and y: boxes of one row, for gathers, and of 16
 };
 
 // The second product of a warp's 16 rows with a group of 32 outputs (`up`: the group's rows, or columns): acc[i] gets
 // outputs 8 i to 8 i + 7.
-template <typename T, bool kTrans>
-__device__ __forceinline__ void multiply_outputs(float (&acc)[4][4], uint32_t h, int term_bytes, int terms, uint32_t up, int block_bytes,
+template <typename T, bool kTrans, int kTerms>
+__device__ __forceinline__ void multiply_outputs(float (&acc)[4][4], uint32_t h, int term_bytes, uint32_t up, int block_bytes,
                                                  int first_chunk, int Rp, int lane) {
+#pragma unroll 1
     for (int kk = 0; kk < Rp / 16; ++kk) {
-        uint32_t b[2][4];
+        uint32_t a[kTerms][4], b[2][4];
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t) ldsm4(h + t * term_bytes + 32 * kk, a[t]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {     // two tiles of 8 outputs at once
             if (!kTrans)                  // rows of 64 ranks
@@ -49,20 +58,22 @@ __device__ __forceinline__ void multiply_outputs(float (&acc)[4][4], uint32_t h,
             else                          // rows of 64 outputs
                 ldsm4_trans(up + swizzled(16 * kk + ((lane >> 3) & 1) * 8 + (lane & 7), first_chunk + 2 * i + (lane >> 4)), b[i]);
         }
-        for (int t = 0; t < terms; ++t) {
-            uint32_t a[4];
-            ldsm4(h + t * term_bytes + 32 * kk, a);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma(T(), acc[i], a, b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
+        for (int t = 0; t < kTerms; ++t) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma(T(), acc[i], a[t], b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
         }
     }
 }
 
-// kLoaders: warps that load, 1 (x and y by TMA) or 4.
-template <typename T, bool kTrans, int kRank, int kLoaders>
+// kLoaders: warps that load, 1 (x and y by TMA) or 4.  kType: y's and out's (branches by it for every value took 3000 cycles a stage).
+template <typename T, bool kTrans, int kType, int kRank, int kLoaders>
 __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoaders == 1 ? 2 : 1)
-    many_kernel(const __grid_constant__ ManyMaps maps, const Params p, const ManyLayout lay, const int terms) {
+    many_kernel(const __grid_constant__ ManyMaps maps, const Params p, const ManyLayout lay) {
     constexpr int kTiles = kRank / 8;
+    constexpr bool kWide = kType == NVFP4_TYPE_F32;
+    constexpr int kCols = kWide ? 32 : 64, kUnits = kWide ? 2 : 1;   // outputs of a stage; 16-bit units of an output
+    constexpr int kTerms = terms_of<T>(kType);
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], sums_ready, h_ready;
     __shared__ float s_undo[kManyRows];
@@ -73,9 +84,8 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_rank());
     const int steps = sub_steps(p.C), c0 = min(rank * kWarps * steps * 16, p.C), c1 = min(c0 + kWarps * steps * 16, p.C);
-    const int chunks = (p.D + lay.cols - 1) / lay.cols, per_cta = (chunks + kSplit - 1) / kSplit;
+    const int chunks = (p.D + kCols - 1) / kCols, per_cta = (chunks + kSplit - 1) / kSplit;
     const int chunk0 = min(rank * per_cta, chunks), chunk1 = min(chunk0 + per_cta, chunks);
-    const int units = p.y_type == NVFP4_TYPE_F32 ? 2 : 1;   // 16-bit units of an output
     if (threadIdx.x == 0) {
         for (int s = 0; s < lay.stages; ++s) {
             mbar_init(&full[s], kLoaders == 1 ? 1 : 32 * kLoaders);
@@ -87,8 +97,8 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
         fence_barrier_init();
     }
     if (threadIdx.x == kThreads) {
-        prefetch_tensormap(&maps.x);
-        prefetch_tensormap(&maps.y);
+        prefetch_tensormap(&maps.x16);
+        prefetch_tensormap(&maps.y16);
         prefetch_tensormap(&maps.down);
         prefetch_tensormap(&maps.up);
     }
@@ -119,10 +129,16 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
             // TMA: a lane's four rows (behind the last: outside the tensor, zeros); otherwise a thread's chunk of every 16th row
             constexpr int kMine = kLoaders == 1 ? 4 : 8;
             int row[kMine];
-            const bool group = 4 * lane < rows && warp == kWarps;
             int four[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) four[i] = 4 * lane + i < rows ? p.tiles.perm[start + 4 * lane + i] : p.T;
+            // 16 rows in a row, as those of one request are, are one box (the rows behind the tile's last are read along)
+            const int group_row = __shfl_sync(kAll, four[0], lane & ~3);
+            bool apart = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) apart |= 4 * lane + i < rows && four[i] != group_row + 4 * (lane & 3) + i;
+            const bool box = (__ballot_sync(kAll, apart) >> (lane & ~3) & 15) == 0;
+            const bool group = 16 * (lane >> 2) < rows && warp == kWarps && (!box || (lane & 3) == 0);
             if (kLoaders > 1) {
 #pragma unroll
                 for (int i = 0; i < kMine; ++i) {
@@ -135,26 +151,29 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
                 if (__any_sync(kAll, failed)) break;
                 const uint32_t at = base + buffer * lay.stage, part = at + kManyRows * 128, bar = smem_u32(&full[buffer]);
                 const bool is_x = s < x_stages, tma = is_x ? x_tma : y_tma, none = !is_x && p.y == nullptr;
-                const int c = is_x ? c0 + 64 * s : (chunk0 + s - x_stages) * lay.cols;
+                const int c = is_x ? c0 + 64 * s : (chunk0 + s - x_stages) * kCols;
                 if (kLoaders > 1) fence_proxy_async_shared();
                 if (thread == 0) {
-                    const int bytes = (adapter < 0 ? 0 : is_x ? lay.down_bytes : lay.up_bytes) + (tma && !none ? (rows + 3) / 4 * 512 : 0);
+                    const int bytes = (adapter < 0 ? 0 : is_x ? lay.down_bytes : lay.up_bytes) + (tma && !none ? (rows + 15) / 16 * 2048 : 0);
                     mbar_arrive_expect_tx(&full[buffer], bytes);
                     if (adapter >= 0 && is_x) {
                         if (!kTrans) load_box(part, &maps.down, bar, c, 0, adapter);
                         else for (int b = 0; b < lay.blocks; ++b) load_box(part + b * 64 * 128, &maps.down, bar, 64 * b, c, adapter);
                     } else if (adapter >= 0) {
                         if (kTrans) load_box(part, &maps.up, bar, c, 0, adapter);
-                        else for (int b = 0; b < lay.blocks; ++b) load_box(part + b * lay.cols * 128, &maps.up, bar, 64 * b, c, adapter);
+                        else for (int b = 0; b < lay.blocks; ++b) load_box(part + b * kCols * 128, &maps.up, bar, 64 * b, c, adapter);
                     }
                 }
                 __syncwarp();
-                if (tma && !none && group) gather4(at + 512 * lane, is_x ? &maps.x : &maps.y, bar, is_x ? c : c * units, four);
+                if (tma && !none && group) {
+                    if (box) load_rows16(at + 512 * lane, is_x ? &maps.x16 : &maps.y16, bar, is_x ? c : c * kUnits, group_row);
+                    else gather4(at + 512 * lane, is_x ? &maps.x : &maps.y, bar, is_x ? c : c * kUnits, four);
+                }
                 if (kLoaders > 1) {
                     if (!tma && !none) {
                         const uint16_t* from = static_cast<const uint16_t*>(is_x ? p.x : p.y);
-                        const int64_t ld = is_x ? p.ldx : p.ldy * units;
-                        const int unit = (is_x ? c : c * units) + 8 * (thread & 7), there = is_x ? p.C : p.D * units;
+                        const int64_t ld = is_x ? p.ldx : p.ldy * kUnits;
+                        const int unit = (is_x ? c : c * kUnits) + 8 * (thread & 7), there = is_x ? p.C : p.D * kUnits;
 #pragma unroll
                         for (int i = 0; i < kMine; i += 4) {
                             Straddle w[4];
@@ -201,7 +220,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = 16 * warp + (lane >> 3) + 4 * i;
-                out[i] = r < rows ? static_cast<uint8_t*>(p.out) + (p.tiles.perm[start + r] * p.ldo + chunk0 * lay.cols) * (2 * units) + 16 * (lane & 7)
+                out[i] = r < rows ? static_cast<uint8_t*>(p.out) + (p.tiles.perm[start + r] * p.ldo + chunk0 * kCols) * (2 * kUnits) + 16 * (lane & 7)
                                   : nullptr;
             }
             if (adapter >= 0) {
@@ -219,20 +238,22 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
                         const uint32_t sd = at + kManyRows * 128 +
                                             (kTrans ? swizzled(((lane >> 3) & 1) * 8 + (lane & 7), lane >> 4) : lane_down<false>(lane, p.R));
                         const int n = min(4, (c1 - c0 - 64 * s + 15) / 16);
-#pragma unroll 1
-                        for (int kk = 0; kk < n; ++kk) {
-                            uint32_t a[4];
-                            ldsm4(sx ^ (kk << 5), a);
+                        uint32_t a[4][4];
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) ldsm4(sx ^ (kk << 5), a[kk]);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if (kk >= n) break;
                             if (!kTrans) {
-                                multiply_down<T, false, kTiles>(acc, a, sd, kk, p.R);
+                                multiply_down<T, false, kTiles>(acc, a[kk], sd, kk, p.R);
                             } else {                        // rows of 64 ranks, 16 to a step
 #pragma unroll
                                 for (int j = 0; j < kTiles; j += 2) {
                                     if (8 * j >= p.R) break;
                                     uint32_t b[4];
                                     ldsm4_trans((sd ^ ((j & 7) << 4)) + (j >> 3) * 64 * 128 + 2048 * kk, b);
-                                    mma(T(), acc[j], a, b[0], b[1]);
-                                    if (8 * (j + 1) < p.R) mma(T(), acc[j + 1], a, b[2], b[3]);
+                                    mma(T(), acc[j], a[kk], b[0], b[1]);
+                                    if (8 * (j + 1) < p.R) mma(T(), acc[j + 1], a[kk], b[2], b[3]);
                                 }
                             }
                             if (--left == 0) {
@@ -271,7 +292,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
                     const bool keep = p.h != nullptr && r < rows;
                     float row_undo;
                     finish_row<T, kRank>(reinterpret_cast<const float*>(smem + lay.sum), r, lay.sum_pitch, p.R,
-                                         p.scale == nullptr ? 1.0f : p.scale[adapter], terms, kManyRows * pitch,
+                                         p.scale == nullptr ? 1.0f : p.scale[adapter], kTerms, kManyRows * pitch,
                                          keep ? p.h + static_cast<int64_t>(p.tiles.perm[start + r]) * p.R : nullptr, p.h_scaled != 0,
                                          lane & 15,
                                          [&](int at, uint32_t v) {
@@ -301,54 +322,76 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
                 undo[0] = s_undo[my_row];
                 undo[1] = s_undo[my_row + 8];
             }
-            for (int chunk = chunk0; chunk < chunk1; ++chunk) {
-                if (!failed && !mbar_wait_bounded(&full[buffer], phase, abort_flag, kWaitBudgetCycles)) failed = true;
-                if (busy && !failed) {
-                    const uint32_t at = base + buffer * lay.stage, part = at + kManyRows * 128;
-#pragma unroll 1
-                    for (int g = 0; 32 * g < lay.cols; ++g) {
-                        float acc[4][4];
+            {
+                // a lane's 2 outputs of 4 tiles of 8, in its two rows
+                const int mine = my_row * 128 + (kWide ? (((lane >> 1) & 1) ^ quad) << 4 | 8 * (lane & 1) : quad << 4 | 4 * (lane & 3));
+                const int line = swizzled(16 * warp + (lane >> 3), lane & 7);
+                const int full_rows = p.out_wide ? min(max(rows - 16 * warp, 0), 16) : 0;
+                for (int chunk = chunk0; chunk < chunk1; ++chunk) {
+                    if (!failed && !mbar_wait_bounded(&full[buffer], phase, abort_flag, kWaitBudgetCycles)) failed = true;
+                    uint4 v[4];
+                    if (busy && !failed) {
+                        uint8_t* y = smem + buffer * lay.stage;
+                        const uint32_t part = smem_u32(y) + kManyRows * 128;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int g = 0; g < kCols / 32; ++g) {
+                            // y where it lies; all read before any is written, which the compiler cannot do by itself
+                            const auto at = [&](int i, int r) { return y + 1024 * r + (mine ^ (kWide ? i << 5 : (4 * g + i) << 4)); };
+                            float2 was[4][2];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-                        }
-                        if (adapter >= 0)
-                            multiply_outputs<T, kTrans>(acc, ha, kManyRows * pitch, terms, part + (kTrans ? 0 : 4096 * g), lay.cols * 128, 4 * g,
-                                                        rank_up(p.R), lane);
-                        // y where it lies: a lane's 2 outputs of 4 tiles of 8, in its two rows
-                        uint8_t* y = smem + buffer * lay.stage + my_row * 128;
+                            for (int i = 0; i < 4; ++i) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                                for (int r = 0; r < 2; ++r) {
+                                    if (kWide) was[i][r] = *reinterpret_cast<const float2*>(at(i, r));
+                                    else was[i][r] = unpack2(*reinterpret_cast<const uint32_t*>(at(i, r)), kType);
+                                    if (p.y == nullptr) was[i][r] = make_float2(0.0f, 0.0f);
+                                }
+                            }
+                            float acc[4][4];
 #pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                float lo = acc[i][2 * r], hi = acc[i][2 * r + 1];
-                                if (std::is_same<T, __half>::value) lo *= undo[r], hi *= undo[r];
-                                if (units == 2) {
-                                    float2* to = reinterpret_cast<float2*>(y + 1024 * r + (((2 * i + ((lane >> 1) & 1)) ^ quad) << 4) + 8 * (lane & 1));
-                                    const float2 was = p.y == nullptr ? make_float2(0.0f, 0.0f) : *to;
-                                    *to = make_float2(was.x + lo, was.y + hi);
-                                } else {
-                                    uint32_t* to = reinterpret_cast<uint32_t*>(y + 1024 * r + (((4 * g + i) ^ quad) << 4) + 4 * (lane & 3));
-                                    const uint32_t was = p.y == nullptr ? 0u : *to;
-                                    *to = p.y_type == NVFP4_TYPE_BF16 ? add2_bf16(was, lo, hi) : add2_f16(was, lo, hi);
+                            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+                            }
+                            if (adapter >= 0)
+                                multiply_outputs<T, kTrans, kTerms>(acc, ha, kManyRows * pitch, part + (kTrans ? 0 : 4096 * g), kCols * 128, 4 * g,
+                                                                    rank_up(p.R), lane);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    float lo = acc[i][2 * r], hi = acc[i][2 * r + 1];
+                                    if (std::is_same<T, __half>::value) lo *= undo[r], hi *= undo[r];
+                                    lo += was[i][r].x, hi += was[i][r].y;
+                                    if (kWide) *reinterpret_cast<float2*>(at(i, r)) = make_float2(lo, hi);
+                                    else *reinterpret_cast<uint32_t*>(at(i, r)) = pack2(lo, hi, kType);
                                 }
                             }
                         }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(y + (line ^ (i & 1) << 6) + 512 * i);
+                        fence_proxy_async_shared();         // this stage was written to; TMA writes it next
                     }
                     __syncwarp();
-                    const int left = (p.D - chunk * lay.cols) * units - 8 * (lane & 7);   // units of the row from the lane's on
+                    if (lane == 0) mbar_arrive(&empty[buffer]);   // in front of the stores, which it would wait for
+                    next_buffer();
+                    const int left = busy && !failed ? (p.D - chunk * kCols) * kUnits - 8 * (lane & 7) : 0;   // units of the row from the lane's on
+                    if (full_rows == 16 && left >= 8) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (out[i] == nullptr || left <= 0) continue;
-                        const uint4 v = *reinterpret_cast<const uint4*>(smem + buffer * lay.stage + swizzled(16 * warp + (lane >> 3) + 4 * i, lane & 7));
-                        if (p.out_wide && left >= 8) {
-                            *reinterpret_cast<uint4*>(out[i]) = v;
-                        } else {
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(out[i]) = v[i];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (out[i] == nullptr || left <= 0) continue;
+                            if (p.out_wide && left >= 8) {
+                                *reinterpret_cast<uint4*>(out[i]) = v[i];
+                                continue;
+                            }
+                            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                if (units == 2) {
+                                if (kWide) {
                                     if (2 * j < left) reinterpret_cast<uint32_t*>(out[i])[j] = w[j];
                                 } else {
                                     if (2 * j < left) reinterpret_cast<uint16_t*>(out[i])[2 * j] = static_cast<uint16_t>(w[j]);
@@ -357,15 +400,11 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
                             }
                         }
                     }
-                    fence_proxy_async_shared();             // this stage was written to; TMA writes it next
-                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (out[i] != nullptr) out[i] += 128;
+                    for (int i = 0; i < 4; ++i) {
+                        if (out[i] != nullptr) out[i] += 128;
+                    }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[buffer]);
-                next_buffer();
             }
         }
         if (failed) {
@@ -377,40 +416,42 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
     cluster_barrier();                                      // no CTA leaves while another may reach into it
 }
 
-template <typename T, bool kTrans, int kRank, int kLoaders>
-cudaError_t launch_many(const ManyMaps& maps, const Params& p, const ManyLayout& lay, int terms, int64_t tiles, bool pdl, cudaStream_t st) {
+template <typename T, bool kTrans, int kType, int kRank, int kLoaders>
+cudaError_t launch_many_kernel(const ManyMaps& maps, const Params& p, const ManyLayout& lay, int64_t tiles, bool pdl, cudaStream_t st) {
     static Ready ready;
-    auto* kernel = many_kernel<T, kTrans, kRank, kLoaders>;
+    auto* kernel = many_kernel<T, kTrans, kType, kRank, kLoaders>;
     cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), kManyShared, ready);
     if (e != cudaSuccess) return e;
     int64_t clusters = 0;                                   // that run at once
-    e = clusters_at_once(kernel, kThreads + 32 * kLoaders, lay.total, p.R, p.y_type == NVFP4_TYPE_F32, ready, clusters);
+    e = clusters_at_once(kernel, kThreads + 32 * kLoaders, lay.total, p.R, ready, clusters);
     if (e != cudaSuccess) return e;
     if (tiles < clusters) clusters = tiles;
     return launch_pdl(pdl, kernel, dim3(static_cast<unsigned>(clusters * kSplit)), dim3(kThreads + 32 * kLoaders),
-                      static_cast<size_t>(lay.total), st, maps, p, lay, terms);
+                      static_cast<size_t>(lay.total), st, maps, p, lay);
 }
 
-template <typename T, bool kTrans>
+template <typename T, bool kTrans, int kType>
 cudaError_t launch_many(const Params& p, int64_t tiles, bool pdl, cudaStream_t st) {
-    const int terms = terms_of<T>(p.y_type), units = p.y_type == NVFP4_TYPE_F32 ? 2 : 1, Rp = rank_up(p.R);
-    const ManyLayout lay(p.R, terms, kTrans, p.y_type);
+    const int units = kType == NVFP4_TYPE_F32 ? 2 : 1, Rp = rank_up(p.R);
+    const ManyLayout lay(p.R, terms_of<T>(kType), kTrans, kType);
     const bool tma_y = p.y != nullptr && p.out_wide;
     ManyMaps maps;
-    // what is not used is x's map again
     bool ok = kTrans ? make_units_map(&maps.down, p.down, p.R, p.C, p.R, p.L, static_cast<int64_t>(p.C) * p.R, 64)
                      : make_units_map(&maps.down, p.down, p.C, p.R, p.C, p.L, static_cast<int64_t>(p.C) * p.R, Rp);
     ok = ok && (kTrans ? make_units_map(&maps.up, p.up, p.D, p.R, p.D, p.L, static_cast<int64_t>(p.D) * p.R, Rp)
                        : make_units_map(&maps.up, p.up, p.R, p.D, p.R, p.L, static_cast<int64_t>(p.D) * p.R, lay.cols));
-    maps.x = maps.y = maps.up;
-    if (ok && p.x_wide) ok = make_units_map(&maps.x, p.x, p.C, p.T, p.ldx, 0, 0, 1);
-    if (ok && tma_y) ok = make_units_map(&maps.y, p.y, static_cast<int64_t>(p.D) * units, p.T, p.ldy * units, 0, 0, 1);
+    maps.x = maps.y = maps.x16 = maps.y16 = maps.up;        // what is not used is another's
+    if (ok && p.x_wide)
+        ok = make_units_map(&maps.x, p.x, p.C, p.T, p.ldx, 0, 0, 1) && make_units_map(&maps.x16, p.x, p.C, p.T, p.ldx, 0, 0, 16);
+    const int64_t row = static_cast<int64_t>(p.D) * units;
+    if (ok && tma_y)
+        ok = make_units_map(&maps.y, p.y, row, p.T, p.ldy * units, 0, 0, 1) && make_units_map(&maps.y16, p.y, row, p.T, p.ldy * units, 0, 0, 16);
     if (!ok) return cudaErrorInvalidValue;
     const bool one = p.x_wide && (tma_y || p.y == nullptr);
     return by_rank(p.R, [&](auto rank) {
         constexpr int kRank = decltype(rank)::value;
-        return one ? launch_many<T, kTrans, kRank, 1>(maps, p, lay, terms, tiles, pdl, st)
-                   : launch_many<T, kTrans, kRank, 4>(maps, p, lay, terms, tiles, pdl, st);
+        return one ? launch_many_kernel<T, kTrans, kType, kRank, 1>(maps, p, lay, tiles, pdl, st)
+                   : launch_many_kernel<T, kTrans, kType, kRank, 4>(maps, p, lay, tiles, pdl, st);
     });
 }
 

@@ -1,0 +1,10 @@
+// Low-rank adapters, tiles of 128 rows: forward, FP16 x, outputs in BF16.
+#include "lora_many.cuh"
+
+namespace nvfp4 {
+namespace lora {
+
+template cudaError_t launch_many<__half, false, NVFP4_TYPE_BF16>(const Params&, int64_t, bool, cudaStream_t);
+
+}  // namespace lora
+}  // namespace nvfp4
