@@ -649,9 +649,9 @@ nvfp4_status lora_add(const lora_adapters* adapters, const void* x_dev, int64_t 
  *  dx_dev         [T][lddx] of dx_type, element aligned, lddx >= K; shares no byte with dy or x.  accumulate 0:
  *                 written (zeros where there is no adapter); 1: added to, in FP32 with one rounding
  *  ddown_dev      float [L][R][K], dup_dev float [L][N][R], written whole (zeros for adapters without tokens)
- *  ws_dev         lora_add_backward_workspace_bytes(T, L, R) bytes, 256-byte aligned
+ *  ws_dev         lora_add_backward_workspace_bytes(T, L, R, K, N) bytes, 256-byte aligned
  * Device error: NVFP4_ERR_BAD_EXPERT_ID. */
-size_t lora_add_backward_workspace_bytes(int64_t T, int L, int R);
+size_t lora_add_backward_workspace_bytes(int64_t T, int L, int R, int64_t K, int64_t N);
 nvfp4_status lora_add_backward(const lora_adapters* adapters, const void* dy_dev, int64_t lddy, const void* x_dev,
                                int64_t ldx, const float* h_dev, const int32_t* adapter_ids_dev, int64_t T, void* dx_dev,
                                int64_t lddx, int dx_type, int accumulate, float* ddown_dev, float* dup_dev, void* ws_dev,

@@ -145,7 +145,7 @@ _SIGNATURES = {
                             _P]),
     "lora_add_workspace_bytes": (_SZ, [_I64, _I32]),
     "lora_add": (_I32, [ctypes.POINTER(lora_adapters), _P, _I64, _I64, _P, _P, _I64, _P, _I64, _I32, _P, _P, _SZ, _P]),
-    "lora_add_backward_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
+    "lora_add_backward_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I64, _I64]),
     "lora_add_backward": (_I32, [ctypes.POINTER(lora_adapters), _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I32, _I32, _P, _P,
                                  _P, _SZ, _P]),
 }
@@ -902,7 +902,7 @@ def lora_add_backward(dy, x, h, adapters, adapter_ids, dx=None, stream=None):
         dx, code, lddx = _empty((T, K), torch.bfloat16, device, stream), 1, K
     ddown = _empty((adapters.L, adapters.R, K), torch.float32, device, stream)
     dup = _empty((adapters.L, adapters.N, adapters.R), torch.float32, device, stream)
-    need = lib().lora_add_backward_workspace_bytes(T, adapters.L, adapters.R)
+    need = lib().lora_add_backward_workspace_bytes(T, adapters.L, adapters.R, K, adapters.N)
     ws = _empty((need,), torch.uint8, device, stream) if need else None
     status = lib().lora_add_backward(adapters.struct, dy.data_ptr(), lddy, x.data_ptr(), ldx, h.data_ptr(),
                                      adapter_ids.data_ptr(), T, dx.data_ptr(), lddx, code, 1 if add else 0, ddown.data_ptr(),

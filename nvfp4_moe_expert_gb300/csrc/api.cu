@@ -930,9 +930,9 @@ bool adapters_ok(const lora_adapters& a) {
 size_t lora_add_workspace_bytes(int64_t T, int L) {
     return T >= 0 && T < kMaxTokens && L >= 1 && L <= 1024 ? lora_workspace(T, L) : 0;
 }
-size_t lora_add_backward_workspace_bytes(int64_t T, int L, int R) {
-    return T > 0 && T < kMaxTokens && L >= 1 && L <= 1024 && R >= 8 && R <= 128 && R % 8 == 0 ? lora_backward_workspace(T, L, R)
-                                                                                              : 0;
+size_t lora_add_backward_workspace_bytes(int64_t T, int L, int R, int64_t K, int64_t N) {
+    const lora_adapters a = {nullptr, nullptr, nullptr, NVFP4_TYPE_BF16, L, R, K, N};
+    return T > 0 && T < kMaxTokens && adapters_shape_ok(a) ? lora_backward_workspace(T, L, R, K, N) : 0;
 }
 
 nvfp4_status lora_add(const lora_adapters* adapters, const void* x_dev, int64_t T, int64_t ldx,
@@ -984,7 +984,7 @@ nvfp4_status lora_add_backward(const lora_adapters* adapters, const void* dy_dev
     if (!dy_dev || !x_dev || !h_dev || !adapter_ids_dev || !dx_dev || !ws_dev || !aligned(dy_dev, 2) || !aligned(x_dev, 16) ||
         !aligned(h_dev, 16) || !aligned(adapter_ids_dev, 4) || !aligned(dx_dev, dx_size) || !aligned(ws_dev, 256))
         return NVFP4_ERR_INVALID_ARG;
-    if (ws_bytes < lora_backward_workspace(T, a.L, a.R)) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
+    if (ws_bytes < lora_backward_workspace(T, a.L, a.R, a.K, a.N)) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
     if (rows_overlap(dy_dev, lddy * 2, a.N * 2, dx_dev, lddx * dx_size, a.K * dx_size, T) ||
         rows_overlap(x_dev, ldx * 2, a.K * 2, dx_dev, lddx * dx_size, a.K * dx_size, T))
         return NVFP4_ERR_INVALID_ARG;

@@ -17,9 +17,9 @@ constexpr int kAhead = 4;                 // loads of ids at a time
 __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kSortThreads, 1)
     sort_kernel(const int32_t* __restrict__ ids, int T, int L, int rows_per_tile, int32_t* __restrict__ perm,
                 int32_t* __restrict__ offsets, int32_t* __restrict__ tile_adapter, int32_t* __restrict__ tile_start,
-                int32_t* __restrict__ tile_count, int* err) {
+                int32_t* __restrict__ tile_count, int32_t* __restrict__ prefix, int* err) {
     extern __shared__ int s_at[];                           // [kSortWarps][bins] rows of a warp, then those in front of it
-    __shared__ int s_scan[2][kSortWarps];
+    __shared__ int s_scan[3][kSortWarps];
     const int bins = L + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_rank());
     int* mine = s_at + warp * bins;
@@ -64,7 +64,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kSortThreads, 1
     cluster_barrier();
     // the adapters one behind the other, 1024 at a time (L is at most that, and one for the rows without); every CTA
     // does all of it, each writes the tiles of every eighth adapter
-    int first_row = 0, first_tile = 0;
+    int first_row = 0, first_tile = 0, first_stage = 0;
     for (int base = 0; base < bins; base += kSortThreads) {
         const int a = base + static_cast<int>(threadIdx.x);
         int own = 0, front = 0;
@@ -77,28 +77,32 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kSortThreads, 1
             }
         }
         const int tiles = (own + rows_per_tile - 1) / rows_per_tile;
-        int r = own, n = tiles;
+        const int stages = a >= L ? 0 : max((own + kStageRows - 1) / kStageRows, 1);
+        int r = own, n = tiles, g = stages;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int ur = __shfl_up_sync(kAll, r, o), un = __shfl_up_sync(kAll, n, o);
-            if (lane >= o) r += ur, n += un;
+            const int ur = __shfl_up_sync(kAll, r, o), un = __shfl_up_sync(kAll, n, o), ug = __shfl_up_sync(kAll, g, o);
+            if (lane >= o) r += ur, n += un, g += ug;
         }
-        if (lane == 31) s_scan[0][warp] = r, s_scan[1][warp] = n;
+        if (lane == 31) s_scan[0][warp] = r, s_scan[1][warp] = n, s_scan[2][warp] = g;
         __syncthreads();
-        int wr = s_scan[0][lane], wn = s_scan[1][lane];     // every warp: the warps in front
+        int wr = s_scan[0][lane], wn = s_scan[1][lane], wg = s_scan[2][lane];   // every warp: the warps in front
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int ur = __shfl_up_sync(kAll, wr, o), un = __shfl_up_sync(kAll, wn, o);
-            if (lane >= o) wr += ur, wn += un;
+            const int ur = __shfl_up_sync(kAll, wr, o), un = __shfl_up_sync(kAll, wn, o), ug = __shfl_up_sync(kAll, wg, o);
+            if (lane >= o) wr += ur, wn += un, wg += ug;
         }
         const int row = first_row + r - own + (warp ? __shfl_sync(kAll, wr, (warp - 1) & 31) : 0);
         const int tile = first_tile + n - tiles + (warp ? __shfl_sync(kAll, wn, (warp - 1) & 31) : 0);
+        const int stage = first_stage + g - stages + (warp ? __shfl_sync(kAll, wg, (warp - 1) & 31) : 0);
+        first_stage += __shfl_sync(kAll, wg, 31);
         first_row += __shfl_sync(kAll, wr, 31);
         first_tile += __shfl_sync(kAll, wn, 31);
         if (a < bins) {
             s_first[a] = row + front;
             if (a % kSplit == rank) {
                 offsets[a] = row;
+                prefix[a] = stage;                          // at L: all
                 for (int i = 0; i < tiles; ++i) {
                     tile_adapter[tile + i] = a < L ? a : -1;
                     tile_start[tile + i] = row + i * rows_per_tile;
@@ -163,7 +167,7 @@ bool make_units_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows
 
 size_t sort_bytes(int64_t T, int L) {
     const size_t tiles = static_cast<size_t>(tiles_bound(T, L, kFewRows));
-    return align_256(static_cast<size_t>(T) * 4) + align_256((L + 2) * 4) + 2 * align_256(tiles * 4) + 256;
+    return align_256(static_cast<size_t>(T) * 4) + 2 * align_256((L + 2) * 4) + 2 * align_256(tiles * 4) + 256;
 }
 
 Tiles sort_layout(void* ws, int64_t T, int L) {
@@ -179,6 +183,8 @@ Tiles sort_layout(void* ws, int64_t T, int L) {
     t.start = reinterpret_cast<int32_t*>(p);
     p += align_256(tiles * 4);
     t.count = reinterpret_cast<int32_t*>(p);
+    p += 256;
+    t.prefix = reinterpret_cast<int32_t*>(p);
     return t;
 }
 
@@ -190,7 +196,8 @@ cudaError_t launch_sort(const int32_t* ids, int64_t T, int L, int rows_per_tile,
     if (e != cudaSuccess) return e;
     return launch_pdl(false, sort_kernel, dim3(kSplit), dim3(kSortThreads), smem, st, ids, static_cast<int>(T), L, rows_per_tile,
                       const_cast<int32_t*>(t.perm), const_cast<int32_t*>(t.offsets), const_cast<int32_t*>(t.adapter),
-                      const_cast<int32_t*>(t.start), const_cast<int32_t*>(t.count), err);
+                      const_cast<int32_t*>(t.start), const_cast<int32_t*>(t.count),
+                      const_cast<int32_t*>(t.prefix), err);
 }
 
 }  // namespace lora
@@ -208,8 +215,10 @@ constexpr int64_t kFewTokens = 1024;
 
 bool lora_sorts(int64_t T) { return T > lora::kInCta; }
 size_t lora_workspace(int64_t T, int L) { return lora_sorts(T) ? lora::sort_bytes(T, L) : 0; }
-size_t lora_backward_workspace(int64_t T, int L, int R) {
-    return lora::align_256(lora::sort_bytes(T, L)) + lora::align_256(static_cast<size_t>(T) * R * sizeof(float));
+// The sort, dh, and the parts of the adapters' gradients.
+size_t lora_backward_workspace(int64_t T, int L, int R, int64_t K, int64_t N) {
+    using namespace lora;
+    return align_256(sort_bytes(T, L)) + align_256(static_cast<size_t>(T) * R * sizeof(float)) + align_256(grad_bytes(T, L, R, K, N));
 }
 
 cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t st) {
@@ -300,7 +309,9 @@ cudaError_t launch_lora_add_backward(const LoraBackwardArgs& a, cudaStream_t st)
     g.N = static_cast<int>(a.N);
     g.ddown = a.ddown;
     g.dup = a.dup;
-    return launch_grad(g, st);
+    g.grads_wide = ((reinterpret_cast<uintptr_t>(a.ddown) | reinterpret_cast<uintptr_t>(a.dup)) & 15) == 0;
+    g.parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(dh) + align_256(static_cast<size_t>(a.T) * a.R * sizeof(float)));
+    return launch_grad(g, a.T, st);
 }
 
 }  // namespace nvfp4

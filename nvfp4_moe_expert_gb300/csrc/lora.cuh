@@ -27,7 +27,7 @@ namespace lora {
 
 constexpr int kThreads = 256, kWarps = 8;
 constexpr int kSplit = 8;                 // CTAs of a cluster
-constexpr int kFewRows = 16, kManyRows = 128;
+constexpr int kFewRows = 16, kManyRows = 128, kStageRows = 32;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 // The tiles that the sort kernel lists, in the workspace.
@@ -37,6 +37,7 @@ struct Tiles {
     const int32_t* start;       // [count] first row of the tile in perm
     const int32_t* offsets;     // [L + 2] first row of each adapter in perm
     const int32_t* count;
+    const int32_t* prefix;      // [L + 1] stages of 32 rows of the adapters in front (one of an adapter without rows)
 };
 
 struct Params {

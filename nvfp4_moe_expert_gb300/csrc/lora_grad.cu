@@ -1,23 +1,29 @@
 // Gradients of low-rank adapters:  dA_a = sum_t dh_t x_t^T  [R][K],  dB_a = sum_t s_a dy_t h_t^T  [N][R],  over the tokens of
 // adapter a in their order.
 //
-// Both are sums over tokens of a column of R values (dh, or s h) times a row of x, or dy.  A CTA takes one adapter, up to 32
-// of its ranks and a slab of 256 columns (a warp 32 of them), 32 tokens a stage, and keeps the sums in registers.  Few
-// slabs of few adapters leave SMs idle, so up to 8 CTAs of a cluster share a slab's tokens and add their sums in order: no
-// atomics, the same bits every time.  More than 32 ranks read the slab again, out of L2.
+// Both are sums over tokens of a column of R values (dh, or s h) times a row of x, or dy.  The work is units (an adapter, up
+// to 32 of its ranks, a slab of 256 columns of x or dy) of stages (32 tokens), one behind the other, cut into as many equal
+// stretches as CTAs run at once: requests are uneven, and with CTAs of a cluster sharing a unit's tokens the longest adapter's
+// took twice the mean, and 1.7 waves two (93 us for 16384 x (4096 + 4096), rank 16).  A unit that lies in one stretch is written by
+// its CTA; of the others each CTA leaves its part in the workspace (at most two: where its stretch begins and where it
+// ends), and a second kernel adds a unit's parts in order.  No atomics, the same bits every time.  More than 32 ranks read
+// a slab again, out of L2.
 //
 // dh and h are FP32; they are taken as sums of three BF16 terms (2^-24 of them is left), as x and dy are BF16 and the sums
 // FP32.  The tensor cores cut an accumulator's low bits off at each step: one chain over 2048 tokens was 6e-6 of the
 // result low, so every 8 stages (48 steps) the chain is added to FP32 sums beside it and starts anew.
+#include <algorithm>
+
 #include "lora_launch.cuh"
 
 namespace nvfp4 {
 namespace lora {
 namespace {
 
-constexpr int kCols = 256, kTokens = 32, kTerms = 3, kRanks = 32;
+constexpr int kCols = 256, kTokens = kStageRows, kTerms = 3, kRanks = 32;
 constexpr int kStages = 4, kChain = 8;    // stages of the ring; of a chain of products
 constexpr int kIndexed = 16;              // stages whose rows are listed at a time
+constexpr int kMaxSms = 160;
 constexpr int kPitch = kCols + 4;         // floats of a row of the sums in shared memory
 
 template <int kM>
@@ -31,30 +37,93 @@ struct GradLayout {
     static_assert(h_at % 128 == 0 && stage % 16 == 0, "16-byte chunks");
 };
 
+// The next BF16 terms of two values, which keep what is left of them (0 where a term is infinite).
+__device__ __forceinline__ uint32_t next_terms(float& a, float& b) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&t);
+    a -= __uint_as_float(w << 16);
+    b -= __uint_as_float(w & 0xFFFF0000u);
+    if (!(a == a)) a = 0.0f;
+    if (!(b == b)) b = 0.0f;
+    return w;
+}
+
+// The units' shape: slabs of K in front of those of N, `rank_parts` units to a slab.
+struct Shape {
+    int slabs_k, rank_parts, units;       // units of an adapter
+};
+// A unit, and what a stretch holds of it.
+struct Segment {
+    int adapter, unit;
+    int64_t begin, end;                   // the unit's stages in the whole
+};
+// The unit that stage `at` of the whole belongs to (at < all).  prefix[a]: stages of a unit of the adapters in front of a.
+__device__ __forceinline__ Segment find_unit(const int32_t* prefix, int L, int units, int64_t at) {
+    int lo = 0, hi = L;                   // prefix[lo] units <= at < prefix[hi] units
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (static_cast<int64_t>(prefix[mid]) * units <= at) lo = mid;
+        else hi = mid;
+    }
+    const int64_t first = static_cast<int64_t>(prefix[lo]) * units;
+    const int stages = prefix[lo + 1] - prefix[lo], unit = static_cast<int>((at - first) / stages);
+    return {lo, unit, first + static_cast<int64_t>(unit) * stages, first + static_cast<int64_t>(unit + 1) * stages};
+}
+__device__ __forceinline__ int64_t stretch_begin(int64_t all, int cta, int ctas) { return all * cta / ctas; }   // all < 2^45
+
+// What is known of a unit's slab.
+struct Slab {
+    bool is_down;
+    int rank0, ranks, col0, width;
+    __device__ __forceinline__ Slab(const GradParams& p, const Shape& sh, int unit) {
+        const int slab = unit / sh.rank_parts;
+        rank0 = unit % sh.rank_parts * kRanks;
+        ranks = min(kRanks, p.R - rank0);
+        is_down = slab < sh.slabs_k;
+        col0 = (is_down ? slab : slab - sh.slabs_k) * kCols;
+        width = is_down ? p.K : p.N;
+    }
+    // rank and column of element i, in the order in which they lie in the gradient (ranks and kCols are multiples of 4)
+    __device__ __forceinline__ void place(int i, int& r, int& c) const {
+        c = is_down ? i % kCols : static_cast<unsigned>(i) / static_cast<unsigned>(ranks);
+        r = is_down ? i / kCols : i - c * ranks;
+    }
+    // elements i to i + 3, which lie side by side
+    __device__ __forceinline__ void store(const GradParams& p, int adapter, int i, const float4& v) const {
+        int r, c;
+        place(i, r, c);
+        const int there = is_down ? width - col0 - c : col0 + c < width ? 4 : 0;
+        float* at = is_down ? p.ddown + (static_cast<int64_t>(adapter) * p.R + rank0 + r) * p.K + col0 + c
+                            : p.dup + (static_cast<int64_t>(adapter) * p.N + col0 + c) * p.R + rank0 + r;
+        const float w[4] = {v.x, v.y, v.z, v.w};
+        if (there >= 4 && p.grads_wide) {
+            *reinterpret_cast<float4*>(at) = v;
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j < there) at[j] = w[j];
+        }
+    }
+};
+
 template <int kM>
-__global__ void __launch_bounds__(kThreads, 2) grad_kernel(const GradParams p, const int slabs_k, const int rank_parts) {
+__device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab, int adapter, int skip, int stages, uint8_t* smem,
+                                           int (&s_rows)[2][kIndexed * kTokens], float (&total)[kM][4][4]) {
     using Lay = GradLayout<kM>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int s_rows[2][kIndexed * kTokens];
     const uint32_t base = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int part = static_cast<int>(cluster_rank()), parts = static_cast<int>(cluster_size());
-    const int unit = blockIdx.x / parts, slab = unit / rank_parts, rank0 = unit % rank_parts * kRanks, adapter = blockIdx.y;
-    const int ranks = min(kRanks, p.R - rank0);
-    const bool is_down = slab < slabs_k;
-    const int col0 = (is_down ? slab : slab - slabs_k) * kCols, width = is_down ? p.K : p.N;
+    const bool is_down = slab.is_down;
+    const int col0 = slab.col0, width = slab.width, ranks = slab.ranks;
     const uint16_t* x = is_down ? p.x : p.dy;
     const int64_t ldx = is_down ? p.ldx : p.lddy;
     const bool wide = is_down ? p.x_wide : p.dy_wide;
-    const float* h = (is_down ? p.dh : p.h) + rank0;
+    const float* h = (is_down ? p.dh : p.h) + slab.rank0;
     const float scale = is_down || p.scale == nullptr ? 1.0f : p.scale[adapter];
-    pdl_wait();
-    const int begin = p.tiles.offsets[adapter], all = p.tiles.offsets[adapter + 1] - begin;
-    const int share = ((all + kTokens - 1) / kTokens + parts - 1) / parts * kTokens;
-    const int first = min(part * share, all), last = min(first + share, all);
-    const int stages = (last - first + kTokens - 1) / kTokens;
+    const int begin = p.tiles.offsets[adapter], first = skip * kTokens, last = p.tiles.offsets[adapter + 1] - begin;
     const int32_t* perm = p.tiles.perm + begin + first;
 
+    const bool full_slab = wide && col0 + kCols <= width;
     // rows of kIndexed stages, block by block; -1 behind the last
     static_assert(kIndexed * kTokens == 2 * kThreads, "two rows to a thread");
     const auto get_rows = [&](int block, int (&to)[2]) {
@@ -74,7 +143,12 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const GradParams p, c
             const uint32_t at = base + s % kStages * Lay::stage;
             const int r = threadIdx.x >> 3, t = row_at(s, r);
             const uint16_t* row = t < 0 ? x : x + t * ldx;
-            if (wide) {
+            if (full_slab && (s + 1) * kTokens <= last - first) {
+                const uint32_t to = at + swizzled(r, threadIdx.x & 7);
+                const uint16_t* from = row + col0 + 8 * (threadIdx.x & 7);
+#pragma unroll
+                for (int i = 0; i < kCols / 64; ++i) cp_async16(to + i * Lay::tile, from + 64 * i);
+            } else if (wide) {
 #pragma unroll
                 for (int i = 0; i < kCols / 64; ++i) {
                     const int c = col0 + 64 * i + 8 * (threadIdx.x & 7), left = t < 0 ? 0 : min(max(width - c, 0), 8);
@@ -105,15 +179,11 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const GradParams p, c
         float v[4] = {held.x * scale, held.y * scale, held.z * scale, held.w * scale};
         uint8_t* to = smem + s % kStages * Lay::stage + Lay::h_at + h_row * Lay::pitch + 2 * h_col;
 #pragma unroll
-        for (int t = 0; t < kTerms; ++t) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = next_term<__nv_bfloat16>(v[k]);
-            *reinterpret_cast<uint2*>(to + t * kTokens * Lay::pitch) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-        }
+        for (int t = 0; t < kTerms; ++t)
+            *reinterpret_cast<uint2*>(to + t * kTokens * Lay::pitch) = make_uint2(next_terms(v[0], v[1]), next_terms(v[2], v[3]));
     };
 
-    float acc[kM][4][4], total[kM][4][4];
+    float acc[kM][4][4];
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
 #pragma unroll
@@ -178,60 +248,119 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const GradParams p, c
         }
     }
 
-    // the CTAs' sums in their order, a part of them each
     cp_wait<0>();
     __syncthreads();
-    float* sums = reinterpret_cast<float*>(smem);
-#pragma unroll
-    for (int m = 0; m < kM; ++m) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            float* at = sums + (16 * m + (lane >> 2)) * kPitch + 32 * warp + 8 * n + 2 * (lane & 3);
-            *reinterpret_cast<float2*>(at) = make_float2(total[m][n][0], total[m][n][1]);
-            *reinterpret_cast<float2*>(at + 8 * kPitch) = make_float2(total[m][n][2], total[m][n][3]);
-        }
-    }
-    cluster_barrier();
-    const int count = ranks * kCols, each = (count + parts - 1) / parts;
-    float* out = is_down ? p.ddown + (static_cast<int64_t>(adapter) * p.R + rank0) * p.K : p.dup + static_cast<int64_t>(adapter) * p.N * p.R + rank0;
-    for (int i = part * each + threadIdx.x; i < min((part + 1) * each, count); i += kThreads) {
-        const int r = is_down ? i / kCols : i % ranks, c = is_down ? i % kCols : i / ranks;
-        if (col0 + c >= width) continue;
-        float v = cluster_load_f32(cluster_addr(sums + r * kPitch + c, 0));
-        for (int k = 1; k < parts; ++k) v += cluster_load_f32(cluster_addr(sums + r * kPitch + c, k));
-        out[is_down ? static_cast<int64_t>(r) * p.K + col0 + c : static_cast<int64_t>(col0 + c) * p.R + r] = v;
-    }
-    cluster_barrier();                                      // no CTA leaves while another reads its sums
 }
 
 template <int kM>
-cudaError_t launch(const GradParams& p, cudaStream_t st) {
-    const int slabs_k = (p.K + kCols - 1) / kCols, slabs_n = (p.N + kCols - 1) / kCols, rank_parts = (p.R + kRanks - 1) / kRanks;
-    const int64_t units = static_cast<int64_t>(slabs_k + slabs_n) * rank_parts * p.L;
-    int parts = 1;                        // CTAs to a slab: about four to an SM
-    while (parts < 8 && units * parts * 2 <= 4 * device_sm_count()) parts *= 2;
+__global__ void __launch_bounds__(kThreads, 2) grad_kernel(const GradParams p, const Shape sh) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int s_rows[2][kIndexed * kTokens];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    const int64_t all = static_cast<int64_t>(p.tiles.prefix[p.L]) * sh.units;
+    const int64_t begin = stretch_begin(all, blockIdx.x, gridDim.x), end = stretch_begin(all, blockIdx.x + 1, gridDim.x);
+    for (int64_t at = begin; at < end;) {
+        const Segment seg = find_unit(p.tiles.prefix, p.L, sh.units, at);
+        const int64_t stop = min(end, seg.end);
+        const Slab slab(p, sh, seg.unit);
+        float total[kM][4][4];
+        add_stages<kM>(p, slab, seg.adapter, static_cast<int>(at - seg.begin), static_cast<int>(stop - at), smem, s_rows, total);
+        float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                float* to = sums + (16 * m + (lane >> 2)) * kPitch + 32 * warp + 8 * n + 2 * (lane & 3);
+                *reinterpret_cast<float2*>(to) = make_float2(total[m][n][0], total[m][n][1]);
+                *reinterpret_cast<float2*>(to + 8 * kPitch) = make_float2(total[m][n][2], total[m][n][3]);
+            }
+        }
+        __syncthreads();
+        const bool whole = at == seg.begin && stop == seg.end;
+        float* part = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (at != begin)) * (kRanks * kCols);
+        for (int i = threadIdx.x; i < slab.ranks * kCols / 4; i += kThreads) {
+            int r, c;
+            slab.place(4 * i, r, c);
+            const float* from = sums + r * kPitch + c;
+            const int step = slab.is_down ? 1 : kPitch;
+            const float4 v = make_float4(from[0], from[step], from[2 * step], from[3 * step]);
+            if (whole) slab.store(p, seg.adapter, 4 * i, v);
+            else *reinterpret_cast<float4*>(part + 4 * i) = v;
+        }
+        __syncthreads();
+        at = stop;
+    }
+}
+
+// Units that lie in several stretches: the CTA of the first stretch that begins inside one adds its parts.
+__global__ void __launch_bounds__(kThreads) grad_join_kernel(const GradParams p, const Shape sh) {
+    pdl_wait();
+    const int ctas = static_cast<int>(gridDim.x), cta = blockIdx.x;
+    const int64_t all = static_cast<int64_t>(p.tiles.prefix[p.L]) * sh.units, begin = stretch_begin(all, cta, ctas);
+    if (cta == 0 || begin >= all) return;
+    const Segment seg = find_unit(p.tiles.prefix, p.L, sh.units, begin);
+    const int64_t before = stretch_begin(all, cta - 1, ctas);
+    if (seg.begin >= begin || before > seg.begin) return;    // begins with the unit, or not the first inside it
+    const Slab slab(p, sh, seg.unit);
+    const float* first = p.parts + (2 * static_cast<int64_t>(cta - 1) + (before != seg.begin)) * (kRanks * kCols);
+    int stop = cta + 1;                   // of the stretches that begin inside the unit (an empty one begins where the next does)
+    while (stop < ctas && stretch_begin(all, stop, ctas) < seg.end) ++stop;
+    // four elements at a time and all of a thread's at once: the parts' latency once for each, not for each element too
+    constexpr int kMine = kRanks * kCols / 4 / kThreads;
+    const int count = slab.ranks * kCols / 4;
+    float4 v[kMine];
+    const auto add = [&](const float* part, bool begin) {
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+            const int i = threadIdx.x + j * kThreads;
+            if (i >= count) break;
+            const float4 w = *reinterpret_cast<const float4*>(part + 4 * i);
+            v[j] = begin ? w : make_float4(v[j].x + w.x, v[j].y + w.y, v[j].z + w.z, v[j].w + w.w);
+        }
+    };
+    add(first, true);
+    for (int k = cta; k < stop; ++k)
+        if (stretch_begin(all, k + 1, ctas) > stretch_begin(all, k, ctas)) add(p.parts + 2 * static_cast<int64_t>(k) * (kRanks * kCols), false);
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        if (i < count) slab.store(p, seg.adapter, 4 * i, v[j]);
+    }
+}
+
+Shape shape_of(int64_t K, int64_t N, int R) {
+    Shape sh;
+    sh.slabs_k = static_cast<int>((K + kCols - 1) / kCols);
+    sh.rank_parts = (R + kRanks - 1) / kRanks;
+    sh.units = (sh.slabs_k + static_cast<int>((N + kCols - 1) / kCols)) * sh.rank_parts;
+    return sh;
+}
+// CTAs: two to an SM, with four stages each at least.
+int ctas_of(int64_t T, int L, const Shape& sh) {
+    const int64_t all = (T / kTokens + L) * sh.units, most = 2 * std::min(device_sm_count(), kMaxSms), few = (all + 3) / 4;
+    return static_cast<int>(few < most ? few : most);
+}
+
+template <int kM>
+cudaError_t launch(const GradParams& p, int64_t T, cudaStream_t st) {
+    const Shape sh = shape_of(p.K, p.N, p.R);
+    const unsigned ctas = static_cast<unsigned>(ctas_of(T, p.L, sh));
     static Ready ready;
-    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(grad_kernel<kM>), GradLayout<kM>::total, ready);
+    cudaError_t e = allow_shared(reinterpret_cast<const void*>(grad_kernel<kM>), GradLayout<kM>::total, ready);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((slabs_k + slabs_n) * rank_parts * parts), static_cast<unsigned>(p.L));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = GradLayout<kM>::total;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(parts);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, grad_kernel<kM>, p, slabs_k, rank_parts);
+    e = launch_pdl(true, grad_kernel<kM>, dim3(ctas), dim3(kThreads), static_cast<size_t>(GradLayout<kM>::total), st, p, sh);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(true, grad_join_kernel, dim3(ctas), dim3(kThreads), 0, st, p, sh);
 }
 
 }  // namespace
 
-cudaError_t launch_grad(const GradParams& p, cudaStream_t st) { return p.R <= 16 ? launch<1>(p, st) : launch<2>(p, st); }
+size_t grad_bytes(int64_t T, int L, int R, int64_t K, int64_t N) {
+    return 2 * static_cast<size_t>(ctas_of(T, L, shape_of(K, N, R))) * kRanks * kCols * sizeof(float);
+}
+
+cudaError_t launch_grad(const GradParams& p, int64_t T, cudaStream_t st) { return p.R <= 16 ? launch<1>(p, T, st) : launch<2>(p, T, st); }
 
 }  // namespace lora
 }  // namespace nvfp4

@@ -85,10 +85,10 @@ struct LoraBackwardArgs {
     bool accumulate;
     float* ddown;
     float* dup;
-    void* ws;                 // lora_backward_workspace(T, L, R) bytes
+    void* ws;                 // lora_backward_workspace(T, L, R, K, N) bytes
     int* err;
 };
-size_t lora_backward_workspace(int64_t T, int L, int R);
+size_t lora_backward_workspace(int64_t T, int L, int R, int64_t K, int64_t N);
 cudaError_t launch_lora_add_backward(const LoraBackwardArgs& a, cudaStream_t st);
 
 // Columns of one 512-byte scale tile: 4 scales of 16 (NVFP4) or 32 (MXFP4) elements.

@@ -51,7 +51,7 @@ def test_refusals(lib):
 
 
 def test_backward_refusals(lib):
-    def call(T=300, dy=Y, lddy=40, x=X, ldx=64, h=P, ids=P, dx=OUT, lddx=64, dx_type=1, add=0, ddown=P, dup=P, ws=P, n=1 << 20, **kw):
+    def call(T=300, dy=Y, lddy=40, x=X, ldx=64, h=P, ids=P, dx=OUT, lddx=64, dx_type=1, add=0, ddown=P, dup=P, ws=P, n=1 << 26, **kw):
         return lib.lora_add_backward(adapters(**kw), dy, lddy, x, ldx, h, ids, T, dx, lddx, dx_type, add, ddown, dup, ws, n, None)
     for kw in BAD_SHAPE + (dict(type=2), dict(T=-1), dict(T=1 << 31), dict(lddy=39), dict(ldx=56), dict(ldx=68), dict(lddx=63),
                            dict(dx_type=3), dict(add=2), dict(lddx=1 << 60)):
@@ -61,9 +61,10 @@ def test_backward_refusals(lib):
                              dict(dx=ODD), dict(ddown=ODD), dict(dup=ODD), dict(ws=V(4112)), dict(dx=X), dict(dx=Y),
                              dict(dx=V((1 << 30) + 300 * 80 - 2)), dict(add=1, dx=X)):
         assert call(**kw) == ARG, kw
-    need = lib.lora_add_backward_workspace_bytes(300, 3, 16)
+    need = lib.lora_add_backward_workspace_bytes(300, 3, 16, 64, 40)
     assert need >= 300 * (4 + 64) and need % 256 == 0 and call(n=need - 1) == WS
-    assert lib.lora_add_backward_workspace_bytes(0, 3, 16) == 0 and lib.lora_add_backward_workspace_bytes(9, 3, 12) == 0
+    size = lib.lora_add_backward_workspace_bytes
+    assert size(0, 3, 16, 64, 40) == 0 and size(9, 3, 12, 64, 40) == 0 and size(9, 3, 16, 60, 40) == 0 and size(9, 3, 16, 64, 0) == 0
     assert lib.lora_add_backward(None, Y, 40, X, 64, P, P, 4, OUT, 64, 1, 0, P, P, P, 1 << 20, None) == ARG
 
 
