@@ -14,10 +14,11 @@ constexpr int kSortThreads = 1024, kSortWarps = 32;
 // rows, 10.4 for 16384.
 constexpr int kAhead = 4;                 // loads of ids at a time
 
-__global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kSortThreads, 1)
+__global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(kSortThreads, 1)
     sort_kernel(const int32_t* __restrict__ ids, int T, int L, int rows_per_tile, int32_t* __restrict__ perm,
                 int32_t* __restrict__ offsets, int32_t* __restrict__ tile_adapter, int32_t* __restrict__ tile_start,
-                int32_t* __restrict__ tile_count, int32_t* __restrict__ prefix, int* err) {
+                int32_t* __restrict__ tile_count, int32_t* __restrict__ prefix,
+                int32_t* __restrict__ pieces, int* err) {
     extern __shared__ int s_at[];                           // [kSortWarps][bins] rows of a warp, then those in front of it
     __shared__ int s_scan[3][kSortWarps];
     const int bins = L + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -26,7 +27,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kSortThreads, 1
     int *s_own = s_at + kSortWarps * bins, *s_first = s_own + bins;   // [bins] the CTA's rows; its first place
     for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) s_at[i] = 0;
     __syncthreads();
-    constexpr unsigned kAllWarps = kSortWarps * kSplit;
+    constexpr unsigned kAllWarps = kSortWarps * kGroups;
     const unsigned rows = T, stretch = ((rows + kAllWarps - 1) / kAllWarps + 31) / 32 * 32;   // T < 2^31 - 256: no overflow below
     const unsigned begin = (rank * kSortWarps + warp) * stretch, end = min(begin + stretch, rows);
     int id[kAhead];
@@ -70,7 +71,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kSortThreads, 1
         int own = 0, front = 0;
         if (a < bins) {
 #pragma unroll
-            for (int c = 0; c < kSplit; ++c) {
+            for (int c = 0; c < kGroups; ++c) {
                 const int v = cluster_load_s32(cluster_addr(s_own + a, c));
                 own += v;
                 if (c < rank) front += v;
@@ -100,7 +101,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kSortThreads, 1
         first_tile += __shfl_sync(kAll, wn, 31);
         if (a < bins) {
             s_first[a] = row + front;
-            if (a % kSplit == rank) {
+            if (a % kGroups == rank) {
                 offsets[a] = row;
                 prefix[a] = stage;                          // at L: all
                 for (int i = 0; i < tiles; ++i) {
@@ -111,6 +112,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kSortThreads, 1
         }
         __syncthreads();
     }
+    if (rank == 0 && threadIdx.x < kMaxCtas) pieces[threadIdx.x] = 0;
     if (threadIdx.x == 0 && rank == 0) {
         offsets[bins] = T;
         *tile_count = first_tile;
@@ -154,20 +156,23 @@ EncodeTiledFn encode_fn() {
 }
 }  // namespace
 
-bool make_units_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t slices, int64_t slice, int box_rows) {
+bool make_units_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t slices, int64_t slice, int box_rows,
+                    int bytes) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(slices)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(slice) * 2};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, estr[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(bytes / 2), static_cast<cuuint32_t>(box_rows), 1}, estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, slices ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t sort_bytes(int64_t T, int L) {
     const size_t tiles = static_cast<size_t>(tiles_bound(T, L, kFewRows));
-    return align_256(static_cast<size_t>(T) * 4) + 2 * align_256((L + 2) * 4) + 2 * align_256(tiles * 4) + 256;
+    return align_256(static_cast<size_t>(T) * 4) + 2 * align_256((L + 2) * 4) + 2 * align_256(tiles * 4) + 256 + align_256(kMaxCtas * 4);
 }
 
 Tiles sort_layout(void* ws, int64_t T, int L) {
@@ -185,6 +190,8 @@ Tiles sort_layout(void* ws, int64_t T, int L) {
     t.count = reinterpret_cast<int32_t*>(p);
     p += 256;
     t.prefix = reinterpret_cast<int32_t*>(p);
+    p += align_256((L + 2) * 4);
+    t.pieces = reinterpret_cast<int32_t*>(p);
     return t;
 }
 
@@ -194,10 +201,10 @@ cudaError_t launch_sort(const int32_t* ids, int64_t T, int L, int rows_per_tile,
     const cudaError_t e = allow_shared(reinterpret_cast<const void*>(sort_kernel),
                                        (kSortWarps + 2) * (kMaxAdapters + 1) * static_cast<int>(sizeof(int)), ready);
     if (e != cudaSuccess) return e;
-    return launch_pdl(false, sort_kernel, dim3(kSplit), dim3(kSortThreads), smem, st, ids, static_cast<int>(T), L, rows_per_tile,
+    return launch_pdl(false, sort_kernel, dim3(kGroups), dim3(kSortThreads), smem, st, ids, static_cast<int>(T), L, rows_per_tile,
                       const_cast<int32_t*>(t.perm), const_cast<int32_t*>(t.offsets), const_cast<int32_t*>(t.adapter),
                       const_cast<int32_t*>(t.start), const_cast<int32_t*>(t.count),
-                      const_cast<int32_t*>(t.prefix), err);
+                      const_cast<int32_t*>(t.prefix), t.pieces, err);
 }
 
 }  // namespace lora

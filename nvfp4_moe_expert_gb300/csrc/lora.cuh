@@ -4,14 +4,14 @@
 //   backward   dh_t = s_a B_a^T dy_t,   dx_t += A_a^T dh_t,   dA_a = sum_t dh_t x_t^T,  dB_a = sum_t s_a dy_t h_t^T
 //
 // Forward and dx have one shape: a row of C columns shrinks to R and expands to D columns.  Tokens of an adapter are put
-// together in tiles of 16 or 128 rows; a cluster of 8 CTAs takes a tile, each CTA an eighth of C, then an eighth of D.
+// together in tiles of 16 or 128 rows; a cluster of CTAs takes a tile, each CTA its share of C, then its share of D.
 //
-// The order of the sum over C goes by C alone, so a token's row does not depend on the batch it is in: C is cut into 64
-// sub-slices of 16 ceil(C / 1024) columns; a sub-slice is one chain of m16n8k16 products from zero, the 8 sub-slices of a
-// CTA are added in order, then the 8 CTAs' sums.  mma.sync serves this better than tcgen05: a tile has as few as one real
-// row and 8 to 128 columns of accumulator, the two products together have 2 R operations to a byte that is moved, and
-// accumulators in registers need no pass through TMEM between the two products (its rate, 600 TFLOP/s measured, is enough
-// for R <= 64 at the memory's rate).
+// The order of the sum over C goes by C alone, so a token's row does not depend on the batch: C is cut into 8 groups of 8
+// sub-slices of 16 ceil(C / 1024) columns; a sub-slice is one chain of m16n8k16 products from zero, the sub-slices of a group
+// are added in order, the groups as a binary tree (which clusters of 2, 4 and 8 CTAs can share).  mma.sync serves this
+// better than tcgen05: a tile has as few as one real row and 8 to 128 columns of accumulator, the two products together
+// have 2 R operations to a byte that is moved, and accumulators in registers need no pass through TMEM between the two
+// products (its rate, 600 TFLOP/s measured, is enough for R <= 64 at the memory's rate).
 //
 // Between the products h is FP32; the second product takes it as a sum of 16-bit terms (two for 16-bit outputs, which leaves
 // 2^-17 of h beside the output's own 2^-9; three for FP32 outputs), so h is not rounded to 16 bits.
@@ -26,8 +26,9 @@ namespace nvfp4 {
 namespace lora {
 
 constexpr int kThreads = 256, kWarps = 8;
-constexpr int kSplit = 8;                 // CTAs of a cluster
+constexpr int kGroups = 8;                // of C; CTAs of a cluster at most
 constexpr int kFewRows = 16, kManyRows = 128, kStageRows = 32;
+constexpr int kMaxCtas = 320;             // of the adapters' gradients
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 // The tiles that the sort kernel lists, in the workspace.
@@ -38,6 +39,7 @@ struct Tiles {
     const int32_t* offsets;     // [L + 2] first row of each adapter in perm
     const int32_t* count;
     const int32_t* prefix;      // [L + 1] stages of 32 rows of the adapters in front (one of an adapter without rows)
+    int32_t* pieces;            // [kMaxCtas] zeros: counters for the adapters' gradients
 };
 
 struct Params {
@@ -91,6 +93,13 @@ __device__ __forceinline__ void mma(__half, float (&c)[4], const uint32_t (&a)[4
 // Tiles of 64 16-bit columns: rows of 128 bytes, their 16-byte chunks exchanged by the row, so that the eight rows of a
 // matrix lie in different banks.
 __device__ __forceinline__ uint32_t swizzled(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+// The same for rows of 32 or 64 bytes, as TMA's 32B and 64B swizzles lay them out.
+template <int kBytes>
+__device__ __forceinline__ uint32_t swizzled_rows(int row, int chunk) {
+    return row * kBytes + ((chunk ^ (row * kBytes >> 7 & (kBytes / 16 - 1))) << 4);
+}
+// Bytes of a row of ranks in shared memory: 16, 32 or 64 of them (two blocks of 64 above that).
+__host__ __device__ constexpr int rank_bytes(int R) { return R <= 16 ? 32 : R <= 32 ? 64 : 128; }
 // Tiles of R columns: rows padded by 16 bytes (the eight rows of a matrix in different banks where R is a multiple of 16).
 __host__ __device__ constexpr int padded_pitch(int R) { return 2 * R + 16; }
 __host__ __device__ constexpr int rank_up(int R) { return (R + 15) / 16 * 16; }   // the second product's steps are 16 wide
@@ -114,7 +123,7 @@ struct Straddle {
         if (left > 0) lo = __ldg(p);
         if (2 * left > 16 - off) hi = __ldg(p + 1);
     }
-    __device__ __forceinline__ void store(uint32_t dst) const {
+    __device__ __forceinline__ uint4 value() const {
         uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
         if (off & 4) {
 #pragma unroll
@@ -129,7 +138,11 @@ struct Straddle {
             w[i] = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
             if (2 * i + 1 >= left) w[i] = 2 * i < left ? w[i] & 0xFFFFu : 0;
         }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void store(uint32_t dst) const {
+        const uint4 v = value();
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
     }
 };
 __device__ __forceinline__ void copy_chunk(uint32_t dst, const uint16_t* row, int c, int units, bool wide) {
@@ -376,30 +389,36 @@ __device__ __forceinline__ int row_exponent(float m) {
     return max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100) - 14;
 }
 
-// A row of h: lane l of 16 sums the 8 CTAs' parts of columns 2 l, 2 l + 1, 2 l + 32, ... in their order, and hands over the
-// row's terms, two columns (32 bits) at a time.
+// A row of h: lane l of 16 sums the 2, 4 or 8 CTAs' parts of columns 2 l, 2 l + 1, 2 l + 32, ... as a tree, and hands over
+// the row's terms, two columns (32 bits) at a time.
 template <typename T, int kRank, typename Store>
-__device__ __forceinline__ void finish_row(const float* part, int row, int pitch, int R, float scale, int terms, int term_bytes,
+__device__ __forceinline__ void finish_row(const float* part, int parts, int row, int pitch, int R, float scale, int terms, int term_bytes,
                                            float* h_out, bool h_scaled, int l, Store&& store, float& undo) {
     constexpr int kMine = (kRank + 31) / 32;
     float v[kMine][2], m = 0.0f;
-    uint32_t from[kSplit];
+    uint32_t from[kGroups];
 #pragma unroll
-    for (int c = 0; c < kSplit; ++c) from[c] = cluster_addr(part, c) + 4 * row * pitch;
+    for (int c = 0; c < kGroups; ++c) from[c] = cluster_addr(part, c < parts ? c : 0) + 4 * row * pitch;
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
         const int r = 2 * l + 32 * i;
         v[i][0] = v[i][1] = 0.0f;
         if (r < R) {
-            float got[kSplit][2];
+            float got[kGroups][2];
 #pragma unroll
-            for (int c = 0; c < kSplit; ++c)
-                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(got[c][0]), "=f"(got[c][1]) : "r"(from[c] + 4 * r) : "memory");
+            for (int c = 0; c < kGroups; ++c) {
+                if (c < parts)
+                    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(got[c][0]), "=f"(got[c][1]) : "r"(from[c] + 4 * r) : "memory");
+            }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                float sum = got[0][k];
 #pragma unroll
-                for (int c = 1; c < kSplit; ++c) sum += got[c][k];
+                for (int n = kGroups / 2; n >= 1; n /= 2) {
+                    if (2 * n > parts) continue;
+#pragma unroll
+                    for (int c = 0; c < n; ++c) got[c][k] = got[2 * c][k] + got[2 * c + 1][k];
+                }
+                const float sum = got[0][k];
                 v[i][k] = sum * scale;
                 got[0][k] = h_scaled ? v[i][k] : sum;
             }

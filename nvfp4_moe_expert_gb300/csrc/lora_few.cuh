@@ -84,7 +84,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* ids, int T, int L, int 
 }
 
 template <typename T, bool kTrans, int kRank>
-__global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads) few_kernel(const Params p, const int terms) {
+__global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(kThreads) few_kernel(const Params p, const int terms) {
     constexpr int kTiles = kRank / 8;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) int s_id[kInCta];
@@ -92,7 +92,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads) few_k
     __shared__ float s_undo[kFewRows];
     const FewLayout<kTrans> lay(p.R, terms);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2;
-    const int rank = static_cast<int>(cluster_rank()), q = blockIdx.x / kSplit;
+    const int rank = static_cast<int>(cluster_rank()), q = blockIdx.x / kGroups;
 
     int adapter, rows;
     if (p.tiles.perm == nullptr) {
@@ -109,7 +109,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads) few_k
     __syncthreads();
 
     // outputs in groups of 32, an eighth of them to each CTA, one at a time to each warp
-    const int groups = (p.D + 31) / 32, per_cta = (groups + kSplit - 1) / kSplit;
+    const int groups = (p.D + 31) / 32, per_cta = (groups + kGroups - 1) / kGroups;
     const int last_group = min((rank + 1) * per_cta, groups), first_group = rank * per_cta + warp;
     const uint16_t* up = static_cast<const uint16_t*>(p.up) + static_cast<int64_t>(max(adapter, 0)) * p.D * p.R;
     const uint32_t my_up = smem_u32(smem) + lay.up_at() + warp * lay.buffers * lay.up;
@@ -193,7 +193,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads) few_k
         const bool keep = p.h != nullptr && row < rows && (row >> 1) == rank;
         float row_undo;
         uint8_t* h = smem + lay.h + row * pitch;
-        finish_row<T, kRank>(sum, row, p.R, p.R, p.scale == nullptr ? 1.0f : p.scale[adapter], terms, kFewRows * pitch,
+        finish_row<T, kRank>(sum, kGroups, row, p.R, p.R, p.scale == nullptr ? 1.0f : p.scale[adapter], terms, kFewRows * pitch,
                              keep ? p.h + static_cast<int64_t>(s_row[row]) * p.R : nullptr, p.h_scaled != 0, lane & 15,
                              [&](int at, uint32_t v) { *reinterpret_cast<uint32_t*>(h + at) = v; }, row_undo);
         if ((lane & 15) == 0) s_undo[row] = row_undo;
@@ -247,7 +247,7 @@ cudaError_t launch_few(const Params& p, int64_t tiles, bool pdl, cudaStream_t st
         auto* kernel = few_kernel<T, kTrans, kRank>;
         const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), FewLayout<kTrans>(kRank, 3).total, ready);
         if (e != cudaSuccess) return e;
-        return launch_pdl(pdl, kernel, dim3(static_cast<unsigned>(tiles * kSplit)), dim3(kThreads), static_cast<size_t>(lay.total), st,
+        return launch_pdl(pdl, kernel, dim3(static_cast<unsigned>(tiles * kGroups)), dim3(kThreads), static_cast<size_t>(lay.total), st,
                           p, terms);
     });
 }

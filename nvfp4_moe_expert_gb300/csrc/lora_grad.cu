@@ -6,7 +6,8 @@
 // stretches as CTAs run at once: requests are uneven, and with CTAs of a cluster sharing a unit's tokens the longest adapter's
 // took twice the mean, and 1.7 waves two (93 us for 16384 x (4096 + 4096), rank 16).  A unit that lies in one stretch is written by
 // its CTA; of the others each CTA leaves its part in the workspace (at most two: where its stretch begins and where it
-// ends), and a second kernel adds a unit's parts in order.  No atomics, the same bits every time.  More than 32 ranks read
+// ends), and the last to do so adds the unit's parts in order, whoever that is: the same bits every time.  (A second kernel
+// for that took 8 to 11 us.)  More than 32 ranks read
 // a slab again, out of L2.
 //
 // dh and h are FP32; they are taken as sums of three BF16 terms (2^-24 of them is left), as x and dy are BF16 and the sums
@@ -23,7 +24,6 @@ namespace {
 constexpr int kCols = 256, kTokens = kStageRows, kTerms = 3, kRanks = 32;
 constexpr int kStages = 4, kChain = 8;    // stages of the ring; of a chain of products
 constexpr int kIndexed = 16;              // stages whose rows are listed at a time
-constexpr int kMaxSms = 160;
 constexpr int kPitch = kCols + 4;         // floats of a row of the sums in shared memory
 
 template <int kM>
@@ -69,7 +69,16 @@ __device__ __forceinline__ Segment find_unit(const int32_t* prefix, int L, int u
     const int stages = prefix[lo + 1] - prefix[lo], unit = static_cast<int>((at - first) / stages);
     return {lo, unit, first + static_cast<int64_t>(unit) * stages, first + static_cast<int64_t>(unit + 1) * stages};
 }
-__device__ __forceinline__ int64_t stretch_begin(int64_t all, int cta, int ctas) { return all * cta / ctas; }   // all < 2^45
+// The whole's stages over the CTAs: the first `more` take one more than `each`.
+struct Stretches {
+    int64_t each, more;
+    __device__ __forceinline__ Stretches(int64_t all, int ctas) : each(all / ctas), more(all - each * ctas) {}
+    __device__ __forceinline__ int64_t begin(int cta) const { return each * cta + min(static_cast<int64_t>(cta), more); }
+    __device__ __forceinline__ int owner(int64_t stage) const {
+        const int64_t large = more * (each + 1);
+        return static_cast<int>(stage < large ? stage / (each + 1) : more + (stage - large) / each);
+    }
+};
 
 // What is known of a unit's slab.
 struct Slab {
@@ -107,7 +116,8 @@ struct Slab {
     }
 };
 
-template <int kM>
+// kWide: all rows start on 16-byte boundaries.
+template <int kM, bool kWide>
 __device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab, int adapter, int skip, int stages, uint8_t* smem,
                                            int (&s_rows)[2][kIndexed * kTokens], float (&total)[kM][4][4]) {
     using Lay = GradLayout<kM>;
@@ -117,7 +127,7 @@ __device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab
     const int col0 = slab.col0, width = slab.width, ranks = slab.ranks;
     const uint16_t* x = is_down ? p.x : p.dy;
     const int64_t ldx = is_down ? p.ldx : p.lddy;
-    const bool wide = is_down ? p.x_wide : p.dy_wide;
+    const bool wide = kWide || is_down || p.dy_wide;
     const float* h = (is_down ? p.dh : p.h) + slab.rank0;
     const float scale = is_down || p.scale == nullptr ? 1.0f : p.scale[adapter];
     const int begin = p.tiles.offsets[adapter], first = skip * kTokens, last = p.tiles.offsets[adapter + 1] - begin;
@@ -138,6 +148,14 @@ __device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab
         for (int i = 0; i < 2; ++i) s_rows[block & 1][i * kThreads + threadIdx.x] = from[i];
     };
     const auto row_at = [&](int s, int r) { return s_rows[(s / kIndexed) & 1][s % kIndexed * kTokens + r]; };
+    // rows on no 16-byte boundary: the aligned words of the stage after the one that is put in place next
+    Straddle words[kWide ? 1 : kCols / 64];
+    const auto fetch = [&](int s) {
+        const int t = s < stages ? row_at(s, threadIdx.x >> 3) : -1;
+#pragma unroll
+        for (int i = 0; i < (kWide ? 0 : kCols / 64); ++i)
+            words[i].load(t < 0 ? x : x + t * ldx, t < 0 ? width : col0 + 64 * i + 8 * (threadIdx.x & 7), width);
+    };
     const auto load_x = [&](int s) {
         if (s < stages) {
             const uint32_t at = base + s % kStages * Lay::stage;
@@ -154,14 +172,12 @@ __device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab
                     const int c = col0 + 64 * i + 8 * (threadIdx.x & 7), left = t < 0 ? 0 : min(max(width - c, 0), 8);
                     cp_async16(at + i * Lay::tile + swizzled(r, threadIdx.x & 7), left ? row + c : row, 2 * left);
                 }
-            } else {
-                Straddle s4[kCols / 64];
+            } else if (!kWide) {
 #pragma unroll
-                for (int i = 0; i < kCols / 64; ++i) s4[i].load(row, t < 0 ? width : col0 + 64 * i + 8 * (threadIdx.x & 7), width);
-#pragma unroll
-                for (int i = 0; i < kCols / 64; ++i) s4[i].store(at + i * Lay::tile + swizzled(r, threadIdx.x & 7));
+                for (int i = 0; i < kCols / 64; ++i) words[i].store(at + i * Lay::tile + swizzled(r, threadIdx.x & 7));
             }
         }
+        if (!kWide && !wide) fetch(s + 1);
         cp_commit();
     };
     // h: 32 tokens x up to 32 ranks, 4 values to a thread
@@ -196,6 +212,7 @@ __device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab
     get_rows(0, first_rows);
     put_rows(0, first_rows);
     __syncthreads();
+    if (!kWide && !wide) fetch(0);
     for (int s = 0; s < kStages - 1; ++s) load_x(s);
     float4 held[kStages - 1];             // of the stages that are under way
 #pragma unroll
@@ -207,9 +224,9 @@ __device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab
         cp_wait<kStages - 2>();
         // the rows of the block that loads reach from the next stage on; its place was last read a block ago
         const int ahead = s % kIndexed;
-        if (ahead == kIndexed - kStages) put_rows(s / kIndexed + 1, listed);
+        if (ahead == kIndexed - kStages - 1) put_rows(s / kIndexed + 1, listed);
         __syncthreads();                                    // the stage is there, the one before is used up
-        if (ahead == kIndexed - kStages - 4) get_rows(s / kIndexed + 1, listed);
+        if (ahead == kIndexed - kStages - 5) get_rows(s / kIndexed + 1, listed);
         load_x(s + kStages - 1);
 #pragma unroll
         for (int i = 0; i + 2 < kStages; ++i) held[i] = held[i + 1];
@@ -252,20 +269,48 @@ __device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab
     __syncthreads();
 }
 
-template <int kM>
+// Adds the parts of a unit that lies in the stretches first_cta to last_cta (the first one's begins with it or not).
+__device__ __forceinline__ void join_parts(const GradParams& p, const Slab& slab, const Segment& seg, const Stretches& cut, int first_cta, int last_cta) {
+    // four elements at a time and all of a thread's at once: the parts' latency once for each, not for each element too
+    constexpr int kMine = kRanks * kCols / 4 / kThreads;
+    const int count = slab.ranks * kCols / 4;
+    float4 v[kMine];
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = first_cta; k <= last_cta; ++k) {
+        const float* part = p.parts + (2 * static_cast<int64_t>(k) + (cut.begin(k) < seg.begin)) * (kRanks * kCols);
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+            const int i = threadIdx.x + j * kThreads;
+            if (i >= count) break;
+            const float4 w = __ldcg(reinterpret_cast<const float4*>(part + 4 * i));
+            v[j] = make_float4(v[j].x + w.x, v[j].y + w.y, v[j].z + w.z, v[j].w + w.w);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        if (i < count) slab.store(p, seg.adapter, 4 * i, v[j]);
+    }
+}
+
+template <int kM, bool kWide>
 __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const GradParams p, const Shape sh) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_rows[2][kIndexed * kTokens];
+    __shared__ int s_last, s_prefix[kMaxAdapters + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
-    const int64_t all = static_cast<int64_t>(p.tiles.prefix[p.L]) * sh.units;
-    const int64_t begin = stretch_begin(all, blockIdx.x, gridDim.x), end = stretch_begin(all, blockIdx.x + 1, gridDim.x);
+    for (int a = threadIdx.x; a <= p.L; a += kThreads) s_prefix[a] = p.tiles.prefix[a];
+    __syncthreads();
+    const Stretches cut(static_cast<int64_t>(s_prefix[p.L]) * sh.units, gridDim.x);
+    const int64_t begin = cut.begin(blockIdx.x), end = cut.begin(blockIdx.x + 1);
     for (int64_t at = begin; at < end;) {
-        const Segment seg = find_unit(p.tiles.prefix, p.L, sh.units, at);
+        const Segment seg = find_unit(s_prefix, p.L, sh.units, at);
         const int64_t stop = min(end, seg.end);
         const Slab slab(p, sh, seg.unit);
         float total[kM][4][4];
-        add_stages<kM>(p, slab, seg.adapter, static_cast<int>(at - seg.begin), static_cast<int>(stop - at), smem, s_rows, total);
+        add_stages<kM, kWide>(p, slab, seg.adapter, static_cast<int>(at - seg.begin), static_cast<int>(stop - at), smem, s_rows, total);
         float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
@@ -288,44 +333,19 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const GradParams p, c
             if (whole) slab.store(p, seg.adapter, 4 * i, v);
             else *reinterpret_cast<float4*>(part + 4 * i) = v;
         }
+        if (!whole) {
+            const int first_cta = cut.owner(seg.begin), last_cta = cut.owner(seg.end - 1);
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) s_last = atomicAdd(p.tiles.pieces + first_cta, 1) == last_cta - first_cta;
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                join_parts(p, slab, seg, cut, first_cta, last_cta);
+            }
+        }
         __syncthreads();
         at = stop;
-    }
-}
-
-// Units that lie in several stretches: the CTA of the first stretch that begins inside one adds its parts.
-__global__ void __launch_bounds__(kThreads) grad_join_kernel(const GradParams p, const Shape sh) {
-    pdl_wait();
-    const int ctas = static_cast<int>(gridDim.x), cta = blockIdx.x;
-    const int64_t all = static_cast<int64_t>(p.tiles.prefix[p.L]) * sh.units, begin = stretch_begin(all, cta, ctas);
-    if (cta == 0 || begin >= all) return;
-    const Segment seg = find_unit(p.tiles.prefix, p.L, sh.units, begin);
-    const int64_t before = stretch_begin(all, cta - 1, ctas);
-    if (seg.begin >= begin || before > seg.begin) return;    // begins with the unit, or not the first inside it
-    const Slab slab(p, sh, seg.unit);
-    const float* first = p.parts + (2 * static_cast<int64_t>(cta - 1) + (before != seg.begin)) * (kRanks * kCols);
-    int stop = cta + 1;                   // of the stretches that begin inside the unit (an empty one begins where the next does)
-    while (stop < ctas && stretch_begin(all, stop, ctas) < seg.end) ++stop;
-    // four elements at a time and all of a thread's at once: the parts' latency once for each, not for each element too
-    constexpr int kMine = kRanks * kCols / 4 / kThreads;
-    const int count = slab.ranks * kCols / 4;
-    float4 v[kMine];
-    const auto add = [&](const float* part, bool begin) {
-#pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-            const int i = threadIdx.x + j * kThreads;
-            if (i >= count) break;
-            const float4 w = *reinterpret_cast<const float4*>(part + 4 * i);
-            v[j] = begin ? w : make_float4(v[j].x + w.x, v[j].y + w.y, v[j].z + w.z, v[j].w + w.w);
-        }
-    };
-    add(first, true);
-    for (int k = cta; k < stop; ++k)
-        if (stretch_begin(all, k + 1, ctas) > stretch_begin(all, k, ctas)) add(p.parts + 2 * static_cast<int64_t>(k) * (kRanks * kCols), false);
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-        const int i = threadIdx.x + j * kThreads;
-        if (i < count) slab.store(p, seg.adapter, 4 * i, v[j]);
     }
 }
 
@@ -338,20 +358,18 @@ Shape shape_of(int64_t K, int64_t N, int R) {
 }
 // CTAs: two to an SM, with four stages each at least.
 int ctas_of(int64_t T, int L, const Shape& sh) {
-    const int64_t all = (T / kTokens + L) * sh.units, most = 2 * std::min(device_sm_count(), kMaxSms), few = (all + 3) / 4;
+    const int64_t all = (T / kTokens + L) * sh.units, most = 2 * std::min(device_sm_count(), kMaxCtas / 2), few = (all + 3) / 4;
     return static_cast<int>(few < most ? few : most);
 }
 
-template <int kM>
+template <int kM, bool kWide>
 cudaError_t launch(const GradParams& p, int64_t T, cudaStream_t st) {
     const Shape sh = shape_of(p.K, p.N, p.R);
     const unsigned ctas = static_cast<unsigned>(ctas_of(T, p.L, sh));
     static Ready ready;
-    cudaError_t e = allow_shared(reinterpret_cast<const void*>(grad_kernel<kM>), GradLayout<kM>::total, ready);
+    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(grad_kernel<kM, kWide>), GradLayout<kM>::total, ready);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(true, grad_kernel<kM>, dim3(ctas), dim3(kThreads), static_cast<size_t>(GradLayout<kM>::total), st, p, sh);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(true, grad_join_kernel, dim3(ctas), dim3(kThreads), 0, st, p, sh);
+    return launch_pdl(true, grad_kernel<kM, kWide>, dim3(ctas), dim3(kThreads), static_cast<size_t>(GradLayout<kM>::total), st, p, sh);
 }
 
 }  // namespace
@@ -360,7 +378,10 @@ size_t grad_bytes(int64_t T, int L, int R, int64_t K, int64_t N) {
     return 2 * static_cast<size_t>(ctas_of(T, L, shape_of(K, N, R))) * kRanks * kCols * sizeof(float);
 }
 
-cudaError_t launch_grad(const GradParams& p, int64_t T, cudaStream_t st) { return p.R <= 16 ? launch<1>(p, T, st) : launch<2>(p, T, st); }
+cudaError_t launch_grad(const GradParams& p, int64_t T, cudaStream_t st) {
+    if (p.dy_wide) return p.R <= 16 ? launch<1, true>(p, T, st) : launch<2, true>(p, T, st);
+    return p.R <= 16 ? launch<1, false>(p, T, st) : launch<2, false>(p, T, st);
+}
 
 }  // namespace lora
 }  // namespace nvfp4

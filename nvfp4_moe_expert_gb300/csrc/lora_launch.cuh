@@ -39,7 +39,7 @@ cudaError_t by_rank(int R, F&& f) {
 struct Ready {
     std::mutex mutex;
     bool on[kMaxDevices] = {};
-    int clusters[kMaxDevices][kMaxRank / 8 + 1] = {};   // that run at once, by rank (0: not asked yet)
+    int clusters[kMaxDevices][3][kMaxRank / 8 + 1] = {};   // that run at once, by size (2, 4, 8) and rank (0: not asked yet)
 };
 inline cudaError_t allow_shared(const void* kernel, int bytes, Ready& ready) {
     int dev = 0;
@@ -55,23 +55,23 @@ inline cudaError_t allow_shared(const void* kernel, int bytes, Ready& ready) {
     return cudaSuccess;
 }
 
-// Clusters of kSplit CTAs of a kernel that run at once on the current device.
+// Clusters of `split` CTAs of a kernel that run at once on the current device.
 template <typename... A>
-cudaError_t clusters_at_once(void (*kernel)(A...), int threads, int smem, int R, Ready& ready, int64_t& clusters) {
+cudaError_t clusters_at_once(void (*kernel)(A...), int threads, int smem, int R, int split, Ready& ready, int64_t& clusters) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(ready.mutex);
-    int& known = ready.clusters[dev][R / 8];
+    int& known = ready.clusters[dev][split / 4][R / 8];
     if (known == 0) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(kSplit);
+        cfg.gridDim = dim3(split);
         cfg.blockDim = dim3(threads);
         cfg.dynamicSmemBytes = smem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = kSplit;
+        attr[0].val.clusterDim.x = split;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
@@ -88,9 +88,9 @@ cudaError_t clusters_at_once(void (*kernel)(A...), int threads, int smem, int R,
 constexpr int kManyShared = 225 * 1024;   // 227 KB to a CTA, less the static variables
 constexpr int kMaxStages = 6;
 // Shared memory of the kernel for many rows: a ring of stages (128 bytes of 128 rows of x, or of y, and the adapter's part
-// that goes with them, in rows of 128 bytes), and beside it the CTA's sums and the terms of h.
+// that goes with them), and beside it the CTA's sums and the terms of h.
 struct ManyLayout {
-    int blocks;                           // of 64 ranks, a row of 128 bytes each
+    int blocks;                           // of 64 ranks, or of fewer in shorter rows
     int down_bytes, up_bytes;             // the adapter's part
     int stage, stages;                    // bytes of a stage; how many
     int sum_pitch, sum, h, total;         // floats of a row of the sums; offsets; all bytes
@@ -99,8 +99,8 @@ struct ManyLayout {
     __host__ __device__ ManyLayout(int R, int terms, bool trans, int y_type) {
         cols = y_type == NVFP4_TYPE_F32 ? 32 : 64;
         blocks = (R + 63) / 64;
-        down_bytes = trans ? 64 * 128 * blocks : rank_up(R) * 128;
-        up_bytes = trans ? rank_up(R) * 128 : cols * 128 * blocks;
+        down_bytes = trans ? 64 * rank_bytes(R) * blocks : rank_up(R) * 128;
+        up_bytes = trans ? rank_up(R) * 128 : cols * rank_bytes(R) * blocks;
         stage = (kManyRows * 128 + (down_bytes > up_bytes ? down_bytes : up_bytes) + 1023) / 1024 * 1024;
         sum_pitch = R + 4;
         const int rest = kManyRows * sum_pitch * 4 + terms * kManyRows * padded_pitch(rank_up(R)) + 1024;
@@ -121,8 +121,9 @@ inline bool many_fits(int R, int terms, bool trans) {
 }
 
 // Map of [slices][rows][cols] 16-bit units, rows `ld` units apart and slices `slice` (multiples of 8): boxes of box_rows rows
-// of 64 units in shared-memory rows of 128 bytes, 128B swizzle; what lies outside reads as zero.
-bool make_units_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t slices, int64_t slice, int box_rows);
+// in shared-memory rows of `bytes` (32, 64 or 128), swizzled as wide; what lies outside reads as zero.
+bool make_units_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t slices, int64_t slice, int box_rows,
+                    int bytes = 128);
 
 size_t sort_bytes(int64_t T, int L);
 Tiles sort_layout(void* ws, int64_t T, int L);

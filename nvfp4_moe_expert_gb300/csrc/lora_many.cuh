@@ -1,13 +1,14 @@
 // Low-rank adapters, tiles of up to 128 rows: prompts and training batches.  lora.cuh says what is computed.
 //
-// Bound by memory, so the loads are not to pause: loader warps keep a ring of stages full, first a tile's eighth of C (64
-// columns of x and of the adapter a stage), then its eighth of D (128 bytes a row of y and the adapter's part), then the next
+// Bound by memory, so the loads are not to pause: loader warps keep a ring of stages full, first its share of C (64
+// columns of x and of the adapter a stage), then its share of D (128 bytes a row of y and the adapter's part), then the next
 // tile's, whatever the 8 other warps are at.  Those take 16 rows each: products of the first phase into registers; the
-// 8 CTAs' sums meet in shared memory over the cluster, each CTA adding 16 rows and handing their terms to all; products of the
+// CTAs' sums meet in shared memory over the cluster, each CTA adding its share of the rows and handing their terms to all; products of the
 // second phase are added to y where it lies in shared memory, which goes out from there in whole rows of 128 bytes.
 //
 // x and y come by TMA, 16 rows to an instruction where they lie in a row, four rows of any place otherwise, where
-// rows start on 16-byte boundaries; otherwise four loader warps read aligned words and shift them together.  (With the loads
+// rows start on 16-byte boundaries; otherwise four loader warps read aligned words and shift them together, a stage's on
+// their way while the last one's are put in place.  (With the loads
 // and the products in the same warps, cp.async and a barrier for each stage, 16384 x 4096 -> 4096 of rank 16 took 145 to 199 us:
 // 500 instructions a stage and warp, half of them addresses.)
 #pragma once
@@ -41,39 +42,81 @@ struct ManyMaps {
     CUtensorMap x, y, x16, y16, down, up;   // of x and y: boxes of one row, for gathers, and of 16
 };
 
-// The second product of a warp's 16 rows with a group of 32 outputs (`up`: the group's rows, or columns): acc[i] gets
-// outputs 8 i to 8 i + 7.
-template <typename T, bool kTrans, int kTerms>
-__device__ __forceinline__ void multiply_outputs(float (&acc)[4][4], uint32_t h, int term_bytes, uint32_t up, int block_bytes,
-                                                 int first_chunk, int Rp, int lane) {
-#pragma unroll 1
-    for (int kk = 0; kk < Rp / 16; ++kk) {
-        uint32_t a[kTerms][4], b[2][4];
+// Step kk of the second product of a warp's 16 rows (`a`: their terms) with a group of 32 outputs (`up`: the group's rows, or
+// columns): acc[i] gets outputs 8 i to 8 i + 7.
+template <typename T, bool kTrans, int kTerms, int kRowBytes>
+__device__ __forceinline__ void multiply_outputs(float (&acc)[4][4], const uint32_t (&a)[kTerms][4], uint32_t up, int block_bytes,
+                                                 int first_chunk, int kk, int lane) {
+    constexpr int kPer = kRowBytes / 32;  // steps of 16 ranks to a row
+    uint32_t b[2][4];
 #pragma unroll
-        for (int t = 0; t < kTerms; ++t) ldsm4(h + t * term_bytes + 32 * kk, a[t]);
+    for (int i = 0; i < 2; ++i) {         // two tiles of 8 outputs at once
+        if (!kTrans)                      // rows of ranks
+            ldsm4(up + kk / kPer * block_bytes + swizzled_rows<kRowBytes>(8 * (2 * i + (lane >> 4)) + (lane & 7), 2 * (kk % kPer) + ((lane >> 3) & 1)), b[i]);
+        else                              // rows of 64 outputs
+            ldsm4_trans(up + swizzled(16 * kk + ((lane >> 3) & 1) * 8 + (lane & 7), first_chunk + 2 * i + (lane >> 4)), b[i]);
+    }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {     // two tiles of 8 outputs at once
-            if (!kTrans)                  // rows of 64 ranks
-                ldsm4(up + (kk >> 2) * block_bytes + swizzled(8 * (2 * i + (lane >> 4)) + (lane & 7), 2 * (kk & 3) + ((lane >> 3) & 1)), b[i]);
-            else                          // rows of 64 outputs
-                ldsm4_trans(up + swizzled(16 * kk + ((lane >> 3) & 1) * 8 + (lane & 7), first_chunk + 2 * i + (lane >> 4)), b[i]);
+    for (int t = 0; t < kTerms; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mma(T(), acc[i], a[t], b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
+    }
+}
+
+// The first `left` of 8 units.
+__device__ __forceinline__ void store_units(uint8_t* to, const uint4& v, int left, int units) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (units == 2) {
+            if (2 * j < left) reinterpret_cast<uint32_t*>(to)[j] = w[j];
+        } else {
+            if (2 * j < left) reinterpret_cast<uint16_t*>(to)[2 * j] = static_cast<uint16_t>(w[j]);
+            if (2 * j + 1 < left) reinterpret_cast<uint16_t*>(to)[2 * j + 1] = static_cast<uint16_t>(w[j] >> 16);
         }
+    }
+}
+// `there` units of a row by 8 lanes that hold 8 each (`to`: the lane's, nullptr: no row), where they start on no 16-byte
+// boundary: each lane shifts its own and its left neighbour's into the aligned word between them, and the units in front of
+// the first and behind the last whole word go one to a lane.
+template <int kUnits>
+__device__ __forceinline__ void store_unaligned(uint8_t* to, const uint4& v, int there, int lane) {
+    const int k = lane & 7, off = static_cast<int>(reinterpret_cast<uintptr_t>(to) & 15), first = off ? (16 - off) / 2 : 0;
+    Straddle w;                           // the word that ends inside the lane's units: from unit 8 k - off / 2 on
+    w.lo = make_uint4(__shfl_up_sync(kAll, v.x, 1), __shfl_up_sync(kAll, v.y, 1), __shfl_up_sync(kAll, v.z, 1), __shfl_up_sync(kAll, v.w, 1));
+    w.hi = v;
+    w.left = 8;
+    w.off = (16 - off) & 15;
+    if (off == 0) w.lo = v;
+    const uint4 word = w.value();
+    if (to != nullptr && (off == 0 || k > 0) && 8 * k - off / 2 + 8 <= there) *reinterpret_cast<uint4*>(to - off) = word;
+    // what is left: units [0, first) and [last, there), at most 14
+    const int last = first + (there > first ? (there - first) / 8 * 8 : 0), head = min(first, there), tail = max(last, head), rest = head + max(there - tail, 0);
+    for (int j = k * kUnits;; j += 8 * kUnits) {
+        if (!__any_sync(kAll, to != nullptr && j < rest)) break;
+        const int unit = j < head ? j : tail + j - head;
+        uint32_t w[4] = {v.x, v.y, v.z, v.w}, got = 0;
+        const int from = (lane & ~7) + (min(unit, 63) >> 3), word = (unit & 7) >> 1;
 #pragma unroll
-        for (int t = 0; t < kTerms; ++t) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mma(T(), acc[i], a[t], b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = __shfl_sync(kAll, w[i], from);
+            if (word == i) got = x;
         }
+        if (to == nullptr || j >= rest) continue;
+        uint8_t* at = to + 2 * (unit - 8 * k);
+        if (kUnits == 2) *reinterpret_cast<uint32_t*>(at) = got;
+        else *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(unit & 1 ? got >> 16 : got);
     }
 }
 
 // kLoaders: warps that load, 1 (x and y by TMA) or 4.  kType: y's and out's (branches by it for every value took 3000 cycles a stage).
 template <typename T, bool kTrans, int kType, int kRank, int kLoaders>
-__global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoaders == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoaders == 1 ? 2 : 1)
     many_kernel(const __grid_constant__ ManyMaps maps, const Params p, const ManyLayout lay) {
     constexpr int kTiles = kRank / 8;
     constexpr bool kWide = kType == NVFP4_TYPE_F32;
     constexpr int kCols = kWide ? 32 : 64, kUnits = kWide ? 2 : 1;   // outputs of a stage; 16-bit units of an output
-    constexpr int kTerms = terms_of<T>(kType);
+    constexpr int kTerms = terms_of<T>(kType), kRankBytes = rank_bytes(kRank);
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], sums_ready, h_ready;
     __shared__ float s_undo[kManyRows];
@@ -82,17 +125,18 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t base = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(cluster_rank());
-    const int steps = sub_steps(p.C), c0 = min(rank * kWarps * steps * 16, p.C), c1 = min(c0 + kWarps * steps * 16, p.C);
-    const int chunks = (p.D + kCols - 1) / kCols, per_cta = (chunks + kSplit - 1) / kSplit;
+    const int rank = static_cast<int>(cluster_rank()), split = static_cast<int>(cluster_size());
+    const int groups = kGroups / split, steps = sub_steps(p.C), group_cols = kWarps * steps * 16;   // a multiple of 64
+    const int c0 = min(rank * groups * group_cols, p.C), c1 = min(c0 + groups * group_cols, p.C);
+    const int chunks = (p.D + kCols - 1) / kCols, per_cta = (chunks + split - 1) / split;
     const int chunk0 = min(rank * per_cta, chunks), chunk1 = min(chunk0 + per_cta, chunks);
     if (threadIdx.x == 0) {
         for (int s = 0; s < lay.stages; ++s) {
             mbar_init(&full[s], kLoaders == 1 ? 1 : 32 * kLoaders);
             mbar_init(&empty[s], kWarps);
         }
-        mbar_init(&sums_ready, kSplit);
-        mbar_init(&h_ready, kSplit);
+        mbar_init(&sums_ready, split);
+        mbar_init(&h_ready, split);
         abort_word = 0;
         fence_barrier_init();
     }
@@ -121,14 +165,12 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
         const int thread = threadIdx.x - kThreads;
         const bool x_tma = kLoaders == 1 || p.x_wide, y_tma = kLoaders == 1 || p.out_wide;
         int issued = 0;
-        for (int q = blockIdx.x / kSplit; q < count; q += gridDim.x / kSplit) {
+        for (int q = blockIdx.x / split; q < count; q += gridDim.x / split) {
             const int adapter = p.tiles.adapter[q], start = p.tiles.start[q];
             const int rows = min(kManyRows, p.tiles.offsets[(adapter < 0 ? p.L : adapter) + 1] - start);
             if (adapter < 0 && p.skip_none) continue;
             const int x_stages = adapter < 0 ? 0 : (c1 - c0 + 63) / 64, all = x_stages + chunk1 - chunk0;
             // TMA: a lane's four rows (behind the last: outside the tensor, zeros); otherwise a thread's chunk of every 16th row
-            constexpr int kMine = kLoaders == 1 ? 4 : 8;
-            int row[kMine];
             int four[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) four[i] = 4 * lane + i < rows ? p.tiles.perm[start + 4 * lane + i] : p.T;
@@ -139,12 +181,27 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
             for (int i = 0; i < 4; ++i) apart |= 4 * lane + i < rows && four[i] != group_row + 4 * (lane & 3) + i;
             const bool box = (__ballot_sync(kAll, apart) >> (lane & ~3) & 15) == 0;
             const bool group = 16 * (lane >> 2) < rows && warp == kWarps && (!box || (lane & 3) == 0);
+            constexpr int kMine = kLoaders == 1 ? 1 : 8;
+            int row[kMine];
+            Straddle words[kMine];                              // of the next stage that is not TMA's
+            const auto fetch = [&](int s) {
+                const bool is_x = s < x_stages;
+                if (s >= all || (is_x ? x_tma : y_tma || p.y == nullptr)) return;
+                const uint16_t* from = static_cast<const uint16_t*>(is_x ? p.x : p.y);
+                const int64_t ld = is_x ? p.ldx : p.ldy * kUnits;
+                const int unit = (is_x ? c0 + 64 * s : (chunk0 + s - x_stages) * kCols * kUnits) + 8 * (thread & 7);
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    if (row[i] >= 0) words[i].load(from + row[i] * ld, unit, is_x ? p.C : p.D * kUnits);
+                }
+            };
             if (kLoaders > 1) {
 #pragma unroll
                 for (int i = 0; i < kMine; ++i) {
                     const int r = (thread >> 3) + 16 * i;
                     row[i] = r < rows ? p.tiles.perm[start + r] : -1;
                 }
+                fetch(0);
             }
             for (int s = 0; s < all; ++s, ++issued) {
                 if (!mbar_wait_bounded(&empty[buffer], phase ^ 1u, abort_flag, kWaitBudgetCycles)) failed = true;
@@ -158,10 +215,10 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
                     mbar_arrive_expect_tx(&full[buffer], bytes);
                     if (adapter >= 0 && is_x) {
                         if (!kTrans) load_box(part, &maps.down, bar, c, 0, adapter);
-                        else for (int b = 0; b < lay.blocks; ++b) load_box(part + b * 64 * 128, &maps.down, bar, 64 * b, c, adapter);
+                        else for (int b = 0; b < lay.blocks; ++b) load_box(part + b * 64 * kRankBytes, &maps.down, bar, 64 * b, c, adapter);
                     } else if (adapter >= 0) {
                         if (kTrans) load_box(part, &maps.up, bar, c, 0, adapter);
-                        else for (int b = 0; b < lay.blocks; ++b) load_box(part + b * kCols * 128, &maps.up, bar, 64 * b, c, adapter);
+                        else for (int b = 0; b < lay.blocks; ++b) load_box(part + b * kCols * kRankBytes, &maps.up, bar, 64 * b, c, adapter);
                     }
                 }
                 __syncwarp();
@@ -171,21 +228,13 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
                 }
                 if (kLoaders > 1) {
                     if (!tma && !none) {
-                        const uint16_t* from = static_cast<const uint16_t*>(is_x ? p.x : p.y);
-                        const int64_t ld = is_x ? p.ldx : p.ldy * kUnits;
-                        const int unit = (is_x ? c : c * kUnits) + 8 * (thread & 7), there = is_x ? p.C : p.D * kUnits;
 #pragma unroll
-                        for (int i = 0; i < kMine; i += 4) {
-                            Straddle w[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                if (row[i + j] >= 0) w[j].load(from + row[i + j] * ld, unit, there);
-                            }
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                if (row[i + j] >= 0) w[j].store(at + swizzled((thread >> 3) + 16 * (i + j), thread & 7));
-                            }
+                        for (int i = 0; i < kMine; ++i) {
+                            if (row[i] >= 0) words[i].store(at + swizzled((thread >> 3) + 16 * i, thread & 7));
                         }
+                        fetch(s + 1);
+                    } else {
+                        fetch(s + 1);
                     }
                     if (thread != 0) mbar_arrive(&full[buffer]);
                 }
@@ -209,7 +258,7 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
         const int quad = lane >> 2, my_row = 16 * warp + quad, pitch = padded_pitch(rank_up(p.R));
         const uint32_t ha = base + lay.h + (16 * warp + (lane & 7) + ((lane >> 3) & 1) * 8) * pitch + 16 * (lane >> 4);
         uint32_t tile_phase = 0;
-        for (int q = blockIdx.x / kSplit; q < count; q += gridDim.x / kSplit) {
+        for (int q = blockIdx.x / split; q < count; q += gridDim.x / split) {
             const int adapter = p.tiles.adapter[q], start = p.tiles.start[q];
             const int rows = min(kManyRows, p.tiles.offsets[(adapter < 0 ? p.L : adapter) + 1] - start);
             if (adapter < 0 && p.skip_none) continue;
@@ -230,13 +279,36 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j][i] = total[j][i] = 0.0f;
                 }
-                int left = steps;                           // of the sub-slice
+                // sums of the groups, a pair's in one place (the sums'), the other pair's in another (h's, not in use now)
+                float* const sums = reinterpret_cast<float*>(smem + lay.sum) + my_row * lay.sum_pitch + 2 * (lane & 3);
+                float* const sums2 = sums + (lay.h - lay.sum) / 4;
+                const auto close_group = [&](int group) {
+                    float* const to = group & 2 ? sums2 : sums;
+#pragma unroll
+                    for (int j = 0; j < kTiles; ++j) {
+                        if (8 * j >= p.R) break;
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            float2* const at = reinterpret_cast<float2*>(to + 8 * r * lay.sum_pitch + 8 * j);
+                            float2 v = make_float2(total[j][2 * r] + acc[j][2 * r], total[j][2 * r + 1] + acc[j][2 * r + 1]);
+                            if (group & 1) {
+                                const float2 was = *at;
+                                v = make_float2(was.x + v.x, was.y + v.y);
+                            }
+                            *at = v;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) total[j][i] = acc[j][i] = 0.0f;
+                    }
+                };
+                int left = steps, group = 0;                // steps of the sub-slice
                 for (int s = 0; s < x_stages; ++s) {
+                    if (s > 0 && 64 * s % group_cols == 0) close_group(group++);
                     if (!failed && !mbar_wait_bounded(&full[buffer], phase, abort_flag, kWaitBudgetCycles)) failed = true;
                     if (busy) {
                         const uint32_t at = base + buffer * lay.stage, sx = at + 2048 * warp + lane_rows(lane);
                         const uint32_t sd = at + kManyRows * 128 +
-                                            (kTrans ? swizzled(((lane >> 3) & 1) * 8 + (lane & 7), lane >> 4) : lane_down<false>(lane, p.R));
+                                            (kTrans ? swizzled_rows<kRankBytes>(((lane >> 3) & 1) * 8 + (lane & 7), lane >> 4) : lane_down<false>(lane, p.R));
                         const int n = min(4, (c1 - c0 - 64 * s + 15) / 16);
                         uint32_t a[4][4];
 #pragma unroll
@@ -244,17 +316,14 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             if (kk >= n) break;
-                            if (!kTrans) {
-                                multiply_down<T, false, kTiles>(acc, a[kk], sd, kk, p.R);
-                            } else {                        // rows of 64 ranks, 16 to a step
+                            // all of kRank: what lies behind R is zeros, or anything, and goes nowhere
 #pragma unroll
-                                for (int j = 0; j < kTiles; j += 2) {
-                                    if (8 * j >= p.R) break;
-                                    uint32_t b[4];
-                                    ldsm4_trans((sd ^ ((j & 7) << 4)) + (j >> 3) * 64 * 128 + 2048 * kk, b);
-                                    mma(T(), acc[j], a[kk], b[0], b[1]);
-                                    if (8 * (j + 1) < p.R) mma(T(), acc[j + 1], a[kk], b[2], b[3]);
-                                }
+                            for (int j = 0; j < kTiles; j += 2) {
+                                uint32_t b[4];
+                                if (!kTrans) ldsm4((sd ^ (kk << 5)) + 1024 * j, b);   // rows of 64 columns
+                                else ldsm4_trans((sd ^ ((j & 7) << 4)) + (j >> 3) * 64 * 128 + 16 * kRankBytes * kk, b);   // of ranks
+                                mma(T(), acc[j], a[kk], b[0], b[1]);
+                                mma(T(), acc[j + 1], a[kk], b[2], b[3]);
                             }
                             if (--left == 0) {
                                 left = steps;
@@ -273,43 +342,50 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
                     if (lane == 0) mbar_arrive(&empty[buffer]);
                     next_buffer();
                 }
-                float* sum = reinterpret_cast<float*>(smem + lay.sum) + my_row * lay.sum_pitch + 2 * (lane & 3);
+                close_group(group);                         // C may end inside it, or in front of others, which are 0
+                if (group & 2) {
 #pragma unroll
-                for (int j = 0; j < kTiles; ++j) {
-                    if (8 * j >= p.R) break;
+                    for (int j = 0; j < kTiles; ++j) {
+                        if (8 * j >= p.R) break;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) total[j][i] += acc[j][i];   // C ends inside a sub-slice, or 0
-                    *reinterpret_cast<float2*>(sum + 8 * j) = make_float2(total[j][0], total[j][1]);
-                    *reinterpret_cast<float2*>(sum + 8 * j + 8 * lay.sum_pitch) = make_float2(total[j][2], total[j][3]);
+                        for (int r = 0; r < 2; ++r) {
+                            float2* const at = reinterpret_cast<float2*>(sums + 8 * r * lay.sum_pitch + 8 * j);
+                            const float2 v = *at, w = *reinterpret_cast<const float2*>(sums2 + 8 * r * lay.sum_pitch + 8 * j);
+                            *at = make_float2(v.x + w.x, v.y + w.y);
+                        }
+                    }
                 }
                 asm volatile("fence.acq_rel.cluster;" ::: "memory");
                 consumer_barrier();
-                if (threadIdx.x < kSplit) cluster_arrive(cluster_addr(&sums_ready, threadIdx.x));
+                if (threadIdx.x < split) cluster_arrive(cluster_addr(&sums_ready, threadIdx.x));
                 if (!failed && !cluster_wait_bounded(&sums_ready, tile_phase, abort_flag, kWaitBudgetCycles)) failed = true;
-                if (16 * rank < rows) {
-                    const int r = 16 * rank + 2 * warp + (lane >> 4);
+                const int share = kManyRows / split;
+#pragma unroll 1
+                for (int first = share * rank; first < min(share * (rank + 1), rows); first += 2 * kWarps) {
+                    const int r = first + 2 * warp + (lane >> 4);
                     const uint32_t to = smem_u32(smem) + lay.h + r * pitch;
                     const bool keep = p.h != nullptr && r < rows;
                     float row_undo;
-                    finish_row<T, kRank>(reinterpret_cast<const float*>(smem + lay.sum), r, lay.sum_pitch, p.R,
+                    finish_row<T, kRank>(reinterpret_cast<const float*>(smem + lay.sum), split, r, lay.sum_pitch, p.R,
                                          p.scale == nullptr ? 1.0f : p.scale[adapter], kTerms, kManyRows * pitch,
                                          keep ? p.h + static_cast<int64_t>(p.tiles.perm[start + r]) * p.R : nullptr, p.h_scaled != 0,
                                          lane & 15,
                                          [&](int at, uint32_t v) {
 #pragma unroll
-                                             for (int c = 0; c < kSplit; ++c) {
+                                             for (int c = 0; c < kGroups; ++c) {
+                                                 if (c >= split) break;
                                                  uint32_t there;
                                                  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(to + at), "r"(c));
                                                  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there), "r"(v) : "memory");
                                              }
                                          },
                                          row_undo);
-                    if ((lane & 15) < kSplit)
+                    if ((lane & 15) < split)
                         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(s_undo + r, lane & 15)), "f"(row_undo) : "memory");
                 }
                 asm volatile("fence.acq_rel.cluster;" ::: "memory");
                 consumer_barrier();
-                if (threadIdx.x < kSplit) cluster_arrive(cluster_addr(&h_ready, threadIdx.x));
+                if (threadIdx.x < split) cluster_arrive(cluster_addr(&h_ready, threadIdx.x));
                 if (!failed && !cluster_wait_bounded(&h_ready, tile_phase, abort_flag, kWaitBudgetCycles)) failed = true;
                 tile_phase ^= 1;
             } else if (p.h != nullptr && rank == 0) {
@@ -326,7 +402,19 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
                 // a lane's 2 outputs of 4 tiles of 8, in its two rows
                 const int mine = my_row * 128 + (kWide ? (((lane >> 1) & 1) ^ quad) << 4 | 8 * (lane & 1) : quad << 4 | 4 * (lane & 3));
                 const int line = swizzled(16 * warp + (lane >> 3), lane & 7);
-                const int full_rows = p.out_wide ? min(max(rows - 16 * warp, 0), 16) : 0;
+                // the rows' terms, read once (of up to 64 ranks: more would take the registers that the rest needs)
+                constexpr bool kHeld = kRank <= 64;
+                uint32_t h_of[kHeld ? kRank / 16 : 1][kTerms][4];
+                if (kHeld && adapter >= 0) {
+#pragma unroll
+                    for (int kk = 0; kk < kRank / 16; ++kk) {
+#pragma unroll
+                        for (int t = 0; t < kTerms; ++t) {
+                            if (16 * kk < p.R) ldsm4(ha + t * kManyRows * pitch + 32 * kk, h_of[kk][t]);
+                        }
+                    }
+                }
+                const int full_rows = kLoaders == 1 || p.out_wide ? min(max(rows - 16 * warp, 0), 16) : 0;
                 for (int chunk = chunk0; chunk < chunk1; ++chunk) {
                     if (!failed && !mbar_wait_bounded(&full[buffer], phase, abort_flag, kWaitBudgetCycles)) failed = true;
                     uint4 v[4];
@@ -353,9 +441,18 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
                             }
-                            if (adapter >= 0)
-                                multiply_outputs<T, kTrans, kTerms>(acc, ha, kManyRows * pitch, part + (kTrans ? 0 : 4096 * g), kCols * 128, 4 * g,
-                                                                    rank_up(p.R), lane);
+                            if (adapter >= 0) {
+#pragma unroll
+                                for (int kk = 0; kk < kRank / 16; ++kk) {
+                                    if (16 * kk >= p.R) break;
+                                    if (!kHeld) {
+#pragma unroll
+                                        for (int t = 0; t < kTerms; ++t) ldsm4(ha + t * kManyRows * pitch + 32 * kk, h_of[0][t]);
+                                    }
+                                    multiply_outputs<T, kTrans, kTerms, kRankBytes>(acc, h_of[kHeld ? kk : 0], part + (kTrans ? 0 : 32 * kRankBytes * g), kCols * kRankBytes,
+                                                                        4 * g, kk, lane);
+                                }
+                            }
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -376,29 +473,20 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads + 32 *
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&empty[buffer]);   // in front of the stores, which it would wait for
                     next_buffer();
-                    const int left = busy && !failed ? (p.D - chunk * kCols) * kUnits - 8 * (lane & 7) : 0;   // units of the row from the lane's on
+                    const int there = busy && !failed ? min((p.D - chunk * kCols) * kUnits, 64) : 0, left = there - 8 * (lane & 7);   // units
                     if (full_rows == 16 && left >= 8) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(out[i]) = v[i];
-                    } else {
+                    } else if (kLoaders == 1 || p.out_wide) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            if (out[i] == nullptr || left <= 0) continue;
-                            if (p.out_wide && left >= 8) {
-                                *reinterpret_cast<uint4*>(out[i]) = v[i];
-                                continue;
-                            }
-                            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                if (kWide) {
-                                    if (2 * j < left) reinterpret_cast<uint32_t*>(out[i])[j] = w[j];
-                                } else {
-                                    if (2 * j < left) reinterpret_cast<uint16_t*>(out[i])[2 * j] = static_cast<uint16_t>(w[j]);
-                                    if (2 * j + 1 < left) reinterpret_cast<uint16_t*>(out[i])[2 * j + 1] = static_cast<uint16_t>(w[j] >> 16);
-                                }
-                            }
+                            if (out[i] == nullptr) continue;
+                            if (left >= 8) *reinterpret_cast<uint4*>(out[i]) = v[i];
+                            else store_units(out[i], v[i], left, kUnits);
                         }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) store_unaligned<kUnits>(out[i], v[i], there, lane);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -422,12 +510,37 @@ cudaError_t launch_many_kernel(const ManyMaps& maps, const Params& p, const Many
     auto* kernel = many_kernel<T, kTrans, kType, kRank, kLoaders>;
     cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), kManyShared, ready);
     if (e != cudaSuccess) return e;
-    int64_t clusters = 0;                                   // that run at once
-    e = clusters_at_once(kernel, kThreads + 32 * kLoaders, lay.total, p.R, ready, clusters);
-    if (e != cudaSuccess) return e;
+    // CTAs to a tile: rounds over the GPU times a CTA's stages of a tile and the pause between its two products (about as long
+    // as 4); with 2, 4 and 8 16384 x 4096 -> 4096 of rank 16 took 95, 98 and 98 us, 2000 x 2048 -> 1536 of rank 64 52, 38 and 31
+    int64_t clusters = 0, best = 0;                         // that run at once
+    int split = 0;
+    const int64_t full = p.T / kManyRows + 1, stages = (p.C + 63) / 64 + (p.D + lay.cols - 1) / lay.cols;
+    for (int n = 2; n <= kGroups; n *= 2) {
+        int64_t at_once = 0;
+        e = clusters_at_once(kernel, kThreads + 32 * kLoaders, lay.total, p.R, n, ready, at_once);
+        if (e != cudaSuccess) return e;
+        const int64_t cost = (full + at_once - 1) / at_once * ((stages + n - 1) / n + 4);
+        if (split == 0 || cost < best) {
+            split = n;
+            best = cost;
+            clusters = at_once;
+        }
+    }
     if (tiles < clusters) clusters = tiles;
-    return launch_pdl(pdl, kernel, dim3(static_cast<unsigned>(clusters * kSplit)), dim3(kThreads + 32 * kLoaders),
-                      static_cast<size_t>(lay.total), st, maps, p, lay);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * split));
+    cfg.blockDim = dim3(kThreads + 32 * kLoaders);
+    cfg.dynamicSmemBytes = static_cast<size_t>(lay.total);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, p, lay);
 }
 
 template <typename T, bool kTrans, int kType>
@@ -436,10 +549,11 @@ cudaError_t launch_many(const Params& p, int64_t tiles, bool pdl, cudaStream_t s
     const ManyLayout lay(p.R, terms_of<T>(kType), kTrans, kType);
     const bool tma_y = p.y != nullptr && p.out_wide;
     ManyMaps maps;
-    bool ok = kTrans ? make_units_map(&maps.down, p.down, p.R, p.C, p.R, p.L, static_cast<int64_t>(p.C) * p.R, 64)
+    const int rank_row = rank_bytes(p.R);
+    bool ok = kTrans ? make_units_map(&maps.down, p.down, p.R, p.C, p.R, p.L, static_cast<int64_t>(p.C) * p.R, 64, rank_row)
                      : make_units_map(&maps.down, p.down, p.C, p.R, p.C, p.L, static_cast<int64_t>(p.C) * p.R, Rp);
     ok = ok && (kTrans ? make_units_map(&maps.up, p.up, p.D, p.R, p.D, p.L, static_cast<int64_t>(p.D) * p.R, Rp)
-                       : make_units_map(&maps.up, p.up, p.R, p.D, p.R, p.L, static_cast<int64_t>(p.D) * p.R, lay.cols));
+                       : make_units_map(&maps.up, p.up, p.R, p.D, p.R, p.L, static_cast<int64_t>(p.D) * p.R, lay.cols, rank_row));
     maps.x = maps.y = maps.x16 = maps.y16 = maps.up;        // what is not used is another's
     if (ok && p.x_wide)
         ok = make_units_map(&maps.x, p.x, p.C, p.T, p.ldx, 0, 0, 1) && make_units_map(&maps.x16, p.x, p.C, p.T, p.ldx, 0, 0, 16);
@@ -447,7 +561,7 @@ cudaError_t launch_many(const Params& p, int64_t tiles, bool pdl, cudaStream_t s
     if (ok && tma_y)
         ok = make_units_map(&maps.y, p.y, row, p.T, p.ldy * units, 0, 0, 1) && make_units_map(&maps.y16, p.y, row, p.T, p.ldy * units, 0, 0, 16);
     if (!ok) return cudaErrorInvalidValue;
-    const bool one = p.x_wide && (tma_y || p.y == nullptr);
+    const bool one = p.x_wide && p.out_wide;
     return by_rank(p.R, [&](auto rank) {
         constexpr int kRank = decltype(rank)::value;
         return one ? launch_many_kernel<T, kTrans, kType, kRank, 1>(maps, p, lay, tiles, pdl, st)
