@@ -178,7 +178,7 @@ struct Slots {
 };
 
 template <typename T, int kPer, int kLanes, int kN>
-__global__ void __launch_bounds__(kThreads) stretch_kernel(const T* __restrict__ logits, const BalanceParams p, const Slots w) {
+__global__ void __launch_bounds__(kThreads, kPer <= 16 ? 3 : 2) stretch_kernel(const T* __restrict__ logits, const BalanceParams p, const Slots w) {
     extern __shared__ float s_sum[];                        // [kWarps][E], then [E] counts
     __shared__ int s_tokens;
     const int E = p.E;
@@ -211,66 +211,71 @@ __global__ void __launch_bounds__(kThreads) stretch_kernel(const T* __restrict__
     pdl_launch_dependents();              // not earlier: the join's CTAs would take this kernel's room
 }
 
-constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinThreads = 512;
 
-// A sequence to a cluster (of 1 or 8 CTAs, a part of the experts each): 32 experts at a time, a warp taking every 16th slot.
+// A sequence to a cluster (of 1 or 8 CTAs, a part of the experts each): an expert to a thread, the threads that are left
+// over take every second, fourth, ... slot.
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const BalanceParams p, const Slots w, const Outputs out) {
-    __shared__ float s_sum[kJoinWarps][33];
-    __shared__ int s_count[kJoinWarps][33], s_tokens;
-    __shared__ float s_loss;
-    const int E = p.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ float s_sum[kJoinThreads], s_loss[kJoinThreads / 32];
+    __shared__ int s_count[kJoinThreads], s_tokens;
+    const int E = p.E, thread = threadIdx.x;
     const int rank = static_cast<int>(cluster_rank()), parts = static_cast<int>(cluster_size());
     const int64_t s = blockIdx.x / parts;
     int64_t begin, end;
     sequence_rows(p.offsets, s, p.T, begin, end);
     const int64_t first = begin / w.rows + s, last = end > begin ? (end - 1) / w.rows + s : first - 1;
-    if (threadIdx.x == 0) s_tokens = 0;
+    const int part = (E + parts - 1) / parts, e0 = rank * part, e1 = min(e0 + part, E);
+    int wide = 32;                        // experts at a time, a power of two
+    while (wide < part && wide < kJoinThreads) wide *= 2;
+    const int apart = kJoinThreads / wide, turn = thread / wide, mine = thread & (wide - 1);
+    if (thread == 0) s_tokens = 0;
     __syncthreads();
     pdl_wait();
-    int mine = 0;
-    for (int64_t at = first + threadIdx.x; at <= last; at += kJoinThreads) mine += w.tokens[at];
-    if (mine) atomicAdd(&s_tokens, mine);
-    __syncthreads();
-    const int n = s_tokens, part = (E + parts - 1) / parts, e1 = min((rank + 1) * part, E);
+    int tokens = 0;
+    for (int64_t at = first + thread; at <= last; at += kJoinThreads) tokens += w.tokens[at];
+    if (tokens) atomicAdd(&s_tokens, tokens);
     float loss = 0.0f;
-    for (int base = rank * part; base < e1; base += 32) {
-        const int e = base + lane;
+    for (int base = e0; base < e1; base += wide) {
+        const int e = base + mine;
         float sum = 0.0f;
         int count = 0;
         if (e < e1) {
-#pragma unroll 4
-            for (int64_t at = first + warp; at <= last; at += kJoinWarps) {
+#pragma unroll 8
+            for (int64_t at = first + turn; at <= last; at += apart) {
                 sum += w.sums[at * E + e];
                 count += w.counts[at * E + e];
             }
         }
-        s_sum[warp][lane] = sum;
-        s_count[warp][lane] = count;
+        s_sum[thread] = sum;
+        s_count[thread] = count;
         __syncthreads();
-        if (warp == 0) {
-            sum = 0.0f;
-            count = 0;
-#pragma unroll
-            for (int i = 0; i < kJoinWarps; ++i) {
-                sum += s_sum[i][lane];
-                count += s_count[i][lane];
+        if (turn == 0) {
+            for (int i = 1; i < apart; ++i) {
+                sum += s_sum[i * wide + mine];
+                count += s_count[i * wide + mine];
             }
+            const int n = s_tokens;
             const float mean = n > 0 ? sum / static_cast<float>(n) : 0.0f;
             if (e < e1) {
                 out.counts[s * E + e] = count;
                 out.probs[s * E + e] = mean;
             }
-            loss += lanes_sum<32>(static_cast<float>(count) * mean);
+            loss += static_cast<float>(count) * mean;
         }
         __syncthreads();
     }
-    if (threadIdx.x == 0) s_loss = loss;
+    loss = lanes_sum<32>(loss);
+    if ((thread & 31) == 0) s_loss[thread >> 5] = loss;
     cluster_barrier();
-    if (rank == 0 && threadIdx.x == 0) {
+    if (rank == 0 && thread == 0) {
         float sum = 0.0f;
-        for (int c = 0; c < parts; ++c) sum += cluster_load_f32(cluster_addr(&s_loss, c));
-        out.loss[s] = loss_of(sum, n, E, p.k);
-        out.tokens[s] = n;
+        for (int c = 0; c < parts; ++c) {
+            float own = 0.0f;
+            for (int i = 0; i < wide / 32; ++i) own += cluster_load_f32(cluster_addr(s_loss + i, c));   // warps of turn 0
+            sum += own;
+        }
+        out.loss[s] = loss_of(sum, s_tokens, E, p.k);
+        out.tokens[s] = s_tokens;
     }
     cluster_barrier();
 }
@@ -332,7 +337,7 @@ cudaError_t launch_balance_loss(const void* logits, int type, const BalanceArgs&
                                                         : forward<__half>(logits, p, out, ws, st);
         if (e != cudaSuccess || !two) return e;
     }
-    const unsigned parts = a.S <= kFewSequences ? kSplit : 1;
+    const unsigned parts = a.S <= 4 * kFewSequences ? kSplit : 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.S * parts));
     cfg.blockDim = dim3(kJoinThreads);

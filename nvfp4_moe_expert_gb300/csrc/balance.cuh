@@ -55,20 +55,26 @@ __device__ __forceinline__ void load_row(const T* row, int E, int sub, float (&v
 }
 
 // Turns logits into terms v whose quotients by their sum are the row's p, and returns 1 / sum (0 where all experts are
-// masked).  kRest: rest_e becomes 1 - s_e (sigmoids only).  bad: the row holds a NaN or +inf.
+// masked).  kRest: rest_e becomes 1 - s_e (sigmoids only).  bad: the row holds a NaN or +inf.  What rows hardly ever need
+// (masks, infinities, sigmoids that may underflow) is looked for by the warp as a whole: a choice for each element took half as
+// many instructions again.
 template <int kPer, int kLanes, bool kRest>
 __device__ __forceinline__ float row_terms(int score, float (&v)[kPer], float (&rest)[kRest ? kPer : 1], bool& bad) {
-    float m = -INFINITY;
-    bad = false;
+    float m = v[0], probe = 0.0f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         m = fmaxf(m, v[i]);               // passes NaN over
-        bad |= !(v[i] < INFINITY);
+        probe = fmaf(v[i], 0.0f, probe);  // 0, or NaN of an infinity or NaN
     }
     m = lanes_max<kLanes>(m);
-    if (__any_sync(kAll, bad)) {
+    bad = false;
+    if (__any_sync(kAll, probe != 0.0f)) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] = score == MOE_SCORE_SOFTMAX ? softmax_logit(masked_nan(v[i]), m) : masked_nan(v[i]);
+        for (int i = 0; i < kPer; ++i) {
+            bad |= !(v[i] < INFINITY);
+            v[i] = score == MOE_SCORE_SOFTMAX ? softmax_logit(masked_nan(v[i]), m) : masked_nan(v[i]);
+        }
+        if (m != m) m = -INFINITY;        // nothing but NaN
     }
     float sum = 0.0f;
     if (score == MOE_SCORE_SOFTMAX) {
@@ -78,13 +84,20 @@ __device__ __forceinline__ float row_terms(int score, float (&v)[kPer], float (&
             v[i] = expf(v[i] - shift);
             sum += v[i];
         }
-    } else {
-        const bool low = m < 0.0f;        // relative to the largest, which does not underflow then
+    } else if (__any_sync(kAll, m < 0.0f)) {   // relative to the largest, which does not underflow then
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const float t = expf(-fabsf(v[i])), y = reciprocal_1_2(1.0f + t);
             if (kRest) rest[i] = v[i] < 0.0f ? y : t * y;
-            v[i] = low ? (m < kLowestLogit ? 0.0f : expf(v[i] - m) * y) : v[i] < 0.0f ? t * y : y;
+            v[i] = m < 0.0f ? (m < kLowestLogit ? 0.0f : expf(v[i] - m) * y) : v[i] < 0.0f ? t * y : y;
+            sum += v[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const float t = expf(-fabsf(v[i])), y = reciprocal_1_2(1.0f + t), ty = t * y;
+            if (kRest) rest[i] = v[i] < 0.0f ? y : ty;
+            v[i] = v[i] < 0.0f ? ty : y;
             sum += v[i];
         }
     }

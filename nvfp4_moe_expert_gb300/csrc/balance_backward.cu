@@ -11,7 +11,7 @@ namespace {
 
 
 template <typename T, int kPer, int kLanes, int kN, bool kSigmoid>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kPer <= 16 ? 3 : 1)
     backward_kernel(const T* __restrict__ logits, const BalanceParams p, int64_t rows_per_cta, const int32_t* __restrict__ counts,
                     const int32_t* __restrict__ tokens, const float* __restrict__ dloss, T* __restrict__ dl, int64_t ld_out,
                     int accumulate) {
