@@ -228,9 +228,10 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(kThreads) few_
             for (int j = 0; j < 8; ++j) o[i][j] *= undo[i];
             const int n = 32 * g + 8 * (lane & 3);
             if (row_of[i] < 0) continue;
-            add_eight(y[i], o[i], p.y_type);
+            Eight v = y[i];               // where there is no y it stays zeros
+            add_eight(v, o[i], p.y_type);
             store_eight(static_cast<uint8_t*>(p.out) + (row_of[i] * p.ldo + n) * (p.y_type == NVFP4_TYPE_F32 ? 4 : 2), p.y_type, n, p.D,
-                        p.out_wide, y[i]);
+                        p.out_wide, v);
         }
         if (g + kWarps < last_group) load_y(g + kWarps);
     }

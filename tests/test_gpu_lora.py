@@ -90,7 +90,8 @@ def check(c, dtype=BF16, out=BF16, **kw):
 
 FEW = [(1, 8, 1, 8, 1), (1, 64, 33, 16, 3), (2, 1024, 512, 16, 1), (5, 128, 70, 24, 2), (16, 1032, 96, 8, 5),
        (17, 2080, 1999, 16, 20), (40, 4096, 64, 64, 4), (33, 5000, 300, 32, 9), (9, 8200, 100, 128, 2), (64, 520, 600, 72, 64),
-       (256, 136, 130, 128, 40), (200, 256, 2100, 16, 2), (255, 96, 40, 40, 300)]
+       (256, 136, 130, 128, 40), (200, 256, 2100, 16, 2), (255, 96, 40, 40, 300),
+       (20, 64, 5000, 16, 3), (3, 64, 4100, 104, 2)]
 SORTED = [(257, 256, 100, 16, 6), (300, 1024, 257, 40, 1), (1000, 136, 72, 16, 1024), (700, 2048, 90, 128, 3)]
 MANY = [(1025, 136, 72, 16, 3), (1300, 2048, 200, 64, 7), (1100, 1088, 513, 128, 2), (1500, 8, 1, 8, 1), (2000, 4104, 70, 24, 9),
         (1200, 1032, 1000, 32, 200)]
@@ -243,7 +244,7 @@ def check_backward(c, dx_type=BF16):
 
 BACKWARD = [(1, 8, 1, 8, 1), (3, 64, 33, 16, 2), (100, 520, 130, 24, 4), (257, 1032, 257, 16, 300), (300, 2048, 768, 64, 1),
             (500, 264, 1999, 128, 3), (1024, 128, 136, 8, 5), (1300, 1088, 999, 40, 2), (1100, 136, 520, 128, 2), (2100, 512, 256, 64, 4),
-            (1500, 256, 8, 32, 7), (1500, 8, 1100, 16, 1)]
+            (1500, 256, 8, 32, 7), (1500, 8, 1100, 16, 1), (2, 3272, 268, 24, 4), (300, 4600, 70, 16, 2), (30, 5000, 33, 72, 2)]
 
 
 @pytest.mark.parametrize("shape", BACKWARD)
