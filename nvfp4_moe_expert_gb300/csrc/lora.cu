@@ -19,6 +19,7 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(kSortThreads, 
                 int32_t* __restrict__ offsets, int32_t* __restrict__ tile_adapter, int32_t* __restrict__ tile_start,
                 int32_t* __restrict__ tile_count, int32_t* __restrict__ prefix,
                 int32_t* __restrict__ pieces, int* err) {
+    pdl_launch_dependents();                                // what reads this kernel's results waits for its end
     extern __shared__ int s_at[];                           // [kSortWarps][bins] rows of a warp, then those in front of it
     __shared__ int s_scan[3][kSortWarps];
     const int bins = L + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -135,7 +136,36 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(kSortThreads, 
     cluster_barrier();                                      // no CTA leaves while another reads its counts
 }
 
+// A thread to 8 elements.  Bound by memory: 8191 x 1999 in 9 us beside the sort; with dy as it came the kernels behind it took
+// 59 us (the adapters' gradients) and 18 us (dx) longer.
+__global__ void __launch_bounds__(256) align_rows_kernel(const uint16_t* __restrict__ rows, int64_t T, int cols, int64_t ld,
+                                                         uint16_t* __restrict__ out, int64_t ld_out) {
+    const unsigned chunks = static_cast<unsigned>(ld_out / 8);
+    const int64_t all = T * chunks, step = static_cast<int64_t>(gridDim.x) * 256;
+    constexpr int kMine = 4;
+    for (int64_t base = blockIdx.x * 256 + threadIdx.x; base < all; base += kMine * step) {
+        Straddle w[kMine];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int64_t at = base + i * step, t = at / chunks;
+            if (at < all) w[i].load(rows + t * ld, 8 * static_cast<int>(at - t * chunks), cols);
+        }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int64_t at = base + i * step;
+            if (at < all) *reinterpret_cast<uint4*>(out + 8 * at) = w[i].value();
+        }
+    }
+    pdl_wait();
+}
+
 }  // namespace
+
+cudaError_t launch_align_rows(const uint16_t* rows, int64_t T, int cols, int64_t ld, uint16_t* out, int64_t ld_out, cudaStream_t st) {
+    const int64_t blocks = (T * (ld_out / 8) + 1023) / 1024, most = 8 * device_sm_count();
+    return launch_pdl(true, align_rows_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, st, rows, T, cols, ld,
+                      out, ld_out);
+}
 
 namespace {
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -215,18 +245,45 @@ bool wide(const void* p, int64_t ld, int type) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * (type == NVFP4_TYPE_F32 ? 4 : 2) % 16 == 0;
 }
 
-// Tiles of 16 rows while the tiles of 128 are too few to fill the GPU.
-constexpr int64_t kFewTokens = 1024;
+// Whether tiles of 16 rows take less time than tiles of 128: 6 us and a time for each of the one, a longer start and a time for
+// each of the other, both with the columns (an adapter's last tile is half full on average).  us of 2048 -> 2048, tiles of 16 and
+// 128, 1 adapter and 64 (* the rule's):
+//   rank 16    512 tokens  8 * 16       13 * 26     rank 64    512 tokens  24 21 *      38 * 79
+//             1024         14 * 17      14 * 26               1024         40 21 *      41 78 *
+//             2048         21 20 *      21 28 *               2048         71 32 *      72 53 *
+//             8192         70 32 *      70 33 *               8192        269 58 *     270 58 *
+//   rank 32   1024         17 * 24      17 * 43     rank 128  1024         57 36 *      60 127 *
+bool few_rows(int64_t T, int L, int R, int64_t K, int64_t N, int terms, bool trans) {
+    using namespace lora;
+    if (!many_fits(R, terms, trans)) return true;
+    const int i = R <= 16 ? 0 : R <= 32 ? 1 : R <= 64 ? 2 : 3;
+    constexpr double kTile16[] = {0.137, 0.216, 0.525, 0.766}, kStart[] = {13, 21, 20, 36}, kTile128[] = {0.28, 0.45, 0.6, 1.2};
+    const double columns = static_cast<double>(K + N) / 4096, tiles16 = T / 16.0 + L / 2.0, tiles128 = T / 128.0 + L / 2.0;
+    return 6 + kTile16[i] * columns * (tiles16 < T ? tiles16 : T) <=
+           10 + ((kStart[i] - 10) + kTile128[i] * (tiles128 < T ? tiles128 : T)) * columns;
+}
 
 }  // namespace
 
 bool lora_sorts(int64_t T) { return T > lora::kInCta; }
 size_t lora_workspace(int64_t T, int L) { return lora_sorts(T) ? lora::sort_bytes(T, L) : 0; }
-// The sort, dh, and the parts of the adapters' gradients.
-size_t lora_backward_workspace(int64_t T, int L, int R, int64_t K, int64_t N) {
-    using namespace lora;
-    return align_256(sort_bytes(T, L)) + align_256(static_cast<size_t>(T) * R * sizeof(float)) + align_256(grad_bytes(T, L, R, K, N));
-}
+namespace {
+// The sort, dh, the parts of the adapters' gradients, and room for dy in aligned rows.
+struct BackwardLayout {
+    size_t dh, parts, dy, total;
+    int64_t lddy;
+    BackwardLayout(int64_t T, int L, int R, int64_t K, int64_t N) {
+        using namespace lora;
+        dh = align_256(sort_bytes(T, L));
+        parts = dh + align_256(static_cast<size_t>(T) * R * sizeof(float));
+        dy = parts + align_256(grad_bytes(T, L, R, K, N));
+        lddy = (N + 7) / 8 * 8;
+        total = dy + align_256(static_cast<size_t>(T) * lddy * 2);
+    }
+};
+}  // namespace
+
+size_t lora_backward_workspace(int64_t T, int L, int R, int64_t K, int64_t N) { return BackwardLayout(T, L, R, K, N).total; }
 
 cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t st) {
     using namespace lora;
@@ -257,7 +314,7 @@ cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t st) {
         const int64_t tiles = tiles_bound(a.T, a.L, kFewRows);
         return bf16 ? launch_few_forward_bf16(p, tiles, false, st) : launch_few_forward_f16(p, tiles, false, st);
     }
-    const int rows = a.T <= kFewTokens || !many_fits(a.R, bf16 && a.y_type == NVFP4_TYPE_F32 ? 3 : 2, false) ? kFewRows : kManyRows;
+    const int rows = few_rows(a.T, a.L, a.R, a.K, a.N, bf16 && a.y_type == NVFP4_TYPE_F32 ? 3 : 2, false) ? kFewRows : kManyRows;
     p.tiles = sort_layout(a.ws, a.T, a.L);
     const cudaError_t e = launch_sort(a.ids, a.T, a.L, rows, p.tiles, a.err, st);
     if (e != cudaSuccess) return e;
@@ -269,14 +326,22 @@ cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t st) {
 cudaError_t launch_lora_add_backward(const LoraBackwardArgs& a, cudaStream_t st) {
     using namespace lora;
     const Tiles tiles = sort_layout(a.ws, a.T, a.L);
-    float* dh = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + align_256(sort_bytes(a.T, a.L)));
-    const int rows = a.T <= kFewTokens || !many_fits(a.R, a.dx_type == NVFP4_TYPE_F32 ? 3 : 2, true) ? kFewRows : kManyRows;
+    const BackwardLayout lay(a.T, a.L, a.R, a.K, a.N);
+    float* dh = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + lay.dh);
+    const int rows = few_rows(a.T, a.L, a.R, a.K, a.N, a.dx_type == NVFP4_TYPE_F32 ? 3 : 2, true) ? kFewRows : kManyRows;
     cudaError_t e = launch_sort(a.ids, a.T, a.L, rows, tiles, a.err, st);
     if (e != cudaSuccess) return e;
     Params p = {};
     p.x = a.dy;
     p.ldx = a.lddy;
-    p.x_wide = wide(a.dy, a.lddy, NVFP4_TYPE_BF16);
+    if (!wide(a.dy, a.lddy, NVFP4_TYPE_BF16)) {
+        uint16_t* dy = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.ws) + lay.dy);
+        e = launch_align_rows(static_cast<const uint16_t*>(a.dy), a.T, static_cast<int>(a.N), a.lddy, dy, lay.lddy, st);
+        if (e != cudaSuccess) return e;
+        p.x = dy;
+        p.ldx = lay.lddy;
+    }
+    p.x_wide = 1;
     p.down = a.up;                        // dh = s dy B: B is [N][R]
     p.up = a.down;                        // dx = dh A: A is [R][K]
     p.scale = a.scale;
@@ -301,11 +366,9 @@ cudaError_t launch_lora_add_backward(const LoraBackwardArgs& a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     GradParams g = {};
     g.x = static_cast<const uint16_t*>(a.x);
-    g.dy = static_cast<const uint16_t*>(a.dy);
+    g.dy = static_cast<const uint16_t*>(p.x);
     g.ldx = a.ldx;
-    g.lddy = a.lddy;
-    g.x_wide = 1;
-    g.dy_wide = p.x_wide;
+    g.lddy = p.ldx;
     g.h = a.h;
     g.dh = dh;
     g.scale = a.scale;
@@ -317,7 +380,7 @@ cudaError_t launch_lora_add_backward(const LoraBackwardArgs& a, cudaStream_t st)
     g.ddown = a.ddown;
     g.dup = a.dup;
     g.grads_wide = ((reinterpret_cast<uintptr_t>(a.ddown) | reinterpret_cast<uintptr_t>(a.dup)) & 15) == 0;
-    g.parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(dh) + align_256(static_cast<size_t>(a.T) * a.R * sizeof(float)));
+    g.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + lay.parts);
     return launch_grad(g, a.T, st);
 }
 

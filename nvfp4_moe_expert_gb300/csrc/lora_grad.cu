@@ -116,8 +116,7 @@ struct Slab {
     }
 };
 
-// kWide: all rows start on 16-byte boundaries.
-template <int kM, bool kWide>
+template <int kM>
 __device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab, int adapter, int skip, int stages, uint8_t* smem,
                                            int (&s_rows)[2][kIndexed * kTokens], float (&total)[kM][4][4]) {
     using Lay = GradLayout<kM>;
@@ -127,13 +126,12 @@ __device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab
     const int col0 = slab.col0, width = slab.width, ranks = slab.ranks;
     const uint16_t* x = is_down ? p.x : p.dy;
     const int64_t ldx = is_down ? p.ldx : p.lddy;
-    const bool wide = kWide || is_down || p.dy_wide;
     const float* h = (is_down ? p.dh : p.h) + slab.rank0;
     const float scale = is_down || p.scale == nullptr ? 1.0f : p.scale[adapter];
     const int begin = p.tiles.offsets[adapter], first = skip * kTokens, last = p.tiles.offsets[adapter + 1] - begin;
     const int32_t* perm = p.tiles.perm + begin + first;
 
-    const bool full_slab = wide && col0 + kCols <= width;
+    const bool full_slab = col0 + kCols <= width;
     // rows of kIndexed stages, block by block; -1 behind the last
     static_assert(kIndexed * kTokens == 2 * kThreads, "two rows to a thread");
     const auto get_rows = [&](int block, int (&to)[2]) {
@@ -148,14 +146,6 @@ __device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab
         for (int i = 0; i < 2; ++i) s_rows[block & 1][i * kThreads + threadIdx.x] = from[i];
     };
     const auto row_at = [&](int s, int r) { return s_rows[(s / kIndexed) & 1][s % kIndexed * kTokens + r]; };
-    // rows on no 16-byte boundary: the aligned words of the stage after the one that is put in place next
-    Straddle words[kWide ? 1 : kCols / 64];
-    const auto fetch = [&](int s) {
-        const int t = s < stages ? row_at(s, threadIdx.x >> 3) : -1;
-#pragma unroll
-        for (int i = 0; i < (kWide ? 0 : kCols / 64); ++i)
-            words[i].load(t < 0 ? x : x + t * ldx, t < 0 ? width : col0 + 64 * i + 8 * (threadIdx.x & 7), width);
-    };
     const auto load_x = [&](int s) {
         if (s < stages) {
             const uint32_t at = base + s % kStages * Lay::stage;
@@ -166,18 +156,14 @@ __device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab
                 const uint16_t* from = row + col0 + 8 * (threadIdx.x & 7);
 #pragma unroll
                 for (int i = 0; i < kCols / 64; ++i) cp_async16(to + i * Lay::tile, from + 64 * i);
-            } else if (wide) {
+            } else {
 #pragma unroll
                 for (int i = 0; i < kCols / 64; ++i) {
                     const int c = col0 + 64 * i + 8 * (threadIdx.x & 7), left = t < 0 ? 0 : min(max(width - c, 0), 8);
                     cp_async16(at + i * Lay::tile + swizzled(r, threadIdx.x & 7), left ? row + c : row, 2 * left);
                 }
-            } else if (!kWide) {
-#pragma unroll
-                for (int i = 0; i < kCols / 64; ++i) words[i].store(at + i * Lay::tile + swizzled(r, threadIdx.x & 7));
             }
         }
-        if (!kWide && !wide) fetch(s + 1);
         cp_commit();
     };
     // h: 32 tokens x up to 32 ranks, 4 values to a thread
@@ -212,7 +198,6 @@ __device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab
     get_rows(0, first_rows);
     put_rows(0, first_rows);
     __syncthreads();
-    if (!kWide && !wide) fetch(0);
     for (int s = 0; s < kStages - 1; ++s) load_x(s);
     float4 held[kStages - 1];             // of the stages that are under way
 #pragma unroll
@@ -224,9 +209,9 @@ __device__ __forceinline__ void add_stages(const GradParams& p, const Slab& slab
         cp_wait<kStages - 2>();
         // the rows of the block that loads reach from the next stage on; its place was last read a block ago
         const int ahead = s % kIndexed;
-        if (ahead == kIndexed - kStages - 1) put_rows(s / kIndexed + 1, listed);
+        if (ahead == kIndexed - kStages) put_rows(s / kIndexed + 1, listed);
         __syncthreads();                                    // the stage is there, the one before is used up
-        if (ahead == kIndexed - kStages - 5) get_rows(s / kIndexed + 1, listed);
+        if (ahead == kIndexed - kStages - 4) get_rows(s / kIndexed + 1, listed);
         load_x(s + kStages - 1);
 #pragma unroll
         for (int i = 0; i + 2 < kStages; ++i) held[i] = held[i + 1];
@@ -294,7 +279,7 @@ __device__ __forceinline__ void join_parts(const GradParams& p, const Slab& slab
     }
 }
 
-template <int kM, bool kWide>
+template <int kM>
 __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const GradParams p, const Shape sh) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_rows[2][kIndexed * kTokens];
@@ -310,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const GradParams p, c
         const int64_t stop = min(end, seg.end);
         const Slab slab(p, sh, seg.unit);
         float total[kM][4][4];
-        add_stages<kM, kWide>(p, slab, seg.adapter, static_cast<int>(at - seg.begin), static_cast<int>(stop - at), smem, s_rows, total);
+        add_stages<kM>(p, slab, seg.adapter, static_cast<int>(at - seg.begin), static_cast<int>(stop - at), smem, s_rows, total);
         float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
@@ -362,14 +347,14 @@ int ctas_of(int64_t T, int L, const Shape& sh) {
     return static_cast<int>(few < most ? few : most);
 }
 
-template <int kM, bool kWide>
+template <int kM>
 cudaError_t launch(const GradParams& p, int64_t T, cudaStream_t st) {
     const Shape sh = shape_of(p.K, p.N, p.R);
     const unsigned ctas = static_cast<unsigned>(ctas_of(T, p.L, sh));
     static Ready ready;
-    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(grad_kernel<kM, kWide>), GradLayout<kM>::total, ready);
+    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(grad_kernel<kM>), GradLayout<kM>::total, ready);
     if (e != cudaSuccess) return e;
-    return launch_pdl(true, grad_kernel<kM, kWide>, dim3(ctas), dim3(kThreads), static_cast<size_t>(GradLayout<kM>::total), st, p, sh);
+    return launch_pdl(true, grad_kernel<kM>, dim3(ctas), dim3(kThreads), static_cast<size_t>(GradLayout<kM>::total), st, p, sh);
 }
 
 }  // namespace
@@ -378,10 +363,7 @@ size_t grad_bytes(int64_t T, int L, int R, int64_t K, int64_t N) {
     return 2 * static_cast<size_t>(ctas_of(T, L, shape_of(K, N, R))) * kRanks * kCols * sizeof(float);
 }
 
-cudaError_t launch_grad(const GradParams& p, int64_t T, cudaStream_t st) {
-    if (p.dy_wide) return p.R <= 16 ? launch<1, true>(p, T, st) : launch<2, true>(p, T, st);
-    return p.R <= 16 ? launch<1, false>(p, T, st) : launch<2, false>(p, T, st);
-}
+cudaError_t launch_grad(const GradParams& p, int64_t T, cudaStream_t st) { return p.R <= 16 ? launch<1>(p, T, st) : launch<2>(p, T, st); }
 
 }  // namespace lora
 }  // namespace nvfp4

@@ -129,6 +129,10 @@ size_t sort_bytes(int64_t T, int L);
 Tiles sort_layout(void* ws, int64_t T, int L);
 cudaError_t launch_sort(const int32_t* ids, int64_t T, int L, int rows_per_tile, const Tiles& t, int* err, cudaStream_t st);
 
+// Copies rows that start on no 16-byte boundary to out [rows][ld_out] that do, ld_out a multiple of 8 (zeros behind cols); a
+// programmatic dependent of the sort, which it has no use for but to end behind it.
+cudaError_t launch_align_rows(const uint16_t* rows, int64_t T, int cols, int64_t ld, uint16_t* out, int64_t ld_out, cudaStream_t st);
+
 // The kernels, each compiled in a file of its own; tiles: clusters to launch.
 cudaError_t launch_few_forward_bf16(const Params& p, int64_t tiles, bool pdl, cudaStream_t st);
 cudaError_t launch_few_forward_f16(const Params& p, int64_t tiles, bool pdl, cudaStream_t st);
@@ -144,10 +148,9 @@ cudaError_t launch_many_any(const Params& p, int64_t tiles, bool pdl, cudaStream
 
 // Gradients of the adapters.
 struct GradParams {
-    const uint16_t* x;          // [T][ldx], K columns
-    const uint16_t* dy;         // [T][lddy], N columns
+    const uint16_t* x;          // [T][ldx], K columns; rows on 16-byte boundaries
+    const uint16_t* dy;         // [T][lddy], N columns; the same
     int64_t ldx, lddy;
-    int x_wide, dy_wide;
     const float* h;             // [T][R]
     const float* dh;            // [T][R], with the scale
     const float* scale;

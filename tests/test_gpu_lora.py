@@ -93,7 +93,7 @@ FEW = [(1, 8, 1, 8, 1), (1, 64, 33, 16, 3), (2, 1024, 512, 16, 1), (5, 128, 70, 
        (256, 136, 130, 128, 40), (200, 256, 2100, 16, 2), (255, 96, 40, 40, 300),
        (20, 64, 5000, 16, 3), (3, 64, 4100, 104, 2)]
 SORTED = [(257, 256, 100, 16, 6), (300, 1024, 257, 40, 1), (1000, 136, 72, 16, 1024), (700, 2048, 90, 128, 3)]
-MANY = [(1025, 136, 72, 16, 3), (1300, 2048, 200, 64, 7), (1100, 1088, 513, 128, 2), (1500, 8, 1, 8, 1), (2000, 4104, 70, 24, 9),
+MANY = [(3025, 136, 72, 16, 3), (1300, 2048, 200, 64, 7), (1100, 1088, 513, 128, 2), (1500, 8, 1, 8, 1), (2000, 4104, 70, 24, 9),
         (1200, 1032, 1000, 32, 200)]
 
 
