@@ -229,7 +229,7 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(kThreads) few_
             const int n = 32 * g + 8 * (lane & 3);
             if (row_of[i] < 0) continue;
             Eight v = y[i];               // where there is no y it stays zeros
-            add_eight(v, o[i], p.y_type);
+            if (adapter >= 0) add_eight(v, o[i], p.y_type);   // a row without one keeps its bits (-0 + 0 is +0)
             store_eight(static_cast<uint8_t*>(p.out) + (row_of[i] * p.ldo + n) * (p.y_type == NVFP4_TYPE_F32 ? 4 : 2), p.y_type, n, p.D,
                         p.out_wide, v);
         }

@@ -63,6 +63,12 @@ __device__ __forceinline__ void multiply_outputs(float (&acc)[4][4], const uint3
     }
 }
 
+// 16 bytes of out.  dx is not to push dy out of L2, which the adapters' gradients read next.
+template <bool kTrans>
+__device__ __forceinline__ void store_chunk(uint8_t* to, const uint4& v) {
+    if (kTrans) __stcs(reinterpret_cast<uint4*>(to), v);
+    else *reinterpret_cast<uint4*>(to) = v;
+}
 // The first `left` of 8 units.
 __device__ __forceinline__ void store_units(uint8_t* to, const uint4& v, int left, int units) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -423,6 +429,7 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
                         const uint32_t part = smem_u32(y) + kManyRows * 128;
 #pragma unroll
                         for (int g = 0; g < kCols / 32; ++g) {
+                            if (adapter < 0 && p.y != nullptr) break;   // a row without one keeps its bits (-0 + 0 is +0)
                             // y where it lies; all read before any is written, which the compiler cannot do by itself
                             const auto at = [&](int i, int r) { return y + 1024 * r + (mine ^ (kWide ? i << 5 : (4 * g + i) << 4)); };
                             float2 was[4][2];
@@ -476,12 +483,12 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
                     const int there = busy && !failed ? min((p.D - chunk * kCols) * kUnits, 64) : 0, left = there - 8 * (lane & 7);   // units
                     if (full_rows == 16 && left >= 8) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(out[i]) = v[i];
+                        for (int i = 0; i < 4; ++i) store_chunk<kTrans>(out[i], v[i]);
                     } else if (kLoaders == 1 || p.out_wide) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             if (out[i] == nullptr) continue;
-                            if (left >= 8) *reinterpret_cast<uint4*>(out[i]) = v[i];
+                            if (left >= 8) store_chunk<kTrans>(out[i], v[i]);
                             else store_units(out[i], v[i], left, kUnits);
                         }
                     } else {
