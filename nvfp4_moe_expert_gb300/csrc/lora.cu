@@ -1,4 +1,6 @@
 // Low-rank adapters: the sort of the tokens by adapter, and the kernel for tiles of 16 rows (lora.cuh says what is computed).
+#include <algorithm>
+
 #include "lora_launch.cuh"
 
 namespace nvfp4 {
@@ -246,21 +248,27 @@ bool wide(const void* p, int64_t ld, int type) {
 }
 
 // Whether tiles of 16 rows take less time than tiles of 128: 6 us and a time for each of the one, a longer start and a time for
-// each of the other, both with the columns (an adapter's last tile is half full on average).  us of 2048 -> 2048, tiles of 16 and
-// 128, 1 adapter and 64 (* the rule's):
-//   rank 16    512 tokens  8 * 16       13 * 26     rank 64    512 tokens  24 21 *      38 * 79
-//             1024         14 * 17      14 * 26               1024         40 21 *      41 78 *
-//             2048         21 20 *      21 28 *               2048         71 32 *      72 53 *
-//             8192         70 32 *      70 33 *               8192        269 58 *     270 58 *
-//   rank 32   1024         17 * 24      17 * 43     rank 128  1024         57 36 *      60 127 *
+// each of the other, both with the columns.  Each adapter is taken to have tokens, its last tile half full on average.  us of
+// 2048 -> 2048, tiles of 16 and of 128, with 1 adapter, 32, 64 and 256 (* what the rule takes):
+//                       1             32             64             256
+//   rank 16   512   9 * 16       12 * 16        17 * 27         40 * 69
+//            2048     26 20 *      25 19 *        25 30 *        41 * 71
+//            8192     78 34 *      74 34 *        75 35 *        78 78 *
+//   rank 32   512  11 * 24       14 * 25        20 * 47         60 * 117
+//            2048     35 35 *      35 29 *      35 * 48         64 * 121
+//   rank 64   512     28 22 *    28 * 28        43 * 55        138 * 178
+//            1024     43 23 *      44 32 *      45 * 54        138 * 178
+//            2048     76 34 *      75 33 *        76 57 *      141 * 179
+//   rank 128  512     38 39 *    39 * 50        61 * 98        202 * 324
+//            2048    108 65 *     107 60 *       108 105 *     204 * 335
 bool few_rows(int64_t T, int L, int R, int64_t K, int64_t N, int terms, bool trans) {
     using namespace lora;
     if (!many_fits(R, terms, trans)) return true;
     const int i = R <= 16 ? 0 : R <= 32 ? 1 : R <= 64 ? 2 : 3;
-    constexpr double kTile16[] = {0.137, 0.216, 0.525, 0.766}, kStart[] = {13, 21, 20, 36}, kTile128[] = {0.28, 0.45, 0.6, 1.2};
-    const double columns = static_cast<double>(K + N) / 4096, tiles16 = T / 16.0 + L / 2.0, tiles128 = T / 128.0 + L / 2.0;
-    return 6 + kTile16[i] * columns * (tiles16 < T ? tiles16 : T) <=
-           10 + ((kStart[i] - 10) + kTile128[i] * (tiles128 < T ? tiles128 : T)) * columns;
+    constexpr double kTile16[] = {0.137, 0.216, 0.525, 0.766}, kStart[] = {13, 23, 17, 24}, kTile128[] = {0.22, 0.365, 0.63, 1.19};
+    const double columns = static_cast<double>(K + N) / 4096, used = static_cast<double>(L < T ? L : T);
+    const double tiles16 = std::max(used, T / 16.0 + used / 2), tiles128 = std::max(used, T / 128.0 + used / 2);
+    return 6 + kTile16[i] * columns * tiles16 <= 10 + ((kStart[i] - 10) + kTile128[i] * tiles128) * columns;
 }
 
 }  // namespace
@@ -379,7 +387,8 @@ cudaError_t launch_lora_add_backward(const LoraBackwardArgs& a, cudaStream_t st)
     g.N = static_cast<int>(a.N);
     g.ddown = a.ddown;
     g.dup = a.dup;
-    g.grads_wide = ((reinterpret_cast<uintptr_t>(a.ddown) | reinterpret_cast<uintptr_t>(a.dup)) & 15) == 0;
+    g.ddown_wide = a.K % 2 == 0 && (reinterpret_cast<uintptr_t>(a.ddown) & 7) == 0;
+    g.err = a.err;
     g.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + lay.parts);
     return launch_grad(g, a.T, st);
 }

@@ -158,8 +158,9 @@ struct GradParams {
     int L, R, K, N;
     float* ddown;               // [L][R][K]
     float* dup;                 // [L][N][R]
-    int grads_wide;             // both on 16-byte boundaries
+    int ddown_wide;             // pairs of its columns on 8-byte boundaries
     float* parts;               // grad_bytes(T, L, R, K, N) bytes
+    int* err;
 };
 size_t grad_bytes(int64_t T, int L, int R, int64_t K, int64_t N);
 cudaError_t launch_grad(const GradParams& p, int64_t T, cudaStream_t st);

@@ -18,26 +18,6 @@
 namespace nvfp4 {
 namespace lora {
 
-// Four rows (`at[i]`) of 64 units from column c on, one behind the other in shared memory.
-__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c, const int (&at)[4]) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(at[0]), "r"(at[1]), "r"(at[2]), "r"(at[3]), "r"(bar)
-        : "memory");
-}
-// Sixteen rows from `row` on.
-__device__ __forceinline__ void load_rows16(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c, int row) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(row), "r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c, int row, int slice) {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(row), "r"(slice), "r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ void consumer_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
 struct ManyMaps {
     CUtensorMap x, y, x16, y16, down, up;   // of x and y: boxes of one row, for gathers, and of 16
 };
@@ -517,11 +497,12 @@ cudaError_t launch_many_kernel(const ManyMaps& maps, const Params& p, const Many
     auto* kernel = many_kernel<T, kTrans, kType, kRank, kLoaders>;
     cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), kManyShared, ready);
     if (e != cudaSuccess) return e;
-    // CTAs to a tile: rounds over the GPU times a CTA's stages of a tile and the pause between its two products (about as long
-    // as 4); with 2, 4 and 8 16384 x 4096 -> 4096 of rank 16 took 95, 98 and 98 us, 2000 x 2048 -> 1536 of rank 64 52, 38 and 31
+    // CTAs to a tile: rounds over the GPU (every other adapter taken to have a tile of its own) times a CTA's stages of a tile and
+    // the pause between its two products (about as long as 4).  With 2, 4 and 8 16384 x 4096 -> 4096 of rank 16 took 98, 105 and
+    // 117 us, 2000 x 2048 -> 1536 of rank 64 and 8 adapters 51, 33 and 40.
     int64_t clusters = 0, best = 0;                         // that run at once
     int split = 0;
-    const int64_t full = p.T / kManyRows + 1, stages = (p.C + 63) / 64 + (p.D + lay.cols - 1) / lay.cols;
+    const int64_t half = (p.L < p.T ? p.L : p.T) / 2, full = (p.T / kManyRows > half ? p.T / kManyRows : half) + 1, stages = (p.C + 63) / 64 + (p.D + lay.cols - 1) / lay.cols;
     for (int n = 2; n <= kGroups; n *= 2) {
         int64_t at_once = 0;
         e = clusters_at_once(kernel, kThreads + 32 * kLoaders, lay.total, p.R, n, ready, at_once);
