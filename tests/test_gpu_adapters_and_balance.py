@@ -217,3 +217,40 @@ def test_a_block_with_adapters_and_a_balanced_router(T):
     assert np.linalg.norm(values(dx) - want) <= 2 * 2.0 ** -8 * np.linalg.norm(want) + 2.0 ** -8 * np.linalg.norm(values(dy) @ values(w))
     for got, w64 in ((ddown, grads[1]), (dup, grads[2])):
         assert np.linalg.norm(values(got) - w64) <= 2.0 ** -17 * np.linalg.norm(w64)
+
+
+def test_the_example_block_with_adapters_and_a_balance_loss():
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import moe_block
+    T, H, I, L, R = 200, 512, 256, 3, 8
+    block = moe_block.MoEBlock(H=H, I=I, E=64, k=6, n_group=8, topk_group=4)
+    g = torch.Generator("cuda").manual_seed(5)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    block.add_adapters((0.1 * n(L, R, I)).to(BF16), (0.1 * n(L, H, R)).to(BF16), n(L))
+    x, dout = n(T, H).to(BF16), n(T, H).to(BF16)
+    who = torch.randint(-1, L, (T,), device="cuda", generator=g).to(torch.int32)
+    cut = torch.tensor([0, 1, 120, T], dtype=torch.int32, device="cuda")
+    plain = block.forward(x)
+    y = block.forward(x, train=True, adapter_ids=who)
+    assert torch.equal(y[who < 0], plain[who < 0]) and not torch.equal(y, plain)
+    assert torch.equal(block.forward(x[7:8], adapter_ids=who[7:8]), y[7:8])
+    block.forward(x, train=True, adapter_ids=who)
+    dw_plain = block.backward(dout)[3]
+    balance = block.balance_loss(cut)
+    _, logits, ids = block.saved
+    block.forward(x, train=True, adapter_ids=who)
+    dw = block.backward(dout, balance, weight=50.0, seq_offsets=cut)[3]
+    ddown, dup = block.adapter_gradients(dout)
+    assert M.nvfp4_get_device_error() == 0
+    loss, counts, _, tokens = OB.loss(values(logits), ids.cpu().numpy(), "sigmoid", offsets=cut.tolist())
+    assert np.allclose(values(balance.loss), loss, rtol=1e-5, atol=0)
+    want = OB.backward(values(logits), 6, counts, tokens, [50.0] * 3, "sigmoid", offsets=cut.tolist())[0].T @ values(x)
+    # two gradients of 32-bit logits' gradients (2e-5 of their terms) and 32-bit products over 200 tokens
+    assert np.linalg.norm(values(dw) - values(dw_plain) - want) <= 1e-4 * (np.linalg.norm(want) + np.linalg.norm(values(dw_plain)))
+    act, h, _ = block.saved_shared
+    down, up, scale = (values(t) for t in block.adapters.tensors)
+    want = OL.backward(values(dout), values(act), values(h), down, up, scale, who.cpu().numpy())
+    for got, w64 in ((ddown, want[1]), (dup, want[2])):
+        assert np.linalg.norm(values(got) - w64) <= 2.0 ** -17 * np.linalg.norm(w64)
