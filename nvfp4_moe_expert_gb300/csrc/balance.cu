@@ -1,10 +1,13 @@
 // The router's balance loss (balance.cuh says what is computed).
 //
 // Two ways to the sums of p and the counts of each sequence.  Few tokens: one cluster of 8 CTAs to a sequence, which join
-// their sums through shared memory: one launch, no workspace.  More: the rows in equal stretches to about three CTAs an SM,
+// their sums through shared memory: one launch, no workspace (128 x 128 4.7 us, a chain of latencies).  More: the rows in equal stretches to about three CTAs an SM,
 // whatever sequences they hold; where a sequence ends in a stretch, or the stretch does, the CTA writes what it has of the
 // sequence to slot (CTA + sequence) of the workspace, which no other pair shares, as each step of the walk moves one of
 // the two on.  A second kernel adds a sequence's slots in their order.  No float atomics: the same bits for the same call.
+// 65537 x 256 FP32, sigmoid, in 37 sequences take 27 + 6 us, 4096 x 128 BF16 4.2 + 6.9.  The rows' kernel is bound by instruction issue
+// (70% of the slots, 282 warp instructions a row: an exponential, a quotient and a sum for each logit), 67 MB at 2.5 TB/s;
+// the second one by its start and three trips to memory.
 #include "balance.cuh"
 
 namespace nvfp4 {
@@ -12,7 +15,6 @@ namespace balance {
 namespace {
 
 constexpr int kSplit = 8;                 // CTAs of a cluster
-constexpr int64_t kFewTokens = 1024, kFewSequences = 32;
 
 // What a CTA holds of a sequence: sums of p (a lane's elements of its rows), counts in shared memory, tokens.
 template <int kPer>
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, kPer <= 16 ? 3 : 2) stretch_kernel(c
 
 constexpr int kJoinThreads = 512;
 
-// A sequence to a cluster (of 1 or 8 CTAs, a part of the experts each): an expert to a thread, the threads that are left
+// A sequence to a cluster (of 1 to 8 CTAs, a part of the experts each): an expert to a thread, the threads that are left
 // over take every second, fourth, ... slot.
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const BalanceParams p, const Slots w, const Outputs out) {
     __shared__ float s_sum[kJoinThreads], s_loss[kJoinThreads / 32];
@@ -280,7 +282,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const BalanceParams 
     cluster_barrier();
 }
 
-bool few(int64_t T, int64_t S) { return T <= kFewTokens && S <= kFewSequences; }
+// Whether a cluster to a sequence takes no longer than two kernels; with four sequences and more one of them is taken not to
+// have all the tokens.  us on the device from the first kernel's start, E = 128 in 8 lanes, BF16, a cluster and two kernels (a
+// second launch and a workspace take the host about 8 us longer):
+//     tokens        512          1024          2048          4096          8192
+//     1 sequence    6.2 * 13     8.9 * 13      13 13 *       22 14 *       40 15 *
+//     4             5.7 * 9.4    5.4 * 9.4     6.8 * 9.6     9.1 * 10      14 11 *
+//     32            6.2 * 12     6.0 * 10      6.2 * 10      6.2 * 10      6.5 9.6 *
+// and 1 sequence with E = 256 8.7 * 8.7, 14 9.3 *, 23 10 *.  More than 64 clusters wait for each other (128: 16 us).
+bool few(int64_t T, int E, int64_t S) { return S <= 64 && T * (E > 128 ? E : 128) <= (S >= 4 ? 4 : 1) * (int64_t(1) << 17); }
 int rows_at_once(int E) { return E <= 128 ? 32 : E <= 256 ? 16 : 8; }   // of a CTA
 // Stretches: three to an SM, of whole turns of a CTA.
 int64_t stretch_rows(int64_t T, int E) {
@@ -305,7 +315,7 @@ cudaError_t forward(const void* logits, const BalanceParams& p, const Outputs& o
     return by_experts(p.E, [&](auto per, auto lanes) {
         return by_width<T>(load_width<T>(logits, p.ld, p.E), [&](auto width) {
             constexpr int kPer = decltype(per)::value, kLanes = decltype(lanes)::value, kN = decltype(width)::value;
-            if (few(p.T, p.S))
+            if (few(p.T, p.E, p.S))
                 return launch_pdl(false, sequence_kernel<T, kPer, kLanes, kN>, dim3(static_cast<unsigned>(p.S * kSplit)),
                                   dim3(kThreads), smem, st, l, p, out);
             const Slots w = slots(ws, p.T, p.E, p.S);
@@ -320,7 +330,7 @@ cudaError_t forward(const void* logits, const BalanceParams& p, const Outputs& o
 
 size_t balance_workspace(int64_t T, int E, int64_t S) {
     using namespace balance;
-    if (few(T, S)) return 0;
+    if (few(T, E, S)) return 0;
     const size_t n = static_cast<size_t>(stretches(T, E) + S);
     return 2 * align_256(n * E * 4) + align_256(n * 4);
 }
@@ -330,14 +340,17 @@ cudaError_t launch_balance_loss(const void* logits, int type, const BalanceArgs&
     using namespace balance;
     const BalanceParams p = {a.T, a.E, a.ld, a.score, a.k, a.ids, a.mask, a.offsets, a.S, err};
     const Outputs out = {loss, counts, probs, tokens};
-    const bool two = !few(a.T, a.S), rows = !two || a.T > 0;
+    const bool two = !few(a.T, a.E, a.S), rows = !two || a.T > 0;
     if (rows) {
         const cudaError_t e = type == NVFP4_TYPE_F32    ? forward<float>(logits, p, out, ws, st)
                               : type == NVFP4_TYPE_BF16 ? forward<__nv_bfloat16>(logits, p, out, ws, st)
                                                         : forward<__half>(logits, p, out, ws, st);
         if (e != cudaSuccess || !two) return e;
     }
-    const unsigned parts = a.S <= 4 * kFewSequences ? kSplit : 1;
+    // CTAs to a sequence: as many as an SM each allows.  One sequence has up to 456 slots, which 8 CTAs read sooner; with 8 for each
+    // of 64 sequences the call took 16 us, with one 9
+    unsigned parts = kSplit;
+    while (parts > 1 && a.S * parts > 152) parts /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.S * parts));
     cfg.blockDim = dim3(kJoinThreads);

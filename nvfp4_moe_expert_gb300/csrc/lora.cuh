@@ -132,8 +132,8 @@ __host__ __device__ constexpr int rank_up(int R) { return (R + 15) / 16 * 16; } 
 __host__ __device__ inline int sub_steps(int C) { return (C + 1023) / 1024; }
 
 // 16 bytes of a row from 16-bit unit c on (zeros from `units` on) into shared memory.  Rows that do not start on a 16-byte
-// boundary are read in the aligned 16-byte words that hold a unit of theirs, two of them shifted together: with loads of
-// single elements 8191 x 1999 took a CTA eight times the instructions.
+// boundary are read in the aligned 16-byte words that hold a unit of theirs, two of them shifted together, in place of eight
+// loads of single elements.
 struct Straddle {
     uint4 lo, hi;
     int left, off;                        // units that are there, bytes in front of them

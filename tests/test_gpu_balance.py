@@ -109,6 +109,20 @@ def test_many_rows_and_sequences(T, S):
     assert M.nvfp4_get_device_error() == 0
 
 
+@pytest.mark.parametrize("T,E,S", [(1024, 128, 1), (1025, 128, 1), (512, 256, 3), (513, 256, 3), (4096, 64, 4), (4097, 64, 4),
+                                   (2048, 256, 5), (900, 64, 64), (900, 64, 65), (4100, 96, 19), (4100, 96, 20),
+                                   (4100, 96, 38), (4100, 96, 39), (4100, 96, 76), (4100, 96, 77), (3000, 96, 152), (3000, 96, 153)])
+def test_where_the_ways_meet(T, E, S):
+    """One kernel or two, and the sizes of the second one's clusters."""
+    l, ids = make(T, E, 6)
+    check(l, ids, "softmax", torch.rand(T, generator=torch.Generator().manual_seed(S)) < 0.9, None if S == 1 else cuts(T, S, S))
+    if S > 1:                              # all the tokens in one of them
+        one = torch.full((S + 1,), T, dtype=torch.int32)
+        one[: S // 2 + 1] = 0
+        check(l, ids, "sigmoid", None, one)
+    assert M.nvfp4_get_device_error() == 0
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_masked_experts(score):
     l, ids = make(50, 40, 4, seed=3)
