@@ -288,3 +288,36 @@ def test_backward_strides(T):
         got = M.lora_add_backward(dy[:, left:left + 97], x[:, :128], h, c.adapters, c.ids, dx=dx[:, left:left + 128])
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert (dx[:, :left] == 7).all() and (dx[:, left + 128:] == 7).all()
+
+
+# The same of tiles of 128 rows, which take over where there are many rows (few_rows in csrc/lora.cu: for small K and N late).
+@pytest.mark.parametrize("body", [
+    lambda T: test_without_scales_and_in_place(T), lambda T: test_one_adapter_or_none(T, "none"), lambda T: test_one_adapter_or_none(T, "last"),
+    lambda T: test_strides_and_alignment(T), lambda T: test_bad_ids_are_reported(T), lambda T: test_nonfinite_rows_stay_theirs(T),
+    lambda T: test_fp16_h_of_any_size(T, 2.0 ** -18), lambda T: test_fp16_h_of_any_size(T, 2.0 ** 6),
+    lambda T: test_backward_of_one_adapter_or_none(T, "none"), lambda T: test_backward_of_one_adapter_or_none(T, "one"),
+    lambda T: test_backward_of_one_adapter_or_none(T, "sorted"), lambda T: test_backward_bad_ids(T), lambda T: test_backward_strides(T)])
+def test_in_tiles_of_128(body):
+    body(40000)
+
+
+@pytest.mark.parametrize("shape", [(60000, 8, 1, 128, 1), (60001, 16, 3, 128, 5), (40000, 128, 64, 64, 1000)])
+def test_many_rows_of_small_sizes(shape):
+    check(Case(*shape))
+    check_backward(Case(*shape))
+    assert M.nvfp4_get_device_error() == 0
+
+
+def test_gradients_on_any_boundary():
+    c = Case(300, 264, 40, 16, 3)
+    _, h = M.lora_add(c.y, c.x, c.adapters, c.ids, save_for_backward=True)
+    want = M.lora_add_backward(c.dy, c.x, h, c.adapters, c.ids)
+    a, ws = c.adapters, torch.empty(M.lib().lora_add_backward_workspace_bytes(300, 3, 16, 264, 40), dtype=torch.uint8, device="cuda")
+    down, up = (torch.full((t.numel() + 2,), 7.0, device="cuda") for t in want[1:])
+    dx = torch.empty_like(want[0])
+    assert M.lib().lora_add_backward(a.struct, c.dy.data_ptr(), 40, c.x.data_ptr(), 264, h.data_ptr(), c.ids.data_ptr(), 300,
+                                     dx.data_ptr(), 264, 1, 0, down.data_ptr() + 4, up.data_ptr() + 4, ws.data_ptr(), ws.numel(),
+                                     torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(dx, want[0])
+    for got, w in ((down, want[1]), (up, want[2])):
+        assert torch.equal(got[1:-1], w.flatten()) and got[0] == 7 and got[-1] == 7
