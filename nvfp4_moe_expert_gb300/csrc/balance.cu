@@ -45,7 +45,7 @@ __device__ __forceinline__ void add_rows(const T* __restrict__ logits, const Bal
             if (sub < p.k) next_id = p.ids[at * p.k + sub];
         } else {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) next[i] = -INFINITY;
+            for (int i = 0; i < kPer; ++i) next[i] = 0.0f;     // adds nothing, and takes no warp out of its way
         }
     };
     const auto count = [&](int id) {
@@ -61,10 +61,10 @@ __device__ __forceinline__ void add_rows(const T* __restrict__ logits, const Bal
         const bool real = next_real;
         if (base + kStep < end) fetch(t + kStep);
         bool bad;
-        const float r = row_terms<kPer, kLanes, false>(p.score, v, none, bad);
+        const float r = row_terms<kPer, kLanes, false>(p.score, v, none, bad), mine = real ? r : 0.0f;
         if (bad) set_device_error(p.err, NVFP4_ERR_NONFINITE);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) held.sum[i] = fmaf(v[i], r, held.sum[i]);
+        for (int i = 0; i < kPer; ++i) held.sum[i] = fmaf(v[i], mine, held.sum[i]);
         if (real) {
             held.tokens += sub == 0;
             if (sub < p.k) count(id);

@@ -56,19 +56,19 @@ __device__ __forceinline__ void load_row(const T* row, int E, int sub, float (&v
 
 // Turns logits into terms v whose quotients by their sum are the row's p, and returns 1 / sum (0 where all experts are
 // masked).  kRest: rest_e becomes 1 - s_e (sigmoids only).  bad: the row holds a NaN or +inf.  What rows hardly ever need
-// (masks, infinities, sigmoids that may underflow) is looked for by the warp as a whole: a choice for each element took half as
-// many instructions again.
+// (NaN, +inf, sigmoids that may underflow) is looked for by the warp as a whole: a choice for each element took half as
+// many instructions again.  -inf, a masked expert or none, gives 0 by itself.
 template <int kPer, int kLanes, bool kRest>
 __device__ __forceinline__ float row_terms(int score, float (&v)[kPer], float (&rest)[kRest ? kPer : 1], bool& bad) {
     float m = v[0], probe = 0.0f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         m = fmaxf(m, v[i]);               // passes NaN over
-        probe = fmaf(v[i], 0.0f, probe);  // 0, or NaN of an infinity or NaN
+        probe += v[i];                    // below +inf without a NaN or +inf (it may reach that without, which does no harm)
     }
     m = lanes_max<kLanes>(m);
     bad = false;
-    if (__any_sync(kAll, probe != 0.0f)) {
+    if (__any_sync(kAll, !(probe < INFINITY))) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             bad |= !(v[i] < INFINITY);

@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads, kPer <= 16 ? 3 : 1)
                 load_row<T, kPer, kLanes, kN>(logits + at * p.ld, E, sub, next);
             } else {
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) next[i] = -INFINITY;
+                for (int i = 0; i < kPer; ++i) next[i] = 0.0f;   // takes no warp out of its way
             }
         };
         fetch(t);
