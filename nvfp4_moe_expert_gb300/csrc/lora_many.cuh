@@ -301,13 +301,12 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
                         const uint32_t at = base + buffer * lay.stage, sx = at + 2048 * warp + lane_rows(lane);
                         const uint32_t sd = at + kManyRows * 128 +
                                             (kTrans ? swizzled_rows<kRankBytes>(((lane >> 3) & 1) * 8 + (lane & 7), lane >> 4) : lane_down<false>(lane, p.R));
-                        const int n = min(4, (c1 - c0 - 64 * s + 15) / 16);
+                        // the whole stage: behind C lie zeros, and a CTA's share ends with a stage or with C
                         uint32_t a[4][4];
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) ldsm4(sx ^ (kk << 5), a[kk]);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            if (kk >= n) break;
                             // all of kRank: what lies behind R is zeros, or anything, and goes nowhere
 #pragma unroll
                             for (int j = 0; j < kTiles; j += 2) {
@@ -394,18 +393,6 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
                 // a lane's 2 outputs of 4 tiles of 8, in its two rows
                 const int mine = my_row * 128 + (kWide ? (((lane >> 1) & 1) ^ quad) << 4 | 8 * (lane & 1) : quad << 4 | 4 * (lane & 3));
                 const int line = swizzled(16 * warp + (lane >> 3), lane & 7);
-                // the rows' terms, read once (of up to 64 ranks: more would take the registers that the rest needs)
-                constexpr bool kHeld = kRank <= 64;
-                uint32_t h_of[kHeld ? kRank / 16 : 1][kTerms][4];
-                if (kHeld && adapter >= 0) {
-#pragma unroll
-                    for (int kk = 0; kk < kRank / 16; ++kk) {
-#pragma unroll
-                        for (int t = 0; t < kTerms; ++t) {
-                            if (16 * kk < p.R) ldsm4(ha + t * kManyRows * pitch + 32 * kk, h_of[kk][t]);
-                        }
-                    }
-                }
                 const int full_rows = kLoaders == 1 || p.out_wide ? min(max(rows - 16 * warp, 0), 16) : 0;
                 for (int chunk = chunk0; chunk < chunk1; ++chunk) {
                     if (!failed && !mbar_wait_bounded(&full[buffer], phase, abort_flag, kWaitBudgetCycles)) failed = true;
@@ -438,11 +425,12 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
 #pragma unroll
                                 for (int kk = 0; kk < kRank / 16; ++kk) {
                                     if (16 * kk >= p.R) break;
-                                    if (!kHeld) {
+                                    // the rows' terms again for each stage: held over them they took the registers of the rest
+                                    // (8191 rows of dx of rank 64 75 us instead of 62, 8192 x 4096 -> 4096 of rank 32 73 instead of 63)
+                                    uint32_t h_of[kTerms][4];
 #pragma unroll
-                                        for (int t = 0; t < kTerms; ++t) ldsm4(ha + t * kManyRows * pitch + 32 * kk, h_of[0][t]);
-                                    }
-                                    multiply_outputs<T, kTrans, kTerms, kRankBytes>(acc, h_of[kHeld ? kk : 0], part + (kTrans ? 0 : 32 * kRankBytes * g), kCols * kRankBytes,
+                                    for (int t = 0; t < kTerms; ++t) ldsm4(ha + t * kManyRows * pitch + 32 * kk, h_of[t]);
+                                    multiply_outputs<T, kTrans, kTerms, kRankBytes>(acc, h_of, part + (kTrans ? 0 : 32 * kRankBytes * g), kCols * kRankBytes,
                                                                         4 * g, kk, lane);
                                 }
                             }
