@@ -5,8 +5,8 @@
 // whatever sequences they hold; where a sequence ends in a stretch, or the stretch does, the CTA writes what it has of the
 // sequence to slot (CTA + sequence) of the workspace, which no other pair shares, as each step of the walk moves one of
 // the two on.  A second kernel adds a sequence's slots in their order.  No float atomics: the same bits for the same call.
-// 65537 x 256 FP32, sigmoid, in 37 sequences take 27 + 6 us, 4096 x 128 BF16 4.2 + 6.9.  The rows' kernel is bound by instruction issue
-// (70% of the slots, 282 warp instructions a row: an exponential, a quotient and a sum for each logit), 67 MB at 2.5 TB/s;
+// 65537 x 256 FP32, sigmoid, in 37 sequences take 22 + 6 us, 4096 x 128 BF16 3.9 + 7.  The rows' kernel is bound by instruction issue
+// (72% of the slots, 257 warp instructions a row: an exponential, a quotient and a sum for each logit), 67 MB at 3.0 TB/s;
 // the second one by its start and three trips to memory.
 #include "balance.cuh"
 

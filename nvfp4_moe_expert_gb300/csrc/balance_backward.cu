@@ -1,9 +1,9 @@
 // The gradient of the router's balance loss (balance.cuh says what is computed).
 //
 // A CTA takes a stretch of rows; the g of the sequence it is in lie in shared memory, a row is read, turned into its gradient in
-// registers and written by 8, 16 or 32 lanes.  4096 x 128 FP32 4.5 us; 65537 x 250, sigmoid, in 37 sequences 41 us, 131 MB at
-// 3.2 TB/s: its rows start on 8-byte boundaries only, and 407 warp instructions a row fill 66% of the issue slots (65536 x 256 31 us,
-// softmax 28: 4.3 and 4.8 TB/s).
+// registers and written by 8, 16 or 32 lanes.  4096 x 128 FP32 4.5 us; 65537 x 250, sigmoid, in 37 sequences, a tenth of the tokens
+// masked, 32 us, 131 MB at 4.1 TB/s (65536 x 256 without masks 31, softmax 29): 357 warp instructions a row at 24 warps an SM, whose
+// latency the loads of one row ahead do not cover.  20000 x 1000 BF16 28 us with two CTAs to an SM, 38 with one.
 #include "balance.cuh"
 
 namespace nvfp4 {
@@ -11,7 +11,7 @@ namespace balance {
 namespace {
 
 template <typename T, int kPer, int kLanes, int kN, bool kSigmoid>
-__global__ void __launch_bounds__(kThreads, kPer <= 16 ? 3 : 1)
+__global__ void __launch_bounds__(kThreads, kPer <= 16 ? 3 : 2)
     backward_kernel(const T* __restrict__ logits, const BalanceParams p, int64_t rows_per_cta, const int32_t* __restrict__ counts,
                     const int32_t* __restrict__ tokens, const float* __restrict__ dloss, T* __restrict__ dl, int64_t ld_out,
                     int accumulate) {
@@ -105,9 +105,9 @@ cudaError_t backward(const void* logits, const BalanceParams& p, const int32_t* 
             constexpr int64_t kRows = kThreads / kLanes;    // of a CTA at a time
             auto* kernel = p.score == MOE_SCORE_SOFTMAX ? backward_kernel<T, kPer, kLanes, kN, false>
                                                         : backward_kernel<T, kPer, kLanes, kN, true>;
-            // turns of a CTA: enough that the search for its sequence and the g are shared, few enough for even loads
-            int64_t turns = p.T / (kRows * 4 * device_sm_count());
-            turns = turns < 1 ? 1 : turns > 8 ? 8 : turns;
+            // turns of a CTA: all of them run at once (of 65537 x 250, 683 CTAs in a wave and a half took 36 us)
+            const int64_t at_once = kRows * (kPer <= 16 ? 3 : 2) * device_sm_count();
+            const int64_t turns = (p.T + at_once - 1) / at_once;
             const int64_t rows = turns * kRows;
             return launch_pdl(false, kernel, dim3(static_cast<unsigned>((p.T + rows - 1) / rows)), dim3(kThreads), 0, st,
                               static_cast<const T*>(logits), p, rows, counts, tokens, dloss, static_cast<T*>(dl), ld_out,

@@ -250,22 +250,24 @@ bool wide(const void* p, int64_t ld, int type) {
 // Whether tiles of 16 rows take less time than tiles of 128: 6 us and a time for each of the one, a longer start and a time for
 // each of the other, both with the columns.  Each adapter is taken to have tokens, its last tile half full on average.  us of
 // 2048 -> 2048, tiles of 16 and of 128, with 1 adapter, 32, 64 and 256 (* what the rule takes):
-//                       1             32             64             256
-//   rank 16   512   9 * 16       12 * 16        17 * 27         40 * 69
-//            2048     26 20 *      25 19 *        25 30 *        41 * 71
-//            8192     78 34 *      74 34 *        75 35 *        78 78 *
-//   rank 32   512  11 * 24       14 * 25        20 * 47         60 * 117
-//            2048     35 35 *      35 29 *      35 * 48         64 * 121
-//   rank 64   512     28 22 *    28 * 28        43 * 55        138 * 178
-//            1024     43 23 *      44 32 *      45 * 54        138 * 178
-//            2048     76 34 *      75 33 *        76 57 *      141 * 179
-//   rank 128  512     38 39 *    39 * 50        61 * 98        202 * 324
-//            2048    108 65 *     107 60 *       108 105 *     204 * 335
+//                    1             32            64            256
+//   rank 16   512   10 * 15      10 * 15      16 * 25      40 * 62
+//            1024   18 * 16      18 * 16      19 * 25      40 * 62
+//            2048   25 19 *      25 18 *      24 27 *      41 * 63
+//            8192   78 30 *      75 31 *      75 32 *      78 68 *
+//   rank 32   512   11 * 20      14 * 20      20 * 36      62 * 92
+//            1024   21 * 21      21 * 22      21 * 36      63 * 93
+//            2048   35 26 *      35 24 *      36 39 *      64 * 94
+//   rank 64   512   28 20 *      28 24 *      43 * 44     138 140 *
+//            2048   76 28 *      75 25 *      76 45 *     140 140 *
+//   rank 128  512   38 37 *      39 * 48      61 * 92     202 * 311
+//            1024   62 35 *      62 52 *      63 * 91     203 * 316
+//            2048  108 57 *     108 55 *     108 97 *     204 * 321
 bool few_rows(int64_t T, int L, int R, int64_t K, int64_t N, int terms, bool trans) {
     using namespace lora;
     if (!many_fits(R, terms, trans)) return true;
     const int i = R <= 16 ? 0 : R <= 32 ? 1 : R <= 64 ? 2 : 3;
-    constexpr double kTile16[] = {0.137, 0.216, 0.525, 0.766}, kStart[] = {13, 23, 17, 24}, kTile128[] = {0.22, 0.365, 0.63, 1.19};
+    constexpr double kTile16[] = {0.137, 0.216, 0.525, 0.766}, kStart[] = {13.5, 17.5, 14, 22}, kTile128[] = {0.195, 0.292, 0.485, 1.12};
     const double columns = static_cast<double>(K + N) / 4096, used = static_cast<double>(L < T ? L : T);
     const double tiles16 = std::max(used, T / 16.0 + used / 2), tiles128 = std::max(used, T / 128.0 + used / 2);
     return 6 + kTile16[i] * columns * tiles16 <= 10 + ((kStart[i] - 10) + kTile128[i] * tiles128) * columns;

@@ -12,11 +12,11 @@
 // and the products in the same warps, cp.async and a barrier for each stage, 16384 x 4096 -> 4096 of rank 16 took 145 to 199 us:
 // 500 instructions a stage and warp, half of them addresses.)
 //
-// 16384 x 4096 -> 4096 of rank 16 take 98 us, 403 MB at 4.1 TB/s, and its dx without the sum 87, 268 MB at 3.1 TB/s; a kernel
-// that only copies so many bytes 128 at a time from row to row takes 61 (52 in longer pieces).  Issue slots are 47% full, of a stage 344 instructions a warp, and with
-// 18 warps an SM the products' and shared memory's latency shows.  At rank 64 registers and shared memory leave one CTA, 9
-// warps, to an SM: 2000 x 2048 -> 1536 30 us, 8191 rows of dx (1999 -> 4096) 75, issue slots 30% and tensor pipe 22% full.  (Two warps to
-// the same 16 rows, ranks and outputs shared out, were within 4%.)
+// 16384 x 4096 -> 4096 of rank 16 take 91 us, 403 MB at 4.4 TB/s, and its dx without the sum 82, 268 MB at 3.3 TB/s; a kernel
+// that only copies so many bytes 128 at a time from row to row takes 61 (52 in longer pieces).  Issue slots are 47% full, of a stage
+// 320 instructions a warp, and with 18 warps an SM the products' and shared memory's latency shows.  At rank 64 registers and shared
+// memory leave one CTA, 9 warps, to an SM: 2000 x 2048 -> 1536 28 us, 8191 rows of dx (1999 -> 4096) 62; issue slots 35% and tensor pipe
+// 27% full, each instruction waits for the last.  (Two warps to the same 16 rows, ranks and outputs shared out, were within 4%.)
 #pragma once
 
 #include "lora_launch.cuh"
@@ -493,7 +493,7 @@ cudaError_t launch_many_kernel(const ManyMaps& maps, const Params& p, const Many
     if (e != cudaSuccess) return e;
     // CTAs to a tile: rounds over the GPU (every other adapter taken to have a tile of its own) times a CTA's stages of a tile and
     // the pause between its two products (about as long as 4).  With 2, 4 and 8 16384 x 4096 -> 4096 of rank 16 took 98, 105 and
-    // 117 us, 2000 x 2048 -> 1536 of rank 64 and 8 adapters 51, 33 and 40.
+    // 117 us, 2000 x 2048 -> 1536 of rank 64 and 8 adapters 51, 33 and 40 (before the products were made shorter).
     int64_t clusters = 0, best = 0;                         // that run at once
     int split = 0;
     const int64_t half = (p.L < p.T ? p.L : p.T) / 2, full = (p.T / kManyRows > half ? p.T / kManyRows : half) + 1, stages = (p.C + 63) / 64 + (p.D + lay.cols - 1) / lay.cols;
