@@ -613,9 +613,10 @@ nvfp4_status mxfp4_linear(const fp4_linear_weights* w, const void* x_dev, int x_
  * Adapters of many requests at once, added to the outputs of a projection that all of them share
  * (nvfp4_linear or mxfp4_linear, whose 4-bit weights stay as they are):
  *   h_t = A_a x_t,   out_t = y_t + scale_a B_a h_t,   a = adapter_ids[t]; out_t = y_t where a is negative
- * The products accumulate in FP32, h stays FP32 between them (held as sums of 16-bit terms), y is added
- * in FP32 and the sum is rounded once to the outputs' type.  K is summed in an order that goes by K alone:
- * a token's row does not depend on T, on the other tokens or on their order. */
+ * The products accumulate in FP32, h stays FP32 between them (held as sums of 16-bit terms, which give NaN
+ * beside an infinite factor; the same for h and dh in the gradients), y is added in FP32 and the sum is
+ * rounded once to the outputs' type.  K is summed in an order that goes by K alone: a token's row does not
+ * depend on T, on the other tokens or on their order. */
 typedef struct {
     const void* down;     /* A: [L][R][K] of `type`, 16-byte aligned */
     const void* up;       /* B: [L][N][R] of `type`, 16-byte aligned */

@@ -289,8 +289,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const BalanceParams 
 //     1 sequence    6.2 * 13     8.9 * 13      13 13 *       22 14 *       40 15 *
 //     4             5.7 * 9.4    5.4 * 9.4     6.8 * 9.6     9.1 * 10      14 11 *
 //     32            6.2 * 12     6.0 * 10      6.2 * 10      6.2 * 10      6.5 9.6 *
-// and 1 sequence with E = 256 8.7 * 8.7, 14 9.3 *, 23 10 *.  More than 64 clusters wait for each other (128: 16 us).
-bool few(int64_t T, int E, int64_t S) { return S <= 64 && T * (E > 128 ? E : 128) <= (S >= 4 ? 4 : 1) * (int64_t(1) << 17); }
+// and 1 sequence with E = 256 8.7 * 8.7, 14 9.3 *, 23 10 *.  More than 32 clusters wait for each other (64: 11 us, two kernels 9).
+bool few(int64_t T, int E, int64_t S) { return S <= 32 && T * (E > 128 ? E : 128) <= (S >= 4 ? 4 : 1) * (int64_t(1) << 17); }
 int rows_at_once(int E) { return E <= 128 ? 32 : E <= 256 ? 16 : 8; }   // of a CTA
 // Stretches: three to an SM, of whole turns of a CTA.
 int64_t stretch_rows(int64_t T, int E) {
