@@ -191,9 +191,12 @@ __global__ void __launch_bounds__(kThreads, kPer <= 16 ? 3 : 2) stretch_kernel(c
         s = 0;
         row = max(row, static_cast<int64_t>(p.offsets[0]));
     }
-    for (; row < end && s < p.S; ++s) {
+    while (row < end && s < p.S) {
         const int64_t stop = p.offsets == nullptr ? end : min(end, static_cast<int64_t>(p.offsets[s + 1]));
-        if (stop <= row) continue;
+        if (stop <= row) {                                  // empty, as any number behind it may be
+            s = max(s + 1, find_sequence(p.offsets, p.S, row));
+            continue;
+        }
         for (int e = threadIdx.x; e < E; e += kThreads) s_count[e] = 0;
         if (threadIdx.x == 0) s_tokens = 0;
         __syncthreads();
@@ -209,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, kPer <= 16 ? 3 : 2) stretch_kernel(c
         if (threadIdx.x == 0) w.tokens[at] = s_tokens;
         __syncthreads();
         row = stop;
+        ++s;
     }
     pdl_launch_dependents();              // not earlier: the join's CTAs would take this kernel's room
 }

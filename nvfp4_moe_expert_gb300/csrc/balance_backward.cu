@@ -25,8 +25,8 @@ __global__ void __launch_bounds__(kThreads, kPer <= 16 ? 3 : 2)
         int64_t stop = end;
         const bool inside = s >= 0 && s < p.S;
         if (p.offsets != nullptr && s < p.S) stop = min(end, static_cast<int64_t>(p.offsets[s + 1]));
-        if (stop <= row) {
-            ++s;
+        if (stop <= row) {                                  // empty, as any number behind it may be
+            s = max(s + 1, find_sequence(p.offsets, p.S, row));
             continue;
         }
         __syncthreads();                                    // the last sequence's are used up

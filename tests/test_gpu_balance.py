@@ -123,6 +123,33 @@ def test_where_the_ways_meet(T, E, S):
     assert M.nvfp4_get_device_error() == 0
 
 
+def test_runs_of_empty_sequences():
+    T, S = 3000, 300000
+    l, ids = make(T, 8, 2)
+    cut = torch.full((S + 1,), 1400, dtype=torch.int32)             # a quarter of a million empty ones between two rows
+    cut[:1000] = torch.arange(1000)
+    cut[260000:] = torch.arange(S + 1 - 260000).clamp(max=1500) + 1400
+    b = M.moe_balance_loss(l, ids, seq_offsets=cut.cuda())
+    tokens = cut.diff()
+    assert torch.equal(b.tokens.cpu(), tokens)
+    some = torch.cat([tokens.nonzero().flatten(), torch.tensor([1000, 200000, S - 1])])
+    dloss = torch.ones(S).cuda()
+    d = M.moe_balance_loss_backward(l, 2, b.counts, b.tokens, dloss, seq_offsets=cut.cuda())
+    p = torch.softmax(l.double().cpu(), 1)
+    for s in some[::97].tolist() + [999, 1000, 259999, 260000, S - 1]:
+        rows = slice(int(cut[s]), int(cut[s + 1]))
+        n = rows.stop - rows.start
+        c = torch.bincount(ids[rows].flatten().cpu().long(), minlength=8)
+        assert torch.equal(b.counts[s].cpu().long(), c)
+        mean = p[rows].mean(0) if n else torch.zeros(8, dtype=torch.float64)
+        want = (c * mean).sum() * 8 / (2 * n) if n else 0.0
+        assert abs(float(b.loss[s]) - float(want)) <= 200 * U * float(want)
+        if n:
+            g = 8.0 * c / (2.0 * n * n)
+            want = p[rows] * (g - (g * p[rows]).sum(1, keepdim=True))
+            assert np.all(np.abs(values(d[rows]) - want.numpy()) <= G_REL * (p[rows] * (g + (g * p[rows]).sum(1, keepdim=True))).numpy() + 1e-37)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_masked_experts(score):
     l, ids = make(50, 40, 4, seed=3)
