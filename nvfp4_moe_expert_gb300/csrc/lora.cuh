@@ -413,26 +413,26 @@ __device__ __forceinline__ int row_exponent(float m) {
     return max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100) - 14;
 }
 
-// A row of h: lane l of 16 sums the 2, 4 or 8 CTAs' parts of columns 2 l, 2 l + 1, 2 l + 32, ... as a tree, and hands over
-// the row's terms, two columns (32 bits) at a time.
-template <typename T, int kRank, typename Store>
+// A row of h: lane l of kLanes sums the 2, 4 or 8 CTAs' parts of columns 2 l, 2 l + 1, 2 l + 2 kLanes, ... as a tree, and hands
+// over the row's terms, two columns (32 bits) at a time.
+template <typename T, int kRank, int kLanes, typename Store>
 __device__ __forceinline__ void finish_row(const float* part, int parts, int row, int pitch, int R, float scale, int terms, int term_bytes,
                                            float* h_out, bool h_scaled, int l, Store&& store, float& undo) {
-    constexpr int kMine = (kRank + 31) / 32;
+    constexpr int kStep = 2 * kLanes, kMine = (kRank + kStep - 1) / kStep;
     float v[kMine][2], m = 0.0f;
     uint32_t from[kGroups];
 #pragma unroll
     for (int c = 0; c < kGroups; ++c) from[c] = cluster_addr(part, c < parts ? c : 0) + 4 * row * pitch;
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-        const int r = 2 * l + 32 * i;
+        const int r = 2 * l + kStep * i;
         v[i][0] = v[i][1] = 0.0f;
         if (r < R) {
             float got[kGroups][2];
 #pragma unroll
             for (int c = 0; c < kGroups; ++c) {
                 if (c < parts)
-                    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(got[c][0]), "=f"(got[c][1]) : "r"(from[c] + 4 * r) : "memory");
+                    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(got[c][0]), "=f"(got[c][1]) : "r"(from[c] + 4 * r));
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -442,18 +442,23 @@ __device__ __forceinline__ void finish_row(const float* part, int parts, int row
 #pragma unroll
                     for (int c = 0; c < n; ++c) got[c][k] = got[2 * c][k] + got[2 * c + 1][k];
                 }
-                const float sum = got[0][k];
-                v[i][k] = sum * scale;
-                got[0][k] = h_scaled ? v[i][k] : sum;
+                v[i][k] = got[0][k];
             }
-            if (h_out != nullptr) *reinterpret_cast<float2*>(h_out + r) = make_float2(got[0][0], got[0][1]);
         }
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int r = 2 * l + kStep * i;
+        const float sum[2] = {v[i][0], v[i][1]};
+        v[i][0] *= scale;
+        v[i][1] *= scale;
+        if (h_out != nullptr && r < R) *reinterpret_cast<float2*>(h_out + r) = h_scaled ? make_float2(v[i][0], v[i][1]) : make_float2(sum[0], sum[1]);
         m = fmaxf(m, fmaxf(fabsf(v[i][0]), fabsf(v[i][1])));
     }
     undo = 1.0f;
     if (std::is_same<T, __half>::value) {
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
         const int e = row_exponent(m);
         undo = ldexpf(1.0f, e);
 #pragma unroll
@@ -464,7 +469,7 @@ __device__ __forceinline__ void finish_row(const float* part, int parts, int row
     }
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-        const int r = 2 * l + 32 * i;
+        const int r = 2 * l + kStep * i;
         if (r >= rank_up(R)) continue;
         for (int t = 0; t < terms; ++t) {
             const uint32_t lo = next_term<T>(v[i][0]), hi = next_term<T>(v[i][1]);

@@ -195,7 +195,7 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(kThreads) few_
         const bool keep = p.h != nullptr && row < rows && (row >> 1) == rank;
         float row_undo;
         uint8_t* h = smem + lay.h + row * pitch;
-        finish_row<T, kRank>(sum, kGroups, row, p.R, p.R, p.scale == nullptr ? 1.0f : p.scale[adapter], terms, kFewRows * pitch,
+        finish_row<T, kRank, 16>(sum, kGroups, row, p.R, p.R, p.scale == nullptr ? 1.0f : p.scale[adapter], terms, kFewRows * pitch,
                              keep ? p.h + static_cast<int64_t>(s_row[row]) * p.R : nullptr, p.h_scaled != 0, lane & 15,
                              [&](int at, uint32_t v) { *reinterpret_cast<uint32_t*>(h + at) = v; }, row_undo);
         if ((lane & 15) == 0) s_undo[row] = row_undo;

@@ -12,10 +12,10 @@
 // and the products in the same warps, cp.async and a barrier for each stage, 16384 x 4096 -> 4096 of rank 16 took 145 to 199 us:
 // 500 instructions a stage and warp, half of them addresses.)
 //
-// 16384 x 4096 -> 4096 of rank 16 take 91 us, 403 MB at 4.4 TB/s, and its dx without the sum 82, 268 MB at 3.3 TB/s; a kernel
+// 16384 x 4096 -> 4096 of rank 16 take 88 us, 403 MB at 4.6 TB/s, and its dx without the sum 80, 268 MB at 3.4 TB/s; a kernel
 // that only copies so many bytes 128 at a time from row to row takes 61 (52 in longer pieces).  Issue slots are 47% full, of a stage
 // 320 instructions a warp, and with 18 warps an SM the products' and shared memory's latency shows.  At rank 64 registers and shared
-// memory leave one CTA, 9 warps, to an SM: 2000 x 2048 -> 1536 28 us, 8191 rows of dx (1999 -> 4096) 62; issue slots 35% and tensor pipe
+// memory leave one CTA, 9 warps, to an SM: 2000 x 2048 -> 1536 27 us, 8191 rows of dx (1999 -> 4096) 60; issue slots 35% and tensor pipe
 // 27% full, each instruction waits for the last.  (Two warps to the same 16 rows, ranks and outputs shared out, were within 4%.)
 #pragma once
 
@@ -349,30 +349,40 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
                 asm volatile("fence.acq_rel.cluster;" ::: "memory");
                 consumer_barrier();
                 if (threadIdx.x < split) cluster_arrive(cluster_addr(&sums_ready, threadIdx.x));
+                // the CTA's share of the rows, 32 at a time, 8 lanes to one; where their h goes is read while the sums come (16 at a
+                // time, and read then, 16384 x 4096 -> 4096 took 91 us instead of 88)
+                const int share = kManyRows / split, row0 = share * rank, end_row = row0 + share;
+                int h_row = 0;
+                if (p.h != nullptr && lane < 8) {
+                    const int r = row0 + 32 * (lane >> 2) + 4 * warp + (lane & 3);
+                    if (r < min(end_row, rows)) h_row = p.tiles.perm[start + r];
+                }
                 if (!failed && !cluster_wait_bounded(&sums_ready, tile_phase, abort_flag, kWaitBudgetCycles)) failed = true;
-                const int share = kManyRows / split;
 #pragma unroll 1
-                for (int first = share * rank; first < min(share * (rank + 1), rows); first += 2 * kWarps) {
-                    const int r = first + 2 * warp + (lane >> 4);
+                for (int pass = 0; row0 + 32 * pass < min(end_row, rows); ++pass) {
+                    const int at_row = row0 + 32 * pass + 4 * warp + (lane >> 3);
+                    const bool mine = at_row < end_row;
+                    const int r = mine ? at_row : row0, to_row = __shfl_sync(kAll, h_row, 4 * pass + (lane >> 3));
                     const uint32_t to = smem_u32(smem) + lay.h + r * pitch;
-                    const bool keep = p.h != nullptr && r < rows;
+                    const bool keep = p.h != nullptr && mine && r < rows;
                     float row_undo;
-                    finish_row<T, kRank>(reinterpret_cast<const float*>(smem + lay.sum), split, r, lay.sum_pitch, p.R,
-                                         p.scale == nullptr ? 1.0f : p.scale[adapter], kTerms, kManyRows * pitch,
-                                         keep ? p.h + static_cast<int64_t>(p.tiles.perm[start + r]) * p.R : nullptr, p.h_scaled != 0,
-                                         lane & 15,
-                                         [&](int at, uint32_t v) {
+                    finish_row<T, kRank, 8>(reinterpret_cast<const float*>(smem + lay.sum), split, r, lay.sum_pitch, p.R,
+                                            p.scale == nullptr ? 1.0f : p.scale[adapter], kTerms, kManyRows * pitch,
+                                            keep ? p.h + static_cast<int64_t>(to_row) * p.R : nullptr, p.h_scaled != 0,
+                                            lane & 7,
+                                            [&](int at, uint32_t v) {
+                                                if (!mine) return;
 #pragma unroll
-                                             for (int c = 0; c < kGroups; ++c) {
-                                                 if (c >= split) break;
-                                                 uint32_t there;
-                                                 asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(to + at), "r"(c));
-                                                 asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there), "r"(v) : "memory");
-                                             }
-                                         },
-                                         row_undo);
-                    if ((lane & 15) < split)
-                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(s_undo + r, lane & 15)), "f"(row_undo) : "memory");
+                                                for (int c = 0; c < kGroups; ++c) {
+                                                    if (c >= split) break;
+                                                    uint32_t there;
+                                                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(to + at), "r"(c));
+                                                    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there), "r"(v) : "memory");
+                                                }
+                                            },
+                                            row_undo);
+                    if (mine && (lane & 7) < split)
+                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(s_undo + r, lane & 7)), "f"(row_undo) : "memory");
                 }
                 asm volatile("fence.acq_rel.cluster;" ::: "memory");
                 consumer_barrier();
@@ -426,7 +436,7 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
                                 for (int kk = 0; kk < kRank / 16; ++kk) {
                                     if (16 * kk >= p.R) break;
                                     // the rows' terms again for each stage: held over them they took the registers of the rest
-                                    // (8191 rows of dx of rank 64 75 us instead of 62, 8192 x 4096 -> 4096 of rank 32 73 instead of 63)
+                                    // (8191 rows of dx of rank 64 75 us instead of 62, 8192 rows of dx of 4096 -> 4096 of rank 32 73 instead of 63)
                                     uint32_t h_of[kTerms][4];
 #pragma unroll
                                     for (int t = 0; t < kTerms; ++t) ldsm4(ha + t * kManyRows * pitch + 32 * kk, h_of[t]);
