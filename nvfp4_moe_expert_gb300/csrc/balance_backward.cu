@@ -2,7 +2,7 @@
 //
 // A CTA takes a stretch of rows; the g of the sequence it is in lie in shared memory, a row is read, turned into its gradient in
 // registers and written by 8, 16 or 32 lanes.  4096 x 128 FP32 4.5 us; 65537 x 250, sigmoid, in 37 sequences, a tenth of the tokens
-// masked, 32 us, 131 MB at 4.1 TB/s (65536 x 256 without masks 31, softmax 29): 357 warp instructions a row at 24 warps an SM, whose
+// masked, 32 us, 131 MB at 4.1 TB/s (65536 x 256 without masks 31, softmax 29): 350 warp instructions a row at 24 warps an SM, whose
 // latency the loads of one row ahead do not cover.  20000 x 1000 BF16 28 us with two CTAs to an SM, 38 with one.
 #include "balance.cuh"
 
