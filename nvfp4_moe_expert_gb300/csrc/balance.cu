@@ -1,20 +1,22 @@
 // The router's balance loss (balance.cuh says what is computed).
 //
-// Two ways to the sums of p and the counts of each sequence.  Few tokens: one cluster of 8 CTAs to a sequence, which join
-// their sums through shared memory: one launch, no workspace (128 x 128 4.7 us, a chain of latencies).  More: the rows in equal stretches to about three CTAs an SM,
+// Two ways to the sums of p and the counts of each sequence.  Few tokens: one cluster of 8 or 16 CTAs to a sequence, which join
+// their sums through shared memory: one launch, no workspace (128 x 128 4.7 us, 4096 x 128 BF16 14: a chain of latencies).  More: the rows in equal stretches to about three CTAs an SM,
 // whatever sequences they hold; where a sequence ends in a stretch, or the stretch does, the CTA writes what it has of the
 // sequence to slot (CTA + sequence) of the workspace, which no other pair shares, as each step of the walk moves one of
 // the two on.  A second kernel adds a sequence's slots in their order.  No float atomics: the same bits for the same call.
-// 65537 x 256 FP32, sigmoid, in 37 sequences take 22 + 6 us, 4096 x 128 BF16 3.9 + 7.  The rows' kernel is bound by instruction issue
+// 65537 x 256 FP32, sigmoid, in 37 sequences take 22 + 6 us.  The rows' kernel is bound by instruction issue
 // (72% of the slots, 257 warp instructions a row: an exponential, a quotient and a sum for each logit), 67 MB at 3.0 TB/s;
 // the second one by its start and three trips to memory.
+#include <atomic>
+
 #include "balance.cuh"
 
 namespace nvfp4 {
 namespace balance {
 namespace {
 
-constexpr int kSplit = 8;                 // CTAs of a cluster
+constexpr int kSplit = 8;                 // CTAs of a cluster; twice as many where there are few sequences
 
 // What a CTA holds of a sequence: sums of p (a lane's elements of its rows), counts in shared memory, tokens.
 template <int kPer>
@@ -112,19 +114,18 @@ __device__ __forceinline__ float loss_of(float sum, int n, int E, int k) {
 
 // ------------------------------------------------------------------ few tokens: a cluster to a sequence
 template <typename T, int kPer, int kLanes, int kN>
-__global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads)
-    sequence_kernel(const T* __restrict__ logits, const BalanceParams p, const Outputs out) {
+__global__ void __launch_bounds__(kThreads) sequence_kernel(const T* __restrict__ logits, const BalanceParams p, const Outputs out) {
     extern __shared__ float s_sum[];                        // [kWarps][E], then [E] counts
     __shared__ int s_tokens;
     __shared__ float s_loss, s_part[kWarps];
     const int E = p.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int* s_count = reinterpret_cast<int*>(s_sum + kWarps * E);
-    const uint32_t rank = cluster_rank();
-    const int64_t s = blockIdx.x / kSplit;
+    const int rank = static_cast<int>(cluster_rank()), split = static_cast<int>(cluster_size());
+    const int64_t s = blockIdx.x / split;
     int64_t begin, end;
     sequence_rows(p.offsets, s, p.T, begin, end);
-    const int64_t share = (end - begin + kSplit - 1) / kSplit;
-    begin = min(begin + static_cast<int64_t>(rank) * share, end);
+    const int64_t share = (end - begin + split - 1) / split;
+    begin = min(begin + rank * share, end);
     end = min(begin + share, end);
     for (int e = threadIdx.x; e < E; e += kThreads) s_count[e] = 0;
     if (threadIdx.x == 0) s_tokens = 0;
@@ -136,16 +137,16 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads)
     cluster_barrier();
 
     int n = 0;
-#pragma unroll
-    for (int c = 0; c < kSplit; ++c) n += cluster_load_s32(cluster_addr(&s_tokens, c));
-    const int part = (E + kSplit - 1) / kSplit;             // at most 128
-    const int e = static_cast<int>(rank) * part + static_cast<int>(threadIdx.x);
+#pragma unroll 8
+    for (int c = 0; c < split; ++c) n += cluster_load_s32(cluster_addr(&s_tokens, c));
+    const int part = (E + split - 1) / split;             // at most 128
+    const int e = rank * part + static_cast<int>(threadIdx.x);
     float term = 0.0f;
     if (static_cast<int>(threadIdx.x) < part && e < E) {
         int count = 0;
         float sum = 0.0f;
-#pragma unroll
-        for (int c = 0; c < kSplit; ++c) {
+#pragma unroll 8
+        for (int c = 0; c < split; ++c) {
             count += cluster_load_s32(cluster_addr(s_count + e, c));
             sum += cluster_load_f32(cluster_addr(s_sum + e, c));
         }
@@ -164,11 +165,40 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads)
     cluster_barrier();
     if (rank == 0 && threadIdx.x == 0) {
         float sum = 0.0f;
-        for (int c = 0; c < kSplit; ++c) sum += cluster_load_f32(cluster_addr(&s_loss, c));
+        for (int c = 0; c < split; ++c) sum += cluster_load_f32(cluster_addr(&s_loss, c));
         out.loss[s] = loss_of(sum, n, E, p.k);
         out.tokens[s] = n;
     }
     cluster_barrier();                                      // no CTA leaves while another reads its shared memory
+}
+
+// Launches a kernel in clusters of `split` CTAs; wide: the devices on which it may ask for more than 8.
+template <typename... P, typename... A>
+cudaError_t launch_clusters(void (*kernel)(P...), unsigned split, int64_t clusters, int threads, size_t smem, cudaStream_t st,
+                            std::atomic<uint64_t>& wide, A... args) {
+    if (split > 8) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        if (!(wide.load() >> dev & 1)) {
+            e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            wide.fetch_or(uint64_t(1) << dev);
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * split));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // ------------------------------------------------------------------ more: stretches of rows, then the slots
@@ -286,15 +316,18 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const BalanceParams 
     cluster_barrier();
 }
 
-// Whether a cluster to a sequence takes no longer than two kernels; with four sequences and more one of them is taken not to
-// have all the tokens.  us on the device from the first kernel's start, E = 128 in 8 lanes, BF16, a cluster and two kernels (a
-// second launch and a workspace take the host about 8 us longer):
+// Whether a cluster to a sequence takes no longer than two kernels, with the second launch and the workspace, which take the host
+// about 8 us.  us on the device from the first kernel's start, E = 128, BF16, a cluster and two kernels:
 //     tokens        512          1024          2048          4096          8192
-//     1 sequence    6.2 * 13     8.9 * 13      13 13 *       22 14 *       40 15 *
-//     4             5.7 * 9.4    5.4 * 9.4     6.8 * 9.6     9.1 * 10      14 11 *
+//     1 sequence    5.9 * 13     7.4 * 13      9.4 * 13      14 * 14       27 13 *
+//     4             6.3 * 9.4    6.3 * 9.4     6.5 * 9.6     8.0 * 10      14 11 *
 //     32            6.2 * 12     6.0 * 10      6.2 * 10      6.2 * 10      6.5 9.6 *
-// and 1 sequence with E = 256 8.7 * 8.7, 14 9.3 *, 23 10 *.  More than 32 clusters wait for each other (64: 11 us, two kernels 9).
-bool few(int64_t T, int E, int64_t S) { return S <= 32 && T * (E > 128 ? E : 128) <= (S >= 4 ? 4 : 1) * (int64_t(1) << 17); }
+// and 1 sequence with E = 256 7.5 * 8.7, 10 * 9.3, 15 * 10, 23 13 * (a call of 4096 x 128 20 us instead of 26).  More than 32 clusters
+// wait for each other (64: 11 us, two kernels 9).
+bool few(int64_t T, int E, int64_t S) { return S <= 32 && T * (E > 128 ? E : 128) <= int64_t(1) << 19; }
+// CTAs of such a cluster: 16 where there are few sequences and more than 512 rows of 128 experts (4096 x 128 14 us with 16, 22 with 8;
+// 128 x 128 6.2 and 5.1).
+unsigned split_of(int64_t T, int E, int64_t S) { return S < 8 && T * (E > 128 ? E : 128) > int64_t(1) << 16 ? 2 * kSplit : kSplit; }
 int rows_at_once(int E) { return E <= 128 ? 32 : E <= 256 ? 16 : 8; }   // of a CTA
 // Stretches: three to an SM, of whole turns of a CTA.
 int64_t stretch_rows(int64_t T, int E) {
@@ -319,9 +352,11 @@ cudaError_t forward(const void* logits, const BalanceParams& p, const Outputs& o
     return by_experts(p.E, [&](auto per, auto lanes) {
         return by_width<T>(load_width<T>(logits, p.ld, p.E), [&](auto width) {
             constexpr int kPer = decltype(per)::value, kLanes = decltype(lanes)::value, kN = decltype(width)::value;
-            if (few(p.T, p.E, p.S))
-                return launch_pdl(false, sequence_kernel<T, kPer, kLanes, kN>, dim3(static_cast<unsigned>(p.S * kSplit)),
-                                  dim3(kThreads), smem, st, l, p, out);
+            if (few(p.T, p.E, p.S)) {
+                static std::atomic<uint64_t> wide{0};
+                return launch_clusters(sequence_kernel<T, kPer, kLanes, kN>, split_of(p.T, p.E, p.S), p.S, kThreads, smem, st,
+                                       wide, l, p, out);
+            }
             const Slots w = slots(ws, p.T, p.E, p.S);
             return launch_pdl(false, stretch_kernel<T, kPer, kLanes, kN>, dim3(static_cast<unsigned>(stretches(p.T, p.E))),
                               dim3(kThreads), smem, st, l, p, w);

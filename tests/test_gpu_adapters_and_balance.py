@@ -47,7 +47,7 @@ def everything(d, cut, k, adapters):
     return [*b, dl, out, h, M.lora_add(d["y"], d["x"], adapters, d["who"]), *M.lora_add_backward(d["dy"], d["x"], h, adapters, d["who"])]
 
 
-SIZES = [(9, 64, 4, 256, 130, 16, 3), (300, 128, 8, 520, 96, 24, 5), (3000, 64, 6, 1032, 264, 16, 4), (2500, 40, 4, 256, 203, 64, 3)]
+SIZES = [(9, 64, 4, 256, 130, 16, 3), (300, 128, 8, 520, 96, 24, 5), (3000, 64, 6, 1032, 264, 16, 4), (2500, 40, 4, 256, 203, 64, 3), (9000, 130, 6, 128, 72, 128, 4)]
 
 
 @pytest.mark.parametrize("size", SIZES)

@@ -109,7 +109,8 @@ def test_many_rows_and_sequences(T, S):
     assert M.nvfp4_get_device_error() == 0
 
 
-@pytest.mark.parametrize("T,E,S", [(1024, 128, 1), (1025, 128, 1), (512, 256, 3), (513, 256, 3), (4096, 64, 4), (4097, 64, 4),
+@pytest.mark.parametrize("T,E,S", [(1024, 128, 1), (1025, 128, 1), (512, 256, 3), (513, 256, 3), (4096, 64, 4), (4097, 64, 4), (512, 128, 1),
+                                   (513, 128, 7), (513, 128, 8), (4096, 128, 1), (4097, 128, 1), (512, 1000, 2), (525, 1000, 2),
                                    (2048, 256, 5), (900, 64, 64), (900, 64, 65), (4100, 96, 19), (4100, 96, 20),
                                    (4100, 96, 38), (4100, 96, 39), (4100, 96, 76), (4100, 96, 77), (3000, 96, 152), (3000, 96, 153)])
 def test_where_the_ways_meet(T, E, S):
