@@ -7,8 +7,11 @@
 // together in tiles of 16 or 128 rows; a cluster of CTAs takes a tile, each CTA its share of C, then its share of D.
 //
 // The order of the sum over C goes by C alone, so a token's row does not depend on the batch: C is cut into 8 groups of 8
-// sub-slices of 16 ceil(C / 1024) columns; a sub-slice is one chain of m16n8k16 products from zero, the sub-slices of a group
-// are added in order, the groups as a binary tree (which clusters of 2, 4 and 8 CTAs can share).  mma.sync serves this
+// sub-slices of 16 ceil(C / 1024) columns, from 32768 columns on of twice, three times, ... as many of no more than 512; a
+// sub-slice is one chain of m16n8k16 products from zero, the sub-slices of a group
+// are added in order, the groups as a binary tree (which clusters of 2, 4 and 8 CTAs can share).  The tensor cores cut an
+// accumulator's low bits off at each step: h of values of one sign is 8e-7 low after chains of 32 steps (32768 columns), and was
+// 8e-5 low with chains of 1024 (2^20 columns).  mma.sync serves this
 // better than tcgen05: a tile has as few as one real row and 8 to 128 columns of accumulator, the two products together
 // have 2 R operations to a byte that is moved, and accumulators in registers need no pass through TMEM between the two
 // products (its rate, 600 TFLOP/s measured, is enough for R <= 64 at the memory's rate).
@@ -128,8 +131,10 @@ __host__ __device__ constexpr int rank_bytes(int R) { return R <= 16 ? 32 : R <=
 __host__ __device__ constexpr int padded_pitch(int R) { return 2 * R + 16; }
 __host__ __device__ constexpr int rank_up(int R) { return (R + 15) / 16 * 16; }   // the second product's steps are 16 wide
 
-// Sub-slices of the first product: 64 of them, of as many steps of 16 columns.
-__host__ __device__ inline int sub_steps(int C) { return (C + 1023) / 1024; }
+// Sub-slices of the first product: 64 to a round, of as many steps of 16 columns, at most kChainSteps.
+constexpr int kChainSteps = 32;
+__host__ __device__ inline int sub_rounds(int C) { return (C + 1024 * kChainSteps - 1) / (1024 * kChainSteps); }
+__host__ __device__ inline int sub_steps(int C) { return (C + 1024 * sub_rounds(C) - 1) / (1024 * sub_rounds(C)); }
 
 // 16 bytes of a row from 16-bit unit c on (zeros from `units` on) into shared memory.  Rows that do not start on a 16-byte
 // boundary are read in the aligned 16-byte words that hold a unit of theirs, two of them shifted together, in place of eight

@@ -9,6 +9,8 @@
 // adapter out of L2 again: from some hundred rows of an adapter on tiles of 128 take less (few_rows).
 #pragma once
 
+#include <algorithm>
+
 #include "lora_launch.cuh"
 
 namespace nvfp4 {
@@ -85,7 +87,8 @@ __device__ __forceinline__ bool find_tile(const int32_t* ids, int T, int L, int 
     return true;
 }
 
-template <typename T, bool kTrans, int kRank>
+// kRounds: C has more than one round of sub-slices (with a loop over them the kernels of fewer columns took up to 39 registers more).
+template <typename T, bool kTrans, int kRank, bool kRounds>
 __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(kThreads) few_kernel(const Params p, const int terms) {
     constexpr int kTiles = kRank / 8;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -127,68 +130,80 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(kThreads) few_
 
     if (adapter >= 0) {
         const uint16_t* down = static_cast<const uint16_t*>(p.down) + static_cast<int64_t>(adapter) * p.C * p.R;
-        const int steps = sub_steps(p.C), sub = rank * kWarps + warp;
-        const int c0 = sub * steps * 16, c1 = min(c0 + steps * 16, p.C);
+        const int steps = sub_steps(p.C), rounds = kRounds ? sub_rounds(p.C) : 1;
         uint8_t* my = smem + warp * (lay.x + lay.down);
         const uint32_t sx = smem_u32(my), sd = sx + lay.x;
-        float acc[kTiles][4];
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-        }
-        const auto load_piece = [&](int c) {
-            const int cols = min(lay.cols, (c1 - c + 15) / 16 * 16);
-            load_down<kTrans>(sd, down, p.R, p.C, c, cols, lane, 32);
-            const int chunk = lane & 7;
-            if (8 * chunk < cols) {
-                for (int r = lane >> 3; r < rows; r += 4)
-                    copy_chunk(sx + swizzled(r, chunk), static_cast<const uint16_t*>(p.x) + s_row[r] * p.ldx, c + 8 * chunk, p.C, p.x_wide);
-            }
-        };
-        if (c0 < c1) load_piece(c0);
-        cp_commit();
-        for (int b = 0; b < lay.buffers; ++b) {
-            if (first_group + 8 * b < last_group)
-                load_up<kTrans>(my_up + b * lay.up, up, p.R, p.D, 32 * (first_group + 8 * b), 32, lane, 32);
-            cp_commit();
-        }
-        if (first_group < last_group) load_y(first_group);
-        if (lay.buffers == 2) cp_wait<2>();
-        else cp_wait<1>();
-        __syncwarp();
-        for (int c = c0; c < c1; c += lay.cols) {
-            if (c > c0) {
-                __syncwarp();
-                load_piece(c);
-                cp_commit();
-                cp_wait<0>();
-                __syncwarp();
-            }
-            const int n = min(lay.cols, c1 - c);
-            for (int kk = 0; 16 * kk < n; ++kk) {
-                uint32_t a[4];
-                ldsm4((sx + lane_rows(lane)) ^ (kk << 5), a);
-                multiply_down<T, kTrans, kTiles>(acc, a, sd + lane_down<kTrans>(lane, p.R), kk, p.R);
-            }
-        }
-        __syncthreads();                                    // every warp's loads are used up
-        float* part = reinterpret_cast<float*>(smem + lay.part) + warp * kFewRows * p.R;
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-            if (8 * j >= p.R) break;
-            float* at = part + quad * p.R + 8 * j + 2 * (lane & 3);
-            *reinterpret_cast<float2*>(at) = make_float2(acc[j][0], acc[j][1]);
-            *reinterpret_cast<float2*>(at + 8 * p.R) = make_float2(acc[j][2], acc[j][3]);
-        }
-        __syncthreads();
         float* sum = reinterpret_cast<float*>(smem + lay.sum);
-        for (int i = threadIdx.x; i < kFewRows * p.R; i += kThreads) {
-            const float* from = reinterpret_cast<const float*>(smem + lay.part) + i;
-            float v = from[0];
+        float mine[kRank / 16];           // of the CTA's sums, while there are rounds
+        for (int round = 0; round < rounds; ++round) {
+            const int c0 = ((rank * rounds + round) * kWarps + warp) * steps * 16, c1 = min(c0 + steps * 16, p.C);
+            float acc[kTiles][4];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) v += from[w * kFewRows * p.R];
-            sum[i] = v;
+            for (int j = 0; j < kTiles; ++j) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+            }
+            const auto load_piece = [&](int c) {
+                const int cols = min(lay.cols, (c1 - c + 15) / 16 * 16);
+                load_down<kTrans>(sd, down, p.R, p.C, c, cols, lane, 32);
+                const int chunk = lane & 7;
+                if (8 * chunk < cols) {
+                    for (int r = lane >> 3; r < rows; r += 4)
+                        copy_chunk(sx + swizzled(r, chunk), static_cast<const uint16_t*>(p.x) + s_row[r] * p.ldx, c + 8 * chunk, p.C, p.x_wide);
+                }
+            };
+            if (c0 < c1) load_piece(c0);
+            cp_commit();
+            if (round == 0) {
+                for (int b = 0; b < lay.buffers; ++b) {
+                    if (first_group + 8 * b < last_group)
+                        load_up<kTrans>(my_up + b * lay.up, up, p.R, p.D, 32 * (first_group + 8 * b), 32, lane, 32);
+                    cp_commit();
+                }
+                if (first_group < last_group) load_y(first_group);
+                if (lay.buffers == 2) cp_wait<2>();
+                else cp_wait<1>();
+            } else {
+                cp_wait<0>();
+            }
+            __syncwarp();
+            for (int c = c0; c < c1; c += lay.cols) {
+                if (c > c0) {
+                    __syncwarp();
+                    load_piece(c);
+                    cp_commit();
+                    cp_wait<0>();
+                    __syncwarp();
+                }
+                const int n = min(lay.cols, c1 - c);
+                for (int kk = 0; 16 * kk < n; ++kk) {
+                    uint32_t a[4];
+                    ldsm4((sx + lane_rows(lane)) ^ (kk << 5), a);
+                    multiply_down<T, kTrans, kTiles>(acc, a, sd + lane_down<kTrans>(lane, p.R), kk, p.R);
+                }
+            }
+            __syncthreads();                                // every warp's loads are used up
+            float* part = reinterpret_cast<float*>(smem + lay.part) + warp * kFewRows * p.R;
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+                if (8 * j >= p.R) break;
+                float* at = part + quad * p.R + 8 * j + 2 * (lane & 3);
+                *reinterpret_cast<float2*>(at) = make_float2(acc[j][0], acc[j][1]);
+                *reinterpret_cast<float2*>(at + 8 * p.R) = make_float2(acc[j][2], acc[j][3]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kRank / 16; ++j) {
+                const int i = threadIdx.x + kThreads * j;
+                if (i >= kFewRows * p.R) break;
+                const float* from = reinterpret_cast<const float*>(smem + lay.part) + i;
+                float v = round > 0 ? mine[j] + from[0] : from[0];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) v += from[w * kFewRows * p.R];
+                mine[j] = v;
+                if (round + 1 == rounds) sum[i] = v;
+            }
+            if (round + 1 < rounds) __syncthreads();        // the next round's loads lie over the parts
         }
         cluster_barrier();
         const int row = 2 * warp + (lane >> 4), pitch = padded_pitch(rank_up(p.R));
@@ -244,15 +259,18 @@ template <typename T, bool kTrans>
 cudaError_t launch_few(const Params& p, int64_t tiles, bool pdl, cudaStream_t st) {
     const int terms = terms_of<T>(p.y_type);
     const FewLayout<kTrans> lay(p.R, terms);
-    return by_rank(p.R, [&](auto rank) {
-        constexpr int kRank = decltype(rank)::value;
+    const auto launch = [&](auto rank, auto rounds, int shared) {
         static Ready ready;
-        auto* kernel = few_kernel<T, kTrans, kRank>;
-        const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), FewLayout<kTrans>(kRank, 3).total, ready);
+        auto* kernel = few_kernel<T, kTrans, decltype(rank)::value, decltype(rounds)::value>;
+        const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), shared, ready);
         if (e != cudaSuccess) return e;
         return launch_pdl(pdl, kernel, dim3(static_cast<unsigned>(tiles * kGroups)), dim3(kThreads), static_cast<size_t>(lay.total), st,
                           p, terms);
-    });
+    };
+    if (sub_rounds(p.C) > 1)              // of any rank; up to 64 some layouts are larger
+        return launch(std::integral_constant<int, 128>(), std::true_type(),
+                      std::max(FewLayout<kTrans>(64, 3).total, FewLayout<kTrans>(128, 3).total));
+    return by_rank(p.R, [&](auto rank) { return launch(rank, std::false_type(), FewLayout<kTrans>(decltype(rank)::value, 3).total); });
 }
 
 }  // namespace lora

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
     const uint32_t base = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_rank()), split = static_cast<int>(cluster_size());
-    const int groups = kGroups / split, steps = sub_steps(p.C), group_cols = kWarps * steps * 16;   // a multiple of 64
+    const int groups = kGroups / split, steps = sub_steps(p.C), group_cols = kWarps * sub_rounds(p.C) * steps * 16;   // a multiple of 64
     const int c0 = min(rank * groups * group_cols, p.C), c1 = min(c0 + groups * group_cols, p.C);
     const int chunks = (p.D + kCols - 1) / kCols, per_cta = (chunks + split - 1) / split;
     const int chunk0 = min(rank * per_cta, chunks), chunk1 = min(chunk0 + per_cta, chunks);
