@@ -271,13 +271,14 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j][i] = total[j][i] = 0.0f;
                 }
-                // sums of the groups, a pair's in one place (the sums'), the other pair's in another, h's.  Warps are only held
-                // together by the ring, and sums2's rows lie over other warps' h: the barrier in front of the first write has all of
-                // them out of the second product of the tile in front (16384 x 4096 -> 4096 of rank 16 took as long without it)
+                // sums of the groups, a pair's in one place (the sums'), the other pair's in another, h's.  Only the ring holds the warps
+                // together, and sums2's rows lie over other warps' h: all of them are to be behind the second product of the tile in
+                // front (16384 x 4096 -> 4096 of rank 16 took as long without the barrier; with one where sums2 is first written, in
+                // the loop, rank 96 to FP32 on odd rows spilled and took 195 us instead of 174)
+                consumer_barrier();
                 float* const sums = reinterpret_cast<float*>(smem + lay.sum) + my_row * lay.sum_pitch + 2 * (lane & 3);
                 float* const sums2 = sums + (lay.h - lay.sum) / 4;
                 const auto close_group = [&](int group) {
-                    if (group == 2) consumer_barrier();
                     float* const to = group & 2 ? sums2 : sums;
 #pragma unroll
                     for (int j = 0; j < kTiles; ++j) {
