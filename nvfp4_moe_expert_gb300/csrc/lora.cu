@@ -300,7 +300,6 @@ cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t st) {
     Params p = {};
     p.x = a.x;
     p.ldx = a.ldx;
-    p.x_wide = 1;
     p.down = a.down;
     p.up = a.up;
     p.scale = a.scale;
@@ -311,7 +310,8 @@ cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t st) {
     p.ldy = a.ldy;
     p.ldo = a.ldo;
     p.y_type = a.y_type;
-    p.out_wide = wide(a.y, a.ldy, a.y_type) && wide(a.out, a.ldo, a.y_type);
+    p.y_wide = wide(a.y, a.ldy, a.y_type);
+    p.out_wide = wide(a.out, a.ldo, a.y_type);
     p.skip_none = a.y == a.out && a.h == nullptr;
     p.T = static_cast<int>(a.T);
     p.L = a.L;
@@ -351,7 +351,6 @@ cudaError_t launch_lora_add_backward(const LoraBackwardArgs& a, cudaStream_t st)
         p.x = dy;
         p.ldx = lay.lddy;
     }
-    p.x_wide = 1;
     p.down = a.up;                        // dh = s dy B: B is [N][R]
     p.up = a.down;                        // dx = dh A: A is [R][K]
     p.scale = a.scale;
@@ -361,7 +360,7 @@ cudaError_t launch_lora_add_backward(const LoraBackwardArgs& a, cudaStream_t st)
     p.h = dh;
     p.ldy = p.ldo = a.lddx;
     p.y_type = a.dx_type;
-    p.out_wide = wide(a.dx, a.lddx, a.dx_type);
+    p.y_wide = p.out_wide = wide(a.dx, a.lddx, a.dx_type);
     p.h_scaled = 1;
     p.skip_none = a.accumulate;           // nobody reads the dh of rows without an adapter
     p.T = static_cast<int>(a.T);

@@ -46,9 +46,8 @@ struct Tiles {
 };
 
 struct Params {
-    const void* x;              // [T][ldx], C columns
+    const void* x;              // [T][ldx], C columns; rows on 16-byte boundaries
     int64_t ldx;
-    int x_wide;                 // rows start on 16-byte boundaries
     const void* down;           // what x is multiplied with: [L][R][C], or [L][C][R] (transposed)
     const void* up;             // and h: [L][D][R], or [L][R][D] (transposed)
     const float* scale;         // [L] or nullptr
@@ -57,7 +56,7 @@ struct Params {
     void* out;                  // [T][ldo]
     float* h;                   // [T][R] or nullptr
     int64_t ldy, ldo;
-    int y_type, out_wide;       // out_wide: y's and out's rows start on 16-byte boundaries
+    int y_type, y_wide, out_wide;   // y's, and out's rows start on 16-byte boundaries
     int h_scaled;               // h holds s_a h
     int skip_none;              // rows without an adapter need no work
     int T, L, R, C, D;
@@ -174,15 +173,10 @@ struct Straddle {
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
     }
 };
-__device__ __forceinline__ void copy_chunk(uint32_t dst, const uint16_t* row, int c, int units, bool wide) {
-    if (wide) {
-        const int left = min(max(units - c, 0), 8);
-        cp_async16(dst, left ? row + c : row, 2 * left);
-    } else {
-        Straddle s;
-        s.load(row, c, units);
-        s.store(dst);
-    }
+// The same of rows that do start on one.
+__device__ __forceinline__ void copy_chunk(uint32_t dst, const uint16_t* row, int c, int units) {
+    const int left = min(max(units - c, 0), 8);
+    cp_async16(dst, left ? row + c : row, 2 * left);
 }
 // Operand of the first product: `cols` (a multiple of 16, at most 64) columns from c on of the adapter's matrix.
 template <bool kTrans>
@@ -191,7 +185,7 @@ __device__ __forceinline__ void load_down(uint32_t dst, const uint16_t* down, in
         const int q = thread & 7;
         if (8 * q < cols) {
             for (int r = thread >> 3; r < R; r += threads >> 3)
-                copy_chunk(dst + swizzled(r, q), down + static_cast<int64_t>(r) * C, c + 8 * q, C, true);
+                copy_chunk(dst + swizzled(r, q), down + static_cast<int64_t>(r) * C, c + 8 * q, C);
         }
     } else {                              // [C][R]: rows of R columns, padded
         const int per = R / 8, at_once = threads / per, n0 = thread / per, q = thread - n0 * per;
@@ -254,7 +248,7 @@ __device__ __forceinline__ void load_up(uint32_t dst, const uint16_t* up, int R,
         const int q = thread & 7;
         if (8 * q < cols) {
             for (int r = thread >> 3; r < Rp; r += threads >> 3) {
-                if (r < R) copy_chunk(dst + swizzled(r, q), up + static_cast<int64_t>(r) * D, n + 8 * q, D, true);
+                if (r < R) copy_chunk(dst + swizzled(r, q), up + static_cast<int64_t>(r) * D, n + 8 * q, D);
                 else cp_async16(dst + swizzled(r, q), up, 0);
             }
         }

@@ -123,7 +123,7 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(kThreads) few_
     const auto load_y = [&](int g) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (p.y != nullptr && row_of[i] >= 0) y[i] = load_eight(p.y, p.y_type, row_of[i], p.ldy, 32 * g + 8 * (lane & 3), p.D, p.out_wide);
+            if (p.y != nullptr && row_of[i] >= 0) y[i] = load_eight(p.y, p.y_type, row_of[i], p.ldy, 32 * g + 8 * (lane & 3), p.D, p.y_wide);
         }
     };
     float undo[2] = {1.0f, 1.0f};
@@ -149,7 +149,7 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(kThreads) few_
                 const int chunk = lane & 7;
                 if (8 * chunk < cols) {
                     for (int r = lane >> 3; r < rows; r += 4)
-                        copy_chunk(sx + swizzled(r, chunk), static_cast<const uint16_t*>(p.x) + s_row[r] * p.ldx, c + 8 * chunk, p.C, p.x_wide);
+                        copy_chunk(sx + swizzled(r, chunk), static_cast<const uint16_t*>(p.x) + s_row[r] * p.ldx, c + 8 * chunk, p.C);
                 }
             };
             if (c0 < c1) load_piece(c0);

@@ -6,8 +6,8 @@
 // CTAs' sums meet in shared memory over the cluster, each CTA adding its share of the rows and handing their terms to all; products of the
 // second phase are added to y where it lies in shared memory, which goes out from there in whole rows of 128 bytes.
 //
-// x and y come by TMA, 16 rows to an instruction where they lie in a row, four rows of any place otherwise, where
-// rows start on 16-byte boundaries; otherwise four loader warps read aligned words and shift them together, a stage's on
+// x and y come by TMA, 16 rows to an instruction where they lie in a row, four rows of any place otherwise.  Where rows of y
+// start on no 16-byte boundary four loader warps read aligned words of them and shift those together, a stage's on
 // their way while the last one's are put in place.  (With the loads
 // and the products in the same warps, cp.async and a barrier for each stage, 16384 x 4096 -> 4096 of rank 16 took 145 to 199 us:
 // 500 instructions a stage and warp, half of them addresses.)
@@ -101,7 +101,8 @@ __device__ __forceinline__ void store_unaligned(uint8_t* to, const uint4& v, int
     }
 }
 
-// kLoaders: warps that load, 1 (x and y by TMA) or 4.  kType: y's and out's (branches by it for every value took 3000 cycles a stage).
+// kLoaders: warps that load, 1 (where rows of y and out start on 16-byte boundaries: all by TMA) or 4 (y by shifted words).
+// kType: y's and out's (branches by it for every value took 3000 cycles a stage).
 template <typename T, bool kTrans, int kType, int kRank, int kLoaders>
 __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoaders == 1 ? 2 : 1)
     many_kernel(const __grid_constant__ ManyMaps maps, const Params p, const ManyLayout lay) {
@@ -155,7 +156,6 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
     if (warp >= kWarps) {
         // ------------------------------------------------------------ loaders
         const int thread = threadIdx.x - kThreads;
-        const bool x_tma = kLoaders == 1 || p.x_wide, y_tma = kLoaders == 1 || p.out_wide;
         int issued = 0;
         for (int q = blockIdx.x / split; q < count; q += gridDim.x / split) {
             const int adapter = p.tiles.adapter[q], start = p.tiles.start[q];
@@ -175,16 +175,15 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
             const bool group = 16 * (lane >> 2) < rows && warp == kWarps && (!box || (lane & 3) == 0);
             constexpr int kMine = kLoaders == 1 ? 1 : 8;
             int row[kMine];
-            Straddle words[kMine];                              // of the next stage that is not TMA's
+            Straddle words[kMine];                              // of y's next stage
             const auto fetch = [&](int s) {
-                const bool is_x = s < x_stages;
-                if (s >= all || (is_x ? x_tma : y_tma || p.y == nullptr)) return;
-                const uint16_t* from = static_cast<const uint16_t*>(is_x ? p.x : p.y);
-                const int64_t ld = is_x ? p.ldx : p.ldy * kUnits;
-                const int unit = (is_x ? c0 + 64 * s : (chunk0 + s - x_stages) * kCols * kUnits) + 8 * (thread & 7);
+                if (s < x_stages || s >= all || p.y == nullptr) return;
+                const uint16_t* from = static_cast<const uint16_t*>(p.y);
+                const int64_t ld = p.ldy * kUnits;
+                const int unit = (chunk0 + s - x_stages) * kCols * kUnits + 8 * (thread & 7);
 #pragma unroll
                 for (int i = 0; i < kMine; ++i) {
-                    if (row[i] >= 0) words[i].load(from + row[i] * ld, unit, is_x ? p.C : p.D * kUnits);
+                    if (row[i] >= 0) words[i].load(from + row[i] * ld, unit, p.D * kUnits);
                 }
             };
             if (kLoaders > 1) {
@@ -199,7 +198,7 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
                 if (!mbar_wait_bounded(&empty[buffer], phase ^ 1u, abort_flag, kWaitBudgetCycles)) failed = true;
                 if (__any_sync(kAll, failed)) break;
                 const uint32_t at = base + buffer * lay.stage, part = at + kManyRows * 128, bar = smem_u32(&full[buffer]);
-                const bool is_x = s < x_stages, tma = is_x ? x_tma : y_tma, none = !is_x && p.y == nullptr;
+                const bool is_x = s < x_stages, tma = is_x || kLoaders == 1, none = !is_x && p.y == nullptr;
                 const int c = is_x ? c0 + 64 * s : (chunk0 + s - x_stages) * kCols;
                 if (kLoaders > 1) fence_proxy_async_shared();
                 if (thread == 0) {
@@ -224,10 +223,8 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
                         for (int i = 0; i < kMine; ++i) {
                             if (row[i] >= 0) words[i].store(at + swizzled((thread >> 3) + 16 * i, thread & 7));
                         }
-                        fetch(s + 1);
-                    } else {
-                        fetch(s + 1);
                     }
+                    fetch(s + 1);
                     if (thread != 0) mbar_arrive(&full[buffer]);
                 }
                 next_buffer();
@@ -543,25 +540,22 @@ template <typename T, bool kTrans, int kType>
 cudaError_t launch_many(const Params& p, int64_t tiles, bool pdl, cudaStream_t st) {
     const int units = kType == NVFP4_TYPE_F32 ? 2 : 1, Rp = rank_up(p.R);
     const ManyLayout lay(p.R, terms_of<T>(kType), kTrans, kType);
-    const bool tma_y = p.y != nullptr && p.out_wide;
     ManyMaps maps;
     const int rank_row = rank_bytes(p.R);
     bool ok = kTrans ? make_units_map(&maps.down, p.down, p.R, p.C, p.R, p.L, static_cast<int64_t>(p.C) * p.R, 64, rank_row)
                      : make_units_map(&maps.down, p.down, p.C, p.R, p.C, p.L, static_cast<int64_t>(p.C) * p.R, Rp);
     ok = ok && (kTrans ? make_units_map(&maps.up, p.up, p.D, p.R, p.D, p.L, static_cast<int64_t>(p.D) * p.R, Rp)
                        : make_units_map(&maps.up, p.up, p.R, p.D, p.R, p.L, static_cast<int64_t>(p.D) * p.R, lay.cols, rank_row));
-    maps.x = maps.y = maps.x16 = maps.y16 = maps.up;        // what is not used is another's
-    if (ok && p.x_wide)
-        ok = make_units_map(&maps.x, p.x, p.C, p.T, p.ldx, 0, 0, 1) && make_units_map(&maps.x16, p.x, p.C, p.T, p.ldx, 0, 0, 16);
+    maps.y = maps.y16 = maps.up;        // what is not used is another's
+    ok = ok && make_units_map(&maps.x, p.x, p.C, p.T, p.ldx, 0, 0, 1) && make_units_map(&maps.x16, p.x, p.C, p.T, p.ldx, 0, 0, 16);
     const int64_t row = static_cast<int64_t>(p.D) * units;
-    if (ok && tma_y)
+    if (ok && p.y != nullptr && p.y_wide)
         ok = make_units_map(&maps.y, p.y, row, p.T, p.ldy * units, 0, 0, 1) && make_units_map(&maps.y16, p.y, row, p.T, p.ldy * units, 0, 0, 16);
     if (!ok) return cudaErrorInvalidValue;
-    const bool one = p.x_wide && p.out_wide;
     return by_rank(p.R, [&](auto rank) {
         constexpr int kRank = decltype(rank)::value;
-        return one ? launch_many_kernel<T, kTrans, kType, kRank, 1>(maps, p, lay, tiles, pdl, st)
-                   : launch_many_kernel<T, kTrans, kType, kRank, 4>(maps, p, lay, tiles, pdl, st);
+        return p.y_wide && p.out_wide ? launch_many_kernel<T, kTrans, kType, kRank, 1>(maps, p, lay, tiles, pdl, st)
+                                      : launch_many_kernel<T, kTrans, kType, kRank, 4>(maps, p, lay, tiles, pdl, st);
     });
 }
 
