@@ -527,7 +527,8 @@ nvfp4_status moe_route_topk_backward(const void* logits_dev, int type, int64_t T
  *  logits_dev       [T][ld] of `type`, the first E of each row used; element aligned; 0 <= T < 2^31 - 256,
  *                   1 <= E <= 1024, ld >= E
  *  score            MOE_SCORE_*
- *  topk_ids_dev     int32 [T][k], 1 <= k <= min(E, 32)
+ *  topk_ids_dev     int32 [T][k], 1 <= k <= min(E, 32); an id that stands twice in a token counts twice (the counts are
+ *                   32-bit: 2^31 slots of one expert, which take a token with repeated ids, do not fit)
  *  mask_dev         uint8 [T], or NULL (every token counts); a masked token's logits and ids are not read
  *  seq_offsets_dev  int32 [S + 1], ascending, inside [0, T]: sequence s has the rows [offset s, offset s + 1);
  *                   rows in front of the first and behind the last belong to none.  NULL: S = 1, all rows
@@ -615,8 +616,10 @@ nvfp4_status mxfp4_linear(const fp4_linear_weights* w, const void* x_dev, int x_
  *   h_t = A_a x_t,   out_t = y_t + scale_a B_a h_t,   a = adapter_ids[t]; out_t = y_t where a is negative
  * The products accumulate in FP32, h stays FP32 between them (held as sums of 16-bit terms, which give NaN
  * beside an infinite factor; the same for h and dh in the gradients), y is added in FP32 and the sum is
- * rounded once to the outputs' type.  K is summed in an order that goes by K alone: a token's row does not
- * depend on T, on the other tokens or on their order. */
+ * rounded once to the outputs' type.  K is summed in an order that goes by K alone, in chains of at most 512
+ * columns on the tensor cores: a token's row does not depend on T, on the other tokens or on their order.
+ * How many tokens share a read of their adapter goes by T and L, every adapter taken to be in use; BF16
+ * adapters of rank 120 and 128 with FP32 outputs (or dx) are read for every 16 tokens. */
 typedef struct {
     const void* down;     /* A: [L][R][K] of `type`, 16-byte aligned */
     const void* up;       /* B: [L][N][R] of `type`, 16-byte aligned */
@@ -633,7 +636,7 @@ typedef struct {
  *                   out may be y itself (the same pointer and pitch; rows without an adapter stay as they are); otherwise
  *                   its rows share no byte with y's, and never one with x's (NVFP4_ERR_INVALID_ARG)
  *  h_dev            float [T][R] out, 16-byte aligned, or NULL: h (zeros where there is no adapter), what
- *                   lora_add_backward takes
+ *                   lora_add_backward takes (of BF16 adapters; FP16 ones have no gradient here)
  *  ws_dev           lora_add_workspace_bytes(T, L) bytes, 256-byte aligned; NULL where that is 0 (few tokens)
  * Device error: NVFP4_ERR_BAD_EXPERT_ID (an adapter id of L or more; its row is as without an adapter). */
 size_t lora_add_workspace_bytes(int64_t T, int L);

@@ -859,7 +859,7 @@ def lora_add(y, x, adapters, adapter_ids, out=None, save_for_backward=False, str
     low-rank adapters of many requests beside a shared projection's outputs y [T, N] (float32, bfloat16 or
     float16), x [T, K] of the adapters' type, rows on 16-byte boundaries.  Returns out (of y's type;
     out=y adds in place), and with save_for_backward h float32 [T, R] beside it, which
-    lora_add_backward takes.  A row does not depend on the others."""
+    lora_add_backward takes (of bfloat16 adapters only).  A row does not depend on the others."""
     _, T, K, ldx = _rows("x", x, _HALVES)
     device = x.device
     if x.dtype != adapters.dtype or K != adapters.K or device != adapters.device:

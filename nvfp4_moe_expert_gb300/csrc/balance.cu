@@ -1,7 +1,7 @@
 // The router's balance loss (balance.cuh says what is computed).
 //
 // Two ways to the sums of p and the counts of each sequence.  Few tokens: one cluster of 8 or 16 CTAs to a sequence, which join
-// their sums through shared memory: one launch, no workspace (128 x 128 4.7 us, 4096 x 128 BF16 14: a chain of latencies).  More: the rows in equal stretches to about three CTAs an SM,
+// their sums through shared memory: one launch, no workspace (128 x 128 5.5 us, 4096 x 128 BF16 14: a chain of latencies).  More: the rows in equal stretches to about three CTAs an SM,
 // whatever sequences they hold; where a sequence ends in a stretch, or the stretch does, the CTA writes what it has of the
 // sequence to slot (CTA + sequence) of the workspace, which no other pair shares, as each step of the walk moves one of
 // the two on.  A second kernel adds a sequence's slots in their order.  No float atomics: the same bits for the same call.
@@ -322,11 +322,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const BalanceParams 
 //     1 sequence    5.9 * 13     7.4 * 13      9.4 * 13      14 * 14       27 13 *
 //     4             6.3 * 9.4    6.3 * 9.4     6.5 * 9.6     8.0 * 10      14 11 *
 //     32            6.2 * 12     6.0 * 10      6.2 * 10      6.2 * 10      6.5 9.6 *
-// and 1 sequence with E = 256 7.5 * 8.7, 10 * 9.3, 15 * 10, 23 13 * (a call of 4096 x 128 20 us instead of 26).  More than 32 clusters
-// wait for each other (64: 11 us, two kernels 9).
+// and 1 sequence with E = 256 7.5 * 8.7, 10 * 9.3, 15 * 10, 23 13 * (a call of 4096 x 128 20 us instead of 26; behind queued work or
+// in a graph, where the host's part does not count, two kernels would be sooner where their figure above is the lower one).  The host does
+// not know the lengths: they are taken to be even.  More than 32 clusters wait for each other (64: 11 us, two kernels 9).
 bool few(int64_t T, int E, int64_t S) { return S <= 32 && T * (E > 128 ? E : 128) <= int64_t(1) << 19; }
 // CTAs of such a cluster: 16 where there are few sequences and more than 512 rows of 128 experts (4096 x 128 14 us with 16, 22 with 8;
-// 128 x 128 6.2 and 5.1).
+// 128 x 128 a microsecond more with 16).
 unsigned split_of(int64_t T, int E, int64_t S) { return S < 8 && T * (E > 128 ? E : 128) > int64_t(1) << 16 ? 2 * kSplit : kSplit; }
 int rows_at_once(int E) { return E <= 128 ? 32 : E <= 256 ? 16 : 8; }   // of a CTA
 // Stretches: three to an SM, of whole turns of a CTA.

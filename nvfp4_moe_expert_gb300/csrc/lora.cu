@@ -248,7 +248,10 @@ bool wide(const void* p, int64_t ld, int type) {
 }
 
 // Whether tiles of 16 rows take less time than tiles of 128: 6 us and a time for each of the one, a longer start and a time for
-// each of the other, both with the columns.  Each adapter is taken to have tokens, its last tile half full on average.  us of
+// each of the other, both with the columns.  The host does not know the ids: each adapter is taken to have tokens, its last tile half full on
+// average, so a batch of 12 requests is slower beside a large pool (8192 x 2048 -> 2048 of rank 16 37 us with 12 adapters or 128, 80
+// with 512, 88 with 1024; of rank 64 53, 55, 57 and 61).  BF16 adapters of rank 120 and 128 with FP32 outputs have no room for two
+// stages of 128 rows (8192 x 2048 -> 2048 127 us of rank 112, 377 of rank 120).  us of
 // 2048 -> 2048, tiles of 16 and of 128, with 1 adapter, 32, 64 and 256 (* what the rule takes):
 //                    1             32            64            256
 //   rank 16   512   10 * 15      10 * 15      16 * 25      40 * 62

@@ -17,6 +17,9 @@
 // rank 64 75 us, 19 GFLOP with the three terms, 250 TFLOP/s of 600: there the products and their operands out of shared memory
 // count, the loads no more.
 //
+// A stage of x or dy is only read by ldmatrix, and each register that was loaded goes into a product in front of the warp's arrival:
+// it goes back to TMA without a proxy fence.
+//
 // dh and h are FP32; they are taken as sums of three BF16 terms (2^-24 of them is left), as x and dy are BF16 and the sums
 // FP32.  The tensor cores cut an accumulator's low bits off at each step: one chain over 2048 tokens was 6e-6 of the
 // result low, so every 8 stages (48 steps) the chain is added to FP32 sums beside it and starts anew.

@@ -12,11 +12,15 @@
 // and the products in the same warps, cp.async and a barrier for each stage, 16384 x 4096 -> 4096 of rank 16 took 145 to 199 us:
 // 500 instructions a stage and warp, half of them addresses.)
 //
-// 16384 x 4096 -> 4096 of rank 16 take 88 us, 403 MB at 4.6 TB/s, and its dx without the sum 80, 268 MB at 3.4 TB/s; a kernel
-// that only copies so many bytes 128 at a time from row to row takes 61 (52 in longer pieces).  Issue slots are 47% full, of a stage
+// 16384 x 4096 -> 4096 of rank 16 take 88 us, 403 MB at 4.6 TB/s, and its dx without the sum 79, 268 MB at 3.4 TB/s; a kernel
+// that only copies 268 MB 128 bytes at a time from row to row takes 61, 4.4 TB/s (52 in longer pieces, 5.1).  Issue slots are 47% full, of a stage
 // 320 instructions a warp, and with 18 warps an SM the products' and shared memory's latency shows.  At rank 64 registers and shared
 // memory leave one CTA, 9 warps, to an SM: 2000 x 2048 -> 1536 27 us, 8191 rows of dx (1999 -> 4096) 60; issue slots 35% and tensor pipe
 // 27% full, each instruction waits for the last.  (Two warps to the same 16 rows, ranks and outputs shared out, were within 4%.)
+//
+// A stage goes back to TMA without a proxy fence where it was only read by ldmatrix: each register that was loaded goes into a product in
+// front of the warp's arrival, so the read is over.  Where a stage was written to (sums beside y, shifted words) or read by ordinary
+// loads (rows on their way out) a fence stands in front of the arrival, or of the copy.
 #pragma once
 
 #include "lora_launch.cuh"
