@@ -299,8 +299,11 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
                     }
                 };
                 int left = steps, group = 0;                // steps of the sub-slice
-                for (int s = 0; s < x_stages; ++s) {
-                    if (s > 0 && 64 * s % group_cols == 0) close_group(group++);
+                for (int s = 0, next = group_cols; s < x_stages; ++s) {
+                    if (64 * s == next) {
+                        close_group(group++);
+                        next += group_cols;
+                    }
                     if (!failed && !mbar_wait_bounded(&full[buffer], phase, abort_flag, kWaitBudgetCycles)) failed = true;
                     if (busy) {
                         const uint32_t at = base + buffer * lay.stage, sx = at + 2048 * warp + lane_rows(lane);
