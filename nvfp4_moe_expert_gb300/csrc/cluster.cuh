@@ -17,9 +17,20 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-// Every thread of the cluster; what they wrote to shared memory before is visible to all after.
+// Every thread of the cluster; what they wrote to shared memory before is visible to all after.  In two parts, between which
+// work goes on.  The warp's lanes come together first: the aligned forms take them to arrive as one, and branches of single
+// lanes often stand in front.
+__device__ __forceinline__ void cluster_barrier_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_barrier_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_barrier_arrive();
+    cluster_barrier_wait();
 }
 // Address of CTA `rank`'s copy of a shared-memory variable.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {

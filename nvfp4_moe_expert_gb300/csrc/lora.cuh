@@ -96,8 +96,11 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, u
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(row), "r"(slice), "r"(bar)
                  : "memory");
 }
-// The 8 warps that multiply.
-__device__ __forceinline__ void consumer_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// The 8 warps that multiply; each arrives as one.
+__device__ __forceinline__ void consumer_barrier() {
+    __syncwarp();
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"

@@ -214,7 +214,7 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(kThreads) few_
                              keep ? p.h + static_cast<int64_t>(s_row[row]) * p.R : nullptr, p.h_scaled != 0, lane & 15,
                              [&](int at, uint32_t v) { *reinterpret_cast<uint32_t*>(h + at) = v; }, row_undo);
         if ((lane & 15) == 0) s_undo[row] = row_undo;
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // the other CTAs' sums are read
+        cluster_barrier_arrive();                           // the other CTAs' sums are read
         __syncthreads();
         undo[0] = s_undo[quad];
         undo[1] = s_undo[quad + 8];
@@ -252,7 +252,7 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(kThreads) few_
         }
         if (g + kWarps < last_group) load_y(g + kWarps);
     }
-    if (adapter >= 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (adapter >= 0) cluster_barrier_wait();
 }
 
 template <typename T, bool kTrans>

@@ -499,7 +499,6 @@ __global__ void __launch_bounds__(kThreads + 32 * kLoaders, kRank <= 32 && kLoad
             *abort_flag = 1;
         }
     }
-    __syncwarp();
     cluster_barrier();                                      // no CTA leaves while another may reach into it
 }
 
